@@ -27,6 +27,7 @@ ATTN_ERR_CUDA = 4
 ATTN_ERR_DEVICE_TIMEOUT = 5
 ATTN_ERR_DEVICE_BOUNDS = 6
 ATTN_ERR_SCRATCH_TOO_SMALL = 7
+ATTN_ERR_DEVICE_POOL = 8
 ATTN_DTYPE_BF16 = 0
 ATTN_DTYPE_F32 = 1
 
@@ -40,6 +41,13 @@ EXPORTED = (
     "attn_decode_paged",
     "attn_decode_multi",
     "attn_decode_workspace_bytes",
+    "attn_page_step",
+    "attn_qk_norm_rope",
+    "attn_kv_q4_page_bytes",
+    "attn_kv_append_q4",
+    "attn_kv_gather_q4",
+    "attn_decode_q4",
+    "attn_decode_q4_workspace_bytes",
     "attn_get_device_status",
     "attn_status_string",
     "attn_release_workspace",
@@ -116,6 +124,62 @@ class attn_decode_params(ctypes.Structure):
     ]
 
 
+class attn_page_step_params(ctypes.Structure):
+    _fields_ = [
+        ("kv_lens", ctypes.c_void_p), ("keep_lens", ctypes.c_void_p), ("new_lens", ctypes.c_void_p),
+        ("block_table", ctypes.c_void_p), ("free_pages", ctypes.c_void_p), ("free_count", ctypes.c_void_p),
+        ("cu_new", ctypes.c_void_p), ("slots", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+        ("B", ctypes.c_int), ("page_size", ctypes.c_int), ("max_pages", ctypes.c_int), ("num_pages", ctypes.c_int),
+        ("max_tokens", ctypes.c_int),
+        ("stream", ctypes.c_void_p),
+    ]
+
+
+class attn_qk_norm_rope_params(ctypes.Structure):
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("q_out", ctypes.c_void_p), ("k_out", ctypes.c_void_p),
+        ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+        ("B", ctypes.c_int), ("L", ctypes.c_int), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int), ("D", ctypes.c_int),
+        ("eps", ctypes.c_float),
+        ("q_stride", ctypes.c_longlong * 3), ("k_stride", ctypes.c_longlong * 3),
+        ("q_out_stride", ctypes.c_longlong * 3), ("k_out_stride", ctypes.c_longlong * 3),
+        ("rope", attn_rope),
+        ("stream", ctypes.c_void_p),
+    ]
+
+
+class attn_kv_append_q4_params(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("pool", ctypes.c_void_p), ("slots", ctypes.c_void_p),
+        ("T", ctypes.c_int), ("Hkv", ctypes.c_int), ("D", ctypes.c_int), ("page_size", ctypes.c_int),
+        ("num_pages", ctypes.c_int),
+        ("k_stride", ctypes.c_longlong * 2), ("v_stride", ctypes.c_longlong * 2),
+        ("stream", ctypes.c_void_p),
+    ]
+
+
+class attn_kv_gather_q4_params(ctypes.Structure):
+    _fields_ = [
+        ("pool", ctypes.c_void_p), ("block_table", ctypes.c_void_p), ("cu_k", ctypes.c_void_p),
+        ("kv_starts", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("B", ctypes.c_int), ("Hkv", ctypes.c_int), ("D", ctypes.c_int), ("page_size", ctypes.c_int),
+        ("max_pages", ctypes.c_int), ("num_pages", ctypes.c_int), ("total_k", ctypes.c_int),
+        ("stream", ctypes.c_void_p),
+    ]
+
+
+class attn_decode_q4_params(ctypes.Structure):
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("pool", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+        ("kv_lens", ctypes.c_void_p), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+        ("B", ctypes.c_int), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int), ("Lq", ctypes.c_int), ("D", ctypes.c_int),
+        ("page_size", ctypes.c_int), ("max_pages", ctypes.c_int), ("num_pages", ctypes.c_int),
+        ("scale", ctypes.c_float), ("out_dtype", ctypes.c_int), ("chunk", ctypes.c_int),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_ulonglong),
+        ("stream", ctypes.c_void_p),
+    ]
+
+
 _lib = None
 _lock = threading.Lock()
 
@@ -146,6 +210,20 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.attn_decode_multi.restype = I
         lib.attn_decode_workspace_bytes.argtypes = [I, I, I, I, I, I]
         lib.attn_decode_workspace_bytes.restype = ctypes.c_ulonglong
+        lib.attn_page_step.argtypes = [ctypes.POINTER(attn_page_step_params)]
+        lib.attn_page_step.restype = I
+        lib.attn_qk_norm_rope.argtypes = [ctypes.POINTER(attn_qk_norm_rope_params)]
+        lib.attn_qk_norm_rope.restype = I
+        lib.attn_kv_q4_page_bytes.argtypes = [I, I, I]
+        lib.attn_kv_q4_page_bytes.restype = ctypes.c_ulonglong
+        lib.attn_kv_append_q4.argtypes = [ctypes.POINTER(attn_kv_append_q4_params)]
+        lib.attn_kv_append_q4.restype = I
+        lib.attn_kv_gather_q4.argtypes = [ctypes.POINTER(attn_kv_gather_q4_params)]
+        lib.attn_kv_gather_q4.restype = I
+        lib.attn_decode_q4.argtypes = [ctypes.POINTER(attn_decode_q4_params)]
+        lib.attn_decode_q4.restype = I
+        lib.attn_decode_q4_workspace_bytes.argtypes = [I, I, I, I]
+        lib.attn_decode_q4_workspace_bytes.restype = ctypes.c_ulonglong
         lib.attn_get_device_status.argtypes = [P]
         lib.attn_get_device_status.restype = I
         lib.attn_status_string.argtypes = [I]
@@ -424,6 +502,257 @@ def attn_decode_noalloc(q, kcache, vcache, kv_lens, out, lse=None, scale=None, c
     _set_rope(p, rope, D, q.device)
     _check(load().attn_decode_noalloc(ctypes.byref(p)), "attn_decode_noalloc")
     return out, lse
+
+
+def _call(fn, p, device, stream, where):
+    """Run one entry point on `device` (made current for the call) and its stream."""
+    p.stream = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+    if device.index == torch.cuda.current_device():
+        status = fn(ctypes.byref(p))
+    else:
+        with torch.cuda.device(device):
+            status = fn(ctypes.byref(p))
+    if status != ATTN_OK:
+        raise AttnError(status, where)
+
+
+def _rows(t, name, ndim, device):
+    """A bf16 tensor whose rows (the last axis) are contiguous; the other axes may have any stride that is a multiple
+    of 8 elements.  Returns its strides."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dims, got shape {tuple(t.shape)}")
+    if not t.is_cuda or (device is not None and t.device != device):
+        raise ValueError(f"{name} must be a CUDA tensor" + (f" on {device}" if device is not None else ""))
+    st = t.stride()
+    if st[-1] != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    return st
+
+
+def _written_once(t, name):
+    """A tensor to be written: no two of its elements may share memory."""
+    need = 1
+    for n, st in sorted(((n, st) for n, st in zip(t.shape, t.stride()) if n > 1), key=lambda a: a[1]):
+        if st < need:
+            raise ValueError(f"{name}: elements overlap")
+        need = st * (n - 1) + need
+
+
+def attn_page_step(kv_lens, block_table, free_pages, free_count, page_size, new_lens=None, keep_lens=None, slots=None,
+                   positions=None, cu_new=None, stream=None):
+    """Pages and slots of a serving step, on the GPU (all int32): row b keeps keep_lens[b] (default: all) of its
+    kv_lens[b] keys and gets new_lens[b] (default: 0) tokens.  kv_lens [B], block_table [B,max_pages],
+    free_pages [num_pages] (a stack) and free_count [1] are updated in place; slots and positions [max_tokens] and
+    cu_new [B+1], where given, are written.  -> (slots, positions, cu_new)"""
+    _need(kv_lens, "kv_lens", torch.int32, 1)
+    dev = kv_lens.device
+    B = kv_lens.shape[0]
+    _need(block_table, "block_table", torch.int32, 2, device=dev)
+    if block_table.shape[0] != B:
+        raise ValueError("block_table must have B rows")
+    _need(free_pages, "free_pages", torch.int32, 1, device=dev)
+    _need(free_count, "free_count", torch.int32, 1, (1,), dev)
+    p = attn_page_step_params()
+    p.max_tokens = -1
+    for t, name, shape in ((new_lens, "new_lens", (B,)), (keep_lens, "keep_lens", (B,)), (cu_new, "cu_new", (B + 1,)),
+                           (slots, "slots", None), (positions, "positions", None)):
+        if t is None:
+            continue
+        _need(t, name, torch.int32, 1, shape, dev)
+        setattr(p, name, t.data_ptr())
+        if shape is None:
+            if p.max_tokens not in (-1, t.shape[0]):
+                raise ValueError("slots and positions must have the same length")
+            p.max_tokens = t.shape[0]
+    p.max_tokens = max(p.max_tokens, 0)
+    p.kv_lens, p.block_table = kv_lens.data_ptr(), block_table.data_ptr()
+    p.free_pages, p.free_count = free_pages.data_ptr(), free_count.data_ptr()
+    p.B, p.page_size, p.max_pages, p.num_pages = B, int(page_size), block_table.shape[1], free_pages.shape[0]
+    _call(load().attn_page_step, p, dev, stream, "attn_page_step")
+    return slots, positions, cu_new
+
+
+def attn_qk_norm_rope(q, k, q_weight=None, k_weight=None, rope=None, positions=None, eps=1e-6, q_out=None, k_out=None,
+                      stream=None):
+    """RMS norm of every q and k head and its rotation, in one pass: q [T,Hq,D] and k [T,Hkv,D] (packed), or
+    [B,H,L,D] (dense), bf16 with any strides over contiguous rows (k may be None); weights bf16 [D] or None;
+    rope = (cos, sin, style); positions int32 [T] or [B,L], -1 for padded rows, which are left as they were.
+    q_out/k_out may be q/k themselves.  -> (q_out, k_out)"""
+    dense = isinstance(q, torch.Tensor) and q.dim() == 4
+    _rows(q, "q", 4 if dense else 3, None)
+    p = attn_qk_norm_rope_params()
+    dev = q.device
+    shapes = []
+    for x, out, w, name in ((q, q_out, q_weight, "q"), (k, k_out, k_weight, "k")):
+        if x is None:
+            if name == "q" or out is not None or w is not None:
+                raise ValueError("q is needed; k_out and k_weight go with k")
+            shapes.append(None)
+            continue
+        st = _rows(x, name, 4 if dense else 3, dev)
+        if out is None:
+            out = torch.empty(x.shape, dtype=torch.bfloat16, device=dev)
+        elif out is not x:
+            _rows(out, name + "_out", 4 if dense else 3, dev)
+            if out.shape != x.shape:
+                raise ValueError(f"{name}_out must have shape {tuple(x.shape)}, got {tuple(out.shape)}")
+        if not out.is_contiguous():
+            _written_once(out, name + "_out")
+        if w is not None:
+            _need(w, name + "_weight", torch.bfloat16, 1, (x.shape[-1],), dev)
+            setattr(p, name + "_weight", w.data_ptr())
+        so = out.stride()
+        setattr(p, name, x.data_ptr())
+        setattr(p, name + "_out", out.data_ptr())
+        # sequence, token, head
+        setattr(p, name + "_stride", (st[0], st[2], st[1]) if dense else (0, st[0], st[1]))
+        setattr(p, name + "_out_stride", (so[0], so[2], so[1]) if dense else (0, so[0], so[1]))
+        shapes.append(x.shape)
+        if name == "q":
+            q_out = out
+        else:
+            k_out = out
+    sq, sk = shapes
+    if dense:
+        p.B, p.Hq, p.L, p.D = sq
+        if sk is not None and (sk[0], sk[2], sk[3]) != (sq[0], sq[2], sq[3]):
+            raise ValueError(f"k shape {tuple(sk)} does not match q {tuple(sq)}")
+    else:
+        p.B, (p.L, p.Hq, p.D) = 1, sq
+        if sk is not None and (sk[0], sk[2]) != (sq[0], sq[2]):
+            raise ValueError(f"k shape {tuple(sk)} does not match q {tuple(sq)}")
+    p.Hkv = 0 if sk is None else sk[1]
+    p.eps = float(eps)
+    if positions is not None:
+        _need(positions, "positions", torch.int32, 2 if dense else 1, (p.B, p.L) if dense else (p.L,), dev)
+        p.positions = positions.data_ptr()
+    if rope is not None and len(rope) > 3:
+        raise ValueError("rope k_out is taken by prefill calls only")
+    _set_rope(p, rope, p.D, dev)
+    _call(load().attn_qk_norm_rope, p, dev, stream, "attn_qk_norm_rope")
+    return q_out, k_out
+
+
+def _pool_q4(pool, p, device, D=None):
+    """Check a 4-bit cache pool, uint8 [num_pages,Hkv,page_size/16,18*D], and note its sizes."""
+    _need(pool, "pool", torch.uint8, 4, device=device)
+    num_pages, Hkv, tiles, tile = pool.shape
+    if tile not in (18 * 64, 18 * 128) or (D is not None and tile != 18 * D):
+        raise ValueError(f"pool tiles must have 18 * D bytes, got {tile}")
+    p.pool = pool.data_ptr()
+    p.num_pages, p.Hkv, p.page_size, p.D = num_pages, Hkv, 16 * tiles, tile // 18
+
+
+def attn_kv_q4_pool(num_pages, Hkv, page_size, D, device="cuda"):
+    """A new 4-bit cache pool, uint8 [num_pages,Hkv,page_size/16,18*D], all zeros."""
+    if attn_kv_q4_page_bytes(page_size, Hkv, D) == 0:
+        raise AttnError(ATTN_ERR_INVALID_ARG, "attn_kv_q4_pool")
+    return torch.zeros((num_pages, Hkv, page_size // 16, 18 * D), dtype=torch.uint8, device=device)
+
+
+def attn_kv_q4_page_bytes(page_size, Hkv, D) -> int:
+    return int(load().attn_kv_q4_page_bytes(page_size, Hkv, D))
+
+
+def attn_kv_append_q4(k, v, pool, slots, stream=None):
+    """Quantise k and v [T,Hkv,D] bf16 (any strides over contiguous rows) into the 4-bit pool at slots int32 [T]
+    (-1: not written; the others must differ)."""
+    p = attn_kv_append_q4_params()
+    sk = _rows(k, "k", 3, None)
+    dev = k.device
+    sv = _rows(v, "v", 3, dev)
+    _pool_q4(pool, p, dev)
+    T = k.shape[0]
+    if tuple(k.shape) != (T, p.Hkv, p.D) or v.shape != k.shape:
+        raise ValueError(f"k/v shapes {tuple(k.shape)} {tuple(v.shape)} do not match the pool {tuple(pool.shape)}")
+    _need(slots, "slots", torch.int32, 1, (T,), dev)
+    p.k, p.v, p.slots, p.T = k.data_ptr(), v.data_ptr(), slots.data_ptr(), T
+    p.k_stride, p.v_stride = sk[:2], sv[:2]
+    _call(load().attn_kv_append_q4, p, dev, stream, "attn_kv_append_q4")
+
+
+def attn_kv_gather_q4(pool, block_table, cu_k, total_k, kv_starts=None, k_out=None, v_out=None, stream=None):
+    """Read rows of the 4-bit pool back as packed bf16 k and v [total_k,Hkv,D]: keys kv_starts[b] (default 0) and on of
+    sequence b become rows cu_k[b] .. cu_k[b+1]-1 (cu_k int32 [B+1]); rows past cu_k[B] stay as they were.
+    -> (k, v)"""
+    p = attn_kv_gather_q4_params()
+    _pool_q4(pool, p, None)
+    dev = pool.device
+    _need(block_table, "block_table", torch.int32, 2, device=dev)
+    B = block_table.shape[0]
+    _need(cu_k, "cu_k", torch.int32, 1, (B + 1,), dev)
+    if kv_starts is not None:
+        _need(kv_starts, "kv_starts", torch.int32, 1, (B,), dev)
+        p.kv_starts = kv_starts.data_ptr()
+    shape = (int(total_k), p.Hkv, p.D)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    _need(k_out, "k_out", torch.bfloat16, 3, shape, dev)
+    _need(v_out, "v_out", torch.bfloat16, 3, shape, dev)
+    p.block_table, p.cu_k, p.k, p.v = block_table.data_ptr(), cu_k.data_ptr(), k_out.data_ptr(), v_out.data_ptr()
+    p.B, p.max_pages, p.total_k = B, block_table.shape[1], shape[0]
+    _call(load().attn_kv_gather_q4, p, dev, stream, "attn_kv_gather_q4")
+    return k_out, v_out
+
+
+def attn_decode_q4(q, pool, block_table, kv_lens, out=None, lse=None, scale=None, chunk=0, out_dtype=torch.bfloat16,
+                   want_lse=True, workspace=None, stream=None):
+    """Decode over the 4-bit pool: q [B,Hq,D], or [B,Hq,Lq,D] for Lq new tokens, bf16 (already rotated); block_table
+    int32 [B,max_pages], kv_lens int32 [B] counting the new tokens' own keys.  ``workspace`` is a buffer from
+    attn_decode_q4_workspace; without one the library's is used, as by attn_decode.  -> (out, lse) shaped like q"""
+    _need(q, "q", torch.bfloat16, 4 if isinstance(q, torch.Tensor) and q.dim() == 4 else 3)
+    dev = q.device
+    p = attn_decode_q4_params()
+    B, Hq, D = q.shape[0], q.shape[1], q.shape[-1]
+    Lq = q.shape[2] if q.dim() == 4 else 1
+    _pool_q4(pool, p, dev, D)
+    _need(block_table, "block_table", torch.int32, 2, device=dev)
+    _need(kv_lens, "kv_lens", torch.int32, 1, (B,), dev)
+    if block_table.shape[0] != B:
+        raise ValueError("block_table must have B rows")
+    if out is None:
+        out = torch.empty(q.shape, dtype=out_dtype, device=dev)
+    else:
+        _need(out, "out", out_dtype, q.dim(), q.shape, dev)
+    if lse is None and want_lse:
+        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev)
+    elif lse is not None:
+        _need(lse, "lse", torch.float32, q.dim() - 1, q.shape[:-1], dev)
+    if lse is not None:
+        p.lse = lse.data_ptr()
+    p.q, p.block_table, p.kv_lens, p.out = q.data_ptr(), block_table.data_ptr(), kv_lens.data_ptr(), out.data_ptr()
+    p.B, p.Hq, p.Lq, p.max_pages = B, Hq, Lq, block_table.shape[1]
+    p.scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("out must be bf16 or fp32")
+    p.out_dtype = ATTN_DTYPE_F32 if out_dtype == torch.float32 else ATTN_DTYPE_BF16
+    p.chunk = int(chunk)
+    if workspace is not None:
+        _need(workspace, "workspace", torch.uint8, 1, device=dev)
+        p.workspace, p.workspace_bytes = workspace.data_ptr(), workspace.shape[0]
+    _call(load().attn_decode_q4, p, dev, stream, "attn_decode_q4")
+    return out, lse
+
+
+def attn_decode_q4_workspace_bytes(Hq, Hkv, Lq, D) -> int:
+    return int(load().attn_decode_q4_workspace_bytes(Hq, Hkv, Lq, D))
+
+
+def attn_decode_q4_workspace(Hq, Hkv, D, Lq=1, device="cuda"):
+    """A workspace of attn_decode_q4 of one's own (uint8, zeroed), for calls or captured graphs that may overlap others
+    on the GPU."""
+    device = torch.device(device)
+    with torch.cuda.device(device):
+        n = attn_decode_q4_workspace_bytes(Hq, Hkv, Lq, D)
+        if n == 0:
+            raise AttnError(ATTN_ERR_INVALID_ARG, "attn_decode_q4_workspace")
+        return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
 def attn_decode_workspace_bytes(B, Hq, Hkv, Lmax, D, chunk=0) -> int:

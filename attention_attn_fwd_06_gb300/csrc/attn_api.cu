@@ -13,6 +13,7 @@
 
 #include "../../include/attn.h"
 #include "kernels.h"
+#include "kv_q4.h"
 
 // Device status word: kernels record the first problem they see (a kv_len out
 // of range, an expired pipeline wait); attn_get_device_status() reads and
@@ -217,6 +218,57 @@ attn::RopeArgs rope_args(const attn_rope& r) {
   return a;
 }
 
+// The current device's state, or why there is none.
+int device_state(DeviceState** out) {
+  std::lock_guard<std::mutex> lock(g_mu);
+  return device_state_locked(out);
+}
+
+constexpr long long kIntMax = 0x7fffffffLL;
+
+// Sizes of a 4-bit cache pool (page_size keys a page, in tiles of 16).
+int validate_pool_q4(int Hkv, int D, int page_size, int num_pages) {
+  if (Hkv <= 0 || D <= 0 || page_size < attn::kTileKeys || page_size > 65536 || page_size % attn::kTileKeys != 0 ||
+      num_pages < 1)
+    return ATTN_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return ATTN_ERR_UNSUPPORTED;
+  if ((long long)num_pages * page_size > kIntMax || Hkv > 65535) return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
+}
+
+// Strides in elements of rows read or written 16 bytes at a time.
+bool strides8(const long long* s, int n) {
+  for (int i = 0; i < n; ++i)
+    if (s[i] % 8 != 0) return false;
+  return true;
+}
+
+bool aligned128(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 127u) == 0; }
+
+struct DecodeQ4Shape {
+  int rows = 0;              // query rows of a kv head
+  int cols = 0;              // of them per CTA
+  size_t part_o_elems = 0;
+  size_t bytes = 0;          // counters + partials
+};
+
+DecodeQ4Shape decode_q4_shape(int Hq, int Hkv, int Lq, int D, int num_sms) {
+  DecodeQ4Shape s;
+  s.rows = (Hq / Hkv) * Lq;
+  s.cols = attn::decode_q4_cols(s.rows);
+  const size_t prows = (size_t)2 * attn::decode_q4_grid(num_sms, s.rows) * s.cols;
+  s.part_o_elems = prows * D;
+  s.bytes = kCounterBytes + prows * (D + 2) * sizeof(float);
+  return s;
+}
+
+int validate_decode_q4_heads(int Hq, int Hkv, int Lq, int D) {
+  if (Hq <= 0 || Hkv <= 0 || Lq < 1 || D <= 0 || Hq % Hkv != 0) return ATTN_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return ATTN_ERR_UNSUPPORTED;
+  if ((long long)(Hq / Hkv) * Lq > 128) return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
+}
+
 bool is_empty_fwd(const attn_fwd_params* p) {
   const bool varlen = p->cu_seqlens_q != nullptr;
   return p->B == 0 || p->Lq == 0 || (varlen && p->total_q == 0);
@@ -251,6 +303,7 @@ const char* attn_status_string(int status) {
     case ATTN_ERR_DEVICE_TIMEOUT: return "ATTN_ERR_DEVICE_TIMEOUT";
     case ATTN_ERR_DEVICE_BOUNDS: return "ATTN_ERR_DEVICE_BOUNDS";
     case ATTN_ERR_SCRATCH_TOO_SMALL: return "ATTN_ERR_SCRATCH_TOO_SMALL";
+    case ATTN_ERR_DEVICE_POOL: return "ATTN_ERR_DEVICE_POOL";
     default: return "ATTN_STATUS_UNKNOWN";
   }
 }
@@ -639,6 +692,233 @@ int attn_fwd(const void* q, const void* k, const void* v, void* out, float* lse,
   p.out_dtype = ATTN_DTYPE_BF16;
   p.stream = stream;
   return attn_fwd_ex(&p);
+}
+
+int attn_page_step(const attn_page_step_params* p) {
+  if (p == nullptr) return ATTN_ERR_INVALID_ARG;
+  if (p->B < 0 || p->page_size < 1 || p->max_pages < 1 || p->num_pages < 1 || p->max_tokens < 0)
+    return ATTN_ERR_INVALID_ARG;
+  if (p->B > attn::kPageStepMaxRows || (long long)p->num_pages * p->page_size > kIntMax ||
+      (long long)p->B * p->max_pages > kIntMax || (long long)p->max_pages * p->page_size > kIntMax)
+    return ATTN_ERR_UNSUPPORTED;
+  if (p->kv_lens == nullptr || p->block_table == nullptr || p->free_pages == nullptr || p->free_count == nullptr) {
+    if (p->B > 0) return ATTN_ERR_INVALID_ARG;
+  }
+  if (!aligned4(p->kv_lens) || !aligned4(p->keep_lens) || !aligned4(p->new_lens) || !aligned4(p->block_table) ||
+      !aligned4(p->free_pages) || !aligned4(p->free_count) || !aligned4(p->cu_new) || !aligned4(p->slots) ||
+      !aligned4(p->positions))
+    return ATTN_ERR_ALIGNMENT;
+  if (p->B == 0) return ATTN_OK;
+  DeviceState* s = nullptr;
+  const int st = device_state(&s);
+  if (st != ATTN_OK) return st;
+  attn::PageStepLaunch L{};
+  L.kv_lens = p->kv_lens;
+  L.keep_lens = p->keep_lens;
+  L.new_lens = p->new_lens;
+  L.block_table = p->block_table;
+  L.free_pages = p->free_pages;
+  L.free_count = p->free_count;
+  L.cu_new = p->cu_new;
+  L.slots = p->slots;
+  L.positions = p->positions;
+  L.B = p->B;
+  L.page_size = p->page_size;
+  L.max_pages = p->max_pages;
+  L.num_pages = p->num_pages;
+  L.max_tokens = p->slots == nullptr && p->positions == nullptr ? 0 : p->max_tokens;
+  L.status = s->status;
+  L.stream = static_cast<cudaStream_t>(p->stream);
+  return map_cuda(attn::launch_page_step(L));
+}
+
+int attn_qk_norm_rope(const attn_qk_norm_rope_params* p) {
+  if (p == nullptr) return ATTN_ERR_INVALID_ARG;
+  if (p->B < 0 || p->L < 0 || p->Hq <= 0 || p->Hkv < 0 || p->D <= 0) return ATTN_ERR_INVALID_ARG;
+  if (p->D != 64 && p->D != 128) return ATTN_ERR_UNSUPPORTED;
+  if (!std::isfinite(p->eps) || p->eps < 0.f) return ATTN_ERR_INVALID_ARG;
+  const bool rope_on = p->rope.style != ATTN_ROPE_NONE && p->rope.cos != nullptr;
+  int st = validate_rope(p->rope, p->D, 0);
+  if (st != ATTN_OK) return st;
+  if (p->B == 0 || p->L == 0) return ATTN_OK;
+  if (p->q == nullptr || p->q_out == nullptr || (p->Hkv > 0 && (p->k == nullptr || p->k_out == nullptr)) ||
+      (rope_on && p->positions == nullptr))
+    return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(p->q) || !aligned16(p->q_out) || !aligned16(p->q_weight) || !aligned16(p->k_weight) ||
+      !aligned4(p->positions) || !strides8(p->q_stride, 3) || !strides8(p->q_out_stride, 3))
+    return ATTN_ERR_ALIGNMENT;
+  if (p->Hkv > 0 &&
+      (!aligned16(p->k) || !aligned16(p->k_out) || !strides8(p->k_stride, 3) || !strides8(p->k_out_stride, 3)))
+    return ATTN_ERR_ALIGNMENT;
+  if ((long long)p->B * p->L > kIntMax || (long long)p->Hq + p->Hkv > 65535) return ATTN_ERR_UNSUPPORTED;
+  DeviceState* s = nullptr;
+  st = device_state(&s);
+  if (st != ATTN_OK) return st;
+  attn::QkNormRopeLaunch L{};
+  L.q = p->q;
+  L.k = p->k;
+  L.q_out = p->q_out;
+  L.k_out = p->k_out;
+  L.q_weight = p->q_weight;
+  L.k_weight = p->k_weight;
+  L.positions = p->positions;
+  L.B = p->B;
+  L.L = p->L;
+  L.Hq = p->Hq;
+  L.Hkv = p->Hkv;
+  L.D = p->D;
+  L.eps = p->eps;
+  for (int i = 0; i < 3; ++i) {
+    L.qs[i] = p->q_stride[i];
+    L.ks[i] = p->k_stride[i];
+    L.qos[i] = p->q_out_stride[i];
+    L.kos[i] = p->k_out_stride[i];
+  }
+  L.rope = rope_args(p->rope);
+  L.status = s->status;
+  L.stream = static_cast<cudaStream_t>(p->stream);
+  return map_cuda(attn::launch_qk_norm_rope(L));
+}
+
+unsigned long long attn_kv_q4_page_bytes(int page_size, int Hkv, int D) {
+  if (validate_pool_q4(Hkv, D, page_size, 1) != ATTN_OK) return 0;
+  return (unsigned long long)(page_size / attn::kTileKeys) * Hkv * attn::kv_q4_tile_bytes(D);
+}
+
+int attn_kv_append_q4(const attn_kv_append_q4_params* p) {
+  if (p == nullptr) return ATTN_ERR_INVALID_ARG;
+  int st = validate_pool_q4(p->Hkv, p->D, p->page_size, p->num_pages);
+  if (st != ATTN_OK) return st;
+  if (p->T < 0) return ATTN_ERR_INVALID_ARG;
+  if (p->T == 0) return ATTN_OK;
+  if (p->k == nullptr || p->v == nullptr || p->pool == nullptr || p->slots == nullptr) return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(p->k) || !aligned16(p->v) || !aligned128(p->pool) || !aligned4(p->slots) ||
+      !strides8(p->k_stride, 2) || !strides8(p->v_stride, 2))
+    return ATTN_ERR_ALIGNMENT;
+  DeviceState* s = nullptr;
+  st = device_state(&s);
+  if (st != ATTN_OK) return st;
+  attn::KvAppendQ4Launch L{};
+  L.k = p->k;
+  L.v = p->v;
+  L.pool = p->pool;
+  L.slots = p->slots;
+  L.T = p->T;
+  L.Hkv = p->Hkv;
+  L.D = p->D;
+  L.page_size = p->page_size;
+  L.num_pages = p->num_pages;
+  for (int i = 0; i < 2; ++i) {
+    L.ks[i] = p->k_stride[i];
+    L.vs[i] = p->v_stride[i];
+  }
+  L.status = s->status;
+  L.stream = static_cast<cudaStream_t>(p->stream);
+  return map_cuda(attn::launch_kv_append_q4(L));
+}
+
+int attn_kv_gather_q4(const attn_kv_gather_q4_params* p) {
+  if (p == nullptr) return ATTN_ERR_INVALID_ARG;
+  int st = validate_pool_q4(p->Hkv, p->D, p->page_size, p->num_pages);
+  if (st != ATTN_OK) return st;
+  if (p->B < 0 || p->max_pages < 1 || p->total_k < 0) return ATTN_ERR_INVALID_ARG;
+  if ((long long)p->max_pages * p->page_size > kIntMax) return ATTN_ERR_UNSUPPORTED;
+  if (p->B == 0 || p->total_k == 0) return ATTN_OK;
+  if (p->pool == nullptr || p->block_table == nullptr || p->cu_k == nullptr || p->k == nullptr || p->v == nullptr)
+    return ATTN_ERR_INVALID_ARG;
+  if (!aligned128(p->pool) || !aligned16(p->k) || !aligned16(p->v) || !aligned4(p->block_table) ||
+      !aligned4(p->cu_k) || !aligned4(p->kv_starts))
+    return ATTN_ERR_ALIGNMENT;
+  DeviceState* s = nullptr;
+  st = device_state(&s);
+  if (st != ATTN_OK) return st;
+  attn::KvGatherQ4Launch L{};
+  L.pool = p->pool;
+  L.block_table = p->block_table;
+  L.cu_k = p->cu_k;
+  L.kv_starts = p->kv_starts;
+  L.k = p->k;
+  L.v = p->v;
+  L.B = p->B;
+  L.Hkv = p->Hkv;
+  L.D = p->D;
+  L.page_size = p->page_size;
+  L.max_pages = p->max_pages;
+  L.num_pages = p->num_pages;
+  L.total_k = p->total_k;
+  L.status = s->status;
+  L.stream = static_cast<cudaStream_t>(p->stream);
+  return map_cuda(attn::launch_kv_gather_q4(L));
+}
+
+unsigned long long attn_decode_q4_workspace_bytes(int Hq, int Hkv, int Lq, int D) {
+  if (validate_decode_q4_heads(Hq, Hkv, Lq, D) != ATTN_OK) return 0;
+  DeviceState* s = nullptr;
+  const int sms = device_state(&s) == ATTN_OK ? s->num_sms : 0;
+  return decode_q4_shape(Hq, Hkv, Lq, D, sms).bytes;
+}
+
+int attn_decode_q4(const attn_decode_q4_params* p) {
+  if (p == nullptr) return ATTN_ERR_INVALID_ARG;
+  int st = validate_decode_q4_heads(p->Hq, p->Hkv, p->Lq, p->D);
+  if (st != ATTN_OK) return st;
+  st = validate_pool_q4(p->Hkv, p->D, p->page_size, p->num_pages);
+  if (st != ATTN_OK) return st;
+  if (p->B < 0 || p->max_pages < 1) return ATTN_ERR_INVALID_ARG;
+  if (p->out_dtype != ATTN_DTYPE_BF16 && p->out_dtype != ATTN_DTYPE_F32) return ATTN_ERR_INVALID_ARG;
+  if (p->chunk < 0 || p->chunk > (1 << 20)) return ATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(p->scale)) return ATTN_ERR_INVALID_ARG;
+  if ((long long)p->max_pages * p->page_size > kIntMax - attn::kTileKeys) return ATTN_ERR_UNSUPPORTED;
+  if (p->B == 0) return ATTN_OK;
+  if (p->q == nullptr || p->pool == nullptr || p->block_table == nullptr || p->kv_lens == nullptr ||
+      p->out == nullptr)
+    return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(p->q) || !aligned128(p->pool) || !aligned16(p->out) || !aligned16(p->workspace) ||
+      !aligned4(p->block_table) || !aligned4(p->kv_lens) || !aligned4(p->lse))
+    return ATTN_ERR_ALIGNMENT;
+  if ((long long)p->B * p->Hq * p->Lq > kIntMax) return ATTN_ERR_UNSUPPORTED;
+  cudaStream_t stream = static_cast<cudaStream_t>(p->stream);
+  std::lock_guard<std::mutex> lock(g_mu);
+  DeviceState* s = nullptr;
+  st = device_state_locked(&s);
+  if (st != ATTN_OK) return st;
+  const DecodeQ4Shape sh = decode_q4_shape(p->Hq, p->Hkv, p->Lq, p->D, s->num_sms);
+  if (2 + (long long)p->B * p->Hkv * ((sh.rows + sh.cols - 1) / sh.cols) > attn::kDecodeCounterSlots)
+    return ATTN_ERR_UNSUPPORTED;
+  char* ws = static_cast<char*>(p->workspace);
+  if (ws == nullptr) {
+    st = ensure_workspace_locked(*s, sh.bytes, stream);
+    if (st != ATTN_OK) return st;
+    ws = static_cast<char*>(s->ws);
+  } else if (p->workspace_bytes < sh.bytes) {
+    return ATTN_ERR_SCRATCH_TOO_SMALL;
+  }
+  attn::DecodeQ4Launch L{};
+  L.q = p->q;
+  L.pool = p->pool;
+  L.block_table = p->block_table;
+  L.kv_lens = p->kv_lens;
+  L.out = p->out;
+  L.lse = p->lse;
+  L.counters = reinterpret_cast<unsigned*>(ws);
+  L.part_o = reinterpret_cast<float*>(ws + kCounterBytes);
+  L.part_ml = L.part_o + sh.part_o_elems;
+  L.B = p->B;
+  L.Hq = p->Hq;
+  L.Hkv = p->Hkv;
+  L.Lq = p->Lq;
+  L.D = p->D;
+  L.page_size = p->page_size;
+  L.max_pages = p->max_pages;
+  L.num_pages = p->num_pages;
+  L.min_tiles = p->chunk > 0 ? (p->chunk + attn::kTileKeys - 1) / attn::kTileKeys : 4;
+  L.scale = p->scale;
+  L.out_f32 = p->out_dtype == ATTN_DTYPE_F32;
+  L.num_sms = s->num_sms;
+  L.status = s->status;
+  L.fault_skip_arrive = fault_skip_arrive();
+  L.stream = stream;
+  return map_cuda(attn::launch_decode_q4(L));
 }
 
 int attn_get_device_status(void* stream) {

@@ -1,0 +1,810 @@
+// decode_q4.cu -- decode attention over the 4-bit paged KV cache (layout: kv_q4.h), one or several new tokens a
+// sequence, split along the keys, with the log-sum-exp combine in the same launch.
+//
+// A cached row x of a group of 64 dims reads back as s u + m, u in 0..15.  So
+//   q . k   = sum over groups of  s_k (q . u_k) + m_k (sum of q over the group)
+//   sum p v = sum over keys of    (p s_v) u_v   + (sum of p m_v)
+// and the matrix products run over the codes themselves: scales and minima are applied to scores and weights, once per
+// key and group, not once per element.
+//
+// What bounds it: 0.5625 bytes an element and 4 heads an element leave 3.5 times fewer bytes than bf16 for the same
+// arithmetic.  At the copy bandwidth an SM takes some 40 elements a clock; four heads' multiply-adds alone would
+// exceed its fp32 units.  So products run on the tensor cores -- mma.sync m16n8k16 in fp16, whose A operand
+// comes straight from registers: K^T and V^T tiles are 16 keys (dims) by 16, the 8 columns are the query rows of one
+// kv head.  A tcgen05 product would need the unpacked tile written to shared or tensor memory first, four times the
+// bytes of the codes, for an N of 8.
+//  * Unpacking costs one mask per two elements: (w & 0x000f000f) is, as a pair of fp16, the subnormals u 2^-24, and
+//    (w & 0x00f000f0) is u 2^-20, both exact; the factors go into q (2^10 and 2^6, q first scaled by a power of two
+//    to a largest element in [16, 32), which is exact) and, for V, into the output.  One shift by 8 gives the
+//    other two pairs of a word.  For V, whose pairs run along keys, a byte permute first joins two keys' halves.
+//  * Scores come as S^T (keys by query rows), so a column's maximum is two registers and three shuffles for 32 keys,
+//    and the weights turn into the second product's B operand by two 8x8 transposes (movmatrix).
+//  * Weights are p s_v 2^x rounded to fp16 (2^-12 relative, against 2^-9 of a bf16 output), x kept such that they stay
+//    below 2^15 and the largest near 2^12; a call with fp32 output carries them as two fp16 terms.  Maxima, sums,
+//    the term in m_v and all accumulators are fp32.
+// The split is decode.cu's: persistent CTAs take equal slices of the tiles of all (sequence, kv head, row chunk) rows, a
+// producer warp streams them with bulk copies (one copy per page and stage) into a shared-memory ring, the CTA
+// that lands a row's last partial merges it.
+#include <cfloat>
+#include <cmath>
+#include <cuda_fp16.h>
+#include <type_traits>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "kv_q4.h"
+#include "rope.cuh"
+#include "slice_map.h"
+
+namespace attn {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+#ifndef ATTN_Q4_ROW_COST
+#define ATTN_Q4_ROW_COST 16
+#endif
+constexpr int kRowCostTiles = ATTN_Q4_ROW_COST;  // tiles charged to every row for its piece-end work
+
+// NT: groups of 8 query rows a CTA serves.
+template <int D, int NT>
+struct Q4Cfg {
+  static constexpr int G = D / 64;                      // scale groups of a row
+  static constexpr int COLS = 8 * NT;                   // query rows per CTA
+  static constexpr int NW = 4;                          // consumer warps
+  static constexpr int KT = 2;                          // tiles of a stage per consumer warp
+  static constexpr int ST = NW * KT;                    // tiles per stage (128 keys)
+  static constexpr int TILE = kv_q4_tile_bytes(D);
+  static constexpr int STAGE = ST * TILE;
+  static constexpr int MINB = NT == 1 ? 3 : 2;          // resident CTAs per SM
+  static constexpr int NS = (NT == 1 ? 4 : 6) * (D == 128 ? 1 : 2);  // ring stages
+  static constexpr int THREADS = 32 * (NW + 1);
+  static constexpr int LENS_CACHE = 384;                // kv_lens kept in shared memory for the walk
+  static constexpr int OSTR = D + 4;                    // floats between columns of a warp's parked O
+  static constexpr int OFF_BAR = NS * STAGE;            // full[NS], empty[NS], info_bar[NS]
+  static constexpr int OFF_INFO = OFF_BAR + 3 * NS * 8;
+  static constexpr int OFF_M = OFF_INFO + NS * 32;      // mbuf[NW][8]
+  static constexpr int OFF_L = OFF_M + NW * 8 * 4;      // lbuf[NW][8]
+  static constexpr int OFF_LENS = OFF_L + NW * 8 * 4;
+  static constexpr int OFF_MISC = OFF_LENS + LENS_CACHE * 4;
+  static constexpr int SMEM = OFF_MISC + 16;
+  static_assert(NW * 8 * OSTR * 4 <= STAGE, "the piece-end merge parks every warp's O in one stage");
+  static_assert(MINB * (SMEM + 1024) <= 228 * 1024, "MINB CTAs per SM");
+  static_assert(ST <= 32, "a stage spans at most one page per lane");
+};
+
+struct Q4StageInfo {
+  int b;       // sequence; -1 marks the end of the work
+  int hg;      // kv head * chunks + chunk
+  int tile0;   // the stage's first tile of the sequence
+  int nt;      // tiles in this stage
+  int flags;   // 1: first stage of a row piece, 2: last
+  int np;      // CTAs holding a piece of this row (0: no keys, 1: whole row here)
+  int slot;    // this CTA's partial slot for the piece
+  int lo_par;  // 2 * first CTA holding a piece + its slot parity
+};
+
+__device__ __forceinline__ int clamp_len(int len, int Lmax) { return len < 0 ? 0 : (len > Lmax ? Lmax : len); }
+
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 8x8 transpose of 16-bit elements across the warp.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ float2 half2_floats(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
+__device__ __forceinline__ void store_out4(void* out, size_t idx, float4 v, int out_f32) {
+  if (out_f32) {
+    *reinterpret_cast<float4*>(reinterpret_cast<float*>(out) + idx) = v;
+  } else {
+    *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(out) + idx) =
+        make_uint2(pack2_bf16(v.x, v.y), pack2_bf16(v.z, v.w));
+  }
+}
+
+constexpr uint32_t kLowNibble = 0x000f000fu, kHighNibble = 0x00f000f0u;
+
+// WIDE: the weights of the second product as two fp16 terms (fp32 output).
+template <int D, int NT, bool WIDE>
+__global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MINB)
+    decode_q4_kernel(const DecodeQ4Launch p, const int chunks, const int rows) {
+  using C = Q4Cfg<D, NT>;
+  constexpr int G = C::G;
+  extern __shared__ __align__(128) uint8_t smem[];
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* empty = full + C::NS;
+  uint64_t* told = empty + C::NS;  // the stage's record is written (its data may still be on the way)
+  Q4StageInfo* info = reinterpret_cast<Q4StageInfo*>(smem + C::OFF_INFO);
+  float* mbuf = reinterpret_cast<float*>(smem + C::OFF_M);
+  float* lbuf = reinterpret_cast<float*>(smem + C::OFF_L);
+  int* lens_s = reinterpret_cast<int*>(smem + C::OFF_LENS);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC);
+  volatile int* last_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int Hg = p.Hkv * chunks;  // rows per sequence
+  const int cta = blockIdx.x;
+  const int Lmax = p.max_pages * p.page_size;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::NS; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], C::NW);
+      mbar_init(&told[s], 1);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  const int len_first = (warp == C::NW && lane < p.B) ? p.kv_lens[lane] : 0;
+  __syncthreads();
+
+  if (warp == C::NW) {
+    // ---------------- producer: walk this CTA's slice of the tiles ----------------
+    long long tsum = 0;
+    int nonempty = 0;
+    for (int b = lane; b < p.B; b += 32) {
+      const int raw = (b == lane) ? len_first : p.kv_lens[b];
+      const int len = clamp_len(raw, Lmax);
+      if (raw != len && cta == 0) record_status(p.status, ATTN_ERR_DEVICE_BOUNDS);
+      if (b < C::LENS_CACHE) lens_s[b] = len;
+      tsum += (len + kTileKeys - 1) / kTileKeys;
+      nonempty += len > 0 ? 1 : 0;
+    }
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) {
+      tsum += __shfl_xor_sync(0xffffffffu, tsum, off);
+      nonempty += __shfl_xor_sync(0xffffffffu, nonempty, off);
+    }
+    __syncwarp();
+    auto seq_len = [&](int b) -> int { return b < C::LENS_CACHE ? lens_s[b] : clamp_len(p.kv_lens[b], Lmax); };
+    auto seq_tiles = [&](int b) -> int { return (seq_len(b) + kTileKeys - 1) / kTileKeys; };
+    const long long W = tsum * Hg;
+    // Slices of at least min_tiles tiles, but never fewer slices than rows with keys.
+    long long geff = floor_div(W + p.min_tiles - 1, p.min_tiles);
+    if (geff < (long long)nonempty * Hg) geff = (long long)nonempty * Hg;
+    if (geff > (long long)gridDim.x) geff = gridDim.x;
+    if (geff < 1) geff = 1;
+    // Every row occupies [rs, rs + kRowCostTiles + tiles) of the cost space, its tiles last.
+    const long long Wc = W + (long long)kRowCostTiles * nonempty * Hg;
+    const SliceMap sm = make_slice_map(Wc, geff, C::MINB, gridDim.x);
+    const long long lo = sm.start(cta);
+    const long long hi = sm.start(cta + 1);
+
+    int t = 0;  // stages issued
+    bool ok = true;
+    const uint64_t policy = l2_policy_evict_first();  // the cache is read once
+    const int tpp = p.page_size / kTileKeys;
+    int win_b = -1, win_base = 0, my_page = 0;  // lane i: block-table entry of page win_base + i of sequence win_b
+    auto need_pages = [&](int b, int first, int last) {
+      if (b == win_b && first >= win_base && last < win_base + 32) return;
+      win_b = b;
+      win_base = first;
+      const int pg = first + lane;
+      my_page = 0;
+      if (pg < p.max_pages && (long long)pg * p.page_size < seq_len(b))
+        my_page = p.block_table[(size_t)b * p.max_pages + pg];
+    };
+    // Tiles [t0, t0 + nt) of (b, hkv) to dst: lane j copies the part on the run's page first + j.
+    auto copy_tiles = [&](int b, int hkv, int t0, int nt, uint8_t* dst, uint64_t* bar) {
+      const int first = t0 / tpp, last = (t0 + nt - 1) / tpp;
+      need_pages(b, first, last);
+      const int pg = first + lane;
+      int page = __shfl_sync(0xffffffffu, my_page, min(pg, last) - win_base);
+      if (pg <= last) {
+        if (page < 0 || page >= p.num_pages) {
+          record_status(p.status, ATTN_ERR_DEVICE_BOUNDS);  // out-of-pool page id: read page 0 instead
+          page = 0;
+        }
+        const int tl = max(t0, pg * tpp), th = min(t0 + nt, (pg + 1) * tpp);
+        bulk_g2s_hint(dst + (size_t)(tl - t0) * C::TILE,
+                      reinterpret_cast<const uint8_t*>(p.pool) + kv_q4_tile_at(page, hkv, tl - pg * tpp, p.Hkv, tpp, D),
+                      (uint32_t)(th - tl) * C::TILE, bar, policy);
+      }
+    };
+    auto wait_empty = [&](int slot_r) -> bool {
+      int okw = 1;
+      if (lane == 0) okw = mbar_wait(&empty[slot_r], ((t / C::NS) - 1) & 1, p.status, abort_flag) ? 1 : 0;
+      return __shfl_sync(0xffffffffu, okw, 0) != 0;
+    };
+    // Stream tiles [tb, te) of row (b, hg), whose tiles sit at cost positions [ks, ks + tiles); te == tb emits one
+    // empty stage (a sequence with no keys).
+    auto emit = [&](int b, int hg, int tb, int te, long long ks, bool first_in_slice) -> bool {
+      const int hkv = hg / chunks;
+      const int n = te - tb;
+      const int nst = n > 0 ? (n + C::ST - 1) / C::ST : 1;
+      int np = 0, slot = 0, lo_par = 0;
+      for (int u = 0; u < nst; ++u, ++t) {
+        const int slot_r = t % C::NS;
+        if (t >= C::NS && !wait_empty(slot_r)) return false;
+        const int t0 = tb + u * C::ST;
+        const int nt = n > 0 ? min(C::ST, te - t0) : 0;
+        if (lane == 0 && nt > 0) mbar_expect_tx(&full[slot_r], (uint32_t)nt * C::TILE);
+        __syncwarp();
+        if (nt > 0) copy_tiles(b, hkv, t0, nt, smem + slot_r * C::STAGE, &full[slot_r]);
+        if (u == 0 && nt > 0) {
+          // Which CTAs hold a piece of this row, and this piece's partial slot.
+          const long long last = ks + seq_tiles(b) - 1;
+          int c_lo = 0, c_hi = cta;
+          for (int top = cta;; top -= 32) {  // c_lo: the largest c <= cta with start(c) <= ks
+            const unsigned m = __ballot_sync(0xffffffffu, top - lane >= 0 && sm.starts_by(top - lane, ks));
+            if (m) {
+              c_lo = top - (__ffs(m) - 1);
+              break;
+            }
+          }
+          for (int bot = cta + 1;; bot += 32) {  // c_hi: the largest c with start(c) <= last
+            const unsigned m = __ballot_sync(0xffffffffu, bot + lane >= sm.g || !sm.starts_by(bot + lane, last));
+            if (m) {
+              c_hi = bot + (__ffs(m) - 1) - 1;
+              break;
+            }
+          }
+          np = c_hi - c_lo + 1;
+          slot = 2 * cta + (first_in_slice ? 0 : 1);
+          lo_par = 2 * c_lo + (sm.starts_by(c_lo, ks - 1) ? 1 : 0);
+        }
+        if (lane == 0) {
+          Q4StageInfo si;
+          si.b = b;
+          si.hg = hg;
+          si.tile0 = t0;
+          si.nt = nt;
+          si.flags = (u == 0 ? 1 : 0) | (u == nst - 1 ? 2 : 0);
+          si.np = np;
+          si.slot = slot;
+          si.lo_par = lo_par;
+          info[slot_r] = si;
+          mbar_arrive(&told[slot_r]);
+          mbar_arrive(&full[slot_r]);
+        }
+      }
+      return true;
+    };
+
+    if (lo < hi) {
+      long long acc = 0;  // first cost position of sequence b
+      int b = 0, nt = 0;
+      for (; b < p.B; ++b) {
+        nt = seq_tiles(b);
+        const long long rc = nt > 0 ? (long long)nt + kRowCostTiles : 0;
+        if (acc + (long long)Hg * rc > lo) break;
+        acc += (long long)Hg * rc;
+      }
+      long long rcost = (long long)nt + kRowCostTiles;
+      int hg = (int)floor_div(lo - acc, rcost);
+      long long rs = acc + (long long)hg * rcost;
+      long long pos = lo;
+      while (ok && pos < hi) {
+        const long long ks = rs + kRowCostTiles;
+        const long long a = max(pos, ks), e = min(hi, ks + nt);
+        if (a < e) ok = emit(b, hg, (int)(a - ks), (int)(e - ks), ks, a == lo);
+        pos = rs + rcost;
+        rs += rcost;
+        if (++hg == Hg) {
+          hg = 0;
+          for (++b; b < p.B; ++b) {
+            nt = seq_tiles(b);
+            if (nt > 0) break;
+          }
+          rcost = (long long)nt + kRowCostTiles;
+        }
+      }
+    }
+    if (nonempty < p.B) {  // rows of sequences with no keys, one row per CTA in turn
+      for (long long e = cta; ok && e < (long long)p.B * Hg; e += gridDim.x) {
+        const int b = (int)floor_div(e, Hg);
+        if (seq_len(b) == 0) ok = emit(b, (int)(e - (long long)b * Hg), 0, 0, 0, false);
+      }
+    }
+    if (ok) {  // end-of-work marker
+      const int slot_r = t % C::NS;
+      if (t < C::NS || wait_empty(slot_r)) {
+        if (lane == 0) {
+          info[slot_r].b = -1;
+          mbar_arrive(&told[slot_r]);
+        }
+      }
+    }
+    if (lane == 0 && *abort_flag) {
+      // Let copies already in flight land before the CTA's shared memory is released.
+      for (int u = (t > C::NS ? t - C::NS : 0); u < t; ++u)
+        mbar_wait(&full[u % C::NS], (u / C::NS) & 1, p.status, nullptr);
+    }
+    return;
+  }
+
+  // ---------------- consumers ----------------
+  const int ctid = threadIdx.x;
+  constexpr int nct = C::NW * 32;
+  const int g = lane >> 2, t4 = lane & 3;
+  const int kg = g ^ ((g >> 2) & 1);             // key of the tile's score row g (row g + 8: kg + 8)
+  const int kv0 = 2 * t4 + (t4 >> 1);            // keys of score rows 2 t4 and 2 t4 + 1: this order keeps
+  const int kv1 = 2 * t4 + 1 - (t4 >> 1);        // the four lanes' 32-byte rows in different banks, for K and for V
+  auto release = [&](int slot, int t) {
+    if (lane == 0 && !(p.fault_skip_arrive && cta == 0 && t == 1)) mbar_arrive(&empty[slot]);
+  };
+
+  int t = 0;  // stages consumed
+  while (true) {
+    int slot = t % C::NS;
+    if (!mbar_wait(&told[slot], (t / C::NS) & 1, p.status, abort_flag)) break;
+    Q4StageInfo si = info[slot];
+    if (si.b < 0) break;
+    const int hkv = si.hg / chunks;
+    const int row0 = (si.hg - hkv * chunks) * C::COLS;  // first query row of the kv head this CTA serves
+    const int len = clamp_len(p.kv_lens[si.b], Lmax);
+    // ---- q of the piece, as the first product's B operand ----
+    uint32_t qf[NT][4 * G][2];
+    float f[NT][2], qs[NT][G][2];  // of columns 2 t4 and 2 t4 + 1: score factor, q's sums
+    int vis[NT][2];                // keys the column sees
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = row0 + 8 * nt + g;
+      const __nv_bfloat16* qrow = reinterpret_cast<const __nv_bfloat16*>(p.q) +
+                                  (((size_t)si.b * p.Hkv + hkv) * rows + min(r, rows - 1)) * D;
+      float v[G][16];
+      float amax = 0.f;
+#pragma unroll
+      for (int gg = 0; gg < G; ++gg) {
+        const uint4* src = reinterpret_cast<const uint4*>(qrow + 64 * gg + 16 * t4);
+        const uint4 w0 = __ldg(src), w1 = __ldg(src + 1);
+        unpack8(w0, *reinterpret_cast<float(*)[8]>(v[gg]));
+        unpack8(w1, *reinterpret_cast<float(*)[8]>(v[gg] + 8));
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          v[gg][j] = r < rows ? v[gg][j] : 0.f;
+          amax = fmaxf(amax, fabsf(v[gg][j]));
+        }
+      }
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      // e with 2^e <= amax < 2^(e+1); q 2^(4 - e) lies below 32 (elements 2^-25 of the largest and less lose bits)
+      const int e = amax > 0.f ? max((int)(__float_as_uint(amax) >> 23) - 127, -100) : 0;
+      const float up = __uint_as_float((unsigned)(127 + 4 - e) << 23);
+      const float fc = p.scale * kLog2e * __uint_as_float((unsigned)(127 - 4 + e) << 23) * 16384.f;
+      float sum[G];
+#pragma unroll
+      for (int gg = 0; gg < G; ++gg) {
+        sum[gg] = 0.f;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          v[gg][j] *= up;
+          sum[gg] += v[gg][j];
+        }
+        sum[gg] += __shfl_xor_sync(0xffffffffu, sum[gg], 1);
+        sum[gg] += __shfl_xor_sync(0xffffffffu, sum[gg], 2);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float* x = v[gg] + 8 * j;
+          qf[nt][4 * gg + 2 * j][0] = half2_bits(x[0] * 1024.f, x[4] * 1024.f);
+          qf[nt][4 * gg + 2 * j][1] = half2_bits(x[1] * 64.f, x[5] * 64.f);
+          qf[nt][4 * gg + 2 * j + 1][0] = half2_bits(x[2] * 1024.f, x[6] * 1024.f);
+          qf[nt][4 * gg + 2 * j + 1][1] = half2_bits(x[3] * 64.f, x[7] * 64.f);
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        f[nt][c] = __shfl_sync(0xffffffffu, fc, 8 * t4 + 4 * c);
+#pragma unroll
+        for (int gg = 0; gg < G; ++gg)
+          qs[nt][gg][c] = __shfl_sync(0xffffffffu, sum[gg], 8 * t4 + 4 * c) * (1.f / 16384.f);
+        vis[nt][c] = len - p.Lq + 1 + (row0 + 8 * nt + 2 * t4 + c) % p.Lq;
+      }
+    }
+    float o[4 * G][NT][4];   // O^T: dims 64 gg + 8 g + 2 mt (+1), columns 2 t4 (+1)
+    float z[G][NT][2];       // this lane's share of sum p m_v
+    float m[NT][2], l[NT][2];
+    float wscale = 1073741824.f;  // power of two the weights carry (2^30 until the first scales are seen)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int i = 0; i < 4 * G; ++i) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        m[nt][c] = -INFINITY;
+        l[nt][c] = 0.f;
+#pragma unroll
+        for (int gg = 0; gg < G; ++gg) z[gg][nt][c] = 0.f;
+      }
+    }
+    const int all_see = len - p.Lq + 1;  // keys below it are seen by every column
+
+    // N tiles at `tp`, the first of which is tile `tile` of the sequence.
+    auto process = [&](const uint8_t* tp, int tile, auto n_c) {
+      constexpr int N = decltype(n_c)::value;
+      const int key0 = tile * kTileKeys;
+      const bool edge = key0 + N * kTileKeys > all_see;
+      float x[N][NT][4];
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const uint8_t* tb = tp + i * C::TILE;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) x[i][nt][0] = x[i][nt][1] = x[i][nt][2] = x[i][nt][3] = 0.f;
+#pragma unroll
+        for (int gg = 0; gg < G; ++gg) {
+          const uint2 wa = *reinterpret_cast<const uint2*>(tb + gg * 512 + kg * 32 + t4 * 8);
+          const uint2 wb = *reinterpret_cast<const uint2*>(tb + gg * 512 + (kg + 8) * 32 + t4 * 8);
+          float acc[NT][4];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t a = j ? wa.y : wa.x, b = j ? wb.y : wb.x;
+            const uint32_t a8 = a >> 8, b8 = b >> 8;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma_16816(acc[nt], a & kLowNibble, b & kLowNibble, a & kHighNibble, b & kHighNibble,
+                        qf[nt][4 * gg + 2 * j][0], qf[nt][4 * gg + 2 * j][1]);
+              mma_16816(acc[nt], a8 & kLowNibble, b8 & kLowNibble, a8 & kHighNibble, b8 & kHighNibble,
+                        qf[nt][4 * gg + 2 * j + 1][0], qf[nt][4 * gg + 2 * j + 1][1]);
+            }
+          }
+          const float2 pa = half2_floats(*reinterpret_cast<const uint32_t*>(tb + kv_q4_kp_off(D) + (kg * G + gg) * 4));
+          const float2 pb =
+              half2_floats(*reinterpret_cast<const uint32_t*>(tb + kv_q4_kp_off(D) + ((kg + 8) * G + gg) * 4));
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              x[i][nt][c] += fmaf(pa.x, acc[nt][c], pa.y * qs[nt][gg][c]);
+              x[i][nt][2 + c] += fmaf(pb.x, acc[nt][2 + c], pb.y * qs[nt][gg][c]);
+            }
+        }
+      }
+      // logits in log2 units, masked; column maxima
+      float mx[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          mx[nt][c] = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            x[i][nt][c] *= f[nt][c];
+            x[i][nt][2 + c] *= f[nt][c];
+            if (edge) {
+              const int k = key0 + i * kTileKeys + kg;
+              if (k >= vis[nt][c]) x[i][nt][c] = -INFINITY;
+              if (k + 8 >= vis[nt][c]) x[i][nt][2 + c] = -INFINITY;
+            }
+            mx[nt][c] = max3f(mx[nt][c], x[i][nt][c], x[i][nt][2 + c]);
+          }
+#pragma unroll
+          for (int mask = 4; mask < 32; mask <<= 1)
+            mx[nt][c] = fmaxf(mx[nt][c], __shfl_xor_sync(0xffffffffu, mx[nt][c], mask));
+        }
+      bool rose = false;
+      float alpha[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float mn = fmaxf(m[nt][c], mx[nt][c]);
+          const float ref = mn == -INFINITY ? 0.f : mn;
+          alpha[nt][c] = ex2_approx(m[nt][c] - ref);  // 0 while the column has seen nothing (all its sums are 0)
+          rose |= mn > m[nt][c];
+          m[nt][c] = mn;
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            x[i][nt][c] = ex2_approx(x[i][nt][c] - ref);
+            x[i][nt][2 + c] = ex2_approx(x[i][nt][2 + c] - ref);
+          }
+        }
+      if (__any_sync(0xffffffffu, rose)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            l[nt][c] *= alpha[nt][c];
+#pragma unroll
+            for (int gg = 0; gg < G; ++gg) z[gg][nt][c] *= alpha[nt][c];
+#pragma unroll
+            for (int i = 0; i < 4 * G; ++i) {
+              o[i][nt][c] *= alpha[nt][c];
+              o[i][nt][2 + c] *= alpha[nt][c];
+            }
+          }
+      }
+      // V's parameters; those of keys past the sequence's end are no data
+      float2 va[N][G], vb[N][G];
+      float smax = 0.f;
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int gg = 0; gg < G; ++gg) {
+          const uint8_t* tb = tp + i * C::TILE + kv_q4_vp_off(D) + gg * 4;
+          uint32_t ra = *reinterpret_cast<const uint32_t*>(tb + kg * G * 4);
+          uint32_t rb = *reinterpret_cast<const uint32_t*>(tb + (kg + 8) * G * 4);
+          if (edge) {
+            const int k = key0 + i * kTileKeys + kg;
+            if (k >= len) ra = 0;
+            if (k + 8 >= len) rb = 0;
+          }
+          va[i][gg] = half2_floats(ra);
+          vb[i][gg] = half2_floats(rb);
+          smax = max3f(smax, va[i][gg].x, vb[i][gg].x);
+        }
+      if (__any_sync(0xffffffffu, smax * wscale > 32768.f)) {  // rare: smaller weights from here on
+#pragma unroll
+        for (int mask = 1; mask < 32; mask <<= 1) smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, mask));
+        const float ws = __uint_as_float((unsigned)(127 + 12 - ((int)(__float_as_uint(smax) >> 23) - 127)) << 23);
+        const float ratio = ws / wscale;
+        wscale = ws;
+#pragma unroll
+        for (int i = 0; i < 4 * G; ++i)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) o[i][nt][c] *= ratio;
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const uint8_t* tb = tp + i * C::TILE + kv_q4_v_off(D);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) l[nt][c] += x[i][nt][c] + x[i][nt][2 + c];
+#pragma unroll
+        for (int gg = 0; gg < G; ++gg) {
+          uint32_t b0[NT], b1[NT];
+          [[maybe_unused]] uint32_t c0[NT], c1[NT];
+          const float sa = va[i][gg].x * wscale, sb = vb[i][gg].x * wscale;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+              z[gg][nt][c] = fmaf(x[i][nt][c], va[i][gg].y, fmaf(x[i][nt][2 + c], vb[i][gg].y, z[gg][nt][c]));
+            const float w0 = x[i][nt][0] * sa, w1 = x[i][nt][1] * sa, w2 = x[i][nt][2] * sb, w3 = x[i][nt][3] * sb;
+            const uint32_t h0 = half2_bits(w0, w1), h1 = half2_bits(w2, w3);
+            b0[nt] = transpose8(h0);
+            b1[nt] = transpose8(h1);
+            if constexpr (WIDE) {
+              const float2 r0 = half2_floats(h0), r1 = half2_floats(h1);
+              c0[nt] = transpose8(half2_bits(w0 - r0.x, w1 - r0.y));
+              c1[nt] = transpose8(half2_bits(w2 - r1.x, w3 - r1.y));
+            }
+          }
+          const uint8_t* tv = tb + gg * 512 + g * 4;
+          const uint32_t u0 = *reinterpret_cast<const uint32_t*>(tv + kv0 * 32);
+          const uint32_t u1 = *reinterpret_cast<const uint32_t*>(tv + kv1 * 32);
+          const uint32_t u8 = *reinterpret_cast<const uint32_t*>(tv + (kv0 + 8) * 32);
+          const uint32_t u9 = *reinterpret_cast<const uint32_t*>(tv + (kv1 + 8) * 32);
+          // two keys' halves in one word: dims 8 g .. 8 g + 3 of the group, then 8 g + 4 .. 8 g + 7
+#pragma unroll
+          for (int mt = 0; mt < 4; ++mt) {
+            const unsigned sel = mt < 2 ? 0x5410u : 0x7632u;
+            uint32_t a = __byte_perm(u0, u1, sel), b = __byte_perm(u8, u9, sel);
+            if (mt & 1) {
+              a >>= 8;
+              b >>= 8;
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma_16816(o[4 * gg + mt][nt], a & kLowNibble, a & kHighNibble, b & kLowNibble, b & kHighNibble, b0[nt],
+                        b1[nt]);
+              if constexpr (WIDE)
+                mma_16816(o[4 * gg + mt][nt], a & kLowNibble, a & kHighNibble, b & kLowNibble, b & kHighNibble, c0[nt],
+                          c1[nt]);
+            }
+          }
+        }
+      }
+    };
+
+    bool alive = true;
+    while (true) {
+      if (!mbar_wait(&full[slot], (t / C::NS) & 1, p.status, abort_flag)) {
+        alive = false;
+        break;
+      }
+      const int j0 = warp * C::KT;  // this warp's tiles of the stage
+      const int mine = min(si.nt - j0, C::KT);
+      const uint8_t* tp = smem + slot * C::STAGE + j0 * C::TILE;
+      if (mine == C::KT) {
+        process(tp, si.tile0 + j0, std::integral_constant<int, C::KT>{});
+      } else {
+        for (int i = 0; i < mine; ++i) process(tp + i * C::TILE, si.tile0 + j0 + i, std::integral_constant<int, 1>{});
+      }
+      __syncwarp();
+      if (si.flags & 2) break;  // the piece's last stage: its slot is released after the merge below
+      release(slot, t);
+      ++t;
+      slot = t % C::NS;
+      if (!mbar_wait(&told[slot], (t / C::NS) & 1, p.status, abort_flag)) {
+        alive = false;
+        break;
+      }
+      si = info[slot];
+    }
+    if (!alive) break;
+
+    // ---------------- end of a row piece: merge the consumer warps, 8 columns at a time ----------------
+    float* scr = reinterpret_cast<float*>(smem + slot * C::STAGE);
+    const float back = 1.f / wscale;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float zz[G][2], ll[2];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        ll[c] = l[nt][c];
+#pragma unroll
+        for (int gg = 0; gg < G; ++gg) zz[gg][c] = z[gg][nt][c];
+      }
+#pragma unroll
+      for (int mask = 4; mask < 32; mask <<= 1)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          ll[c] += __shfl_xor_sync(0xffffffffu, ll[c], mask);
+#pragma unroll
+          for (int gg = 0; gg < G; ++gg) zz[gg][c] += __shfl_xor_sync(0xffffffffu, zz[gg][c], mask);
+        }
+      named_bar_sync(1, nct);  // every warp is done with the stage (and with the columns before)
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int gg = 0; gg < G; ++gg) {
+          float y[8];
+#pragma unroll
+          for (int mt = 0; mt < 4; ++mt) {
+            y[2 * mt] = fmaf(o[4 * gg + mt][nt][c], back * 16777216.f, zz[gg][c]);
+            y[2 * mt + 1] = fmaf(o[4 * gg + mt][nt][2 + c], back * 1048576.f, zz[gg][c]);
+          }
+          float4* dst = reinterpret_cast<float4*>(scr + (warp * 8 + 2 * t4 + c) * C::OSTR + 64 * gg + 8 * g);
+          dst[0] = make_float4(y[0], y[1], y[2], y[3]);
+          dst[1] = make_float4(y[4], y[5], y[6], y[7]);
+        }
+      if (g == 0) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          mbuf[warp * 8 + 2 * t4 + c] = m[nt][c];
+          lbuf[warp * 8 + 2 * t4 + c] = ll[c];
+        }
+      }
+      named_bar_sync(1, nct);
+      const int cols = min(8, rows - row0 - 8 * nt);
+      for (int e = ctid; e < cols * D / 4; e += nct) {
+        const int c = (4 * e) / D;
+        const int d = 4 * e - c * D;
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < C::NW; ++w) M = fmaxf(M, mbuf[w * 8 + c]);
+        float L = 0.f;
+        float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < C::NW; ++w) {
+          const float mw = mbuf[w * 8 + c];
+          const float wt = (mw == -INFINITY) ? 0.f : ex2_approx(mw - M);
+          L = fmaf(wt, lbuf[w * 8 + c], L);
+          const float4 v = *reinterpret_cast<const float4*>(scr + (w * 8 + c) * C::OSTR + d);
+          O = make_float4(fmaf(wt, v.x, O.x), fmaf(wt, v.y, O.y), fmaf(wt, v.z, O.z), fmaf(wt, v.w, O.w));
+        }
+        if (si.np <= 1) {
+          const size_t orow = ((size_t)si.b * p.Hkv + hkv) * rows + row0 + 8 * nt + c;
+          const float inv = M == -INFINITY ? 0.f : 1.f / L;  // a column that sees no key: O = 0, lse = -inf
+          store_out4(p.out, orow * D + d, make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv), p.out_f32);
+          if (d == 0 && p.lse != nullptr) p.lse[orow] = M == -INFINITY ? -INFINITY : (M + log2f(L)) * kLn2;
+        } else {
+          const size_t prow = (size_t)si.slot * C::COLS + 8 * nt + c;
+          *reinterpret_cast<float4*>(p.part_o + prow * D + d) = O;
+          if (d == 0) reinterpret_cast<float2*>(p.part_ml)[prow] = make_float2(M, L);
+        }
+      }
+    }
+    fence_proxy_async_smem();  // the scratch stores come before the copy that refills the slot
+    named_bar_sync(1, nct);
+    release(slot, t);
+    ++t;
+    if (si.np > 1) {
+      // Publish the partial; the CTA that lands a row's last partial merges them all.
+      if (ctid == 0) {
+        const unsigned ctr = 2u + (unsigned)(si.b * Hg + si.hg);
+        const unsigned old = atomic_add_acq_rel_gpu(&p.counters[ctr], 1u);
+        const int is_last = (old == (unsigned)si.np - 1u);
+        if (is_last) atomicExch(&p.counters[ctr], 0u);  // re-arm for the next call
+        *last_flag = is_last;
+      }
+      named_bar_sync(1, nct);
+      if (*last_flag) {
+        const int cta_lo = si.lo_par >> 1;
+        const int cols = min(C::COLS, rows - row0);
+        const float2* ml_base = reinterpret_cast<const float2*>(p.part_ml);
+        for (int e = ctid; e < cols * D / 4; e += nct) {
+          const int c = (e * 4) / D;
+          const int d = e * 4 - c * D;
+          float M = -INFINITY, L = 0.f;
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+          auto fold = [&](float2 ml, float4 ov) {
+            if (ml.x > M) {
+              const float sc = (M == -INFINITY) ? 0.f : ex2_approx(M - ml.x);
+              acc = make_float4(acc.x * sc, acc.y * sc, acc.z * sc, acc.w * sc);
+              L *= sc;
+              M = ml.x;
+            }
+            const float w = (ml.x == -INFINITY) ? 0.f : ex2_approx(ml.x - M);
+            acc = make_float4(fmaf(w, ov.x, acc.x), fmaf(w, ov.y, acc.y), fmaf(w, ov.z, acc.z), fmaf(w, ov.w, acc.w));
+            L = fmaf(w, ml.y, L);
+          };
+          auto slot_of = [&](int i) { return i == 0 ? si.lo_par : 2 * (cta_lo + i); };
+          auto batch = [&](int i, auto n_c) {
+            constexpr int N = decltype(n_c)::value;
+            float2 ml[N];
+            float4 ov[N];
+#pragma unroll
+            for (int u = 0; u < N; ++u) {
+              const size_t prow = (size_t)slot_of(i + u) * C::COLS + c;
+              ml[u] = __ldcg(ml_base + prow);
+              ov[u] = __ldcg(reinterpret_cast<const float4*>(p.part_o + prow * D + d));
+            }
+#pragma unroll
+            for (int u = 0; u < N; ++u) fold(ml[u], ov[u]);
+          };
+          int i = 0;
+          for (; i + 7 < si.np; i += 8) batch(i, std::integral_constant<int, 8>{});
+          for (; i + 1 < si.np; i += 2) batch(i, std::integral_constant<int, 2>{});
+          if (i < si.np) batch(i, std::integral_constant<int, 1>{});
+          const float inv = M == -INFINITY ? 0.f : 1.f / L;
+          const size_t orow = ((size_t)si.b * p.Hkv + hkv) * rows + row0 + c;
+          store_out4(p.out, orow * D + d, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv), p.out_f32);
+          if (d == 0 && p.lse != nullptr) p.lse[orow] = M == -INFINITY ? -INFINITY : (M + log2f(L)) * kLn2;
+        }
+      }
+    }
+    named_bar_sync(1, nct);  // mbuf/lbuf/last_flag are reused by the next piece
+  }
+}
+
+template <int D, int NT, bool WIDE>
+cudaError_t launch_one(const DecodeQ4Launch& p) {
+  using C = Q4Cfg<D, NT>;
+  static bool attr_set[64] = {};  // the shared-memory opt-in is per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!attr_set[dev]) {
+    e = cudaFuncSetAttribute(decode_q4_kernel<D, NT, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    attr_set[dev] = true;
+  }
+  const int rows = (p.Hq / p.Hkv) * p.Lq;
+  decode_q4_kernel<D, NT, WIDE><<<C::MINB * p.num_sms, C::THREADS, C::SMEM, p.stream>>>(
+      p, (rows + C::COLS - 1) / C::COLS, rows);
+  return cudaGetLastError();
+}
+
+template <int D, int NT>
+cudaError_t launch_wide(const DecodeQ4Launch& p) {
+  return p.out_f32 ? launch_one<D, NT, true>(p) : launch_one<D, NT, false>(p);
+}
+
+}  // namespace
+
+int decode_q4_cols(int rows) { return rows <= 8 ? 8 : 16; }
+
+int decode_q4_grid(int num_sms, int rows) { return (rows <= 8 ? 3 : 2) * (num_sms > 0 ? num_sms : 152); }
+
+cudaError_t launch_decode_q4(const DecodeQ4Launch& p) {
+  const bool one = (p.Hq / p.Hkv) * p.Lq <= 8;
+  if (p.D == 64) return one ? launch_wide<64, 1>(p) : launch_wide<64, 2>(p);
+  return one ? launch_wide<128, 1>(p) : launch_wide<128, 2>(p);
+}
+
+}  // namespace attn

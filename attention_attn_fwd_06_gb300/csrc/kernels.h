@@ -112,6 +112,93 @@ struct RopeRowsLaunch {
 
 cudaError_t launch_rope_rows(const RopeRowsLaunch& p);
 
+// Page bookkeeping of a serving step (attn_page_step).
+constexpr int kPageStepMaxRows = 8192;
+struct PageStepLaunch {
+  int* kv_lens;
+  const int* keep_lens;  // or null: all keys are kept
+  const int* new_lens;   // or null: no new tokens
+  int* block_table;
+  int* free_pages;
+  int* free_count;
+  int* cu_new;           // or null
+  int* slots;            // or null
+  int* positions;        // or null
+  int B, page_size, max_pages, num_pages, max_tokens;
+  unsigned* status;
+  cudaStream_t stream;
+};
+cudaError_t launch_page_step(const PageStepLaunch& p);
+
+// RMS norm of query and key heads with rotation; strides in elements: sequence, token, head.
+struct QkNormRopeLaunch {
+  const void* q;
+  const void* k;
+  void* q_out;
+  void* k_out;
+  const void* q_weight;  // or null: ones
+  const void* k_weight;
+  const int* positions;  // [B, L], or null: every row valid, no rotation
+  int B, L, Hq, Hkv, D;
+  float eps;
+  long long qs[3], ks[3], qos[3], kos[3];
+  RopeArgs rope;
+  unsigned* status;
+  cudaStream_t stream;
+};
+cudaError_t launch_qk_norm_rope(const QkNormRopeLaunch& p);
+
+// Rows into the 4-bit cache pool (kv_q4.h), and back; strides in elements: token, head.
+struct KvAppendQ4Launch {
+  const void* k;
+  const void* v;
+  void* pool;
+  const int* slots;
+  int T, Hkv, D, page_size, num_pages;
+  long long ks[2], vs[2];
+  unsigned* status;
+  cudaStream_t stream;
+};
+cudaError_t launch_kv_append_q4(const KvAppendQ4Launch& p);
+
+struct KvGatherQ4Launch {
+  const void* pool;
+  const int* block_table;
+  const int* cu_k;
+  const int* kv_starts;  // or null: zeros
+  void* k;
+  void* v;
+  int B, Hkv, D, page_size, max_pages, num_pages, total_k;
+  unsigned* status;
+  cudaStream_t stream;
+};
+cudaError_t launch_kv_gather_q4(const KvGatherQ4Launch& p);
+
+// Decode over the 4-bit paged cache.
+struct DecodeQ4Launch {
+  const void* q;           // bf16 [B, Hq, Lq, D]
+  const void* pool;
+  const int* block_table;  // [B, max_pages]
+  const int* kv_lens;      // [B], the Lq new tokens' keys included
+  void* out;               // [B, Hq, Lq, D], bf16 or fp32
+  float* lse;              // [B, Hq, Lq] or null
+  float* part_o;           // fp32 [2 * grid][cols][D]
+  float* part_ml;          // fp32 [2 * grid][cols][2]
+  unsigned* counters;      // [2 + row]; zero between calls
+  int B, Hq, Hkv, Lq, D, page_size, max_pages, num_pages;
+  int min_tiles;           // smallest slice of the tiles one CTA takes (>= 1)
+  float scale;
+  int out_f32;
+  int num_sms;
+  unsigned* status;
+  int fault_skip_arrive;   // test hook: CTA 0 withholds one slot release
+  cudaStream_t stream;
+};
+// Query rows one CTA serves, and the CTAs of the persistent launch, for `rows` = (Hq / Hkv) * Lq.
+int decode_q4_cols(int rows);
+int decode_q4_grid(int num_sms, int rows);
+cudaError_t launch_decode_q4(const DecodeQ4Launch& p);
+
 // One thread waits on a barrier nothing arrives on, with the kernels' bounded wait and a limit of limit_ns.
 cudaError_t launch_selftest_timeout(unsigned long long limit_ns, unsigned* status, cudaStream_t stream);
 

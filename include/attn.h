@@ -55,7 +55,8 @@ typedef enum attn_status {
   ATTN_ERR_CUDA = 4,            /* a CUDA runtime call or launch failed                */
   ATTN_ERR_DEVICE_TIMEOUT = 5,  /* device status: a bounded pipeline wait expired      */
   ATTN_ERR_DEVICE_BOUNDS = 6,   /* device status: a kv_len was outside [0, Lmax]       */
-  ATTN_ERR_SCRATCH_TOO_SMALL = 7 /* attn_decode_noalloc: partials exceed its fixed buffer */
+  ATTN_ERR_SCRATCH_TOO_SMALL = 7, /* attn_decode_noalloc: partials exceed its fixed buffer; a caller's workspace is too small */
+  ATTN_ERR_DEVICE_POOL = 8      /* device status: attn_page_step found too few free pages  */
 } attn_status;
 
 typedef enum attn_dtype { ATTN_DTYPE_BF16 = 0, ATTN_DTYPE_F32 = 1 } attn_dtype;
@@ -321,6 +322,224 @@ int attn_decode_multi(const attn_decode_multi_params* p);
  * on B, Lmax or chunk: 256 KiB of counters plus two partials per CTA.
  */
 unsigned long long attn_decode_workspace_bytes(int B, int Hq, int Hkv, int Lmax, int D, int chunk);
+
+/*
+ * ---------------------------------------------------------------------------
+ * A serving step around a paged cache.  The calls below go together: pages and
+ * slots for the step's tokens (attn_page_step), norm and rotation of their q and
+ * k (attn_qk_norm_rope), their rows into a cache held in 4 bits
+ * (attn_kv_append_q4), then decode over it (attn_decode_q4) or, for prefill over
+ * cached keys, the rows read back as bf16 (attn_kv_gather_q4) for attn_fwd_ex.
+ * (The source pages name fused RMSNorm + RoPE, "Что такое kernel fusion и как он
+ * применяется в LLM serving?" §3.5, and PagedAttention, §6; they give no formulas.)
+ * None of them allocates or synchronises, so all can be captured into CUDA graphs
+ * (attn_decode_q4 without a workspace of the caller's: see there).  For all of
+ * them every host-visible size is checked before anything is enqueued, and a row
+ * whose index the device finds out of range is skipped and flagged
+ * ATTN_ERR_DEVICE_BOUNDS in the device status word.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * attn_page_step -- block tables and slot maps of a step, from request lengths,
+ * on the GPU (no host round trip).
+ *
+ * Row b holds a = kv_lens[b] keys on the first ceil(a / page_size) pages of its
+ * block-table row.  The step keeps the first keep_lens[b] keys and adds
+ * new_lens[b] tokens: a decode step adds one, a prompt its length, refused draft
+ * tokens are dropped by keeping less, a finished request keeps 0.  Pages past the
+ * row's new length are given back, missing ones are taken, kept ones stay.
+ *
+ *   kv_lens      int32 [B]  in: a; out: keep + new
+ *   keep_lens    int32 [B]  0 <= keep <= a; NULL: keep everything
+ *   new_lens     int32 [B]  >= 0; NULL: nothing is added
+ *   block_table  int32 [B, max_pages]  entries of pages taken are written, those of
+ *                pages given back become -1, the others stay as they are
+ *   free_pages   int32 [num_pages]  the stack of free pages: entries below
+ *                *free_count; pages are taken from its end in row-major order and
+ *                given back in reverse, so that taking back a step's tokens restores
+ *                it exactly.  Entries at and above the count hold anything.
+ *   free_count   int32 [1]  in/out
+ *   cu_new       int32 [B + 1]  running sum of new_lens (cu_seqlens_q of the step);
+ *                may be NULL
+ *   slots        int32 [max_tokens]  token i of the step (rows in order, positions
+ *                rising): page * page_size + offset within the page, what
+ *                attn_kv_append_q4 takes; -1 past the last token; may be NULL
+ *   positions    int32 [max_tokens]  its position, what attn_qk_norm_rope takes; -1
+ *                past the last token; may be NULL
+ *
+ * All or nothing: lengths out of range, a row beyond max_pages pages or more than
+ * max_tokens tokens while slots or positions is given (ATTN_ERR_DEVICE_BOUNDS), or
+ * too few free pages (ATTN_ERR_DEVICE_POOL; pages given back by the same step
+ * count) leave lengths, table and stack as they were; every slot and position is
+ * then -1 and cu_new 0.  A page id out of [0, num_pages) met on the way is flagged
+ * ATTN_ERR_DEVICE_BOUNDS and its tokens' slots are -1.  The buffers must not
+ * overlap, except that an input not written may be passed twice.
+ *
+ * B at most 8192; num_pages * page_size, B * max_pages and max_pages * page_size
+ * below 2^31 (ATTN_ERR_UNSUPPORTED otherwise).  int32 pointers are 4-byte aligned
+ * here and in the calls below.
+ */
+typedef struct attn_page_step_params {
+  int* kv_lens;
+  const int* keep_lens;
+  const int* new_lens;
+  int* block_table;
+  int* free_pages;
+  int* free_count;
+  int* cu_new;
+  int* slots;
+  int* positions;
+  int B, page_size, max_pages, num_pages, max_tokens;
+  void* stream;
+} attn_page_step_params;
+
+int attn_page_step(const attn_page_step_params* p);
+
+/*
+ * attn_qk_norm_rope -- RMS norm of every query and key head over its D elements,
+ * and the rotation of attn_rope, in one pass:
+ *     y = x / sqrt(mean(x^2) + eps) * weight,   then (a, b) -> (a cos - b sin, b cos + a sin),
+ * in fp32, rounded to bf16 once.  Rows are addressed by strides, in elements, of
+ * sequence, token and head, so q and k may be views of a fused projection's output
+ * and either [B, H, L, D] or [B, L, H, D]; a row's D elements are contiguous.
+ *
+ *   q, k          bf16, B sequences of L tokens with Hq (Hkv) heads; Hkv = 0: no k
+ *   q_out, k_out  bf16; either apart from every input, or exactly an input's rows
+ *                 (same pointer and strides: in place)
+ *   q_weight, k_weight  bf16 [D], or NULL for ones
+ *   positions     int32 [B, L]; -1 marks a padded row, which is left as it was.  Any
+ *                 other value outside [0, max_pos) is flagged and its row left as it
+ *                 was.  May be NULL without rotation.
+ *   rope          tables and style (k_out unused); ATTN_ROPE_NONE: norm only
+ *   eps           finite, >= 0 (a row of zeros with eps = 0 is 0 * inf = NaN)
+ * Pointers are 16-byte aligned, strides multiples of 8 elements.
+ */
+typedef struct attn_qk_norm_rope_params {
+  const void* q;
+  const void* k;
+  void* q_out;
+  void* k_out;
+  const void* q_weight;
+  const void* k_weight;
+  const int* positions;
+  int B, L, Hq, Hkv, D;
+  float eps;
+  long long q_stride[3], k_stride[3], q_out_stride[3], k_out_stride[3];
+  attn_rope rope;
+  void* stream;
+} attn_qk_norm_rope_params;
+
+int attn_qk_norm_rope(const attn_qk_norm_rope_params* p);
+
+/*
+ * The 4-bit cache.  A pool of num_pages pages, each Hkv * page_size / 16 tiles of
+ * 16 keys of one kv head (18 * D bytes a tile, 4.5 bits an element), G = D / 64:
+ *     K codes [G][16 keys][32 bytes], V codes alike, then K's and V's fp16 pairs
+ *     (scale, minimum) [16 keys][G][2].
+ * Byte j of a code row holds dims 2j (low four bits) and 2j + 1 of its group of 64
+ * dims; code u reads back as scale * u + minimum.  page_size is a multiple of 16;
+ * slot = page * page_size + offset.  The pool is 128-byte aligned.
+ *
+ * attn_kv_q4_page_bytes -- bytes of one page (0 on invalid sizes).
+ */
+unsigned long long attn_kv_q4_page_bytes(int page_size, int Hkv, int D);
+
+/*
+ * attn_kv_append_q4 -- quantises T rows of k and v into their slots.  Per group of 64
+ * dims: minimum = fp16(min x), scale = fp16((max x - min x) / 15), code =
+ * clamp(round((x - minimum) / scale), 0, 15), ties to even (0 where scale is 0).  NaN
+ * counts as 0, values beyond +-65504 as that.
+ *
+ *   k, v   bf16 [T, Hkv, D] with strides of token and head in elements (multiples of
+ *          8; D contiguous; 16-byte aligned): views of a projection's output will do
+ *   slots  int32 [T]; -1: the row is not written.  Any other slot outside the pool is
+ *          flagged and not written.  The slots of one call must differ: rows of the same
+ *          slot would be written over each other in no order.
+ */
+typedef struct attn_kv_append_q4_params {
+  const void* k;
+  const void* v;
+  void* pool;
+  const int* slots;
+  int T, Hkv, D, page_size, num_pages;
+  long long k_stride[2], v_stride[2];
+  void* stream;
+} attn_kv_append_q4_params;
+
+int attn_kv_append_q4(const attn_kv_append_q4_params* p);
+
+/*
+ * attn_kv_gather_q4 -- reads rows back: key kv_starts[b] + i of sequence b becomes row
+ * cu_k[b] + i of the packed k and v (the layout of attn_fwd_ex), rounded to bf16, for
+ * i < cu_k[b + 1] - cu_k[b].
+ *
+ *   block_table  int32 [B, max_pages]; only entries of pages read are looked at
+ *   cu_k         int32 [B + 1], non-decreasing, cu_k[0] = 0, cu_k[B] <= total_k
+ *   kv_starts    int32 [B], or NULL for zeros
+ *   k, v         bf16 [total_k, Hkv, D]; rows at and past cu_k[B] stay as they were, and
+ *                so do rows of positions or pages out of range, which are flagged
+ */
+typedef struct attn_kv_gather_q4_params {
+  const void* pool;
+  const int* block_table;
+  const int* cu_k;
+  const int* kv_starts;
+  void* k;
+  void* v;
+  int B, Hkv, D, page_size, max_pages, num_pages, total_k;
+  void* stream;
+} attn_kv_gather_q4_params;
+
+int attn_kv_gather_q4(const attn_kv_gather_q4_params* p);
+
+/*
+ * attn_decode_q4 -- decode over the 4-bit cache, one or Lq new tokens a sequence, with
+ * the masks and results of attn_decode_multi on the values the cache stands for
+ * (Lq = 1: of attn_decode).  q is taken as it is (rotated by attn_qk_norm_rope).
+ *
+ *   q            bf16 [B, Hq, Lq, D]
+ *   pool, block_table, page_size, max_pages, num_pages  as above; kv_lens int32 [B], at
+ *                most max_pages * page_size (clamped and flagged otherwise).  Only
+ *                entries of pages that hold keys are read; a page id outside the pool
+ *                is flagged and page 0 read instead.
+ *   out, lse     as attn_decode_multi
+ *   chunk        0 = default; otherwise the smallest number of keys of one CTA's slice,
+ *                in [1, 1048576]
+ *   workspace    NULL: the library's split-KV workspace, with attn_decode's rules (not
+ *                grown during capture; calls that can overlap on the GPU race on it).
+ *                Otherwise a DEVICE buffer of workspace_bytes (at least
+ *                attn_decode_q4_workspace_bytes; ATTN_ERR_SCRATCH_TOO_SMALL if not),
+ *                16-byte aligned, whose first 256 KiB were zero before its first call;
+ *                the calls keep them so.  Calls that can overlap, and graphs that can be
+ *                replayed at once, each take a buffer of their own.  After
+ *                ATTN_ERR_DEVICE_TIMEOUT the caller zeroes it again.
+ * (Hq / Hkv) * Lq at most 128.  Weights are rounded to fp16 before the second product;
+ * with out_dtype = ATTN_DTYPE_F32 they are carried in two fp16 terms.
+ * B * Hkv * ceil((Hq / Hkv) * Lq / 16) at most 65534 (ATTN_ERR_UNSUPPORTED otherwise).
+ */
+typedef struct attn_decode_q4_params {
+  const void* q;
+  const void* pool;
+  const int* block_table;
+  const int* kv_lens;
+  void* out;
+  float* lse;
+  int B, Hq, Hkv, Lq, D;
+  int page_size, max_pages, num_pages;
+  float scale;
+  int out_dtype;
+  int chunk;
+  void* workspace;
+  unsigned long long workspace_bytes;
+  void* stream;
+} attn_decode_q4_params;
+
+int attn_decode_q4(const attn_decode_q4_params* p);
+
+/* attn_decode_q4_workspace_bytes -- bytes a workspace of attn_decode_q4 needs on the current device (0 on invalid
+ * sizes; 152 SMs assumed when no device is visible).  It depends on (Hq / Hkv) * Lq and D only. */
+unsigned long long attn_decode_q4_workspace_bytes(int Hq, int Hkv, int Lq, int D);
 
 /*
  * attn_get_device_status -- synchronises `stream`, then returns and clears the

@@ -27,3 +27,4 @@ from .sdpa import (  # noqa: F401
     visible_mask,
 )
 from .brute import attention_loops  # noqa: F401
+from .serving import page_step, quantise_q4, read_q4, rms_norm, values_q4, write_q4  # noqa: F401
