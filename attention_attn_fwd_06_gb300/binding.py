@@ -135,15 +135,18 @@ class attn_page_step_params(ctypes.Structure):
     ]
 
 
+# The stride arrays and the rope member of the next two are spelled out field by field (the same layout): filling a
+# nested member from Python costs as much as ten plain ones.
 class attn_qk_norm_rope_params(ctypes.Structure):
     _fields_ = [
         ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("q_out", ctypes.c_void_p), ("k_out", ctypes.c_void_p),
         ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("positions", ctypes.c_void_p),
         ("B", ctypes.c_int), ("L", ctypes.c_int), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int), ("D", ctypes.c_int),
         ("eps", ctypes.c_float),
-        ("q_stride", ctypes.c_longlong * 3), ("k_stride", ctypes.c_longlong * 3),
-        ("q_out_stride", ctypes.c_longlong * 3), ("k_out_stride", ctypes.c_longlong * 3),
-        ("rope", attn_rope),
+        *((f"{t}_{axis}_stride", ctypes.c_longlong) for t in ("q", "k", "q_out", "k_out")
+          for axis in ("sequence", "token", "head")),
+        ("rope_cos", ctypes.c_void_p), ("rope_sin", ctypes.c_void_p), ("rope_max_pos", ctypes.c_int),
+        ("rope_style", ctypes.c_int), ("rope_k_out", ctypes.c_void_p),
         ("stream", ctypes.c_void_p),
     ]
 
@@ -153,7 +156,7 @@ class attn_kv_append_q4_params(ctypes.Structure):
         ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("pool", ctypes.c_void_p), ("slots", ctypes.c_void_p),
         ("T", ctypes.c_int), ("Hkv", ctypes.c_int), ("D", ctypes.c_int), ("page_size", ctypes.c_int),
         ("num_pages", ctypes.c_int),
-        ("k_stride", ctypes.c_longlong * 2), ("v_stride", ctypes.c_longlong * 2),
+        *((f"{t}_{axis}_stride", ctypes.c_longlong) for t in ("k", "v") for axis in ("token", "head")),
         ("stream", ctypes.c_void_p),
     ]
 
@@ -187,6 +190,8 @@ _lock = threading.Lock()
 def load(path: str = LIB_PATH) -> ctypes.CDLL:
     """Load the library once (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -504,30 +509,50 @@ def attn_decode_noalloc(q, kcache, vcache, kv_lens, out, lse=None, scale=None, c
     return out, lse
 
 
-def _call(fn, p, device, stream, where):
-    """Run one entry point on `device` (made current for the call) and its stream."""
-    p.stream = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
-    if device.index == torch.cuda.current_device():
+# The raw handle of a device's current stream without building a Stream object (2 us of a small call on the host).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(stream, index):
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
+
+
+def _call(fn, p, index, where):
+    """Run one entry point with device `index` current."""
+    if index == torch.cuda.current_device():
         status = fn(ctypes.byref(p))
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             status = fn(ctypes.byref(p))
     if status != ATTN_OK:
         raise AttnError(status, where)
 
 
-def _rows(t, name, ndim, device):
-    """A bf16 tensor whose rows (the last axis) are contiguous; the other axes may have any stride that is a multiple
-    of 8 elements.  Returns its strides."""
+def _fit(t, name, dtype, shape, index):
+    """The address of a contiguous tensor of just this type and shape on device `index` (_need, told shortly: a decode
+    step's calls take microseconds, and so may their checks)."""
+    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and t.get_device() == index >= 0
+            and t.is_contiguous()):
+        _need(t, name, dtype, len(shape), shape, torch.device("cuda", max(index, 0)))
+        raise ValueError(f"{name}: not a contiguous CUDA tensor of shape {tuple(shape)}")
+    return t.data_ptr()
+
+
+def _rows(t, name, ndim, index=None):
+    """A bf16 CUDA tensor (on device `index`) whose rows (the last axis) are contiguous; the other axes may have any
+    stride that is a multiple of 8 elements.  Returns its strides."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != torch.bfloat16:
         raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if t.dim() != ndim:
-        raise ValueError(f"{name} must have {ndim} dims, got shape {tuple(t.shape)}")
-    if not t.is_cuda or (device is not None and t.device != device):
-        raise ValueError(f"{name} must be a CUDA tensor" + (f" on {device}" if device is not None else ""))
     st = t.stride()
+    if len(st) != ndim:
+        raise ValueError(f"{name} must have {ndim} dims, got shape {tuple(t.shape)}")
+    at = t.get_device()
+    if at < 0 or (index is not None and at != index):
+        raise ValueError(f"{name} must be a CUDA tensor" + (f" on cuda:{index}" if index is not None else ""))
     if st[-1] != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
     return st
@@ -548,31 +573,28 @@ def attn_page_step(kv_lens, block_table, free_pages, free_count, page_size, new_
     kv_lens[b] keys and gets new_lens[b] (default: 0) tokens.  kv_lens [B], block_table [B,max_pages],
     free_pages [num_pages] (a stack) and free_count [1] are updated in place; slots and positions [max_tokens] and
     cu_new [B+1], where given, are written.  -> (slots, positions, cu_new)"""
-    _need(kv_lens, "kv_lens", torch.int32, 1)
-    dev = kv_lens.device
+    i32 = torch.int32
+    _need(kv_lens, "kv_lens", i32, 1)
+    at = kv_lens.get_device()
     B = kv_lens.shape[0]
-    _need(block_table, "block_table", torch.int32, 2, device=dev)
-    if block_table.shape[0] != B:
-        raise ValueError("block_table must have B rows")
-    _need(free_pages, "free_pages", torch.int32, 1, device=dev)
-    _need(free_count, "free_count", torch.int32, 1, (1,), dev)
-    p = attn_page_step_params()
-    p.max_tokens = -1
-    for t, name, shape in ((new_lens, "new_lens", (B,)), (keep_lens, "keep_lens", (B,)), (cu_new, "cu_new", (B + 1,)),
-                           (slots, "slots", None), (positions, "positions", None)):
-        if t is None:
-            continue
-        _need(t, name, torch.int32, 1, shape, dev)
-        setattr(p, name, t.data_ptr())
-        if shape is None:
-            if p.max_tokens not in (-1, t.shape[0]):
-                raise ValueError("slots and positions must have the same length")
-            p.max_tokens = t.shape[0]
-    p.max_tokens = max(p.max_tokens, 0)
-    p.kv_lens, p.block_table = kv_lens.data_ptr(), block_table.data_ptr()
-    p.free_pages, p.free_count = free_pages.data_ptr(), free_count.data_ptr()
-    p.B, p.page_size, p.max_pages, p.num_pages = B, int(page_size), block_table.shape[1], free_pages.shape[0]
-    _call(load().attn_page_step, p, dev, stream, "attn_page_step")
+    width = block_table.shape[-1] if isinstance(block_table, torch.Tensor) and block_table.dim() else 0
+    pages = free_pages.shape[0] if isinstance(free_pages, torch.Tensor) and free_pages.dim() else 0
+    rooms = [t.shape[0] for t in (slots, positions) if isinstance(t, torch.Tensor) and t.dim()]
+    room = rooms[0] if rooms else 0
+    if len(rooms) == 2 and rooms[1] != room:
+        raise ValueError("slots and positions must have the same length")
+    p = attn_page_step_params(
+        kv_lens.data_ptr(),
+        None if keep_lens is None else _fit(keep_lens, "keep_lens", i32, (B,), at),
+        None if new_lens is None else _fit(new_lens, "new_lens", i32, (B,), at),
+        _fit(block_table, "block_table", i32, (B, width), at),
+        _fit(free_pages, "free_pages", i32, (pages,), at),
+        _fit(free_count, "free_count", i32, (1,), at),
+        None if cu_new is None else _fit(cu_new, "cu_new", i32, (B + 1,), at),
+        None if slots is None else _fit(slots, "slots", i32, (room,), at),
+        None if positions is None else _fit(positions, "positions", i32, (room,), at),
+        B, int(page_size), width, pages, room, _stream_of(stream, at))
+    _call(load().attn_page_step, p, at, "attn_page_step")
     return slots, positions, cu_new
 
 
@@ -583,68 +605,77 @@ def attn_qk_norm_rope(q, k, q_weight=None, k_weight=None, rope=None, positions=N
     rope = (cos, sin, style); positions int32 [T] or [B,L], -1 for padded rows, which are left as they were.
     q_out/k_out may be q/k themselves.  -> (q_out, k_out)"""
     dense = isinstance(q, torch.Tensor) and q.dim() == 4
-    _rows(q, "q", 4 if dense else 3, None)
-    p = attn_qk_norm_rope_params()
-    dev = q.device
-    shapes = []
-    for x, out, w, name in ((q, q_out, q_weight, "q"), (k, k_out, k_weight, "k")):
-        if x is None:
-            if name == "q" or out is not None or w is not None:
-                raise ValueError("q is needed; k_out and k_weight go with k")
-            shapes.append(None)
-            continue
-        st = _rows(x, name, 4 if dense else 3, dev)
-        if out is None:
-            out = torch.empty(x.shape, dtype=torch.bfloat16, device=dev)
-        elif out is not x:
-            _rows(out, name + "_out", 4 if dense else 3, dev)
-            if out.shape != x.shape:
-                raise ValueError(f"{name}_out must have shape {tuple(x.shape)}, got {tuple(out.shape)}")
-        if not out.is_contiguous():
-            _written_once(out, name + "_out")
-        if w is not None:
-            _need(w, name + "_weight", torch.bfloat16, 1, (x.shape[-1],), dev)
-            setattr(p, name + "_weight", w.data_ptr())
-        so = out.stride()
-        setattr(p, name, x.data_ptr())
-        setattr(p, name + "_out", out.data_ptr())
-        # sequence, token, head
-        setattr(p, name + "_stride", (st[0], st[2], st[1]) if dense else (0, st[0], st[1]))
-        setattr(p, name + "_out_stride", (so[0], so[2], so[1]) if dense else (0, so[0], so[1]))
-        shapes.append(x.shape)
-        if name == "q":
-            q_out = out
-        else:
-            k_out = out
-    sq, sk = shapes
+    ndim = 4 if dense else 3
+    sq = _rows(q, "q", ndim)
+    at = q.get_device()
     if dense:
-        p.B, p.Hq, p.L, p.D = sq
-        if sk is not None and (sk[0], sk[2], sk[3]) != (sq[0], sq[2], sq[3]):
-            raise ValueError(f"k shape {tuple(sk)} does not match q {tuple(sq)}")
+        B, Hq, L, D = q.shape
     else:
-        p.B, (p.L, p.Hq, p.D) = 1, sq
-        if sk is not None and (sk[0], sk[2]) != (sq[0], sq[2]):
-            raise ValueError(f"k shape {tuple(sk)} does not match q {tuple(sq)}")
-    p.Hkv = 0 if sk is None else sk[1]
-    p.eps = float(eps)
-    if positions is not None:
-        _need(positions, "positions", torch.int32, 2 if dense else 1, (p.B, p.L) if dense else (p.L,), dev)
-        p.positions = positions.data_ptr()
-    if rope is not None and len(rope) > 3:
-        raise ValueError("rope k_out is taken by prefill calls only")
-    _set_rope(p, rope, p.D, dev)
-    _call(load().attn_qk_norm_rope, p, dev, stream, "attn_qk_norm_rope")
+        B, (L, Hq, D) = 1, q.shape
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    sqo = _out_rows(q_out, "q_out", q, ndim, at)
+    if k is None:
+        if k_out is not None or k_weight is not None:
+            raise ValueError("k_out and k_weight go with k")
+        Hkv, sk, sko, kp, kop = 0, sq, sqo, None, None
+    else:
+        sk = _rows(k, "k", ndim, at)
+        Hkv = k.shape[1]
+        if k.shape != ((B, Hkv, L, D) if dense else (L, Hkv, D)):
+            raise ValueError(f"k shape {tuple(k.shape)} does not match q {tuple(q.shape)}")
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=k.device)
+        sko = _out_rows(k_out, "k_out", k, ndim, at)
+        kp, kop = k.data_ptr(), k_out.data_ptr()
+    # as sequence, token, head
+    if dense:
+        strides = tuple(st[i] for st in (sq, sk, sqo, sko) for i in (0, 2, 1))
+    else:
+        strides = (0, sq[0], sq[1], 0, sk[0], sk[1], 0, sqo[0], sqo[1], 0, sko[0], sko[1])
+    if rope is None:
+        r = _NO_ROPE
+    else:
+        if len(rope) > 3 and rope[3] is not None:
+            raise ValueError("rope k_out is taken by prefill calls only")
+        cos, sin, style = rope[:3]
+        if style not in _ROPE_STYLES:
+            raise ValueError("rope style must be 'half' or 'interleaved'")
+        tab = (cos.shape[0] if isinstance(cos, torch.Tensor) and cos.dim() else 0, D // 2)
+        r = (_fit(cos, "rope cos", torch.float32, tab, at), _fit(sin, "rope sin", torch.float32, tab, at), tab[0],
+             _ROPE_STYLES[style], None)
+    p = attn_qk_norm_rope_params(
+        q.data_ptr(), kp, q_out.data_ptr(), kop,
+        None if q_weight is None else _fit(q_weight, "q_weight", torch.bfloat16, (D,), at),
+        None if k_weight is None else _fit(k_weight, "k_weight", torch.bfloat16, (D,), at),
+        None if positions is None else _fit(positions, "positions", torch.int32, (B, L) if dense else (L,), at),
+        B, L, Hq, Hkv, D, eps, *strides, *r, _stream_of(stream, at))
+    _call(load().attn_qk_norm_rope, p, at, "attn_qk_norm_rope")
     return q_out, k_out
 
 
-def _pool_q4(pool, p, device, D=None):
-    """Check a 4-bit cache pool, uint8 [num_pages,Hkv,page_size/16,18*D], and note its sizes."""
-    _need(pool, "pool", torch.uint8, 4, device=device)
+_NO_ROPE = (None, None, 0, ATTN_ROPE_NONE, None)
+
+
+def _out_rows(out, name, like, ndim, at):
+    """The strides of an output shaped like `like` whose rows are written once each."""
+    st = _rows(out, name, ndim, at)
+    if out.shape != like.shape:
+        raise ValueError(f"{name} must have shape {tuple(like.shape)}, got {tuple(out.shape)}")
+    if not out.is_contiguous():
+        _written_once(out, name)
+    return st
+
+
+def _pool_q4(pool, D=None):
+    """Check a 4-bit cache pool, uint8 [num_pages,Hkv,page_size/16,18*D] -> num_pages, Hkv, page_size, D, device."""
+    if not (isinstance(pool, torch.Tensor) and pool.dtype == torch.uint8 and pool.dim() == 4 and pool.is_cuda
+            and pool.is_contiguous()):
+        _need(pool, "pool", torch.uint8, 4)
     num_pages, Hkv, tiles, tile = pool.shape
     if tile not in (18 * 64, 18 * 128) or (D is not None and tile != 18 * D):
         raise ValueError(f"pool tiles must have 18 * D bytes, got {tile}")
-    p.pool = pool.data_ptr()
-    p.num_pages, p.Hkv, p.page_size, p.D = num_pages, Hkv, 16 * tiles, tile // 18
+    return num_pages, Hkv, 16 * tiles, tile // 18, pool.get_device()
 
 
 def attn_kv_q4_pool(num_pages, Hkv, page_size, D, device="cuda"):
@@ -661,43 +692,35 @@ def attn_kv_q4_page_bytes(page_size, Hkv, D) -> int:
 def attn_kv_append_q4(k, v, pool, slots, stream=None):
     """Quantise k and v [T,Hkv,D] bf16 (any strides over contiguous rows) into the 4-bit pool at slots int32 [T]
     (-1: not written; the others must differ)."""
-    p = attn_kv_append_q4_params()
-    sk = _rows(k, "k", 3, None)
-    dev = k.device
-    sv = _rows(v, "v", 3, dev)
-    _pool_q4(pool, p, dev)
+    num_pages, Hkv, page_size, D, at = _pool_q4(pool)
+    sk, sv = _rows(k, "k", 3, at), _rows(v, "v", 3, at)
     T = k.shape[0]
-    if tuple(k.shape) != (T, p.Hkv, p.D) or v.shape != k.shape:
+    if k.shape != (T, Hkv, D) or v.shape != k.shape:
         raise ValueError(f"k/v shapes {tuple(k.shape)} {tuple(v.shape)} do not match the pool {tuple(pool.shape)}")
-    _need(slots, "slots", torch.int32, 1, (T,), dev)
-    p.k, p.v, p.slots, p.T = k.data_ptr(), v.data_ptr(), slots.data_ptr(), T
-    p.k_stride, p.v_stride = sk[:2], sv[:2]
-    _call(load().attn_kv_append_q4, p, dev, stream, "attn_kv_append_q4")
+    p = attn_kv_append_q4_params(k.data_ptr(), v.data_ptr(), pool.data_ptr(),
+                                 _fit(slots, "slots", torch.int32, (T,), at), T, Hkv, D, page_size, num_pages,
+                                 sk[0], sk[1], sv[0], sv[1], _stream_of(stream, at))
+    _call(load().attn_kv_append_q4, p, at, "attn_kv_append_q4")
 
 
 def attn_kv_gather_q4(pool, block_table, cu_k, total_k, kv_starts=None, k_out=None, v_out=None, stream=None):
     """Read rows of the 4-bit pool back as packed bf16 k and v [total_k,Hkv,D]: keys kv_starts[b] (default 0) and on of
     sequence b become rows cu_k[b] .. cu_k[b+1]-1 (cu_k int32 [B+1]); rows past cu_k[B] stay as they were.
     -> (k, v)"""
-    p = attn_kv_gather_q4_params()
-    _pool_q4(pool, p, None)
-    dev = pool.device
-    _need(block_table, "block_table", torch.int32, 2, device=dev)
-    B = block_table.shape[0]
-    _need(cu_k, "cu_k", torch.int32, 1, (B + 1,), dev)
-    if kv_starts is not None:
-        _need(kv_starts, "kv_starts", torch.int32, 1, (B,), dev)
-        p.kv_starts = kv_starts.data_ptr()
-    shape = (int(total_k), p.Hkv, p.D)
+    num_pages, Hkv, page_size, D, at = _pool_q4(pool)
+    i32 = torch.int32
+    B, width = block_table.shape if isinstance(block_table, torch.Tensor) and block_table.dim() == 2 else (0, 0)
+    shape = (int(total_k), Hkv, D)
     if k_out is None:
-        k_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        k_out = torch.empty(shape, dtype=torch.bfloat16, device=pool.device)
     if v_out is None:
-        v_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-    _need(k_out, "k_out", torch.bfloat16, 3, shape, dev)
-    _need(v_out, "v_out", torch.bfloat16, 3, shape, dev)
-    p.block_table, p.cu_k, p.k, p.v = block_table.data_ptr(), cu_k.data_ptr(), k_out.data_ptr(), v_out.data_ptr()
-    p.B, p.max_pages, p.total_k = B, block_table.shape[1], shape[0]
-    _call(load().attn_kv_gather_q4, p, dev, stream, "attn_kv_gather_q4")
+        v_out = torch.empty(shape, dtype=torch.bfloat16, device=pool.device)
+    p = attn_kv_gather_q4_params(
+        pool.data_ptr(), _fit(block_table, "block_table", i32, (B, width), at), _fit(cu_k, "cu_k", i32, (B + 1,), at),
+        None if kv_starts is None else _fit(kv_starts, "kv_starts", i32, (B,), at),
+        _fit(k_out, "k_out", torch.bfloat16, shape, at), _fit(v_out, "v_out", torch.bfloat16, shape, at),
+        B, Hkv, D, page_size, width, num_pages, shape[0], _stream_of(stream, at))
+    _call(load().attn_kv_gather_q4, p, at, "attn_kv_gather_q4")
     return k_out, v_out
 
 
@@ -706,37 +729,32 @@ def attn_decode_q4(q, pool, block_table, kv_lens, out=None, lse=None, scale=None
     """Decode over the 4-bit pool: q [B,Hq,D], or [B,Hq,Lq,D] for Lq new tokens, bf16 (already rotated); block_table
     int32 [B,max_pages], kv_lens int32 [B] counting the new tokens' own keys.  ``workspace`` is a buffer from
     attn_decode_q4_workspace; without one the library's is used, as by attn_decode.  -> (out, lse) shaped like q"""
-    _need(q, "q", torch.bfloat16, 4 if isinstance(q, torch.Tensor) and q.dim() == 4 else 3)
-    dev = q.device
-    p = attn_decode_q4_params()
-    B, Hq, D = q.shape[0], q.shape[1], q.shape[-1]
-    Lq = q.shape[2] if q.dim() == 4 else 1
-    _pool_q4(pool, p, dev, D)
-    _need(block_table, "block_table", torch.int32, 2, device=dev)
-    _need(kv_lens, "kv_lens", torch.int32, 1, (B,), dev)
-    if block_table.shape[0] != B:
-        raise ValueError("block_table must have B rows")
-    if out is None:
-        out = torch.empty(q.shape, dtype=out_dtype, device=dev)
-    else:
-        _need(out, "out", out_dtype, q.dim(), q.shape, dev)
-    if lse is None and want_lse:
-        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev)
-    elif lse is not None:
-        _need(lse, "lse", torch.float32, q.dim() - 1, q.shape[:-1], dev)
-    if lse is not None:
-        p.lse = lse.data_ptr()
-    p.q, p.block_table, p.kv_lens, p.out = q.data_ptr(), block_table.data_ptr(), kv_lens.data_ptr(), out.data_ptr()
-    p.B, p.Hq, p.Lq, p.max_pages = B, Hq, Lq, block_table.shape[1]
-    p.scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    many = isinstance(q, torch.Tensor) and q.dim() == 4
+    _need(q, "q", torch.bfloat16, 4 if many else 3)
+    qs = q.shape
+    B, Hq, D = qs[0], qs[1], qs[-1]
+    num_pages, Hkv, page_size, _, at = _pool_q4(pool, D)
+    if q.get_device() != at:
+        raise ValueError(f"q must be on cuda:{at}, got {q.device}")
     if out_dtype not in (torch.bfloat16, torch.float32):
         raise TypeError("out must be bf16 or fp32")
-    p.out_dtype = ATTN_DTYPE_F32 if out_dtype == torch.float32 else ATTN_DTYPE_BF16
-    p.chunk = int(chunk)
+    width = block_table.shape[-1] if isinstance(block_table, torch.Tensor) and block_table.dim() else 0
+    if out is None:
+        out = torch.empty(qs, dtype=out_dtype, device=q.device)
+    if lse is None and want_lse:
+        lse = torch.empty(qs[:-1], dtype=torch.float32, device=q.device)
     if workspace is not None:
-        _need(workspace, "workspace", torch.uint8, 1, device=dev)
-        p.workspace, p.workspace_bytes = workspace.data_ptr(), workspace.shape[0]
-    _call(load().attn_decode_q4, p, dev, stream, "attn_decode_q4")
+        _need(workspace, "workspace", torch.uint8, 1, device=q.device)
+    p = attn_decode_q4_params(
+        q.data_ptr(), pool.data_ptr(), _fit(block_table, "block_table", torch.int32, (B, width), at),
+        _fit(kv_lens, "kv_lens", torch.int32, (B,), at), _fit(out, "out", out_dtype, qs, at),
+        None if lse is None else _fit(lse, "lse", torch.float32, qs[:-1], at),
+        B, Hq, Hkv, qs[2] if many else 1, D, page_size, width, num_pages,
+        1.0 / math.sqrt(D) if scale is None else scale,
+        ATTN_DTYPE_F32 if out_dtype == torch.float32 else ATTN_DTYPE_BF16, int(chunk),
+        None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.shape[0],
+        _stream_of(stream, at))
+    _call(load().attn_decode_q4, p, at, "attn_decode_q4")
     return out, lse
 
 

@@ -115,9 +115,10 @@ def test_page_step_refusals(lib, kw, code):
     assert lib.attn_page_step(params(B.attn_page_step_params, **{**PAGE, **kw})) == code
 
 
-S3 = (0, 512, 128)
-NORM = dict(q=FAKE, k=FAKE, q_out=FAKE, k_out=FAKE, positions=FAKE, B=1, L=4, Hq=4, Hkv=2, D=128, eps=1e-6, q_stride=S3,
-            k_stride=S3, q_out_stride=S3, k_out_stride=S3, rope=B.attn_rope(FAKE, FAKE, 16, B.ATTN_ROPE_HALF, None))
+NORM = dict(q=FAKE, k=FAKE, q_out=FAKE, k_out=FAKE, positions=FAKE, B=1, L=4, Hq=4, Hkv=2, D=128, eps=1e-6,
+            **{f"{t}_{axis}_stride": n for t in ("q", "k", "q_out", "k_out") for axis, n in
+               (("sequence", 0), ("token", 512), ("head", 128))},
+            rope_cos=FAKE, rope_sin=FAKE, rope_max_pos=16, rope_style=B.ATTN_ROPE_HALF)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -128,22 +129,22 @@ NORM = dict(q=FAKE, k=FAKE, q_out=FAKE, k_out=FAKE, positions=FAKE, B=1, L=4, Hq
     (dict(L=-1), B.ATTN_ERR_INVALID_ARG),
     (dict(eps=-1e-6), B.ATTN_ERR_INVALID_ARG),
     (dict(eps=float("nan")), B.ATTN_ERR_INVALID_ARG),
-    (dict(rope=B.attn_rope(FAKE, FAKE, 16, 9, None)), B.ATTN_ERR_INVALID_ARG),
-    (dict(rope=B.attn_rope(FAKE, None, 16, 1, None)), B.ATTN_ERR_INVALID_ARG),
+    (dict(rope_style=9), B.ATTN_ERR_INVALID_ARG),
+    (dict(rope_sin=None), B.ATTN_ERR_INVALID_ARG),
     (dict(D=96), B.ATTN_ERR_UNSUPPORTED),
     (dict(B=1 << 16, L=1 << 16), B.ATTN_ERR_UNSUPPORTED),
     (dict(q=FAKE + 8), B.ATTN_ERR_ALIGNMENT),
     (dict(k_weight=FAKE + 2), B.ATTN_ERR_ALIGNMENT),
-    (dict(q_stride=(0, 512, 132)), B.ATTN_ERR_ALIGNMENT),
-    (dict(k_out_stride=(0, 260, 128)), B.ATTN_ERR_ALIGNMENT),
+    (dict(q_head_stride=132), B.ATTN_ERR_ALIGNMENT),
+    (dict(k_out_token_stride=260), B.ATTN_ERR_ALIGNMENT),
     (dict(positions=FAKE + 2), B.ATTN_ERR_ALIGNMENT),
 ])
 def test_qk_norm_rope_refusals(lib, kw, code):
     assert lib.attn_qk_norm_rope(params(B.attn_qk_norm_rope_params, **{**NORM, **kw})) == code
 
 
-APPEND = dict(k=FAKE, v=FAKE, pool=FAKE, slots=FAKE, T=2, Hkv=2, D=128, page_size=16, num_pages=4, k_stride=(256, 128),
-              v_stride=(256, 128))
+APPEND = dict(k=FAKE, v=FAKE, pool=FAKE, slots=FAKE, T=2, Hkv=2, D=128, page_size=16, num_pages=4,
+              k_token_stride=256, k_head_stride=128, v_token_stride=256, v_head_stride=128)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -157,7 +158,7 @@ APPEND = dict(k=FAKE, v=FAKE, pool=FAKE, slots=FAKE, T=2, Hkv=2, D=128, page_siz
     (dict(D=32), B.ATTN_ERR_UNSUPPORTED),
     (dict(num_pages=1 << 28), B.ATTN_ERR_UNSUPPORTED),
     (dict(pool=FAKE + 64), B.ATTN_ERR_ALIGNMENT),
-    (dict(k_stride=(256, 4)), B.ATTN_ERR_ALIGNMENT),
+    (dict(k_head_stride=4), B.ATTN_ERR_ALIGNMENT),
     (dict(slots=FAKE + 2), B.ATTN_ERR_ALIGNMENT),
 ])
 def test_kv_append_refusals(lib, kw, code):
@@ -211,6 +212,23 @@ def test_empty_calls_succeed_without_a_device(lib):
     assert lib.attn_kv_append_q4(params(B.attn_kv_append_q4_params, **{**APPEND, "T": 0})) == B.ATTN_OK
     assert lib.attn_kv_gather_q4(params(B.attn_kv_gather_q4_params, **{**GATHER, "total_k": 0})) == B.ATTN_OK
     assert lib.attn_decode_q4(params(B.attn_decode_q4_params, **{**DECODE, "B": 0})) == B.ATTN_OK
+
+
+def test_parameter_structs_match_the_header(tmp_path):
+    """Offsets of the last field and sizes of the ctypes mirrors against a C compiler's view of the header."""
+    import os
+    import subprocess
+    names = ["attn_page_step_params", "attn_qk_norm_rope_params", "attn_kv_append_q4_params",
+             "attn_kv_gather_q4_params", "attn_decode_q4_params"]
+    src = tmp_path / "sizes.c"
+    src.write_text('#include <stddef.h>\n#include <stdio.h>\n#include "attn.h"\nint main(void) {\n' + "".join(
+        f'  printf("%zu %zu\\n", sizeof({n}), offsetof({n}, stream));\n' for n in names) + "  return 0;\n}\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    subprocess.run(["gcc", "-std=c11", "-I", os.path.join(root, "include"), str(src), "-o", str(tmp_path / "sizes")],
+                   check=True)
+    out = subprocess.run([str(tmp_path / "sizes")], check=True, capture_output=True, text=True).stdout.split()
+    want = [x for n in names for x in (ctypes.sizeof(getattr(B, n)), getattr(B, n).stream.offset)]
+    assert [int(x) for x in out] == want
 
 
 def test_sizes(lib):
