@@ -45,6 +45,9 @@ constexpr float kLn2 = 0.6931471805599453f;
 #ifndef ATTN_Q4_ROW_COST
 #define ATTN_Q4_ROW_COST 16
 #endif
+#ifndef ATTN_Q4_KT
+#define ATTN_Q4_KT 2
+#endif
 constexpr int kRowCostTiles = ATTN_Q4_ROW_COST;  // tiles charged to every row for its piece-end work
 
 // NT: groups of 8 query rows a CTA serves.
@@ -53,12 +56,12 @@ struct Q4Cfg {
   static constexpr int G = D / 64;                      // scale groups of a row
   static constexpr int COLS = 8 * NT;                   // query rows per CTA
   static constexpr int NW = 4;                          // consumer warps
-  static constexpr int KT = 2;                          // tiles of a stage per consumer warp
+  static constexpr int KT = ATTN_Q4_KT;                 // tiles of a stage per consumer warp
   static constexpr int ST = NW * KT;                    // tiles per stage (128 keys)
   static constexpr int TILE = kv_q4_tile_bytes(D);
   static constexpr int STAGE = ST * TILE;
   static constexpr int MINB = NT == 1 ? 3 : 2;          // resident CTAs per SM
-  static constexpr int NS = (NT == 1 ? 4 : 6) * (D == 128 ? 1 : 2);  // ring stages
+  static constexpr int NS = (NT == 1 ? 8 : 12) / KT * (D == 128 ? 1 : 2);  // ring stages
   static constexpr int THREADS = 32 * (NW + 1);
   static constexpr int LENS_CACHE = 384;                // kv_lens kept in shared memory for the walk
   static constexpr int OSTR = D + 4;                    // floats between columns of a warp's parked O
@@ -74,12 +77,13 @@ struct Q4Cfg {
   static_assert(ST <= 32, "a stage spans at most one page per lane");
 };
 
-struct Q4StageInfo {
+// What the first stage of a row piece tells about the piece.
+struct Q4PieceInfo {
   int b;       // sequence; -1 marks the end of the work
   int hg;      // kv head * chunks + chunk
-  int tile0;   // the stage's first tile of the sequence
-  int nt;      // tiles in this stage
-  int flags;   // 1: first stage of a row piece, 2: last
+  int tile0;   // the piece's first tile of the sequence
+  int tiles;   // and their number
+  int len;     // keys of the sequence
   int np;      // CTAs holding a piece of this row (0: no keys, 1: whole row here)
   int slot;    // this CTA's partial slot for the piece
   int lo_par;  // 2 * first CTA holding a piece + its slot parity
@@ -130,8 +134,8 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MINB)
   extern __shared__ __align__(128) uint8_t smem[];
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* empty = full + C::NS;
-  uint64_t* told = empty + C::NS;  // the stage's record is written (its data may still be on the way)
-  Q4StageInfo* info = reinterpret_cast<Q4StageInfo*>(smem + C::OFF_INFO);
+  uint64_t* told = empty + C::NS;  // a piece's record is written (its data may still be on the way)
+  Q4PieceInfo* info = reinterpret_cast<Q4PieceInfo*>(smem + C::OFF_INFO);
   float* mbuf = reinterpret_cast<float*>(smem + C::OFF_M);
   float* lbuf = reinterpret_cast<float*>(smem + C::OFF_L);
   int* lens_s = reinterpret_cast<int*>(smem + C::OFF_LENS);
@@ -262,17 +266,19 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MINB)
           lo_par = 2 * c_lo + (sm.starts_by(c_lo, ks - 1) ? 1 : 0);
         }
         if (lane == 0) {
-          Q4StageInfo si;
-          si.b = b;
-          si.hg = hg;
-          si.tile0 = t0;
-          si.nt = nt;
-          si.flags = (u == 0 ? 1 : 0) | (u == nst - 1 ? 2 : 0);
-          si.np = np;
-          si.slot = slot;
-          si.lo_par = lo_par;
-          info[slot_r] = si;
-          mbar_arrive(&told[slot_r]);
+          if (u == 0) {
+            Q4PieceInfo pi;
+            pi.b = b;
+            pi.hg = hg;
+            pi.tile0 = tb;
+            pi.tiles = n;
+            pi.len = seq_len(b);
+            pi.np = np;
+            pi.slot = slot;
+            pi.lo_par = lo_par;
+            info[slot_r] = pi;
+          }
+          mbar_arrive(&told[slot_r]);  // every stage, so that its phases run with the others'
           mbar_arrive(&full[slot_r]);
         }
       }
@@ -346,14 +352,14 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MINB)
   while (true) {
     int slot = t % C::NS;
     if (!mbar_wait(&told[slot], (t / C::NS) & 1, p.status, abort_flag)) break;
-    Q4StageInfo si = info[slot];
+    const Q4PieceInfo si = info[slot];
     if (si.b < 0) break;
     const int hkv = si.hg / chunks;
     const int row0 = (si.hg - hkv * chunks) * C::COLS;  // first query row of the kv head this CTA serves
-    const int len = clamp_len(p.kv_lens[si.b], Lmax);
+    const int len = si.len;
     // ---- q of the piece, as the first product's B operand ----
     uint32_t qf[NT][4 * G][2];
-    float f[NT][2], qs[NT][G][2];  // of columns 2 t4 and 2 t4 + 1: score factor, q's sums
+    float f[NT][2], qs[NT][G][2];  // of columns 2 t4 and 2 t4 + 1: score factor (>= 0), q's sums
     int vis[NT][2];                // keys the column sees
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -378,8 +384,8 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MINB)
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
       // e with 2^e <= amax < 2^(e+1); q 2^(4 - e) lies below 32 (elements 2^-25 of the largest and less lose bits)
       const int e = amax > 0.f ? max((int)(__float_as_uint(amax) >> 23) - 127, -100) : 0;
-      const float up = __uint_as_float((unsigned)(127 + 4 - e) << 23);
-      const float fc = p.scale * kLog2e * __uint_as_float((unsigned)(127 - 4 + e) << 23) * 16384.f;
+      const float up = copysignf(__uint_as_float((unsigned)(127 + 4 - e) << 23), p.scale);  // so that f >= 0
+      const float fc = fabsf(p.scale) * kLog2e * __uint_as_float((unsigned)(127 - 4 + e) << 23) * 16384.f;
       float sum[G];
 #pragma unroll
       for (int gg = 0; gg < G; ++gg) {
@@ -412,7 +418,8 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MINB)
     float o[4 * G][NT][4];   // O^T: dims 64 gg + 8 g + 2 mt (+1), columns 2 t4 (+1)
     float z[G][NT][2];       // this lane's share of sum p m_v
     float m[NT][2], l[NT][2];
-    float wscale = 1073741824.f;  // power of two the weights carry (2^30 until the first scales are seen)
+    // Weights, their sums l and z, and O all carry the factor 2^wexp (2^30 until the first scales are seen).
+    float wexp = 30.f;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -427,17 +434,15 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MINB)
     }
     const int all_see = len - p.Lq + 1;  // keys below it are seen by every column
 
-    // N tiles at `tp`, the first of which is tile `tile` of the sequence.
-    auto process = [&](const uint8_t* tp, int tile, auto n_c) {
+    // N tiles at `tp`, the first of which is tile `tile` of the sequence; EDGE: some column does not see all their keys.
+    auto process = [&](const uint8_t* tp, int tile, auto n_c, auto edge_c) {
       constexpr int N = decltype(n_c)::value;
+      constexpr bool EDGE = decltype(edge_c)::value;
       const int key0 = tile * kTileKeys;
-      const bool edge = key0 + N * kTileKeys > all_see;
       float x[N][NT][4];
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const uint8_t* tb = tp + i * C::TILE;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) x[i][nt][0] = x[i][nt][1] = x[i][nt][2] = x[i][nt][3] = 0.f;
 #pragma unroll
         for (int gg = 0; gg < G; ++gg) {
           const uint2 wa = *reinterpret_cast<const uint2*>(tb + gg * 512 + kg * 32 + t4 * 8);
@@ -464,48 +469,47 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MINB)
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              x[i][nt][c] += fmaf(pa.x, acc[nt][c], pa.y * qs[nt][gg][c]);
-              x[i][nt][2 + c] += fmaf(pb.x, acc[nt][2 + c], pb.y * qs[nt][gg][c]);
+              const float q = qs[nt][gg][c];
+              x[i][nt][c] = fmaf(pa.x, acc[nt][c], gg ? fmaf(pa.y, q, x[i][nt][c]) : pa.y * q);
+              x[i][nt][2 + c] = fmaf(pb.x, acc[nt][2 + c], gg ? fmaf(pb.y, q, x[i][nt][2 + c]) : pb.y * q);
             }
         }
       }
-      // logits in log2 units, masked; column maxima
-      float mx[NT][2];
+      // column maxima (of x, or at an edge of the masked logits f x), and with them the weights 2^(f x - max + wexp)
+      float alpha[NT][2];
+      bool rose = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          mx[nt][c] = -INFINITY;
+          float mx = -INFINITY;
 #pragma unroll
           for (int i = 0; i < N; ++i) {
-            x[i][nt][c] *= f[nt][c];
-            x[i][nt][2 + c] *= f[nt][c];
-            if (edge) {
+            if constexpr (EDGE) {
               const int k = key0 + i * kTileKeys + kg;
-              if (k >= vis[nt][c]) x[i][nt][c] = -INFINITY;
-              if (k + 8 >= vis[nt][c]) x[i][nt][2 + c] = -INFINITY;
+              x[i][nt][c] = k < vis[nt][c] ? x[i][nt][c] * f[nt][c] : -INFINITY;
+              x[i][nt][2 + c] = k + 8 < vis[nt][c] ? x[i][nt][2 + c] * f[nt][c] : -INFINITY;
             }
-            mx[nt][c] = max3f(mx[nt][c], x[i][nt][c], x[i][nt][2 + c]);
+            mx = max3f(mx, x[i][nt][c], x[i][nt][2 + c]);
           }
 #pragma unroll
-          for (int mask = 4; mask < 32; mask <<= 1)
-            mx[nt][c] = fmaxf(mx[nt][c], __shfl_xor_sync(0xffffffffu, mx[nt][c], mask));
-        }
-      bool rose = false;
-      float alpha[NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const float mn = fmaxf(m[nt][c], mx[nt][c]);
+          for (int mask = 4; mask < 32; mask <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, mask));
+          if constexpr (!EDGE) mx *= f[nt][c];
+          const float mn = fmaxf(m[nt][c], mx);
           const float ref = mn == -INFINITY ? 0.f : mn;
           alpha[nt][c] = ex2_approx(m[nt][c] - ref);  // 0 while the column has seen nothing (all its sums are 0)
           rose |= mn > m[nt][c];
           m[nt][c] = mn;
+          const float sub = wexp - ref;
 #pragma unroll
           for (int i = 0; i < N; ++i) {
-            x[i][nt][c] = ex2_approx(x[i][nt][c] - ref);
-            x[i][nt][2 + c] = ex2_approx(x[i][nt][2 + c] - ref);
+            if constexpr (EDGE) {
+              x[i][nt][c] = ex2_approx(x[i][nt][c] + sub);
+              x[i][nt][2 + c] = ex2_approx(x[i][nt][2 + c] + sub);
+            } else {
+              x[i][nt][c] = ex2_approx(fmaf(x[i][nt][c], f[nt][c], sub));
+              x[i][nt][2 + c] = ex2_approx(fmaf(x[i][nt][2 + c], f[nt][c], sub));
+            }
           }
         }
       if (__any_sync(0xffffffffu, rose)) {
@@ -523,37 +527,47 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MINB)
             }
           }
       }
-      // V's parameters; those of keys past the sequence's end are no data
-      float2 va[N][G], vb[N][G];
-      float smax = 0.f;
+      // V's pairs (those of keys past the sequence's end are no data).  All scales or-ed together lie above the largest
+      // (by less than a factor of 2 unless the or-ed exponents make infinity or NaN, which count as 65504).
+      uint32_t va[N][G], vb[N][G];
+      uint32_t all = 0;
 #pragma unroll
       for (int i = 0; i < N; ++i)
 #pragma unroll
         for (int gg = 0; gg < G; ++gg) {
           const uint8_t* tb = tp + i * C::TILE + kv_q4_vp_off(D) + gg * 4;
-          uint32_t ra = *reinterpret_cast<const uint32_t*>(tb + kg * G * 4);
-          uint32_t rb = *reinterpret_cast<const uint32_t*>(tb + (kg + 8) * G * 4);
-          if (edge) {
+          va[i][gg] = *reinterpret_cast<const uint32_t*>(tb + kg * G * 4);
+          vb[i][gg] = *reinterpret_cast<const uint32_t*>(tb + (kg + 8) * G * 4);
+          if constexpr (EDGE) {
             const int k = key0 + i * kTileKeys + kg;
-            if (k >= len) ra = 0;
-            if (k + 8 >= len) rb = 0;
+            if (k >= len) va[i][gg] = 0;
+            if (k + 8 >= len) vb[i][gg] = 0;
           }
-          va[i][gg] = half2_floats(ra);
-          vb[i][gg] = half2_floats(rb);
-          smax = max3f(smax, va[i][gg].x, vb[i][gg].x);
+          all |= va[i][gg] | vb[i][gg];
         }
-      if (__any_sync(0xffffffffu, smax * wscale > 32768.f)) {  // rare: smaller weights from here on
+      const float smax = half2_floats(all & 0x7fffu).x;
+      if (__any_sync(0xffffffffu, !(smax * ex2_approx(wexp) <= 32768.f))) {  // rare: smaller weights from here on
+        float sm = smax;
 #pragma unroll
-        for (int mask = 1; mask < 32; mask <<= 1) smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, mask));
-        const float ws = __uint_as_float((unsigned)(127 + 12 - ((int)(__float_as_uint(smax) >> 23) - 127)) << 23);
-        const float ratio = ws / wscale;
-        wscale = ws;
+        for (int mask = 1; mask < 32; mask <<= 1) sm = fmaxf(sm, __shfl_xor_sync(0xffffffffu, sm, mask));
+        // 2^wexp times the largest scale (below 2^16) lies in [2^11, 2^13)
+        const float we = (float)(12 - ((int)(__float_as_uint(fminf(sm, 65504.f)) >> 23) - 127));
+        const float ratio = ex2_approx(we - wexp);
+        wexp = we;
 #pragma unroll
-        for (int i = 0; i < 4 * G; ++i)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int c = 0; c < 4; ++c) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) o[i][nt][c] *= ratio;
+            for (int i = 0; i < N; ++i) x[i][nt][c] *= ratio;
+#pragma unroll
+            for (int i = 0; i < 4 * G; ++i) o[i][nt][c] *= ratio;
+            if (c < 2) {
+              l[nt][c] *= ratio;
+#pragma unroll
+              for (int gg = 0; gg < G; ++gg) z[gg][nt][c] *= ratio;
+            }
+          }
       }
 #pragma unroll
       for (int i = 0; i < N; ++i) {
@@ -566,13 +580,14 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MINB)
         for (int gg = 0; gg < G; ++gg) {
           uint32_t b0[NT], b1[NT];
           [[maybe_unused]] uint32_t c0[NT], c1[NT];
-          const float sa = va[i][gg].x * wscale, sb = vb[i][gg].x * wscale;
+          const float2 sa = half2_floats(va[i][gg]), sb = half2_floats(vb[i][gg]);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int c = 0; c < 2; ++c)
-              z[gg][nt][c] = fmaf(x[i][nt][c], va[i][gg].y, fmaf(x[i][nt][2 + c], vb[i][gg].y, z[gg][nt][c]));
-            const float w0 = x[i][nt][0] * sa, w1 = x[i][nt][1] * sa, w2 = x[i][nt][2] * sb, w3 = x[i][nt][3] * sb;
+              z[gg][nt][c] = fmaf(x[i][nt][c], sa.y, fmaf(x[i][nt][2 + c], sb.y, z[gg][nt][c]));
+            const float w0 = x[i][nt][0] * sa.x, w1 = x[i][nt][1] * sa.x, w2 = x[i][nt][2] * sb.x,
+                        w3 = x[i][nt][3] * sb.x;
             const uint32_t h0 = half2_bits(w0, w1), h1 = half2_bits(w2, w3);
             b0[nt] = transpose8(h0);
             b1[nt] = transpose8(h1);
@@ -610,43 +625,40 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MINB)
     };
 
     bool alive = true;
-    while (true) {
+    const int j0 = warp * C::KT;  // this warp's tiles of a stage
+    for (int done = 0;; done += C::ST) {
       if (!mbar_wait(&full[slot], (t / C::NS) & 1, p.status, abort_flag)) {
         alive = false;
         break;
       }
-      const int j0 = warp * C::KT;  // this warp's tiles of the stage
-      const int mine = min(si.nt - j0, C::KT);
+      const int mine = min(si.tiles - done - j0, C::KT);
+      const int tile = si.tile0 + done + j0;
       const uint8_t* tp = smem + slot * C::STAGE + j0 * C::TILE;
-      if (mine == C::KT) {
-        process(tp, si.tile0 + j0, std::integral_constant<int, C::KT>{});
+      if (mine == C::KT && (tile + C::KT) * kTileKeys <= all_see) {
+        process(tp, tile, std::integral_constant<int, C::KT>{}, std::false_type{});
       } else {
-        for (int i = 0; i < mine; ++i) process(tp + i * C::TILE, si.tile0 + j0 + i, std::integral_constant<int, 1>{});
+        for (int i = 0; i < mine; ++i)
+          process(tp + i * C::TILE, tile + i, std::integral_constant<int, 1>{}, std::true_type{});
       }
       __syncwarp();
-      if (si.flags & 2) break;  // the piece's last stage: its slot is released after the merge below
+      if (done + C::ST >= si.tiles) break;  // the piece's last stage: its slot is released after the merge below
       release(slot, t);
       ++t;
       slot = t % C::NS;
-      if (!mbar_wait(&told[slot], (t / C::NS) & 1, p.status, abort_flag)) {
-        alive = false;
-        break;
-      }
-      si = info[slot];
     }
     if (!alive) break;
 
     // ---------------- end of a row piece: merge the consumer warps, 8 columns at a time ----------------
     float* scr = reinterpret_cast<float*>(smem + slot * C::STAGE);
-    const float back = 1.f / wscale;
+    const float back = ex2_approx(-wexp);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       float zz[G][2], ll[2];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        ll[c] = l[nt][c];
+        ll[c] = l[nt][c] * back;
 #pragma unroll
-        for (int gg = 0; gg < G; ++gg) zz[gg][c] = z[gg][nt][c];
+        for (int gg = 0; gg < G; ++gg) zz[gg][c] = z[gg][nt][c] * back;
       }
 #pragma unroll
       for (int mask = 4; mask < 32; mask <<= 1)
