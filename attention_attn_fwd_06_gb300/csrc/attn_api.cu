@@ -34,6 +34,8 @@ struct DeviceState {
   unsigned* status = nullptr;
   void* ws = nullptr;
   size_t ws_bytes = 0;
+  void* ws_q4 = nullptr;  // attn_decode_q4's partials: all zeros between calls
+  size_t ws_q4_bytes = 0;
 };
 
 std::mutex g_mu;
@@ -95,34 +97,38 @@ int map_cuda(cudaError_t e) {
   return ATTN_ERR_CUDA;
 }
 
-// Ensures the workspace of `s` holds `bytes`.  Refuses to allocate while the
-// stream is being captured into a CUDA graph.  Caller holds g_mu.
-int ensure_workspace_locked(DeviceState& s, size_t bytes, cudaStream_t stream) {
-  if (bytes <= s.ws_bytes) return ATTN_OK;
+// Ensures the workspace (ws, ws_bytes) holds `bytes`, its first `zeroed` bytes zero when it is made.  Refuses to
+// allocate while the stream is being captured into a CUDA graph.  Caller holds g_mu.
+int ensure_buffer_locked(void*& ws, size_t& ws_bytes, size_t bytes, size_t zeroed, cudaStream_t stream) {
+  if (bytes <= ws_bytes) return ATTN_OK;
   cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
   if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess) {
     cudaGetLastError();
     return ATTN_ERR_CUDA;
   }
   if (cap != cudaStreamCaptureStatusNone) return ATTN_ERR_INVALID_ARG;
-  if (s.ws != nullptr) {
-    cudaFree(s.ws);  // synchronises the device: no earlier decode can still be using it
-    s.ws = nullptr;
-    s.ws_bytes = 0;
+  if (ws != nullptr) {
+    cudaFree(ws);  // synchronises the device: no earlier decode can still be using it
+    ws = nullptr;
+    ws_bytes = 0;
   }
-  if (cudaMalloc(&s.ws, bytes) != cudaSuccess) {
+  if (cudaMalloc(&ws, bytes) != cudaSuccess) {
     cudaGetLastError();
-    s.ws = nullptr;
+    ws = nullptr;
     return ATTN_ERR_CUDA;
   }
-  if (cudaMemset(s.ws, 0, kCounterBytes) != cudaSuccess) {  // counters start at zero
+  if (cudaMemset(ws, 0, zeroed) != cudaSuccess) {
     cudaGetLastError();
-    cudaFree(s.ws);
-    s.ws = nullptr;
+    cudaFree(ws);
+    ws = nullptr;
     return ATTN_ERR_CUDA;
   }
-  s.ws_bytes = bytes;
+  ws_bytes = bytes;
   return ATTN_OK;
+}
+
+int ensure_workspace_locked(DeviceState& s, size_t bytes, cudaStream_t stream) {
+  return ensure_buffer_locked(s.ws, s.ws_bytes, bytes, kCounterBytes, stream);  // counters start at zero
 }
 
 struct DecodeShape {
@@ -249,16 +255,17 @@ struct DecodeQ4Shape {
   int rows = 0;              // query rows of a kv head
   int cols = 0;              // of them per CTA
   size_t part_o_elems = 0;
-  size_t bytes = 0;          // counters + partials
+  size_t bytes = 0;
 };
 
+// One partial per CTA: cols x D sums, and for each of the CTA's warps its lanes' (max, sum) of two columns of eight.
 DecodeQ4Shape decode_q4_shape(int Hq, int Hkv, int Lq, int D, int num_sms) {
   DecodeQ4Shape s;
   s.rows = (Hq / Hkv) * Lq;
   s.cols = attn::decode_q4_cols(s.rows);
-  const size_t prows = (size_t)2 * attn::decode_q4_grid(num_sms, s.rows) * s.cols;
+  const size_t prows = (size_t)attn::decode_q4_grid(num_sms, s.rows) * s.cols;
   s.part_o_elems = prows * D;
-  s.bytes = kCounterBytes + prows * (D + 2) * sizeof(float);
+  s.bytes = prows * (D + attn::kDecodeQ4Warps * 16) * sizeof(float);
   return s;
 }
 
@@ -883,13 +890,11 @@ int attn_decode_q4(const attn_decode_q4_params* p) {
   st = device_state_locked(&s);
   if (st != ATTN_OK) return st;
   const DecodeQ4Shape sh = decode_q4_shape(p->Hq, p->Hkv, p->Lq, p->D, s->num_sms);
-  if (2 + (long long)p->B * p->Hkv * ((sh.rows + sh.cols - 1) / sh.cols) > attn::kDecodeCounterSlots)
-    return ATTN_ERR_UNSUPPORTED;
   char* ws = static_cast<char*>(p->workspace);
   if (ws == nullptr) {
-    st = ensure_workspace_locked(*s, sh.bytes, stream);
+    st = ensure_buffer_locked(s->ws_q4, s->ws_q4_bytes, sh.bytes, sh.bytes, stream);
     if (st != ATTN_OK) return st;
-    ws = static_cast<char*>(s->ws);
+    ws = static_cast<char*>(s->ws_q4);
   } else if (p->workspace_bytes < sh.bytes) {
     return ATTN_ERR_SCRATCH_TOO_SMALL;
   }
@@ -900,8 +905,7 @@ int attn_decode_q4(const attn_decode_q4_params* p) {
   L.kv_lens = p->kv_lens;
   L.out = p->out;
   L.lse = p->lse;
-  L.counters = reinterpret_cast<unsigned*>(ws);
-  L.part_o = reinterpret_cast<float*>(ws + kCounterBytes);
+  L.part_o = reinterpret_cast<float*>(ws);
   L.part_ml = L.part_o + sh.part_o_elems;
   L.B = p->B;
   L.Hq = p->Hq;
@@ -935,10 +939,11 @@ int attn_get_device_status(void* stream) {
   const unsigned zero = 0;
   if (cudaMemcpy(s->status, &zero, sizeof(zero), cudaMemcpyHostToDevice) != cudaSuccess) return ATTN_ERR_CUDA;
   if (v == ATTN_ERR_DEVICE_TIMEOUT) {
-    // A decode that gave up part-way may have left its work counters armed: clear them.
+    // A decode that gave up part-way may have left its work counters armed, or partials unread: clear them.
     int dev = -1;
     cudaGetDevice(&dev);
     if (s->ws != nullptr) cudaMemset(s->ws, 0, kCounterBytes);
+    if (s->ws_q4 != nullptr) cudaMemset(s->ws_q4, 0, s->ws_q4_bytes);
     if (dev >= 0 && dev < kMaxDevices && g_noalloc_ptr[dev] != nullptr) cudaMemset(g_noalloc_ptr[dev], 0, kCounterBytes);
     cudaDeviceSynchronize();
     cudaGetLastError();
@@ -957,6 +962,9 @@ void attn_release_workspace(void) {
   if (s.ws != nullptr) cudaFree(s.ws);
   s.ws = nullptr;
   s.ws_bytes = 0;
+  if (s.ws_q4 != nullptr) cudaFree(s.ws_q4);
+  s.ws_q4 = nullptr;
+  s.ws_q4_bytes = 0;
 }
 
 }  // extern "C"

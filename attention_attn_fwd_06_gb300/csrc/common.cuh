@@ -132,6 +132,19 @@ __device__ __forceinline__ unsigned atomic_add_acq_rel_gpu(unsigned* addr, unsig
   return old;
 }
 
+// Single words that other CTAs store and load at the same time (each of the four on its own).
+__device__ __forceinline__ uint4 ld_relaxed_gpu(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.relaxed.gpu.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p)
+               : "memory");
+  return v;
+}
+
+__device__ __forceinline__ void st_relaxed_gpu(uint4* p, uint4 v) {
+  asm volatile("st.relaxed.gpu.global.v4.u32 [%0], {%1,%2,%3,%4};" ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+
 // Release/acquire fence at GPU scope (lighter than the sequentially consistent __threadfence()).
 __device__ __forceinline__ void fence_acq_rel_gpu() { asm volatile("fence.acq_rel.gpu;" ::: "memory"); }
 

@@ -23,8 +23,10 @@
 //    below 2^15 and the largest near 2^12; a call with fp32 output carries them as two fp16 terms.  Maxima, sums,
 //    the term in m_v and all accumulators are fp32.
 // The split is decode.cu's: persistent CTAs take equal slices of the tiles of all (sequence, kv head, row chunk) rows, a
-// producer warp streams them with bulk copies (one copy per page and stage) into a shared-memory ring, the CTA
-// that lands a row's last partial merges it.
+// producer warp streams them with bulk copies (one copy per page and stage) into a shared-memory ring.  At a piece's
+// end each warp sums a quarter of the accumulators over the warps; a row split between CTAs is merged by the CTA that
+// holds its first piece, which reads the others' partials as they arrive.  CTAs start in order, and what a CTA waits
+// for no other CTA's wait holds up (it is the first thing that CTA does), so the wait ends with any number of CTAs resident.
 #include <cfloat>
 #include <cmath>
 #include <cuda_fp16.h>
@@ -45,6 +47,9 @@ constexpr float kLn2 = 0.6931471805599453f;
 #ifndef ATTN_Q4_ROW_COST
 #define ATTN_Q4_ROW_COST 16
 #endif
+#ifndef ATTN_Q4_NS
+#define ATTN_Q4_NS 4
+#endif
 #ifndef ATTN_Q4_KT
 #define ATTN_Q4_KT 2
 #endif
@@ -55,24 +60,27 @@ template <int D, int NT>
 struct Q4Cfg {
   static constexpr int G = D / 64;                      // scale groups of a row
   static constexpr int COLS = 8 * NT;                   // query rows per CTA
-  static constexpr int NW = 4;                          // consumer warps
+  static constexpr int NW = kDecodeQ4Warps;             // consumer warps
   static constexpr int KT = ATTN_Q4_KT;                 // tiles of a stage per consumer warp
   static constexpr int ST = NW * KT;                    // tiles per stage (128 keys)
   static constexpr int TILE = kv_q4_tile_bytes(D);
   static constexpr int STAGE = ST * TILE;
   static constexpr int MINB = NT == 1 ? 3 : 2;          // resident CTAs per SM
-  static constexpr int NS = (NT == 1 ? 8 : 12) / KT * (D == 128 ? 1 : 2);  // ring stages
+  static constexpr int NS = ATTN_Q4_NS * 2 / KT * (D == 128 ? 1 : 2);  // ring stages
   static constexpr int THREADS = 32 * (NW + 1);
-  static constexpr int LENS_CACHE = 384;                // kv_lens kept in shared memory for the walk
-  static constexpr int OSTR = D + 4;                    // floats between columns of a warp's parked O
-  static constexpr int OFF_BAR = NS * STAGE;            // full[NS], empty[NS], info_bar[NS]
+  static constexpr int LENS_CACHE = 128;                // kv_lens kept in shared memory for the walk
+  static constexpr int OW = 4 * G / NW;                 // accumulators of a column group a warp owns at a piece's end
+  static constexpr int SCR_BYTES = NW * (NW - 1) * NT * OW * 512;  // [owner][other warps][NT][OW][lane] float4
+  static constexpr bool SCR_IN_STAGE = SCR_BYTES <= STAGE;  // the exchange takes the piece's last stage, or its own room
+  static constexpr int OFF_SCR = NS * STAGE;
+  static constexpr int OFF_BAR = OFF_SCR + (SCR_IN_STAGE ? 0 : SCR_BYTES);  // full[NS], empty[NS], told[NS]
   static constexpr int OFF_INFO = OFF_BAR + 3 * NS * 8;
-  static constexpr int OFF_M = OFF_INFO + NS * 32;      // mbuf[NW][8]
-  static constexpr int OFF_L = OFF_M + NW * 8 * 4;      // lbuf[NW][8]
-  static constexpr int OFF_LENS = OFF_L + NW * 8 * 4;
+  static constexpr int OFF_ML = OFF_INFO + NS * 32;     // (m, l) [NW][COLS]
+  static constexpr int OFF_LENS = OFF_ML + NW * COLS * 8;
   static constexpr int OFF_MISC = OFF_LENS + LENS_CACHE * 4;
   static constexpr int SMEM = OFF_MISC + 16;
-  static_assert(NW * 8 * OSTR * 4 <= STAGE, "the piece-end merge parks every warp's O in one stage");
+  static_assert(4 * G % NW == 0, "every warp owns as many accumulators");
+  static_assert(OFF_BAR % 16 == 0 && OFF_ML % 8 == 0, "aligned regions");
   static_assert(MINB * (SMEM + 1024) <= 228 * 1024, "MINB CTAs per SM");
   static_assert(ST <= 32, "a stage spans at most one page per lane");
 };
@@ -85,8 +93,7 @@ struct Q4PieceInfo {
   int tiles;   // and their number
   int len;     // keys of the sequence
   int np;      // CTAs holding a piece of this row (0: no keys, 1: whole row here)
-  int slot;    // this CTA's partial slot for the piece
-  int lo_par;  // 2 * first CTA holding a piece + its slot parity
+  int first;   // whether this CTA holds the row's first piece (and merges the others')
 };
 
 __device__ __forceinline__ int clamp_len(int len, int Lmax) { return len < 0 ? 0 : (len > Lmax ? Lmax : len); }
@@ -114,15 +121,6 @@ __device__ __forceinline__ float2 half2_floats(uint32_t w) {
   return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
-__device__ __forceinline__ void store_out4(void* out, size_t idx, float4 v, int out_f32) {
-  if (out_f32) {
-    *reinterpret_cast<float4*>(reinterpret_cast<float*>(out) + idx) = v;
-  } else {
-    *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(out) + idx) =
-        make_uint2(pack2_bf16(v.x, v.y), pack2_bf16(v.z, v.w));
-  }
-}
-
 constexpr uint32_t kLowNibble = 0x000f000fu, kHighNibble = 0x00f000f0u;
 
 // WIDE: the weights of the second product as two fp16 terms (fp32 output).
@@ -136,11 +134,9 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MINB)
   uint64_t* empty = full + C::NS;
   uint64_t* told = empty + C::NS;  // a piece's record is written (its data may still be on the way)
   Q4PieceInfo* info = reinterpret_cast<Q4PieceInfo*>(smem + C::OFF_INFO);
-  float* mbuf = reinterpret_cast<float*>(smem + C::OFF_M);
-  float* lbuf = reinterpret_cast<float*>(smem + C::OFF_L);
+  float2* mlbuf = reinterpret_cast<float2*>(smem + C::OFF_ML);
   int* lens_s = reinterpret_cast<int*>(smem + C::OFF_LENS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC);
-  volatile int* last_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -230,21 +226,23 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MINB)
     };
     // Stream tiles [tb, te) of row (b, hg), whose tiles sit at cost positions [ks, ks + tiles); te == tb emits one
     // empty stage (a sequence with no keys).
-    auto emit = [&](int b, int hg, int tb, int te, long long ks, bool first_in_slice) -> bool {
+    auto emit = [&](int b, int hg, int tb, int te, long long ks) -> bool {
       const int hkv = hg / chunks;
       const int n = te - tb;
       const int nst = n > 0 ? (n + C::ST - 1) / C::ST : 1;
-      int np = 0, slot = 0, lo_par = 0;
+      int np = 0, first = 0;
       for (int u = 0; u < nst; ++u, ++t) {
         const int slot_r = t % C::NS;
         if (t >= C::NS && !wait_empty(slot_r)) return false;
         const int t0 = tb + u * C::ST;
         const int nt = n > 0 ? min(C::ST, te - t0) : 0;
-        if (lane == 0 && nt > 0) mbar_expect_tx(&full[slot_r], (uint32_t)nt * C::TILE);
+        if (lane == 0) {
+          if (nt > 0) mbar_expect_tx(&full[slot_r], (uint32_t)nt * C::TILE);
+        }
         __syncwarp();
         if (nt > 0) copy_tiles(b, hkv, t0, nt, smem + slot_r * C::STAGE, &full[slot_r]);
         if (u == 0 && nt > 0) {
-          // Which CTAs hold a piece of this row, and this piece's partial slot.
+          // Which CTAs hold a piece of this row.
           const long long last = ks + seq_tiles(b) - 1;
           int c_lo = 0, c_hi = cta;
           for (int top = cta;; top -= 32) {  // c_lo: the largest c <= cta with start(c) <= ks
@@ -262,8 +260,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MINB)
             }
           }
           np = c_hi - c_lo + 1;
-          slot = 2 * cta + (first_in_slice ? 0 : 1);
-          lo_par = 2 * c_lo + (sm.starts_by(c_lo, ks - 1) ? 1 : 0);
+          first = c_lo == cta;
         }
         if (lane == 0) {
           if (u == 0) {
@@ -274,8 +271,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MINB)
             pi.tiles = n;
             pi.len = seq_len(b);
             pi.np = np;
-            pi.slot = slot;
-            pi.lo_par = lo_par;
+            pi.first = first;
             info[slot_r] = pi;
           }
           mbar_arrive(&told[slot_r]);  // every stage, so that its phases run with the others'
@@ -286,13 +282,27 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MINB)
     };
 
     if (lo < hi) {
+      // the row whose cost interval holds position lo: sequences 32 at a time
       long long acc = 0;  // first cost position of sequence b
       int b = 0, nt = 0;
-      for (; b < p.B; ++b) {
-        nt = seq_tiles(b);
-        const long long rc = nt > 0 ? (long long)nt + kRowCostTiles : 0;
-        if (acc + (long long)Hg * rc > lo) break;
-        acc += (long long)Hg * rc;
+      for (int b32 = 0;; b32 += 32) {
+        const int my_nt = b32 + lane < p.B ? seq_tiles(b32 + lane) : 0;
+        const long long mine = my_nt > 0 ? Hg * ((long long)my_nt + kRowCostTiles) : 0;
+        long long upto = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+          const long long v = __shfl_up_sync(0xffffffffu, upto, off);
+          if (lane >= off) upto += v;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, acc + upto > lo);
+        if (past != 0) {
+          const int src = __ffs(past) - 1;
+          acc += __shfl_sync(0xffffffffu, upto - mine, src);
+          nt = __shfl_sync(0xffffffffu, my_nt, src);
+          b = b32 + src;
+          break;
+        }
+        acc += __shfl_sync(0xffffffffu, upto, 31);
       }
       long long rcost = (long long)nt + kRowCostTiles;
       int hg = (int)floor_div(lo - acc, rcost);
@@ -301,7 +311,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MINB)
       while (ok && pos < hi) {
         const long long ks = rs + kRowCostTiles;
         const long long a = max(pos, ks), e = min(hi, ks + nt);
-        if (a < e) ok = emit(b, hg, (int)(a - ks), (int)(e - ks), ks, a == lo);
+        if (a < e) ok = emit(b, hg, (int)(a - ks), (int)(e - ks), ks);
         pos = rs + rcost;
         rs += rcost;
         if (++hg == Hg) {
@@ -317,7 +327,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MINB)
     if (nonempty < p.B) {  // rows of sequences with no keys, one row per CTA in turn
       for (long long e = cta; ok && e < (long long)p.B * Hg; e += gridDim.x) {
         const int b = (int)floor_div(e, Hg);
-        if (seq_len(b) == 0) ok = emit(b, (int)(e - (long long)b * Hg), 0, 0, 0, false);
+        if (seq_len(b) == 0) ok = emit(b, (int)(e - (long long)b * Hg), 0, 0, 0);
       }
     }
     if (ok) {  // end-of-work marker
@@ -338,7 +348,6 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MINB)
   }
 
   // ---------------- consumers ----------------
-  const int ctid = threadIdx.x;
   constexpr int nct = C::NW * 32;
   const int g = lane >> 2, t4 = lane & 3;
   const int kg = g ^ ((g >> 2) & 1);             // key of the tile's score row g (row g + 8: kg + 8)
@@ -641,16 +650,20 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MINB)
           process(tp + i * C::TILE, tile + i, std::integral_constant<int, 1>{}, std::true_type{});
       }
       __syncwarp();
-      if (done + C::ST >= si.tiles) break;  // the piece's last stage: its slot is released after the merge below
+      if (done + C::ST >= si.tiles) break;  // the piece's last stage: its slot is released after the exchange below
       release(slot, t);
       ++t;
       slot = t % C::NS;
     }
     if (!alive) break;
 
-    // ---------------- end of a row piece: merge the consumer warps, 8 columns at a time ----------------
-    float* scr = reinterpret_cast<float*>(smem + slot * C::STAGE);
+    // ---------------- end of a row piece: each warp gathers its share of the accumulators from all ----------------
+    // Accumulators i = warp * OW .. + OW-1 of every column group are summed by `warp`, weighted by 2^(m_w - M), in warp
+    // order (bitwise reproducible).  A row held by one CTA is written; otherwise the share is this CTA's partial.
     const float back = ex2_approx(-wexp);
+    float own[NT][C::OW][4];
+    float4* const scr = reinterpret_cast<float4*>(smem + (C::SCR_IN_STAGE ? slot * C::STAGE : C::OFF_SCR));
+    named_bar_sync(1, nct);  // every warp is done with the stage and with the last piece's exchange
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       float zz[G][2], ll[2];
@@ -668,118 +681,195 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MINB)
 #pragma unroll
           for (int gg = 0; gg < G; ++gg) zz[gg][c] += __shfl_xor_sync(0xffffffffu, zz[gg][c], mask);
         }
-      named_bar_sync(1, nct);  // every warp is done with the stage (and with the columns before)
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
+      for (int w = 0; w < C::NW; ++w)
 #pragma unroll
-        for (int gg = 0; gg < G; ++gg) {
-          float y[8];
+        for (int k = 0; k < C::OW; ++k) {
+          const int i = w * C::OW + k;
+          float(&oo)[4] = o[i][nt];
 #pragma unroll
-          for (int mt = 0; mt < 4; ++mt) {
-            y[2 * mt] = fmaf(o[4 * gg + mt][nt][c], back * 16777216.f, zz[gg][c]);
-            y[2 * mt + 1] = fmaf(o[4 * gg + mt][nt][2 + c], back * 1048576.f, zz[gg][c]);
+          for (int c = 0; c < 4; ++c) oo[c] = fmaf(oo[c], back * (c < 2 ? 16777216.f : 1048576.f), zz[i / 4][c & 1]);
+          if (w == warp) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) own[nt][k][c] = oo[c];
+          } else {
+            const int from = warp < w ? warp : warp - 1;
+            scr[(((w * (C::NW - 1) + from) * NT + nt) * C::OW + k) * 32 + lane] = make_float4(oo[0], oo[1], oo[2], oo[3]);
           }
-          float4* dst = reinterpret_cast<float4*>(scr + (warp * 8 + 2 * t4 + c) * C::OSTR + 64 * gg + 8 * g);
-          dst[0] = make_float4(y[0], y[1], y[2], y[3]);
-          dst[1] = make_float4(y[4], y[5], y[6], y[7]);
         }
       if (g == 0) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          mbuf[warp * 8 + 2 * t4 + c] = m[nt][c];
-          lbuf[warp * 8 + 2 * t4 + c] = ll[c];
-        }
+        for (int c = 0; c < 2; ++c) mlbuf[warp * C::COLS + 8 * nt + 2 * t4 + c] = make_float2(m[nt][c], ll[c]);
       }
-      named_bar_sync(1, nct);
-      const int cols = min(8, rows - row0 - 8 * nt);
-      for (int e = ctid; e < cols * D / 4; e += nct) {
-        const int c = (4 * e) / D;
-        const int d = 4 * e - c * D;
-        float M = -INFINITY;
+    }
+    named_bar_sync(1, nct);
+    float M[NT][2], L[NT][2];
 #pragma unroll
-        for (int w = 0; w < C::NW; ++w) M = fmaxf(M, mbuf[w * 8 + c]);
-        float L = 0.f;
-        float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int nt = 0; nt < NT; ++nt) {
+      float wt[C::NW][2];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float2 ml[C::NW];
+        M[nt][c] = -INFINITY;
+        L[nt][c] = 0.f;
 #pragma unroll
         for (int w = 0; w < C::NW; ++w) {
-          const float mw = mbuf[w * 8 + c];
-          const float wt = (mw == -INFINITY) ? 0.f : ex2_approx(mw - M);
-          L = fmaf(wt, lbuf[w * 8 + c], L);
-          const float4 v = *reinterpret_cast<const float4*>(scr + (w * 8 + c) * C::OSTR + d);
-          O = make_float4(fmaf(wt, v.x, O.x), fmaf(wt, v.y, O.y), fmaf(wt, v.z, O.z), fmaf(wt, v.w, O.w));
+          ml[w] = mlbuf[w * C::COLS + 8 * nt + 2 * t4 + c];
+          M[nt][c] = fmaxf(M[nt][c], ml[w].x);
         }
-        if (si.np <= 1) {
-          const size_t orow = ((size_t)si.b * p.Hkv + hkv) * rows + row0 + 8 * nt + c;
-          const float inv = M == -INFINITY ? 0.f : 1.f / L;  // a column that sees no key: O = 0, lse = -inf
-          store_out4(p.out, orow * D + d, make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv), p.out_f32);
-          if (d == 0 && p.lse != nullptr) p.lse[orow] = M == -INFINITY ? -INFINITY : (M + log2f(L)) * kLn2;
-        } else {
-          const size_t prow = (size_t)si.slot * C::COLS + 8 * nt + c;
-          *reinterpret_cast<float4*>(p.part_o + prow * D + d) = O;
-          if (d == 0) reinterpret_cast<float2*>(p.part_ml)[prow] = make_float2(M, L);
+#pragma unroll
+        for (int w = 0; w < C::NW; ++w) {
+          wt[w][c] = ml[w].x == -INFINITY ? 0.f : ex2_approx(ml[w].x - M[nt][c]);
+          L[nt][c] = fmaf(wt[w][c], ml[w].y, L[nt][c]);
         }
       }
+#pragma unroll
+      for (int k = 0; k < C::OW; ++k) {
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < C::NW; ++w) {
+          const int from = w < warp ? w : w - 1;
+          float4 v = make_float4(own[nt][k][0], own[nt][k][1], own[nt][k][2], own[nt][k][3]);
+          if (w != warp) v = scr[(((warp * (C::NW - 1) + from) * NT + nt) * C::OW + k) * 32 + lane];
+          sum[0] = fmaf(wt[w][0], v.x, sum[0]);
+          sum[1] = fmaf(wt[w][1], v.y, sum[1]);
+          sum[2] = fmaf(wt[w][0], v.z, sum[2]);
+          sum[3] = fmaf(wt[w][1], v.w, sum[3]);
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) own[nt][k][c] = sum[c];
+      }
     }
-    fence_proxy_async_smem();  // the scratch stores come before the copy that refills the slot
-    named_bar_sync(1, nct);
+    if constexpr (C::SCR_IN_STAGE) {
+      fence_proxy_async_smem();  // the exchange comes before the copy that refills the slot
+      __syncwarp();
+    }
     release(slot, t);
     ++t;
-    if (si.np > 1) {
-      // Publish the partial; the CTA that lands a row's last partial merges them all.
-      if (ctid == 0) {
-        const unsigned ctr = 2u + (unsigned)(si.b * Hg + si.hg);
-        const unsigned old = atomic_add_acq_rel_gpu(&p.counters[ctr], 1u);
-        const int is_last = (old == (unsigned)si.np - 1u);
-        if (is_last) atomicExch(&p.counters[ctr], 0u);  // re-arm for the next call
-        *last_flag = is_last;
+    const size_t orow0 = ((size_t)si.b * p.Hkv + hkv) * rows + row0;
+    // The row's output from the sums `own`, M and L: two neighbouring dims of two columns for each accumulator.
+    auto write_out = [&]() {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int col = 8 * nt + 2 * t4 + c;
+          if (row0 + col >= rows) continue;
+          const bool none = M[nt][c] == -INFINITY;  // a column that sees no key: O = 0, lse = -inf
+          const float inv = none ? 0.f : 1.f / L[nt][c];
+          const size_t at = (orow0 + col) * D;
+#pragma unroll
+          for (int k = 0; k < C::OW; ++k) {
+            const int i = warp * C::OW + k;
+            const int d = 64 * (i / 4) + 8 * g + 2 * (i % 4);
+            const float a = own[nt][k][c] * inv, b = own[nt][k][2 + c] * inv;
+            if (p.out_f32)
+              *reinterpret_cast<float2*>(reinterpret_cast<float*>(p.out) + at + d) = make_float2(a, b);
+            else
+              *reinterpret_cast<uint32_t*>(reinterpret_cast<__nv_bfloat16*>(p.out) + at + d) = pack2_bf16(a, b);
+          }
+          if (warp == 0 && g == 0 && p.lse != nullptr)
+            p.lse[orow0 + col] = none ? -INFINITY : (M[nt][c] + log2f(L[nt][c])) * kLn2;
+        }
+    };
+    if (si.np <= 1) {
+      write_out();
+      continue;
+    }
+    // A row split between CTAs: the CTA with its first piece -- the last of that CTA's slice -- merges, each warp its
+    // share; every other piece starts its CTA's slice, so a CTA publishes at most one partial.  A partial's words are
+    // stored complemented over zeros, and no sum has the bits ~0 (a NaN that arithmetic does not make), so a word that is
+    // not zero has arrived: no fence, no count, no second round trip.  The merging warp zeroes what it has read.
+    uint4* const part_o = reinterpret_cast<uint4*>(p.part_o);
+    uint4* const part_ml = reinterpret_cast<uint4*>(p.part_ml);
+    auto o_at = [&](int sl, int nt, int k) {
+      return part_o + ((((size_t)sl * C::NW + warp) * NT + nt) * C::OW + k) * 32 + lane;
+    };
+    auto ml_at = [&](int sl, int nt) { return part_ml + (((size_t)sl * C::NW + warp) * NT + nt) * 32 + lane; };
+    auto inverted = [](float a, float b, float c, float d) {
+      return make_uint4(~__float_as_uint(a), ~__float_as_uint(b), ~__float_as_uint(c), ~__float_as_uint(d));
+    };
+    if (!si.first) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        if (row0 + 8 * nt + 2 * t4 >= rows) continue;
+        st_relaxed_gpu(ml_at(cta, nt), inverted(M[nt][0], L[nt][0], M[nt][1], L[nt][1]));
+#pragma unroll
+        for (int k = 0; k < C::OW; ++k)
+          st_relaxed_gpu(o_at(cta, nt, k), inverted(own[nt][k][0], own[nt][k][1], own[nt][k][2], own[nt][k][3]));
       }
-      named_bar_sync(1, nct);
-      if (*last_flag) {
-        const int cta_lo = si.lo_par >> 1;
-        const int cols = min(C::COLS, rows - row0);
-        const float2* ml_base = reinterpret_cast<const float2*>(p.part_ml);
-        for (int e = ctid; e < cols * D / 4; e += nct) {
-          const int c = (e * 4) / D;
-          const int d = e * 4 - c * D;
-          float M = -INFINITY, L = 0.f;
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-          auto fold = [&](float2 ml, float4 ov) {
-            if (ml.x > M) {
-              const float sc = (M == -INFINITY) ? 0.f : ex2_approx(M - ml.x);
-              acc = make_float4(acc.x * sc, acc.y * sc, acc.z * sc, acc.w * sc);
-              L *= sc;
-              M = ml.x;
-            }
-            const float w = (ml.x == -INFINITY) ? 0.f : ex2_approx(ml.x - M);
-            acc = make_float4(fmaf(w, ov.x, acc.x), fmaf(w, ov.y, acc.y), fmaf(w, ov.z, acc.z), fmaf(w, ov.w, acc.w));
-            L = fmaf(w, ml.y, L);
-          };
-          auto slot_of = [&](int i) { return i == 0 ? si.lo_par : 2 * (cta_lo + i); };
-          auto batch = [&](int i, auto n_c) {
-            constexpr int N = decltype(n_c)::value;
-            float2 ml[N];
-            float4 ov[N];
+      continue;
+    }
+    // Fold the others' partials in slice order with running maxima (a fixed order: bitwise reproducible), the loads of
+    // up to N in flight at a time.
+    auto fold = [&](int i, auto n_c) -> bool {
+      constexpr int N = decltype(n_c)::value;
 #pragma unroll
-            for (int u = 0; u < N; ++u) {
-              const size_t prow = (size_t)slot_of(i + u) * C::COLS + c;
-              ml[u] = __ldcg(ml_base + prow);
-              ov[u] = __ldcg(reinterpret_cast<const float4*>(p.part_o + prow * D + d));
-            }
+      for (int nt = 0; nt < NT; ++nt) {
+        const bool have = row0 + 8 * nt + 2 * t4 < rows;
+        uint4 ml[N], ov[N][C::OW];
+        uint64_t since = 0;
+        while (true) {
+          uint32_t least = 1;
 #pragma unroll
-            for (int u = 0; u < N; ++u) fold(ml[u], ov[u]);
-          };
-          int i = 0;
-          for (; i + 7 < si.np; i += 8) batch(i, std::integral_constant<int, 8>{});
-          for (; i + 1 < si.np; i += 2) batch(i, std::integral_constant<int, 2>{});
-          if (i < si.np) batch(i, std::integral_constant<int, 1>{});
-          const float inv = M == -INFINITY ? 0.f : 1.f / L;
-          const size_t orow = ((size_t)si.b * p.Hkv + hkv) * rows + row0 + c;
-          store_out4(p.out, orow * D + d, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv), p.out_f32);
-          if (d == 0 && p.lse != nullptr) p.lse[orow] = M == -INFINITY ? -INFINITY : (M + log2f(L)) * kLn2;
+          for (int u = 0; u < N; ++u) {
+            ml[u] = make_uint4(1, 1, 1, 1);
+            if (have) ml[u] = ld_relaxed_gpu(ml_at(cta + i + u, nt));
+#pragma unroll
+            for (int k = 0; k < C::OW; ++k) {
+              ov[u][k] = make_uint4(1, 1, 1, 1);
+              if (have) ov[u][k] = ld_relaxed_gpu(o_at(cta + i + u, nt, k));
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < N; ++u) {
+            least = min(least, min(min(ml[u].x, ml[u].y), min(ml[u].z, ml[u].w)));
+#pragma unroll
+            for (int k = 0; k < C::OW; ++k)
+              least = min(least, min(min(ov[u][k].x, ov[u][k].y), min(ov[u][k].z, ov[u][k].w)));
+          }
+          if (__all_sync(0xffffffffu, least != 0)) break;
+          const uint64_t now = globaltimer_ns();
+          if (since == 0) since = now;
+          if (__any_sync(0xffffffffu, now - since > kWaitLimitNs)) {
+            record_status(p.status, ATTN_ERR_DEVICE_TIMEOUT);
+            return false;
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+          const float mc[2] = {__uint_as_float(~ml[u].x), __uint_as_float(~ml[u].z)};
+          const float lc[2] = {__uint_as_float(~ml[u].y), __uint_as_float(~ml[u].w)};
+          float sc[2], w[2];
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const float mn = fmaxf(M[nt][c], mc[c]);
+            sc[c] = M[nt][c] == -INFINITY ? 0.f : ex2_approx(M[nt][c] - mn);
+            w[c] = mc[c] == -INFINITY ? 0.f : ex2_approx(mc[c] - mn);
+            M[nt][c] = mn;
+            L[nt][c] = fmaf(w[c], lc[c], L[nt][c] * sc[c]);
+          }
+#pragma unroll
+          for (int k = 0; k < C::OW; ++k) {
+            const uint32_t v[4] = {ov[u][k].x, ov[u][k].y, ov[u][k].z, ov[u][k].w};
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              own[nt][k][c] = fmaf(w[c & 1], __uint_as_float(~v[c]), own[nt][k][c] * sc[c & 1]);
+          }
+          if (have) {
+            st_relaxed_gpu(ml_at(cta + i + u, nt), make_uint4(0, 0, 0, 0));
+#pragma unroll
+            for (int k = 0; k < C::OW; ++k) st_relaxed_gpu(o_at(cta + i + u, nt, k), make_uint4(0, 0, 0, 0));
+          }
         }
       }
-    }
-    named_bar_sync(1, nct);  // mbuf/lbuf/last_flag are reused by the next piece
+      return true;
+    };
+    int i = 1;
+    bool got = true;
+    for (; got && i + 3 < si.np; i += 4) got = fold(i, std::integral_constant<int, 4>{});
+    for (; got && i < si.np; ++i) got = fold(i, std::integral_constant<int, 1>{});
+    if (got) write_out();
   }
 }
 

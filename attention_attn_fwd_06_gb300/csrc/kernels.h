@@ -182,9 +182,8 @@ struct DecodeQ4Launch {
   const int* kv_lens;      // [B], the Lq new tokens' keys included
   void* out;               // [B, Hq, Lq, D], bf16 or fp32
   float* lse;              // [B, Hq, Lq] or null
-  float* part_o;           // fp32 [2 * grid][cols][D]
-  float* part_ml;          // fp32 [2 * grid][cols][2]
-  unsigned* counters;      // [2 + row]; zero between calls
+  float* part_o;           // fp32 [grid][cols * D], in the order of the warps' accumulators; zero between calls
+  float* part_ml;          // fp32 [grid][4 warps][cols / 8][32 lanes][4]; zero between calls
   int B, Hq, Hkv, Lq, D, page_size, max_pages, num_pages;
   int min_tiles;           // smallest slice of the tiles one CTA takes (>= 1)
   float scale;
@@ -194,6 +193,7 @@ struct DecodeQ4Launch {
   int fault_skip_arrive;   // test hook: CTA 0 withholds one slot release
   cudaStream_t stream;
 };
+constexpr int kDecodeQ4Warps = 4;
 // Query rows one CTA serves, and the CTAs of the persistent launch, for `rows` = (Hq / Hkv) * Lq.
 int decode_q4_cols(int rows);
 int decode_q4_grid(int num_sms, int rows);

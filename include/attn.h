@@ -506,17 +506,17 @@ int attn_kv_gather_q4(const attn_kv_gather_q4_params* p);
  *   out, lse     as attn_decode_multi
  *   chunk        0 = default; otherwise the smallest number of keys of one CTA's slice,
  *                in [1, 1048576]
- *   workspace    NULL: the library's split-KV workspace, with attn_decode's rules (not
- *                grown during capture; calls that can overlap on the GPU race on it).
- *                Otherwise a DEVICE buffer of workspace_bytes (at least
- *                attn_decode_q4_workspace_bytes; ATTN_ERR_SCRATCH_TOO_SMALL if not),
- *                16-byte aligned, whose first 256 KiB were zero before its first call;
- *                the calls keep them so.  Calls that can overlap, and graphs that can be
- *                replayed at once, each take a buffer of their own.  After
- *                ATTN_ERR_DEVICE_TIMEOUT the caller zeroes it again.
+ *   workspace    NULL: a workspace of the library (its own, apart from attn_decode's, with
+ *                the same rules: grown on demand but not during capture, calls that can
+ *                overlap on the GPU race on it, and growing it invalidates graphs captured
+ *                with the smaller one).  Otherwise a DEVICE buffer of workspace_bytes (at
+ *                least attn_decode_q4_workspace_bytes; ATTN_ERR_SCRATCH_TOO_SMALL if not),
+ *                16-byte aligned, all zeros before its first call; the calls leave it so.
+ *                Calls that can overlap, and graphs that can be replayed at once, each take
+ *                a buffer of their own.  After ATTN_ERR_DEVICE_TIMEOUT the caller zeroes it
+ *                again.
  * (Hq / Hkv) * Lq at most 128.  Weights are rounded to fp16 before the second product;
  * with out_dtype = ATTN_DTYPE_F32 they are carried in two fp16 terms.
- * B * Hkv * ceil((Hq / Hkv) * Lq / 16) at most 65534 (ATTN_ERR_UNSUPPORTED otherwise).
  */
 typedef struct attn_decode_q4_params {
   const void* q;
@@ -552,7 +552,7 @@ int attn_get_device_status(void* stream);
 const char* attn_status_string(int status);
 
 /*
- * attn_release_workspace -- frees the current device's split-KV workspace.
+ * attn_release_workspace -- frees the current device's split-KV workspaces.
  * The caller must ensure no decode call using it is still in flight (for
  * example by synchronising the streams it was used on).
  */
