@@ -784,6 +784,7 @@ int attn_qk_norm_rope(const attn_qk_norm_rope_params* p) {
   L.rope = rope_args(p->rope);
   L.status = s->status;
   L.stream = static_cast<cudaStream_t>(p->stream);
+  L.num_sms = s->num_sms;
   return map_cuda(attn::launch_qk_norm_rope(L));
 }
 

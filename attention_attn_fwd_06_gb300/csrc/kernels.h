@@ -143,6 +143,7 @@ struct QkNormRopeLaunch {
   float eps;
   long long qs[3], ks[3], qos[3], kos[3];
   RopeArgs rope;
+  int num_sms;
   unsigned* status;
   cudaStream_t stream;
 };

@@ -5,11 +5,20 @@
 // minimum are held in fp16: eleven bits, so that a code's step is off by 2^-12 at most against the step's half that
 // the four bits themselves cost.  NaN is stored as 0, values beyond fp16's range as its largest.
 //
-// What bounds both: HBM.  Writing takes 2 bytes in and 0.5625 out per element, reading back the reverse.  A thread
-// takes 16 dims (32 bytes of bf16, 8 bytes of codes), so four lanes hold a group and its extremes take two shuffles.
+// What bounds both: HBM, once the arithmetic is short.  Writing takes 2 bytes in and 0.5625 out per element, reading
+// back the reverse.  A lane takes 16 dims (32 bytes of bf16, 8 bytes of codes), so four lanes hold a group and its
+// extremes take two shuffles.  One such piece of work a lane and as many warps as fit: 70k tokens of 8 heads at D = 128
+// take 89 us to write and 72 us to read back (a plain fill of as many bytes takes 75 us), against 113 and 79 us with a warp for each token and two rounds of its heads
+// in flight, 124 and 111 us with one wave of warps that walk runs of tokens.
 //
-// The rounding is decided without a division: k = floor of the approximate quotient brackets it, and the sign of
-// x - m - (k + 1/2) s, one fused multiply-add over an exact product, says whether k or k + 1 is nearer.
+// Writing: extremes by packed bf16 min and max that pass NaN on; quotients correctly rounded, by a product with the
+// rounded reciprocal and its residual's share (Markstein's theorem), so that a tie between two codes is seen as one; their
+// rounding is that of an add of 1.5 2^23, whose low bits are the code (a conversion instruction runs at an eighth of the
+// rate); all of it in packed pairs.  Issue-bound before (floor, conversions and a decision by residual: 166 us, 112 us with
+// the residual only checked, which bf16's coarse values tie too often for).  A group whose codes or values leave
+// their range (NaN, infinities, a scale of 0, a minimum that fp16 rounds) is decided code by code.
+// Reading: a code masked in place in a 16-bit half is, as fp16, the subnormal u 2^-24 or u 2^-20, so the conversion to
+// fp32 and one fused multiply-add with the scale make the value.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -22,136 +31,219 @@ namespace attn {
 namespace {
 
 constexpr float kF16Max = 65504.f;
+constexpr int kKvThreads = 256;
 
-template <int D>
-__global__ void __launch_bounds__(256) kv_append_q4_kernel(const KvAppendQ4Launch p, long long threads) {
-  constexpr int G = D / 64, TPR = D / 16;
-  const long long tid = (long long)blockIdx.x * 256 + threadIdx.x;
-  if (tid >= threads) return;  // whole rows: a multiple of TPR threads
-  const int sub = (int)(tid % TPR);
-  const long long row = tid / TPR;  // (token, K then V, head)
-  const int heads2 = 2 * p.Hkv;
-  const long long tok = row / heads2;
-  const int hh = (int)(row - tok * heads2);
-  const bool is_v = hh >= p.Hkv;
-  const int h = is_v ? hh - p.Hkv : hh;
-  const int slot = p.slots[tok];
-  const bool live = slot >= 0 && slot < p.num_pages * p.page_size;
-  if (!live && slot != -1 && sub == 0) record_status(p.status, ATTN_ERR_DEVICE_BOUNDS);
-  const __nv_bfloat16* src = is_v ? reinterpret_cast<const __nv_bfloat16*>(p.v) + tok * p.vs[0] + h * p.vs[1]
-                                  : reinterpret_cast<const __nv_bfloat16*>(p.k) + tok * p.ks[0] + h * p.ks[1];
+// The codes of 16 dims, decided one by one (u_j = the nearest code, ties to even, in 0..15).
+__device__ __noinline__ uint2 quantise_slow(uint4 w0, uint4 w1, float s, float m) {
   float x[16];
-  unpack8(*reinterpret_cast<const uint4*>(src + 16 * sub), *reinterpret_cast<float(*)[8]>(x));
-  unpack8(*reinterpret_cast<const uint4*>(src + 16 * sub + 8), *reinterpret_cast<float(*)[8]>(x + 8));
+  unpack8(w0, *reinterpret_cast<float(*)[8]>(x));
+  unpack8(w1, *reinterpret_cast<float(*)[8]>(x + 8));
+  unsigned out[2] = {0, 0};
+  if (!(s > 0.f)) return make_uint2(0, 0);
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const float v = x[j] == x[j] ? fminf(fmaxf(x[j], -kF16Max), kF16Max) : 0.f;
+    const float t = v - m;
+    const float k = fminf(fmaxf(floorf(t / s), 0.f), 14.f);
+    const float e = fmaf(-(k + 0.5f), s, t);  // its sign is exact
+    const int ki = (int)k;
+    out[j / 8] |= (unsigned)(ki + ((e > 0.f || (e == 0.f && (ki & 1))) ? 1 : 0)) << (4 * (j % 8));
+  }
+  return make_uint2(out[0], out[1]);
+}
+
+// Extremes of a group with NaN as 0 and values beyond fp16's range as its largest (one lane's 16 dims).
+__device__ __noinline__ float2 extremes_slow(uint4 w0, uint4 w1) {
+  float x[16];
+  unpack8(w0, *reinterpret_cast<float(*)[8]>(x));
+  unpack8(w1, *reinterpret_cast<float(*)[8]>(x + 8));
   float lo = INFINITY, hi = -INFINITY;
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
-    x[j] = x[j] == x[j] ? fminf(fmaxf(x[j], -kF16Max), kF16Max) : 0.f;
-    lo = fminf(lo, x[j]);
-    hi = fmaxf(hi, x[j]);
+    const float v = x[j] == x[j] ? fminf(fmaxf(x[j], -kF16Max), kF16Max) : 0.f;
+    lo = fminf(lo, v);
+    hi = fmaxf(hi, v);
   }
-  const unsigned team = 0xfu << (threadIdx.x & 28);  // the group's four lanes (rows end on a multiple of four)
+  return make_float2(lo, hi);
+}
+
+__device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t w) { return *reinterpret_cast<__nv_bfloat162*>(&w); }
+__device__ __forceinline__ uint32_t bits_of(__nv_bfloat162 v) { return *reinterpret_cast<uint32_t*>(&v); }
+
+template <int D>
+__global__ void __launch_bounds__(kKvThreads) kv_append_q4_kernel(const KvAppendQ4Launch p, const unsigned nrows) {
+  constexpr int G = D / 64, TPR = D / 16;  // groups and lanes of a row
+  const unsigned row = blockIdx.x * (kKvThreads / TPR) + threadIdx.x / TPR;  // (token, K's heads then V's)
+  if (row >= nrows) return;  // whole groups of lanes
+  const int sub = threadIdx.x % TPR;
+  const unsigned tok = row / (2u * p.Hkv);
+  const int hh = (int)(row - tok * (2u * p.Hkv));
+  const bool is_v = hh >= p.Hkv;
+  const int h = is_v ? hh - p.Hkv : hh;
+  const uint4* src = reinterpret_cast<const uint4*>(
+      is_v ? reinterpret_cast<const __nv_bfloat16*>(p.v) + (long long)tok * p.vs[0] + h * p.vs[1] + 16 * sub
+           : reinterpret_cast<const __nv_bfloat16*>(p.k) + (long long)tok * p.ks[0] + h * p.ks[1] + 16 * sub);
+  const int slot = p.slots[tok];
+  const uint4 wa = src[0], wb = src[1];
+  const unsigned team = 0xfu << (threadIdx.x & 28);  // the group's four lanes
+  const uint32_t q[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
+  __nv_bfloat162 mn = as_bf162(q[0]), mx = mn;
+#pragma unroll
+  for (int j = 1; j < 8; ++j) {
+    mn = __hmin2_nan(mn, as_bf162(q[j]));
+    mx = __hmax2_nan(mx, as_bf162(q[j]));
+  }
 #pragma unroll
   for (int mask = 1; mask < 4; mask <<= 1) {
-    lo = fminf(lo, __shfl_xor_sync(team, lo, mask));
-    hi = fmaxf(hi, __shfl_xor_sync(team, hi, mask));
+    mn = __hmin2_nan(mn, as_bf162(__shfl_xor_sync(team, bits_of(mn), mask)));
+    mx = __hmax2_nan(mx, as_bf162(__shfl_xor_sync(team, bits_of(mx), mask)));
   }
-  if (!live) return;
-  const __half sh = __float2half_rn(__fdiv_rn(hi - lo, 15.f)), mh = __float2half_rn(lo);
-  const float s = __half2float(sh), m = __half2float(mh);
-  const float inv = s > 0.f ? 1.f / s : 0.f;
-  unsigned w[2] = {0, 0};
+  mn = __hmin2_nan(mn, __lowhigh2highlow(mn));
+  mx = __hmax2_nan(mx, __lowhigh2highlow(mx));
+  float lo = __low2float(mn), hi = __low2float(mx);
+  bool odd = !(lo >= -kF16Max) || !(hi <= kF16Max);  // too large, or NaN: the same for the group's four lanes
+  if (odd) {
+    float2 ex = extremes_slow(wa, wb);
 #pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    const float t = x[j] - m;
-    const float k = fminf(fmaxf(floorf(t * inv), 0.f), 14.f);
-    const float e = fmaf(-(k + 0.5f), s, t);
-    const int ki = (int)k;
-    const int u = ki + ((e > 0.f || (e == 0.f && (ki & 1))) ? 1 : 0);
-    w[j / 8] |= (unsigned)u << (4 * (j % 8));
+    for (int mask = 1; mask < 4; mask <<= 1) {
+      ex.x = fminf(ex.x, __shfl_xor_sync(team, ex.x, mask));
+      ex.y = fmaxf(ex.y, __shfl_xor_sync(team, ex.y, mask));
+    }
+    lo = ex.x;
+    hi = ex.y;
   }
-  if (!(s > 0.f)) w[0] = w[1] = 0;
+  if (slot < 0 || slot >= p.num_pages * p.page_size) {  // -1: not written; anything else is an error
+    if (slot != -1 && sub == 0) record_status(p.status, ATTN_ERR_DEVICE_BOUNDS);
+    return;
+  }
+  // (hi - lo) / 15: a product, and its residual's share added (correctly rounded, as by Markstein's theorem)
+  const float d = hi - lo;
+  const float d0 = d * (1.f / 15.f);
+  const __half sh = __float2half_rn(fmaf(fmaf(-15.f, d0, d), 1.f / 15.f, d0)), mh = __float2half_rn(lo);
+  const float s = __half2float(sh), m = __half2float(mh);
+  const float inv = __frcp_rn(s);
+  // all quotients lie between those of lo and hi (infinite or NaN where s is 0)
+  odd |= !((lo - m) * inv > -0.25f) || !((hi - m) * inv < 15.25f);
+  constexpr float kMagic = 12582912.f;  // 1.5 2^23: adding it rounds to an integer, ties to even
+  const float2 m2 = make_float2(-m, -m), i2 = make_float2(inv, inv), s2 = make_float2(-s, -s);
+  const float2 up = make_float2(kMagic, kMagic);
+  uint32_t c[2] = {0, 0};
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    float2 x;
+    bf16x2_to_f32(q[j], x.x, x.y);
+    const float2 t = __fadd2_rn(x, m2);
+    const float2 q0 = __fmul2_rn(t, i2);
+    const float2 b = __fadd2_rn(__ffma2_rn(__ffma2_rn(q0, s2, t), i2, q0), up);
+    c[j / 4] += (__float_as_uint(b.x) << (8 * (j % 4))) + (__float_as_uint(b.y) << (8 * (j % 4) + 4));
+  }
+  // the sums of the adds' exponent bits: sum of 0x4b400000 << 4 j, j = 0..7, modulo 2^32
+  constexpr uint32_t kBias = 0x4b400000u + (0x4b400000u << 4) + (0x4b400000u << 8) + (0x4b400000u << 12) +
+                             (0x4b400000u << 16) + (0x4b400000u << 20) + (0x4b400000u << 24) + (0x4b400000u << 28);
+  uint2 code = make_uint2(c[0] - kBias, c[1] - kBias);
+  if (odd) code = quantise_slow(wa, wb, s, m);
   const int page = slot / p.page_size, in_page = slot - page * p.page_size;
-  const int tile = in_page / kTileKeys, key = in_page - tile * kTileKeys;
+  const int tile = in_page / kTileKeys, key = in_page % kTileKeys;
   uint8_t* dst = reinterpret_cast<uint8_t*>(p.pool) + kv_q4_tile_at(page, h, tile, p.Hkv, p.page_size / kTileKeys, D);
   const int g = sub / 4;
-  *reinterpret_cast<uint2*>(dst + (is_v ? kv_q4_v_off(D) : 0) + (g * kTileKeys + key) * 32 + (sub % 4) * 8) =
-      make_uint2(w[0], w[1]);
+  *reinterpret_cast<uint2*>(dst + (is_v ? kv_q4_v_off(D) : 0) + (g * kTileKeys + key) * 32 + (sub % 4) * 8) = code;
   if (sub % 4 == 0)
     *reinterpret_cast<__half2*>(dst + (is_v ? kv_q4_vp_off(D) : kv_q4_kp_off(D)) + (key * G + g) * 4) =
         __halves2half2(sh, mh);
 }
 
-__device__ __forceinline__ void codes_to_bf16(uint2 w, __half2 par, __nv_bfloat16* dst) {
-  const float s = __low2float(par), m = __high2float(par);
-  float x[16];
+__device__ __forceinline__ void codes_to_bf16(uint2 w, uint32_t pair, __nv_bfloat16* dst) {
+  const float2 sm = __half22float2(*reinterpret_cast<__half2*>(&pair));
+  const float s24 = sm.x * 16777216.f, s20 = sm.x * 1048576.f;
 #pragma unroll
-  for (int j = 0; j < 16; ++j) x[j] = fmaf(s, (float)(((j < 8 ? w.x : w.y) >> (4 * (j % 8))) & 15u), m);
-  *reinterpret_cast<uint4*>(dst) = pack8(*reinterpret_cast<float(*)[8]>(x));
-  *reinterpret_cast<uint4*>(dst + 8) = pack8(*reinterpret_cast<float(*)[8]>(x + 8));
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t v = i ? w.y : w.x;
+    float x[8];
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {  // dims n and n + 4 of the word
+      const uint32_t h = (n < 2 ? v : v >> 8) & (n % 2 ? 0x00f000f0u : 0x000f000fu);
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+      x[n] = fmaf(f.x, n % 2 ? s20 : s24, sm.y);
+      x[n + 4] = fmaf(f.y, n % 2 ? s20 : s24, sm.y);
+    }
+    *reinterpret_cast<uint4*>(dst + 8 * i) = pack8(x);
+  }
 }
 
 template <int D>
-__global__ void __launch_bounds__(256) kv_gather_q4_kernel(const KvGatherQ4Launch p, long long threads) {
+__global__ void __launch_bounds__(kKvThreads) kv_gather_q4_kernel(const KvGatherQ4Launch p, const unsigned nrows) {
   constexpr int G = D / 64, TPR = D / 16;
-  const long long tid = (long long)blockIdx.x * 256 + threadIdx.x;
-  if (tid >= threads) return;
-  const int sub = (int)(tid % TPR);
-  const long long row = tid / TPR;  // (token, head)
-  const long long tok = row / p.Hkv;
-  const int h = (int)(row - tok * p.Hkv);
-  if (tok >= p.cu_k[p.B] || tok < p.cu_k[0]) return;  // rows of no sequence stay as they were
-  int lo = 0, hi = p.B;  // the sequence with cu[s] <= tok < cu[s + 1]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (p.cu_k[mid] <= tok) lo = mid; else hi = mid;
+  const unsigned row = blockIdx.x * (kKvThreads / TPR) + threadIdx.x / TPR;  // (token, head)
+  if (row >= nrows) return;
+  const int sub = threadIdx.x % TPR;
+  const int tok = (int)(row / (unsigned)p.Hkv);
+  const int h = (int)(row - (unsigned)tok * p.Hkv);
+  int seq = 0;
+  for (int n = p.B; n > 1;) {  // the last of the sequences that start at or before tok
+    const int half = n / 2;
+    if (p.cu_k[seq + half] <= tok) {
+      seq += half;
+      n -= half;
+    } else {
+      n = half;
+    }
   }
-  const long long pos = tok - p.cu_k[lo] + (p.kv_starts != nullptr ? p.kv_starts[lo] : 0);
-  const long long pg = pos >= 0 ? pos / p.page_size : -1;
+  const int first = p.cu_k[seq];
+  if (tok < first || tok >= p.cu_k[seq + 1]) return;  // rows of no sequence stay as they were
+  const long long pos = (long long)tok - first + (p.kv_starts != nullptr ? p.kv_starts[seq] : 0);
+  const int pg = pos >= 0 && pos <= 0x7fffffffLL ? (int)pos / p.page_size : -1;
   int page = -1;
-  if (pg >= 0 && pg < p.max_pages) page = p.block_table[(size_t)lo * p.max_pages + pg];
+  if (pg >= 0 && pg < p.max_pages) page = p.block_table[(size_t)seq * p.max_pages + pg];
   if (page < 0 || page >= p.num_pages) {  // the row stays as it was
     if (sub == 0) record_status(p.status, ATTN_ERR_DEVICE_BOUNDS);
     return;
   }
-  const int in_page = (int)(pos - pg * p.page_size);
-  const int tile = in_page / kTileKeys, key = in_page - tile * kTileKeys;
+  const int in_page = (int)pos - pg * p.page_size;
+  const int tile = in_page / kTileKeys, key = in_page % kTileKeys;
   const uint8_t* src =
       reinterpret_cast<const uint8_t*>(p.pool) + kv_q4_tile_at(page, h, tile, p.Hkv, p.page_size / kTileKeys, D);
   const int g = sub / 4;
   const int code = (g * kTileKeys + key) * 32 + (sub % 4) * 8, par = (key * G + g) * 4;
   const uint2 wk = *reinterpret_cast<const uint2*>(src + code);
   const uint2 wv = *reinterpret_cast<const uint2*>(src + kv_q4_v_off(D) + code);
-  const __half2 pk = *reinterpret_cast<const __half2*>(src + kv_q4_kp_off(D) + par);
-  const __half2 pv = *reinterpret_cast<const __half2*>(src + kv_q4_vp_off(D) + par);
+  const uint32_t pk = *reinterpret_cast<const uint32_t*>(src + kv_q4_kp_off(D) + par);
+  const uint32_t pv = *reinterpret_cast<const uint32_t*>(src + kv_q4_vp_off(D) + par);
   const size_t at = (size_t)row * D + 16 * sub;
   codes_to_bf16(wk, pk, reinterpret_cast<__nv_bfloat16*>(p.k) + at);
   codes_to_bf16(wv, pv, reinterpret_cast<__nv_bfloat16*>(p.v) + at);
 }
 
+// Blocks for `rows` rows of D elements; cudaErrorNotSupported past 2^31 rows (more than any GPU's memory).
+cudaError_t kv_blocks(long long rows, int D, unsigned& blocks) {
+  if (rows > 0x7fffffffLL) return cudaErrorNotSupported;
+  const int per = kKvThreads / (D / 16);
+  blocks = (unsigned)((rows + per - 1) / per);
+  return cudaSuccess;
+}
+
 }  // namespace
 
 cudaError_t launch_kv_append_q4(const KvAppendQ4Launch& p) {
-  const long long threads = (long long)p.T * 2 * p.Hkv * (p.D / 16);
-  if (threads == 0) return cudaSuccess;
-  const long long blocks = (threads + 255) / 256;
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const long long rows = 2ll * p.T * p.Hkv;
+  unsigned blocks;
+  const cudaError_t e = kv_blocks(rows, p.D, blocks);
+  if (e != cudaSuccess || blocks == 0) return e;
   if (p.D == 64)
-    kv_append_q4_kernel<64><<<(unsigned)blocks, 256, 0, p.stream>>>(p, threads);
+    kv_append_q4_kernel<64><<<blocks, kKvThreads, 0, p.stream>>>(p, (unsigned)rows);
   else
-    kv_append_q4_kernel<128><<<(unsigned)blocks, 256, 0, p.stream>>>(p, threads);
+    kv_append_q4_kernel<128><<<blocks, kKvThreads, 0, p.stream>>>(p, (unsigned)rows);
   return cudaGetLastError();
 }
 
 cudaError_t launch_kv_gather_q4(const KvGatherQ4Launch& p) {
-  const long long threads = (long long)p.total_k * p.Hkv * (p.D / 16);
-  if (threads == 0) return cudaSuccess;
-  const long long blocks = (threads + 255) / 256;
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const long long rows = (long long)p.total_k * p.Hkv;
+  unsigned blocks;
+  const cudaError_t e = kv_blocks(rows, p.D, blocks);
+  if (e != cudaSuccess || blocks == 0) return e;
   if (p.D == 64)
-    kv_gather_q4_kernel<64><<<(unsigned)blocks, 256, 0, p.stream>>>(p, threads);
+    kv_gather_q4_kernel<64><<<blocks, kKvThreads, 0, p.stream>>>(p, (unsigned)rows);
   else
-    kv_gather_q4_kernel<128><<<(unsigned)blocks, 256, 0, p.stream>>>(p, threads);
+    kv_gather_q4_kernel<128><<<blocks, kKvThreads, 0, p.stream>>>(p, (unsigned)rows);
   return cudaGetLastError();
 }
 

@@ -17,14 +17,20 @@
 namespace attn {
 namespace {
 
+#ifndef ATTN_NORM_U
+#define ATTN_NORM_U 4
+#endif
+#ifndef ATTN_NORM_MINB
+#define ATTN_NORM_MINB 2
+#endif
 constexpr int kNormWarps = 8;
 
 // STYLE 0: no rotation, 1: pairs (i, i + D/2), 2: pairs (2i, 2i + 1).
 template <int D, int STYLE>
-__global__ void __launch_bounds__(32 * kNormWarps) qk_norm_rope_kernel(const QkNormRopeLaunch p, int chunks, int rounds) {
+__global__ void __launch_bounds__(32 * kNormWarps, ATTN_NORM_MINB) qk_norm_rope_kernel(const QkNormRopeLaunch p, int chunks, int rounds) {
   constexpr int TPR = D / 16;    // lanes per head
   constexpr int HPW = 32 / TPR;  // heads per warp and round
-  constexpr int U = 4;           // rounds in flight
+  constexpr int U = ATTN_NORM_U;  // rounds in flight
   constexpr int OFF_B = STYLE == 1 ? D / 2 : 8;  // from a lane's first 8 elements to its other 8
   const int lane = threadIdx.x & 31;
   const long long job = (long long)blockIdx.x * kNormWarps + (threadIdx.x >> 5);
@@ -35,51 +41,46 @@ __global__ void __launch_bounds__(32 * kNormWarps) qk_norm_rope_kernel(const QkN
   const int i0 = 8 * sub;                          // the lane's first pair
   const int d0 = STYLE == 1 ? 8 * sub : 16 * sub;  // its first element
   const long long sb = tok / p.L, st = tok - sb * p.L;
-  float c[8], s[8];
-  if (p.positions != nullptr) {
-    const int pos = p.positions[tok];
-    if (pos < 0 || (STYLE != 0 && pos >= p.rope.max_pos)) {  // -1 pads; anything else out of range is an error
-      if (pos != -1 && lane == 0) record_status(p.status, ATTN_ERR_DEVICE_BOUNDS);
-      return;
-    }
-    if constexpr (STYLE != 0) {
-      const float4* cr = reinterpret_cast<const float4*>(p.rope.cos + (size_t)pos * (D / 2) + i0);
-      const float4* sr = reinterpret_cast<const float4*>(p.rope.sin + (size_t)pos * (D / 2) + i0);
-      *reinterpret_cast<float4*>(c) = __ldg(cr);
-      *reinterpret_cast<float4*>(c + 4) = __ldg(cr + 1);
-      *reinterpret_cast<float4*>(s) = __ldg(sr);
-      *reinterpret_cast<float4*>(s + 4) = __ldg(sr + 1);
-    }
-  }
+  const int pos = p.positions != nullptr ? p.positions[tok] : 0;
   const __nv_bfloat16* qrow = reinterpret_cast<const __nv_bfloat16*>(p.q) + sb * p.qs[0] + st * p.qs[1] + d0;
   const __nv_bfloat16* krow = reinterpret_cast<const __nv_bfloat16*>(p.k) + sb * p.ks[0] + st * p.ks[1] + d0;
-  __nv_bfloat16* qdst = reinterpret_cast<__nv_bfloat16*>(p.q_out) + sb * p.qos[0] + st * p.qos[1] + d0;
-  __nv_bfloat16* kdst = reinterpret_cast<__nv_bfloat16*>(p.k_out) + sb * p.kos[0] + st * p.kos[1] + d0;
-  const uint4 one = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
-  uint4 wq[2] = {one, one}, wk[2] = {one, one};
-  if (p.q_weight != nullptr) {
-    wq[0] = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.q_weight) + d0));
-    wq[1] = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.q_weight) + d0 + OFF_B));
-  }
-  if (p.k_weight != nullptr) {
-    wk[0] = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.k_weight) + d0));
-    wk[1] = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.k_weight) + d0 + OFF_B));
-  }
   const int H = p.Hq + p.Hkv;
   const int r1 = min((chunk + 1) * rounds, (H + HPW - 1) / HPW);
-  for (int r0 = chunk * rounds; r0 < r1; r0 += U) {
-    uint4 x[U][2];
+  uint4 x[U][2];
+  auto load = [&](int r0) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int h = (r0 + u) * HPW + hw;
+      x[u][0] = x[u][1] = make_uint4(0, 0, 0, 0);
       if (r0 + u < r1 && h < H) {
         const __nv_bfloat16* src = h < p.Hq ? qrow + h * p.qs[2] : krow + (h - p.Hq) * p.ks[2];
         x[u][0] = *reinterpret_cast<const uint4*>(src);
         x[u][1] = *reinterpret_cast<const uint4*>(src + OFF_B);
-      } else {
-        x[u][0] = x[u][1] = make_uint4(0, 0, 0, 0);
       }
     }
+  };
+  int r0 = chunk * rounds;
+  load(r0);  // while the position, and then the tables, are on their way
+  if (pos < 0 || (STYLE != 0 && pos >= p.rope.max_pos)) {  // -1 pads; anything else out of range is an error
+    if (pos != -1 && lane == 0) record_status(p.status, ATTN_ERR_DEVICE_BOUNDS);
+    return;
+  }
+  float c[8], s[8];
+  if constexpr (STYLE != 0) {
+    const float4* cr = reinterpret_cast<const float4*>(p.rope.cos + (size_t)pos * (D / 2) + i0);
+    const float4* sr = reinterpret_cast<const float4*>(p.rope.sin + (size_t)pos * (D / 2) + i0);
+    *reinterpret_cast<float4*>(c) = __ldg(cr);
+    *reinterpret_cast<float4*>(c + 4) = __ldg(cr + 1);
+    *reinterpret_cast<float4*>(s) = __ldg(sr);
+    *reinterpret_cast<float4*>(s + 4) = __ldg(sr + 1);
+  }
+  __nv_bfloat16* qdst = reinterpret_cast<__nv_bfloat16*>(p.q_out) + sb * p.qos[0] + st * p.qos[1] + d0;
+  __nv_bfloat16* kdst = reinterpret_cast<__nv_bfloat16*>(p.k_out) + sb * p.kos[0] + st * p.kos[1] + d0;
+  const uint4* wq = reinterpret_cast<const uint4*>(
+      p.q_weight != nullptr ? reinterpret_cast<const __nv_bfloat16*>(p.q_weight) + d0 : nullptr);
+  const uint4* wk = reinterpret_cast<const uint4*>(
+      p.k_weight != nullptr ? reinterpret_cast<const __nv_bfloat16*>(p.k_weight) + d0 : nullptr);
+  while (true) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (r0 + u >= r1) break;  // warp-uniform
@@ -94,11 +95,17 @@ __global__ void __launch_bounds__(32 * kNormWarps) qk_norm_rope_kernel(const QkN
       for (int mask = 1; mask < TPR; mask <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, mask);
       const float inv = rsqrtf(ss * (1.f / D) + p.eps);
       const bool is_q = h < p.Hq;
-      float w[16];
-      unpack8(is_q ? wq[0] : wk[0], *reinterpret_cast<float(*)[8]>(w));
-      unpack8(is_q ? wq[1] : wk[1], *reinterpret_cast<float(*)[8]>(w + 8));
+      const uint4* wp = is_q ? wq : wk;  // (from L1: held in registers they would cost a quarter of the warps)
+      if (wp != nullptr) {
+        float w[16];
+        unpack8(__ldg(wp), *reinterpret_cast<float(*)[8]>(w));
+        unpack8(__ldg(wp + OFF_B / 8), *reinterpret_cast<float(*)[8]>(w + 8));
 #pragma unroll
-      for (int j = 0; j < 16; ++j) v[j] *= inv * w[j];
+        for (int j = 0; j < 16; ++j) v[j] *= inv * w[j];
+      } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] *= inv;
+      }
       float y[16];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -117,6 +124,9 @@ __global__ void __launch_bounds__(32 * kNormWarps) qk_norm_rope_kernel(const QkN
         *reinterpret_cast<uint4*>(dst + OFF_B) = pack8(*reinterpret_cast<float(*)[8]>(y + 8));
       }
     }
+    r0 += U;
+    if (r0 >= r1) break;
+    load(r0);
   }
 }
 
