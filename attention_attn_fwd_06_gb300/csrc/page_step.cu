@@ -17,10 +17,15 @@
 namespace attn {
 namespace {
 
-constexpr int kPageThreads = 1024;
+constexpr int kPageThreads = 1024;  // at most; kPageThreadsSmall for a decode step
+constexpr int kPageThreadsSmall = 256;
 
-__device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+// All CTAs of the launch: what each has read comes before what any writes next.
+__device__ __forceinline__ void launch_barrier() {
+  if (gridDim.x == 1)
+    __syncthreads();
+  else
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
 __device__ __forceinline__ int ceil_div_pos(int x, int d) { return (int)(((unsigned)x + (unsigned)d - 1u) / (unsigned)d); }
@@ -44,16 +49,17 @@ __global__ void __launch_bounds__(kPageThreads) page_step_kernel(const PageStepL
   int* kept = given + B + 1;    // [B] keys kept
   int* have = kept + B;         // [B] pages before the step
   int* need = have + B;         // [B] pages after it
-  __shared__ long long wsum[3][32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int gtid = blockIdx.x * kPageThreads + tid, gthreads = gridDim.x * kPageThreads;
+  __shared__ int wsum[4][32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
+  const int gtid = blockIdx.x * threads + tid, gthreads = gridDim.x * threads;
   const int count = *p.free_count;
 
   // ---- lengths and their running sums (every CTA: all rows) ----
   const long long cap = (long long)p.max_pages * ps;  // below 2^31
-  const int per = (B + kPageThreads - 1) / kPageThreads;
+  const int per = (B + threads - 1) / threads;
   const int b0 = min(tid * per, B), b1 = min(b0 + per, B);
-  long long s0 = 0, s1 = 0, s2 = 0;
+  int s0 = 0, s1 = 0, s2 = 0;            // the thread's tokens (modulo 2^32), pages taken, pages given back
+  unsigned n_low = 0, n_high = 0;        // tokens again, in halves that cannot overflow
   int bad = 0;
   for (int b = b0; b < b1; ++b) {
     const int a = p.kv_lens[b];
@@ -66,58 +72,64 @@ __global__ void __launch_bounds__(kPageThreads) page_step_kernel(const PageStepL
     have[b] = h;
     need[b] = d;
     s0 += ok ? n : 0;
+    n_low += ok ? n & 0xffff : 0;
+    n_high += ok ? n >> 16 : 0;
     s1 += max(d - h, 0);
     s2 += max(h - d, 0);
   }
-  long long i0 = s0, i1 = s1, i2 = s2;
+  int i0 = s0, i1 = s1, i2 = s2;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
-    const long long t0 = __shfl_up_sync(0xffffffffu, i0, off), t1 = __shfl_up_sync(0xffffffffu, i1, off),
-                    t2 = __shfl_up_sync(0xffffffffu, i2, off);
+    const int t0 = __shfl_up_sync(0xffffffffu, i0, off), t1 = __shfl_up_sync(0xffffffffu, i1, off),
+              t2 = __shfl_up_sync(0xffffffffu, i2, off);
     if (lane >= off) {
       i0 += t0;
       i1 += t1;
       i2 += t2;
     }
   }
+  n_low = __reduce_add_sync(0xffffffffu, n_low);
+  n_high = __reduce_add_sync(0xffffffffu, n_high);
   if (lane == 31) {
-    wsum[0][warp] = i0;
-    wsum[1][warp] = i1;
-    wsum[2][warp] = i2;
+    wsum[0][warp] = (int)n_low;
+    wsum[1][warp] = (int)n_high;
+    wsum[2][warp] = i1;
+    wsum[3][warp] = i2;
   }
   bad = __syncthreads_or(bad);
-  long long e0 = i0 - s0, e1 = i1 - s1, e2 = i2 - s2, total = 0, ntaken = 0, ngiven = 0;
-  for (int w = 0; w < kPageThreads / 32; ++w) {
-    if (w < warp) {
-      e0 += wsum[0][w];
-      e1 += wsum[1][w];
-      e2 += wsum[2][w];
-    }
-    total += wsum[0][w];
-    ntaken += wsum[1][w];
-    ngiven += wsum[2][w];
-  }
+  // lane w: warp w's sums; totals, and what comes before this warp
+  int ws[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) ws[k] = lane < threads / 32 ? wsum[k][lane] : 0;
+  const long long total = ((long long)__reduce_add_sync(0xffffffffu, (unsigned)ws[1]) << 16) +
+                          __reduce_add_sync(0xffffffffu, (unsigned)ws[0]);
+  const int ntaken = (int)__reduce_add_sync(0xffffffffu, (unsigned)ws[2]);
+  const int ngiven = (int)__reduce_add_sync(0xffffffffu, (unsigned)ws[3]);
+  const bool before = lane < warp;
+  int e0 = (int)__reduce_add_sync(0xffffffffu, before ? ((unsigned)ws[1] << 16) + (unsigned)ws[0] : 0u) + i0 - s0;
+  int e1 = (int)__reduce_add_sync(0xffffffffu, before ? (unsigned)ws[2] : 0u) + i1 - s1;
+  int e2 = (int)__reduce_add_sync(0xffffffffu, before ? (unsigned)ws[3] : 0u) + i2 - s2;
   const bool listed = p.slots != nullptr || p.positions != nullptr;
-  const bool wrong = bad || count < 0 || count + ngiven > p.num_pages || (listed && total > p.max_tokens) ||
+  const bool wrong = bad || count < 0 || (long long)count + ngiven > p.num_pages || (listed && total > p.max_tokens) ||
                      total > 0x7fffffffLL;
   const bool refused = wrong || count + ngiven < ntaken;
   if (!refused) {
     for (int b = b0; b < b1; ++b) {  // the row's sums again, from what it kept
-      cu[b] = (int)e0;
-      taken[b] = (int)e1;
-      given[b] = (int)e2;
+      cu[b] = e0;
+      taken[b] = e1;
+      given[b] = e2;
       e0 += p.new_lens != nullptr ? p.new_lens[b] : 0;
       e1 += max(need[b] - have[b], 0);
       e2 += max(have[b] - need[b], 0);
     }
     if (tid == 0) {
       cu[B] = (int)total;
-      taken[B] = (int)ntaken;
-      given[B] = (int)ngiven;
+      taken[B] = ntaken;
+      given[B] = ngiven;
     }
   }
   __syncthreads();
-  cluster_barrier();  // every CTA has read the lengths and the count: they may change now
+  if (gridDim.x > 1) launch_barrier();  // every CTA has read the lengths and the count: they may change now
 
   if (refused) {  // nothing changes but the lists, which name no token
     if (gtid == 0) record_status(p.status, wrong ? ATTN_ERR_DEVICE_BOUNDS : ATTN_ERR_DEVICE_POOL);
@@ -131,17 +143,17 @@ __global__ void __launch_bounds__(kPageThreads) page_step_kernel(const PageStepL
   }
 
   // ---- pages given back, onto the stack ----
-  for (int r = gtid; r < (int)ngiven; r += gthreads) {
+  for (int r = gtid; r < ngiven; r += gthreads) {
     const int b = row_of(given, B, r);
     int* entry = p.block_table + (size_t)b * p.max_pages + need[b] + (r - given[b]);
-    p.free_pages[count + (int)ngiven - 1 - r] = *entry;
+    p.free_pages[count + ngiven - 1 - r] = *entry;
     *entry = -1;
   }
-  if (ngiven > 0) cluster_barrier();  // (the same in every CTA) pages just given back can be taken below
-  const int top = count + (int)ngiven;
+  if (ngiven > 0) launch_barrier();  // (the same in every CTA) pages just given back can be taken below
+  const int top = count + ngiven;
 
   // ---- pages taken, lengths, running sums ----
-  for (int r = gtid; r < (int)ntaken; r += gthreads) {
+  for (int r = gtid; r < ntaken; r += gthreads) {
     const int b = row_of(taken, B, r);
     const int id = __ldcg(p.free_pages + top - 1 - r);
     if (id < 0 || id >= p.num_pages) record_status(p.status, ATTN_ERR_DEVICE_BOUNDS);
@@ -152,14 +164,15 @@ __global__ void __launch_bounds__(kPageThreads) page_step_kernel(const PageStepL
     if (p.cu_new != nullptr) p.cu_new[b] = cu[b];
   }
   if (gtid == 0) {
-    *p.free_count = top - (int)ntaken;
+    *p.free_count = top - ntaken;
     if (p.cu_new != nullptr) p.cu_new[B] = (int)total;
   }
 
   // ---- the new tokens: four in a row for each thread, which mostly share one row and one page ----
   if (!listed) return;
   const bool vec = ((reinterpret_cast<uintptr_t>(p.slots) | reinterpret_cast<uintptr_t>(p.positions)) & 15u) == 0;
-  for (long long i4 = 4ll * gtid; i4 < p.max_tokens; i4 += 4ll * gthreads) {
+  // (from the last thread on: other warps than those that work on rows, when there are few of both)
+  for (long long i4 = 4ll * (gthreads - 1 - gtid); i4 < p.max_tokens; i4 += 4ll * gthreads) {
     int slot[4], at[4];
     int b = i4 < total ? row_of(cu, B, (int)i4) : B;
     int pg = -1, id = -1, pgb = -1;
@@ -216,17 +229,22 @@ cudaError_t launch_page_step(const PageStepLaunch& p) {
     attr_set[dev] = true;
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kPageThreads);
+  // One CTA until the tokens fill it, or the pages that may move where no list of tokens bounds them; then the largest
+  // portable cluster.  (8 rows, a token each: 3.3 us a call with 256 threads, 5.9 us with 1024; 70k prompt tokens and their
+  // release, 4.4k pages: 13.9 us with clusters for both calls, 19.5 us with one CTA for the release.)
+  const bool unbounded = p.keep_lens != nullptr || p.max_tokens == 0;
+  const bool many = p.max_tokens > 2 * kPageThreads || (unbounded && (long long)p.B * p.max_pages > 4 * kPageThreads);
+  cfg.gridDim = dim3(many ? 8 : 1);
+  cfg.blockDim = dim3(many || p.B > kPageThreadsSmall || p.max_tokens > 4 * kPageThreadsSmall ? kPageThreads
+                                                                                               : kPageThreadsSmall);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = p.stream;
-  // One CTA for a decode step, the largest portable cluster once the tokens fill it.
-  cfg.gridDim = dim3(p.max_tokens > 2 * kPageThreads ? 8 : 1);
   cudaLaunchAttribute attr = {};
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = cfg.gridDim.x;
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = many ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, page_step_kernel, p);
 }
 
