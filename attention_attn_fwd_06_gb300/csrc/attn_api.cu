@@ -265,7 +265,7 @@ DecodeQ4Shape decode_q4_shape(int Hq, int Hkv, int Lq, int D, int num_sms) {
   s.cols = attn::decode_q4_cols(s.rows);
   const size_t prows = (size_t)attn::decode_q4_grid(num_sms, s.rows) * s.cols;
   s.part_o_elems = prows * D;
-  s.bytes = prows * (D + attn::kDecodeQ4Warps * 16) * sizeof(float);
+  s.bytes = prows * (D + attn::kDecodeQ4Owners * 16) * sizeof(float);
   return s;
 }
 

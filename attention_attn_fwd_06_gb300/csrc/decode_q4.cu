@@ -47,11 +47,20 @@ constexpr float kLn2 = 0.6931471805599453f;
 #ifndef ATTN_Q4_ROW_COST
 #define ATTN_Q4_ROW_COST 16
 #endif
-#ifndef ATTN_Q4_NS
-#define ATTN_Q4_NS 4
+#ifndef ATTN_Q4_NW
+#define ATTN_Q4_NW 4
 #endif
 #ifndef ATTN_Q4_KT
 #define ATTN_Q4_KT 2
+#endif
+#ifndef ATTN_Q4_KT2
+#define ATTN_Q4_KT2 2
+#endif
+#ifndef ATTN_Q4_TILES
+#define ATTN_Q4_TILES 32
+#endif
+#ifndef ATTN_Q4_TILES2
+#define ATTN_Q4_TILES2 32
 #endif
 constexpr int kRowCostTiles = ATTN_Q4_ROW_COST;  // tiles charged to every row for its piece-end work
 
@@ -60,17 +69,18 @@ template <int D, int NT>
 struct Q4Cfg {
   static constexpr int G = D / 64;                      // scale groups of a row
   static constexpr int COLS = 8 * NT;                   // query rows per CTA
-  static constexpr int NW = kDecodeQ4Warps;             // consumer warps
-  static constexpr int KT = ATTN_Q4_KT;                 // tiles of a stage per consumer warp
-  static constexpr int ST = NW * KT;                    // tiles per stage (128 keys)
+  static constexpr int NW = NT == 1 ? ATTN_Q4_NW : 4;  // consumer warps
+  static constexpr int KT = NT == 1 ? ATTN_Q4_KT : ATTN_Q4_KT2;    // tiles of a stage per consumer warp
+  static constexpr int ST = NW * KT;                    // tiles per stage
   static constexpr int TILE = kv_q4_tile_bytes(D);
   static constexpr int STAGE = ST * TILE;
-  static constexpr int MINB = NT == 1 ? 3 : 2;          // resident CTAs per SM
-  static constexpr int NS = ATTN_Q4_NS * 2 / KT * (D == 128 ? 1 : 2);  // ring stages
+  static constexpr int MINB = NW > 4 || NT == 2 ? 2 : 3;  // resident CTAs per SM
+  static constexpr int NS = (NT == 1 ? ATTN_Q4_TILES : ATTN_Q4_TILES2) * (D == 128 ? 1 : 2) / ST;  // ring stages
   static constexpr int THREADS = 32 * (NW + 1);
   static constexpr int LENS_CACHE = 128;                // kv_lens kept in shared memory for the walk
-  static constexpr int OW = 4 * G / NW;                 // accumulators of a column group a warp owns at a piece's end
-  static constexpr int SCR_BYTES = NW * (NW - 1) * NT * OW * 512;  // [owner][other warps][NT][OW][lane] float4
+  static constexpr int OWN = kDecodeQ4Owners;           // warps that gather the accumulators at a piece's end,
+  static constexpr int OW = 4 * G / OWN;                // each this many of a column group
+  static constexpr int SCR_BYTES = OWN * (NW - 1) * NT * OW * 512;  // [owner][other warps][NT][OW][lane] float4
   static constexpr bool SCR_IN_STAGE = SCR_BYTES <= STAGE;  // the exchange takes the piece's last stage, or its own room
   static constexpr int OFF_SCR = NS * STAGE;
   static constexpr int OFF_BAR = OFF_SCR + (SCR_IN_STAGE ? 0 : SCR_BYTES);  // full[NS], empty[NS], told[NS]
@@ -79,7 +89,7 @@ struct Q4Cfg {
   static constexpr int OFF_LENS = OFF_ML + NW * COLS * 8;
   static constexpr int OFF_MISC = OFF_LENS + LENS_CACHE * 4;
   static constexpr int SMEM = OFF_MISC + 16;
-  static_assert(4 * G % NW == 0, "every warp owns as many accumulators");
+  static_assert(OWN <= NW && 4 * G % OWN == 0, "every owner has as many accumulators");
   static_assert(OFF_BAR % 16 == 0 && OFF_ML % 8 == 0, "aligned regions");
   static_assert(MINB * (SMEM + 1024) <= 228 * 1024, "MINB CTAs per SM");
   static_assert(ST <= 32, "a stage spans at most one page per lane");
@@ -353,14 +363,21 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MINB)
   const int kg = g ^ ((g >> 2) & 1);             // key of the tile's score row g (row g + 8: kg + 8)
   const int kv0 = 2 * t4 + (t4 >> 1);            // keys of score rows 2 t4 and 2 t4 + 1: this order keeps
   const int kv1 = 2 * t4 + 1 - (t4 >> 1);        // the four lanes' 32-byte rows in different banks, for K and for V
-  auto release = [&](int slot, int t) {
-    if (lane == 0 && !(p.fault_skip_arrive && cta == 0 && t == 1)) mbar_arrive(&empty[slot]);
+  // The test hook withholds CTA 0's release of its second stage: the producer's bounded wait then runs out.
+  int to_skip = p.fault_skip_arrive && cta == 0 ? 1 : -1;
+  int slot = 0;
+  uint32_t phase = 0;  // of the ring
+  auto release = [&]() {
+    if (lane == 0 && to_skip != 0) mbar_arrive(&empty[slot]);
+    --to_skip;
+    if (++slot == C::NS) {
+      slot = 0;
+      phase ^= 1;
+    }
   };
 
-  int t = 0;  // stages consumed
   while (true) {
-    int slot = t % C::NS;
-    if (!mbar_wait(&told[slot], (t / C::NS) & 1, p.status, abort_flag)) break;
+    if (!mbar_wait(&told[slot], phase, p.status, abort_flag)) break;
     const Q4PieceInfo si = info[slot];
     if (si.b < 0) break;
     const int hkv = si.hg / chunks;
@@ -429,6 +446,13 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MINB)
     float m[NT][2], l[NT][2];
     // Weights, their sums l and z, and O all carry the factor 2^wexp (2^30 until the first scales are seen).
     float wexp = 30.f;
+    uint32_t wlimit;         // the largest scale, as fp16 bits, that wexp allows: 2^(15 - wexp) or less
+    float sub[NT][2];        // wexp - max of a column
+    auto set_wlimit = [&]() {
+      const __half h = __float2half_rz(ex2_approx(15.f - wexp) * 0.9990234375f);
+      wlimit = *reinterpret_cast<const uint16_t*>(&h);
+    };
+    set_wlimit();
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -436,6 +460,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MINB)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         m[nt][c] = -INFINITY;
+        sub[nt][c] = wexp;
         l[nt][c] = 0.f;
 #pragma unroll
         for (int gg = 0; gg < G; ++gg) z[gg][nt][c] = 0.f;
@@ -484,58 +509,6 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MINB)
             }
         }
       }
-      // column maxima (of x, or at an edge of the masked logits f x), and with them the weights 2^(f x - max + wexp)
-      float alpha[NT][2];
-      bool rose = false;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float mx = -INFINITY;
-#pragma unroll
-          for (int i = 0; i < N; ++i) {
-            if constexpr (EDGE) {
-              const int k = key0 + i * kTileKeys + kg;
-              x[i][nt][c] = k < vis[nt][c] ? x[i][nt][c] * f[nt][c] : -INFINITY;
-              x[i][nt][2 + c] = k + 8 < vis[nt][c] ? x[i][nt][2 + c] * f[nt][c] : -INFINITY;
-            }
-            mx = max3f(mx, x[i][nt][c], x[i][nt][2 + c]);
-          }
-#pragma unroll
-          for (int mask = 4; mask < 32; mask <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, mask));
-          if constexpr (!EDGE) mx *= f[nt][c];
-          const float mn = fmaxf(m[nt][c], mx);
-          const float ref = mn == -INFINITY ? 0.f : mn;
-          alpha[nt][c] = ex2_approx(m[nt][c] - ref);  // 0 while the column has seen nothing (all its sums are 0)
-          rose |= mn > m[nt][c];
-          m[nt][c] = mn;
-          const float sub = wexp - ref;
-#pragma unroll
-          for (int i = 0; i < N; ++i) {
-            if constexpr (EDGE) {
-              x[i][nt][c] = ex2_approx(x[i][nt][c] + sub);
-              x[i][nt][2 + c] = ex2_approx(x[i][nt][2 + c] + sub);
-            } else {
-              x[i][nt][c] = ex2_approx(fmaf(x[i][nt][c], f[nt][c], sub));
-              x[i][nt][2 + c] = ex2_approx(fmaf(x[i][nt][2 + c], f[nt][c], sub));
-            }
-          }
-        }
-      if (__any_sync(0xffffffffu, rose)) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            l[nt][c] *= alpha[nt][c];
-#pragma unroll
-            for (int gg = 0; gg < G; ++gg) z[gg][nt][c] *= alpha[nt][c];
-#pragma unroll
-            for (int i = 0; i < 4 * G; ++i) {
-              o[i][nt][c] *= alpha[nt][c];
-              o[i][nt][2 + c] *= alpha[nt][c];
-            }
-          }
-      }
       // V's pairs (those of keys past the sequence's end are no data).  All scales or-ed together lie above the largest
       // (by less than a factor of 2 unless the or-ed exponents make infinity or NaN, which count as 65504).
       uint32_t va[N][G], vb[N][G];
@@ -554,30 +527,68 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MINB)
           }
           all |= va[i][gg] | vb[i][gg];
         }
-      const float smax = half2_floats(all & 0x7fffu).x;
-      if (__any_sync(0xffffffffu, !(smax * ex2_approx(wexp) <= 32768.f))) {  // rare: smaller weights from here on
-        float sm = smax;
+      // column maxima (of x, or at an edge of the masked logits f x)
+      float mx[NT][2];
+      bool change = (all & 0x7fffu) > wlimit;
 #pragma unroll
-        for (int mask = 1; mask < 32; mask <<= 1) sm = fmaxf(sm, __shfl_xor_sync(0xffffffffu, sm, mask));
-        // 2^wexp times the largest scale (below 2^16) lies in [2^11, 2^13)
-        const float we = (float)(12 - ((int)(__float_as_uint(fminf(sm, 65504.f)) >> 23) - 127));
-        const float ratio = ex2_approx(we - wexp);
-        wexp = we;
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float v = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            if constexpr (EDGE) {
+              const int k = key0 + i * kTileKeys + kg;
+              x[i][nt][c] = k < vis[nt][c] ? x[i][nt][c] * f[nt][c] : -INFINITY;
+              x[i][nt][2 + c] = k + 8 < vis[nt][c] ? x[i][nt][2 + c] * f[nt][c] : -INFINITY;
+            }
+            v = max3f(v, x[i][nt][c], x[i][nt][2 + c]);
+          }
+#pragma unroll
+          for (int mask = 4; mask < 32; mask <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, mask));
+          mx[nt][c] = EDGE ? v : v * f[nt][c];
+          change |= mx[nt][c] > m[nt][c];
+        }
+      // A maximum rises, or the weights' factor has to fall (then its bound is met for a long time): rescale what is there.
+      if (__any_sync(0xffffffffu, change)) {
+        uint32_t top = all & 0x7fffu;
+#pragma unroll
+        for (int mask = 1; mask < 32; mask <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, mask));
+        float ratio = 1.f;
+        if (top > wlimit) {  // 2^wexp times the largest scale (below 2^16) is to lie in [2^11, 2^13)
+          const float we = (float)(12 - ((int)(__float_as_uint(fminf(half2_floats(top).x, 65504.f)) >> 23) - 127));
+          ratio = ex2_approx(we - wexp);
+          wexp = we;
+          set_wlimit();
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < 2; ++c) {
+            const float mn = fmaxf(m[nt][c], mx[nt][c]);
+            // (no key seen yet: all sums are 0)
+            const float a = (m[nt][c] == -INFINITY ? 0.f : ex2_approx(m[nt][c] - mn)) * ratio;
+            m[nt][c] = mn;
+            sub[nt][c] = wexp - (mn == -INFINITY ? 0.f : mn);
+            l[nt][c] *= a;
 #pragma unroll
-            for (int i = 0; i < N; ++i) x[i][nt][c] *= ratio;
+            for (int gg = 0; gg < G; ++gg) z[gg][nt][c] *= a;
 #pragma unroll
-            for (int i = 0; i < 4 * G; ++i) o[i][nt][c] *= ratio;
-            if (c < 2) {
-              l[nt][c] *= ratio;
-#pragma unroll
-              for (int gg = 0; gg < G; ++gg) z[gg][nt][c] *= ratio;
+            for (int i = 0; i < 4 * G; ++i) {
+              o[i][nt][c] *= a;
+              o[i][nt][2 + c] *= a;
             }
           }
       }
+      // the weights 2^(f x - max + wexp)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            x[i][nt][c] = EDGE ? ex2_approx(x[i][nt][c] + sub[nt][c & 1])
+                               : ex2_approx(fmaf(x[i][nt][c], f[nt][c & 1], sub[nt][c & 1]));
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const uint8_t* tb = tp + i * C::TILE + kv_q4_v_off(D);
@@ -635,25 +646,33 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MINB)
 
     bool alive = true;
     const int j0 = warp * C::KT;  // this warp's tiles of a stage
-    for (int done = 0;; done += C::ST) {
-      if (!mbar_wait(&full[slot], (t / C::NS) & 1, p.status, abort_flag)) {
+    const int last = si.tiles > 0 ? (si.tiles - 1) / C::ST : 0;  // the piece's last stage
+    // stages whose tiles of this warp are all there and seen by every column
+    const int whole = min(si.tiles, max(0, all_see) / kTileKeys - si.tile0) - j0 - C::KT;
+    const int interior = whole < 0 ? 0 : whole / C::ST + 1;
+    int stage = 0;
+    for (; stage < interior; ++stage) {
+      if (!mbar_wait(&full[slot], phase, p.status, abort_flag)) {
         alive = false;
         break;
       }
-      const int mine = min(si.tiles - done - j0, C::KT);
-      const int tile = si.tile0 + done + j0;
-      const uint8_t* tp = smem + slot * C::STAGE + j0 * C::TILE;
-      if (mine == C::KT && (tile + C::KT) * kTileKeys <= all_see) {
-        process(tp, tile, std::integral_constant<int, C::KT>{}, std::false_type{});
-      } else {
-        for (int i = 0; i < mine; ++i)
-          process(tp + i * C::TILE, tile + i, std::integral_constant<int, 1>{}, std::true_type{});
-      }
+      process(smem + slot * C::STAGE + j0 * C::TILE, 0, std::integral_constant<int, C::KT>{}, std::false_type{});
       __syncwarp();
-      if (done + C::ST >= si.tiles) break;  // the piece's last stage: its slot is released after the exchange below
-      release(slot, t);
-      ++t;
-      slot = t % C::NS;
+      if (stage == last) break;  // its slot is released after the exchange below
+      release();
+    }
+    for (; alive && stage <= last && !(stage == last && interior > last); ++stage) {
+      if (!mbar_wait(&full[slot], phase, p.status, abort_flag)) {
+        alive = false;
+        break;
+      }
+      const int first = stage * C::ST + j0;
+      const int mine = min(si.tiles - first, C::KT);
+      for (int i = 0; i < mine; ++i)
+        process(smem + slot * C::STAGE + (j0 + i) * C::TILE, si.tile0 + first + i, std::integral_constant<int, 1>{},
+                std::true_type{});
+      __syncwarp();
+      if (stage < last) release();
     }
     if (!alive) break;
 
@@ -682,7 +701,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MINB)
           for (int gg = 0; gg < G; ++gg) zz[gg][c] += __shfl_xor_sync(0xffffffffu, zz[gg][c], mask);
         }
 #pragma unroll
-      for (int w = 0; w < C::NW; ++w)
+      for (int w = 0; w < C::OWN; ++w)
 #pragma unroll
         for (int k = 0; k < C::OW; ++k) {
           const int i = w * C::OW + k;
@@ -703,6 +722,10 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MINB)
       }
     }
     named_bar_sync(1, nct);
+    if (C::NW > C::OWN && warp >= C::OWN) {
+      release();
+      continue;
+    }
     float M[NT][2], L[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -744,8 +767,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MINB)
       fence_proxy_async_smem();  // the exchange comes before the copy that refills the slot
       __syncwarp();
     }
-    release(slot, t);
-    ++t;
+    release();
     const size_t orow0 = ((size_t)si.b * p.Hkv + hkv) * rows + row0;
     // The row's output from the sums `own`, M and L: two neighbouring dims of two columns for each accumulator.
     auto write_out = [&]() {
@@ -783,9 +805,9 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MINB)
     uint4* const part_o = reinterpret_cast<uint4*>(p.part_o);
     uint4* const part_ml = reinterpret_cast<uint4*>(p.part_ml);
     auto o_at = [&](int sl, int nt, int k) {
-      return part_o + ((((size_t)sl * C::NW + warp) * NT + nt) * C::OW + k) * 32 + lane;
+      return part_o + ((((size_t)sl * C::OWN + warp) * NT + nt) * C::OW + k) * 32 + lane;
     };
-    auto ml_at = [&](int sl, int nt) { return part_ml + (((size_t)sl * C::NW + warp) * NT + nt) * 32 + lane; };
+    auto ml_at = [&](int sl, int nt) { return part_ml + (((size_t)sl * C::OWN + warp) * NT + nt) * 32 + lane; };
     auto inverted = [](float a, float b, float c, float d) {
       return make_uint4(~__float_as_uint(a), ~__float_as_uint(b), ~__float_as_uint(c), ~__float_as_uint(d));
     };
@@ -901,7 +923,7 @@ cudaError_t launch_wide(const DecodeQ4Launch& p) {
 
 int decode_q4_cols(int rows) { return rows <= 8 ? 8 : 16; }
 
-int decode_q4_grid(int num_sms, int rows) { return (rows <= 8 ? 3 : 2) * (num_sms > 0 ? num_sms : 152); }
+int decode_q4_grid(int num_sms, int rows) { return (rows <= 8 ? Q4Cfg<128, 1>::MINB : Q4Cfg<128, 2>::MINB) * (num_sms > 0 ? num_sms : 152); }
 
 cudaError_t launch_decode_q4(const DecodeQ4Launch& p) {
   const bool one = (p.Hq / p.Hkv) * p.Lq <= 8;

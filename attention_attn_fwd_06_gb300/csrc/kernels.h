@@ -194,7 +194,7 @@ struct DecodeQ4Launch {
   int fault_skip_arrive;   // test hook: CTA 0 withholds one slot release
   cudaStream_t stream;
 };
-constexpr int kDecodeQ4Warps = 4;
+constexpr int kDecodeQ4Owners = 4;  // warps of a CTA that hold its partial
 // Query rows one CTA serves, and the CTAs of the persistent launch, for `rows` = (Hq / Hkv) * Lq.
 int decode_q4_cols(int rows);
 int decode_q4_grid(int num_sms, int rows);
