@@ -47,35 +47,25 @@ constexpr float kLn2 = 0.6931471805599453f;
 #ifndef ATTN_Q4_ROW_COST
 #define ATTN_Q4_ROW_COST 16
 #endif
-#ifndef ATTN_Q4_NW
-#define ATTN_Q4_NW 4
-#endif
-#ifndef ATTN_Q4_KT
-#define ATTN_Q4_KT 2
-#endif
-#ifndef ATTN_Q4_KT2
-#define ATTN_Q4_KT2 2
-#endif
-#ifndef ATTN_Q4_TILES
-#define ATTN_Q4_TILES 32
-#endif
-#ifndef ATTN_Q4_TILES2
-#define ATTN_Q4_TILES2 32
+#ifndef ATTN_Q4_KT4
+#define ATTN_Q4_KT4 2
 #endif
 constexpr int kRowCostTiles = ATTN_Q4_ROW_COST;  // tiles charged to every row for its piece-end work
 
-// NT: groups of 8 query rows a CTA serves.
-template <int D, int NT>
+// R4: groups of 4 query rows a CTA serves (1, 2 or 4).
+template <int D, int R4>
 struct Q4Cfg {
   static constexpr int G = D / 64;                      // scale groups of a row
-  static constexpr int COLS = 8 * NT;                   // query rows per CTA
-  static constexpr int NW = NT == 1 ? ATTN_Q4_NW : 4;  // consumer warps
-  static constexpr int KT = NT == 1 ? ATTN_Q4_KT : ATTN_Q4_KT2;    // tiles of a stage per consumer warp
+  static constexpr int ROWS = 4 * R4;                   // query rows per CTA
+  static constexpr int NT = (R4 + 1) / 2;               // column tiles of the second product
+  static constexpr int NC = R4 == 1 ? 1 : 2;            // query rows a lane keeps of each
+  static constexpr int NW = 4;                          // consumer warps
+  static constexpr int KT = R4 == 4 ? ATTN_Q4_KT4 : 2;  // tiles of a stage per consumer warp
   static constexpr int ST = NW * KT;                    // tiles per stage
   static constexpr int TILE = kv_q4_tile_bytes(D);
   static constexpr int STAGE = ST * TILE;
-  static constexpr int MINB = NW > 4 || NT == 2 ? 2 : 3;  // resident CTAs per SM
-  static constexpr int NS = (NT == 1 ? ATTN_Q4_TILES : ATTN_Q4_TILES2) * (D == 128 ? 1 : 2) / ST;  // ring stages
+  static constexpr int MINB = NT == 1 ? 3 : 2;          // resident CTAs per SM
+  static constexpr int NS = 8 / KT * (D == 128 ? 1 : 2);  // ring stages
   static constexpr int THREADS = 32 * (NW + 1);
   static constexpr int LENS_CACHE = 128;                // kv_lens kept in shared memory for the walk
   static constexpr int OWN = kDecodeQ4Owners;           // warps that gather the accumulators at a piece's end,
@@ -85,8 +75,8 @@ struct Q4Cfg {
   static constexpr int OFF_SCR = NS * STAGE;
   static constexpr int OFF_BAR = OFF_SCR + (SCR_IN_STAGE ? 0 : SCR_BYTES);  // full[NS], empty[NS], told[NS]
   static constexpr int OFF_INFO = OFF_BAR + 3 * NS * 8;
-  static constexpr int OFF_ML = OFF_INFO + NS * 32;     // (m, l) [NW][COLS]
-  static constexpr int OFF_LENS = OFF_ML + NW * COLS * 8;
+  static constexpr int OFF_ML = OFF_INFO + NS * 32;     // (m, l) [NW][8 NT]
+  static constexpr int OFF_LENS = OFF_ML + NW * 8 * NT * 8;
   static constexpr int OFF_MISC = OFF_LENS + LENS_CACHE * 4;
   static constexpr int SMEM = OFF_MISC + 16;
   static_assert(OWN <= NW && 4 * G % OWN == 0, "every owner has as many accumulators");
@@ -134,11 +124,11 @@ __device__ __forceinline__ float2 half2_floats(uint32_t w) {
 constexpr uint32_t kLowNibble = 0x000f000fu, kHighNibble = 0x00f000f0u;
 
 // WIDE: the weights of the second product as two fp16 terms (fp32 output).
-template <int D, int NT, bool WIDE>
-__global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MINB)
+template <int D, int R4, bool WIDE>
+__global__ void __launch_bounds__(Q4Cfg<D, R4>::THREADS, Q4Cfg<D, R4>::MINB)
     decode_q4_kernel(const DecodeQ4Launch p, const int chunks, const int rows) {
-  using C = Q4Cfg<D, NT>;
-  constexpr int G = C::G;
+  using C = Q4Cfg<D, R4>;
+  constexpr int G = C::G, NT = C::NT, NC = C::NC;
   extern __shared__ __align__(128) uint8_t smem[];
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* empty = full + C::NS;
@@ -381,15 +371,16 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MINB)
     const Q4PieceInfo si = info[slot];
     if (si.b < 0) break;
     const int hkv = si.hg / chunks;
-    const int row0 = (si.hg - hkv * chunks) * C::COLS;  // first query row of the kv head this CTA serves
+    const int row0 = (si.hg - hkv * chunks) * C::ROWS;  // first query row of the kv head this CTA serves
     const int len = si.len;
-    // ---- q of the piece, as the first product's B operand ----
+    // ---- q of the piece, as the first product's B operand: column 2 t + c of column tile nt is query row
+    // 8 nt + 4 c + t (with up to 4 rows, row t twice), so that every lane's scores are of rows there are ----
     uint32_t qf[NT][4 * G][2];
-    float f[NT][2], qs[NT][G][2];  // of columns 2 t4 and 2 t4 + 1: score factor (>= 0), q's sums
-    int vis[NT][2];                // keys the column sees
+    float f[NT][NC], qs[NT][G][NC];  // of row 8 nt + 4 c + t4: score factor (>= 0), q's sums
+    int vis[NT][NC];                 // keys it sees
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int r = row0 + 8 * nt + g;
+      const int r = row0 + 8 * nt + (NC == 2 ? 4 * (g & 1) : 0) + (g >> 1);
       const __nv_bfloat16* qrow = reinterpret_cast<const __nv_bfloat16*>(p.q) +
                                   (((size_t)si.b * p.Hkv + hkv) * rows + min(r, rows - 1)) * D;
       float v[G][16];
@@ -433,21 +424,21 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MINB)
         }
       }
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
+      for (int c = 0; c < NC; ++c) {
         f[nt][c] = __shfl_sync(0xffffffffu, fc, 8 * t4 + 4 * c);
 #pragma unroll
         for (int gg = 0; gg < G; ++gg)
           qs[nt][gg][c] = __shfl_sync(0xffffffffu, sum[gg], 8 * t4 + 4 * c) * (1.f / 16384.f);
-        vis[nt][c] = len - p.Lq + 1 + (row0 + 8 * nt + 2 * t4 + c) % p.Lq;
+        vis[nt][c] = len - p.Lq + 1 + (row0 + 8 * nt + 4 * c + t4) % p.Lq;
       }
     }
-    float o[4 * G][NT][4];   // O^T: dims 64 gg + 8 g + 2 mt (+1), columns 2 t4 (+1)
-    float z[G][NT][2];       // this lane's share of sum p m_v
-    float m[NT][2], l[NT][2];
+    float o[4 * G][NT][4];   // O^T: dims 64 gg + 8 g + 2 mt (+1), rows 8 nt + t4 (+4)
+    float z[G][NT][NC];      // this lane's share of sum p m_v
+    float m[NT][NC], l[NT][NC];
     // Weights, their sums l and z, and O all carry the factor 2^wexp (2^30 until the first scales are seen).
     float wexp = 30.f;
     uint32_t wlimit;         // the largest scale, as fp16 bits, that wexp allows: 2^(15 - wexp) or less
-    float sub[NT][2];        // wexp - max of a column
+    float sub[NT][NC];       // wexp - max of a row
     auto set_wlimit = [&]() {
       const __half h = __float2half_rz(ex2_approx(15.f - wexp) * 0.9990234375f);
       wlimit = *reinterpret_cast<const uint16_t*>(&h);
@@ -458,7 +449,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MINB)
 #pragma unroll
       for (int i = 0; i < 4 * G; ++i) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
+      for (int c = 0; c < NC; ++c) {
         m[nt][c] = -INFINITY;
         sub[nt][c] = wexp;
         l[nt][c] = 0.f;
@@ -502,7 +493,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MINB)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
+            for (int c = 0; c < NC; ++c) {
               const float q = qs[nt][gg][c];
               x[i][nt][c] = fmaf(pa.x, acc[nt][c], gg ? fmaf(pa.y, q, x[i][nt][c]) : pa.y * q);
               x[i][nt][2 + c] = fmaf(pb.x, acc[nt][2 + c], gg ? fmaf(pb.y, q, x[i][nt][2 + c]) : pb.y * q);
@@ -527,13 +518,13 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MINB)
           }
           all |= va[i][gg] | vb[i][gg];
         }
-      // column maxima (of x, or at an edge of the masked logits f x)
-      float mx[NT][2];
+      // row maxima (of x, or at an edge of the masked logits f x)
+      float mx[NT][NC];
       bool change = (all & 0x7fffu) > wlimit;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        for (int c = 0; c < NC; ++c) {
           float v = -INFINITY;
 #pragma unroll
           for (int i = 0; i < N; ++i) {
@@ -564,7 +555,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MINB)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
+          for (int c = 0; c < NC; ++c) {
             const float mn = fmaxf(m[nt][c], mx[nt][c]);
             // (no key seen yet: all sums are 0)
             const float a = (m[nt][c] == -INFINITY ? 0.f : ex2_approx(m[nt][c] - mn)) * ratio;
@@ -577,6 +568,10 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MINB)
             for (int i = 0; i < 4 * G; ++i) {
               o[i][nt][c] *= a;
               o[i][nt][2 + c] *= a;
+              if (NC == 1 && WIDE) {  // the second column holds the weights' second term
+                o[i][nt][1] *= a;
+                o[i][nt][3] *= a;
+              }
             }
           }
       }
@@ -586,16 +581,17 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MINB)
 #pragma unroll
         for (int i = 0; i < N; ++i)
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            x[i][nt][c] = EDGE ? ex2_approx(x[i][nt][c] + sub[nt][c & 1])
-                               : ex2_approx(fmaf(x[i][nt][c], f[nt][c & 1], sub[nt][c & 1]));
+          for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int k = c; k < 4; k += 2)
+              x[i][nt][k] = EDGE ? ex2_approx(x[i][nt][k] + sub[nt][c]) : ex2_approx(fmaf(x[i][nt][k], f[nt][c], sub[nt][c]));
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const uint8_t* tb = tp + i * C::TILE + kv_q4_v_off(D);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int c = 0; c < 2; ++c) l[nt][c] += x[i][nt][c] + x[i][nt][2 + c];
+          for (int c = 0; c < NC; ++c) l[nt][c] += x[i][nt][c] + x[i][nt][2 + c];
 #pragma unroll
         for (int gg = 0; gg < G; ++gg) {
           uint32_t b0[NT], b1[NT];
@@ -604,14 +600,21 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MINB)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
+            for (int c = 0; c < NC; ++c)
               z[gg][nt][c] = fmaf(x[i][nt][c], sa.y, fmaf(x[i][nt][2 + c], sb.y, z[gg][nt][c]));
-            const float w0 = x[i][nt][0] * sa.x, w1 = x[i][nt][1] * sa.x, w2 = x[i][nt][2] * sb.x,
-                        w3 = x[i][nt][3] * sb.x;
+            const float w0 = x[i][nt][0] * sa.x, w2 = x[i][nt][2] * sb.x;
+            float w1 = 0.f, w3 = 0.f;
+            if constexpr (NC == 2) {
+              w1 = x[i][nt][1] * sa.x;
+              w3 = x[i][nt][3] * sb.x;
+            } else if constexpr (WIDE) {
+              w1 = w0 - half2_floats(half2_bits(w0, 0.f)).x;
+              w3 = w2 - half2_floats(half2_bits(w2, 0.f)).x;
+            }
             const uint32_t h0 = half2_bits(w0, w1), h1 = half2_bits(w2, w3);
             b0[nt] = transpose8(h0);
             b1[nt] = transpose8(h1);
-            if constexpr (WIDE) {
+            if constexpr (WIDE && NC == 2) {
               const float2 r0 = half2_floats(h0), r1 = half2_floats(h1);
               c0[nt] = transpose8(half2_bits(w0 - r0.x, w1 - r0.y));
               c1[nt] = transpose8(half2_bits(w2 - r1.x, w3 - r1.y));
@@ -635,7 +638,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MINB)
             for (int nt = 0; nt < NT; ++nt) {
               mma_16816(o[4 * gg + mt][nt], a & kLowNibble, a & kHighNibble, b & kLowNibble, b & kHighNibble, b0[nt],
                         b1[nt]);
-              if constexpr (WIDE)
+              if constexpr (WIDE && NC == 2)
                 mma_16816(o[4 * gg + mt][nt], a & kLowNibble, a & kHighNibble, b & kLowNibble, b & kHighNibble, c0[nt],
                           c1[nt]);
             }
@@ -685,9 +688,9 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MINB)
     named_bar_sync(1, nct);  // every warp is done with the stage and with the last piece's exchange
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float zz[G][2], ll[2];
+      float zz[G][2] = {}, ll[2] = {0.f, 0.f};
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
+      for (int c = 0; c < NC; ++c) {
         ll[c] = l[nt][c] * back;
 #pragma unroll
         for (int gg = 0; gg < G; ++gg) zz[gg][c] = z[gg][nt][c] * back;
@@ -695,7 +698,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MINB)
 #pragma unroll
       for (int mask = 4; mask < 32; mask <<= 1)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        for (int c = 0; c < NC; ++c) {
           ll[c] += __shfl_xor_sync(0xffffffffu, ll[c], mask);
 #pragma unroll
           for (int gg = 0; gg < G; ++gg) zz[gg][c] += __shfl_xor_sync(0xffffffffu, zz[gg][c], mask);
@@ -706,6 +709,13 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MINB)
         for (int k = 0; k < C::OW; ++k) {
           const int i = w * C::OW + k;
           float(&oo)[4] = o[i][nt];
+          if constexpr (NC == 1) {
+            if constexpr (WIDE) {
+              oo[0] += oo[1];
+              oo[2] += oo[3];
+            }
+            oo[1] = oo[3] = 0.f;
+          }
 #pragma unroll
           for (int c = 0; c < 4; ++c) oo[c] = fmaf(oo[c], back * (c < 2 ? 16777216.f : 1048576.f), zz[i / 4][c & 1]);
           if (w == warp) {
@@ -718,7 +728,8 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MINB)
         }
       if (g == 0) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) mlbuf[warp * C::COLS + 8 * nt + 2 * t4 + c] = make_float2(m[nt][c], ll[c]);
+        for (int c = 0; c < 2; ++c)
+          mlbuf[(warp * NT + nt) * 8 + 2 * t4 + c] = make_float2(c < NC ? m[nt][c < NC ? c : 0] : -INFINITY, ll[c]);
       }
     }
     named_bar_sync(1, nct);
@@ -737,7 +748,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MINB)
         L[nt][c] = 0.f;
 #pragma unroll
         for (int w = 0; w < C::NW; ++w) {
-          ml[w] = mlbuf[w * C::COLS + 8 * nt + 2 * t4 + c];
+          ml[w] = mlbuf[(w * NT + nt) * 8 + 2 * t4 + c];
           M[nt][c] = fmaxf(M[nt][c], ml[w].x);
         }
 #pragma unroll
@@ -769,17 +780,17 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MINB)
     }
     release();
     const size_t orow0 = ((size_t)si.b * p.Hkv + hkv) * rows + row0;
-    // The row's output from the sums `own`, M and L: two neighbouring dims of two columns for each accumulator.
+    // The row's output from the sums `own`, M and L: two neighbouring dims of two rows for each accumulator.
     auto write_out = [&]() {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int col = 8 * nt + 2 * t4 + c;
-          if (row0 + col >= rows) continue;
-          const bool none = M[nt][c] == -INFINITY;  // a column that sees no key: O = 0, lse = -inf
+        for (int c = 0; c < NC; ++c) {
+          const int row = 8 * nt + 4 * c + t4;
+          if (row0 + row >= rows) continue;
+          const bool none = M[nt][c] == -INFINITY;  // a row that sees no key: O = 0, lse = -inf
           const float inv = none ? 0.f : 1.f / L[nt][c];
-          const size_t at = (orow0 + col) * D;
+          const size_t at = (orow0 + row) * D;
 #pragma unroll
           for (int k = 0; k < C::OW; ++k) {
             const int i = warp * C::OW + k;
@@ -791,7 +802,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MINB)
               *reinterpret_cast<uint32_t*>(reinterpret_cast<__nv_bfloat16*>(p.out) + at + d) = pack2_bf16(a, b);
           }
           if (warp == 0 && g == 0 && p.lse != nullptr)
-            p.lse[orow0 + col] = none ? -INFINITY : (M[nt][c] + log2f(L[nt][c])) * kLn2;
+            p.lse[orow0 + row] = none ? -INFINITY : (M[nt][c] + log2f(L[nt][c])) * kLn2;
         }
     };
     if (si.np <= 1) {
@@ -814,7 +825,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MINB)
     if (!si.first) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        if (row0 + 8 * nt + 2 * t4 >= rows) continue;
+        if (row0 + 8 * nt + t4 >= rows) continue;
         st_relaxed_gpu(ml_at(cta, nt), inverted(M[nt][0], L[nt][0], M[nt][1], L[nt][1]));
 #pragma unroll
         for (int k = 0; k < C::OW; ++k)
@@ -828,7 +839,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MINB)
       constexpr int N = decltype(n_c)::value;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const bool have = row0 + 8 * nt + 2 * t4 < rows;
+        const bool have = row0 + 8 * nt + t4 < rows;
         uint4 ml[N], ov[N][C::OW];
         uint64_t since = 0;
         while (true) {
@@ -895,40 +906,42 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MINB)
   }
 }
 
-template <int D, int NT, bool WIDE>
+template <int D, int R4, bool WIDE>
 cudaError_t launch_one(const DecodeQ4Launch& p) {
-  using C = Q4Cfg<D, NT>;
+  using C = Q4Cfg<D, R4>;
   static bool attr_set[64] = {};  // the shared-memory opt-in is per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!attr_set[dev]) {
-    e = cudaFuncSetAttribute(decode_q4_kernel<D, NT, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    e = cudaFuncSetAttribute(decode_q4_kernel<D, R4, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
   }
   const int rows = (p.Hq / p.Hkv) * p.Lq;
-  decode_q4_kernel<D, NT, WIDE><<<C::MINB * p.num_sms, C::THREADS, C::SMEM, p.stream>>>(
-      p, (rows + C::COLS - 1) / C::COLS, rows);
+  decode_q4_kernel<D, R4, WIDE><<<C::MINB * p.num_sms, C::THREADS, C::SMEM, p.stream>>>(
+      p, (rows + C::ROWS - 1) / C::ROWS, rows);
   return cudaGetLastError();
 }
 
-template <int D, int NT>
-cudaError_t launch_wide(const DecodeQ4Launch& p) {
-  return p.out_f32 ? launch_one<D, NT, true>(p) : launch_one<D, NT, false>(p);
+template <int D, bool WIDE>
+cudaError_t launch_rows(const DecodeQ4Launch& p) {
+  const int rows = (p.Hq / p.Hkv) * p.Lq;
+  return rows <= 4 ? launch_one<D, 1, WIDE>(p) : rows <= 8 ? launch_one<D, 2, WIDE>(p) : launch_one<D, 4, WIDE>(p);
 }
 
 }  // namespace
 
 int decode_q4_cols(int rows) { return rows <= 8 ? 8 : 16; }
 
-int decode_q4_grid(int num_sms, int rows) { return (rows <= 8 ? Q4Cfg<128, 1>::MINB : Q4Cfg<128, 2>::MINB) * (num_sms > 0 ? num_sms : 152); }
+int decode_q4_grid(int num_sms, int rows) {
+  return (rows <= 8 ? Q4Cfg<128, 2>::MINB : Q4Cfg<128, 4>::MINB) * (num_sms > 0 ? num_sms : 152);
+}
 
 cudaError_t launch_decode_q4(const DecodeQ4Launch& p) {
-  const bool one = (p.Hq / p.Hkv) * p.Lq <= 8;
-  if (p.D == 64) return one ? launch_wide<64, 1>(p) : launch_wide<64, 2>(p);
-  return one ? launch_wide<128, 1>(p) : launch_wide<128, 2>(p);
+  if (p.D == 64) return p.out_f32 ? launch_rows<64, true>(p) : launch_rows<64, false>(p);
+  return p.out_f32 ? launch_rows<128, true>(p) : launch_rows<128, false>(p);
 }
 
 }  // namespace attn
