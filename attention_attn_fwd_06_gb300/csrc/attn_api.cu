@@ -252,20 +252,16 @@ bool strides8(const long long* s, int n) {
 bool aligned128(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 127u) == 0; }
 
 struct DecodeQ4Shape {
-  int rows = 0;              // query rows of a kv head
-  int cols = 0;              // of them per CTA
   size_t part_o_elems = 0;
   size_t bytes = 0;
 };
 
-// One partial per CTA: cols x D sums, and for each of the CTA's warps its lanes' (max, sum) of two columns of eight.
-DecodeQ4Shape decode_q4_shape(int Hq, int Hkv, int Lq, int D, int num_sms) {
+// The partials of any variant: sums, and for each of a CTA's warps that hold one every column's (max, sum).
+DecodeQ4Shape decode_q4_shape(int D, int num_sms) {
   DecodeQ4Shape s;
-  s.rows = (Hq / Hkv) * Lq;
-  s.cols = attn::decode_q4_cols(s.rows);
-  const size_t prows = (size_t)attn::decode_q4_grid(num_sms, s.rows) * s.cols;
-  s.part_o_elems = prows * D;
-  s.bytes = prows * (D + attn::kDecodeQ4Owners * 16) * sizeof(float);
+  const size_t cols = attn::decode_q4_partials(num_sms);
+  s.part_o_elems = cols * D;
+  s.bytes = cols * (D + attn::kDecodeQ4Owners * 2) * sizeof(float);
   return s;
 }
 
@@ -863,7 +859,7 @@ unsigned long long attn_decode_q4_workspace_bytes(int Hq, int Hkv, int Lq, int D
   if (validate_decode_q4_heads(Hq, Hkv, Lq, D) != ATTN_OK) return 0;
   DeviceState* s = nullptr;
   const int sms = device_state(&s) == ATTN_OK ? s->num_sms : 0;
-  return decode_q4_shape(Hq, Hkv, Lq, D, sms).bytes;
+  return decode_q4_shape(D, sms).bytes;
 }
 
 int attn_decode_q4(const attn_decode_q4_params* p) {
@@ -890,7 +886,7 @@ int attn_decode_q4(const attn_decode_q4_params* p) {
   DeviceState* s = nullptr;
   st = device_state_locked(&s);
   if (st != ATTN_OK) return st;
-  const DecodeQ4Shape sh = decode_q4_shape(p->Hq, p->Hkv, p->Lq, p->D, s->num_sms);
+  const DecodeQ4Shape sh = decode_q4_shape(p->D, s->num_sms);
   char* ws = static_cast<char*>(p->workspace);
   if (ws == nullptr) {
     st = ensure_buffer_locked(s->ws_q4, s->ws_q4_bytes, sh.bytes, sh.bytes, stream);
@@ -916,7 +912,7 @@ int attn_decode_q4(const attn_decode_q4_params* p) {
   L.page_size = p->page_size;
   L.max_pages = p->max_pages;
   L.num_pages = p->num_pages;
-  L.min_tiles = p->chunk > 0 ? (p->chunk + attn::kTileKeys - 1) / attn::kTileKeys : 4;
+  L.min_tiles = p->chunk > 0 ? (p->chunk + attn::kTileKeys - 1) / attn::kTileKeys : 0;
   L.scale = p->scale;
   L.out_f32 = p->out_dtype == ATTN_DTYPE_F32;
   L.num_sms = s->num_sms;

@@ -28,6 +28,7 @@
 // holds its first piece, which reads the others' partials as they arrive.  CTAs start in order, and what a CTA waits
 // for no other CTA's wait holds up (it is the first thing that CTA does), so the wait ends with any number of CTAs resident.
 #include <cfloat>
+#include <algorithm>
 #include <cmath>
 #include <cuda_fp16.h>
 #include <type_traits>
@@ -44,13 +45,13 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-#ifndef ATTN_Q4_ROW_COST
-#define ATTN_Q4_ROW_COST 16
-#endif
-#ifndef ATTN_Q4_KT4
-#define ATTN_Q4_KT4 2
-#endif
-constexpr int kRowCostTiles = ATTN_Q4_ROW_COST;  // tiles charged to every row for its piece-end work
+// Tiles charged to every row for its piece-end work (8 x 4096 GQA / 64 short rows of D = 64: 8 tiles 15.4 / 22.9 us, 16
+// 14.4 / 21.1, 32 14.5 / 22.0, with the merge of that day).
+constexpr int kRowCostTiles = 16;
+// From this many tiles a CTA at the caches' capacity on, 16 query rows a CTA (two CTAs an SM, each tile unpacked once for
+// all 16) beat 8 (three): 32 rows over 131k keys 213 against 252 us; below, 8 rows win by their cheaper piece ends: 32
+// rows over 8 x 4096 keys 29.4 against 31.1 us, 16 rows 18.7 against 24.3 us.
+constexpr long long kWideTiles = 256;
 
 // R4: groups of 4 query rows a CTA serves (1, 2 or 4).
 template <int D, int R4>
@@ -60,12 +61,12 @@ struct Q4Cfg {
   static constexpr int NT = (R4 + 1) / 2;               // column tiles of the second product
   static constexpr int NC = R4 == 1 ? 1 : 2;            // query rows a lane keeps of each
   static constexpr int NW = 4;                          // consumer warps
-  static constexpr int KT = R4 == 4 ? ATTN_Q4_KT4 : 2;  // tiles of a stage per consumer warp
+  static constexpr int KT = 2;                          // tiles of a stage per consumer warp
   static constexpr int ST = NW * KT;                    // tiles per stage
   static constexpr int TILE = kv_q4_tile_bytes(D);
   static constexpr int STAGE = ST * TILE;
   static constexpr int MINB = NT == 1 ? 3 : 2;          // resident CTAs per SM
-  static constexpr int NS = 8 / KT * (D == 128 ? 1 : 2);  // ring stages
+  static constexpr int NS = D == 128 ? 4 : 8;           // ring stages
   static constexpr int THREADS = 32 * (NW + 1);
   static constexpr int LENS_CACHE = 128;                // kv_lens kept in shared memory for the walk
   static constexpr int OWN = kDecodeQ4Owners;           // warps that gather the accumulators at a piece's end,
@@ -177,8 +178,13 @@ __global__ void __launch_bounds__(Q4Cfg<D, R4>::THREADS, Q4Cfg<D, R4>::MINB)
     auto seq_len = [&](int b) -> int { return b < C::LENS_CACHE ? lens_s[b] : clamp_len(p.kv_lens[b], Lmax); };
     auto seq_tiles = [&](int b) -> int { return (seq_len(b) + kTileKeys - 1) / kTileKeys; };
     const long long W = tsum * Hg;
-    // Slices of at least min_tiles tiles, but never fewer slices than rows with keys.
-    long long geff = floor_div(W + p.min_tiles - 1, p.min_tiles);
+    // Slices of at least min_tiles tiles, but never fewer slices than rows with keys.  By default a slice's time is not
+    // to fall far below the merge of the partials it makes: with T tiles a row in slices of s, both (T / s and s) are
+    // alike at s ~ sqrt(T); 2 sqrt(T) measured best over one sequence of 4096 keys (11.8 us against 16.5 us with slices of
+    // 4 tiles, sqrt(2 T) 11.2 us) and eight (14.1 against 14.4 us, 14.1 us).
+    int min_tiles = p.min_tiles;
+    if (min_tiles == 0) min_tiles = max(4, (int)(2.f * sqrtf(to_f32(W) / (float)max(1, nonempty * Hg))));
+    long long geff = floor_div(W + min_tiles - 1, min_tiles);
     if (geff < (long long)nonempty * Hg) geff = (long long)nonempty * Hg;
     if (geff > (long long)gridDim.x) geff = gridDim.x;
     if (geff < 1) geff = 1;
@@ -813,23 +819,27 @@ __global__ void __launch_bounds__(Q4Cfg<D, R4>::THREADS, Q4Cfg<D, R4>::MINB)
     // share; every other piece starts its CTA's slice, so a CTA publishes at most one partial.  A partial's words are
     // stored complemented over zeros, and no sum has the bits ~0 (a NaN that arithmetic does not make), so a word that is
     // not zero has arrived: no fence, no count, no second round trip.  The merging warp zeroes what it has read.
+    // Words of four: an accumulator's two dims of two rows; with one row a lane two accumulators, and the row's (m, l).
+    constexpr int OV = NC == 1 ? (C::OW + 1) / 2 : C::OW;
     uint4* const part_o = reinterpret_cast<uint4*>(p.part_o);
     uint4* const part_ml = reinterpret_cast<uint4*>(p.part_ml);
-    auto o_at = [&](int sl, int nt, int k) {
-      return part_o + ((((size_t)sl * C::OWN + warp) * NT + nt) * C::OW + k) * 32 + lane;
-    };
-    auto ml_at = [&](int sl, int nt) { return part_ml + (((size_t)sl * C::OWN + warp) * NT + nt) * 32 + lane; };
-    auto inverted = [](float a, float b, float c, float d) {
-      return make_uint4(~__float_as_uint(a), ~__float_as_uint(b), ~__float_as_uint(c), ~__float_as_uint(d));
+    auto o_at = [&](int sl, int nt, int k) { return part_o + ((((size_t)sl * C::OWN + warp) * NT + nt) * OV + k) * 32 + lane; };
+    auto ml_at = [&](int sl, int nt) { return part_ml + (((size_t)sl * C::OWN + warp) * NT + nt) * 4 + t4; };
+    // value v of word k of column tile nt
+    auto value = [&](int nt, int k, int v) -> float& {
+      return NC == 1 ? own[nt][min(2 * k + v / 2, C::OW - 1)][2 * (v & 1)] : own[nt][k][v];
     };
     if (!si.first) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         if (row0 + 8 * nt + t4 >= rows) continue;
-        st_relaxed_gpu(ml_at(cta, nt), inverted(M[nt][0], L[nt][0], M[nt][1], L[nt][1]));
 #pragma unroll
-        for (int k = 0; k < C::OW; ++k)
-          st_relaxed_gpu(o_at(cta, nt, k), inverted(own[nt][k][0], own[nt][k][1], own[nt][k][2], own[nt][k][3]));
+        for (int k = 0; k < OV; ++k)
+          st_relaxed_gpu(o_at(cta, nt, k), make_uint4(~__float_as_uint(value(nt, k, 0)), ~__float_as_uint(value(nt, k, 1)),
+                                                      ~__float_as_uint(value(nt, k, 2)), ~__float_as_uint(value(nt, k, 3))));
+        if (g == 0)
+          st_relaxed_gpu(ml_at(cta, nt), make_uint4(~__float_as_uint(M[nt][0]), ~__float_as_uint(L[nt][0]),
+                                                    ~__float_as_uint(M[nt][1]), ~__float_as_uint(L[nt][1])));
       }
       continue;
     }
@@ -840,7 +850,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, R4>::THREADS, Q4Cfg<D, R4>::MINB)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const bool have = row0 + 8 * nt + t4 < rows;
-        uint4 ml[N], ov[N][C::OW];
+        uint4 ml[N], ov[N][OV];
         uint64_t since = 0;
         while (true) {
           uint32_t least = 1;
@@ -849,7 +859,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, R4>::THREADS, Q4Cfg<D, R4>::MINB)
             ml[u] = make_uint4(1, 1, 1, 1);
             if (have) ml[u] = ld_relaxed_gpu(ml_at(cta + i + u, nt));
 #pragma unroll
-            for (int k = 0; k < C::OW; ++k) {
+            for (int k = 0; k < OV; ++k) {
               ov[u][k] = make_uint4(1, 1, 1, 1);
               if (have) ov[u][k] = ld_relaxed_gpu(o_at(cta + i + u, nt, k));
             }
@@ -858,7 +868,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, R4>::THREADS, Q4Cfg<D, R4>::MINB)
           for (int u = 0; u < N; ++u) {
             least = min(least, min(min(ml[u].x, ml[u].y), min(ml[u].z, ml[u].w)));
 #pragma unroll
-            for (int k = 0; k < C::OW; ++k)
+            for (int k = 0; k < OV; ++k)
               least = min(least, min(min(ov[u][k].x, ov[u][k].y), min(ov[u][k].z, ov[u][k].w)));
           }
           if (__all_sync(0xffffffffu, least != 0)) break;
@@ -873,9 +883,9 @@ __global__ void __launch_bounds__(Q4Cfg<D, R4>::THREADS, Q4Cfg<D, R4>::MINB)
         for (int u = 0; u < N; ++u) {
           const float mc[2] = {__uint_as_float(~ml[u].x), __uint_as_float(~ml[u].z)};
           const float lc[2] = {__uint_as_float(~ml[u].y), __uint_as_float(~ml[u].w)};
-          float sc[2], w[2];
+          float sc[2] = {0.f, 0.f}, w[2] = {0.f, 0.f};
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
+          for (int c = 0; c < NC; ++c) {
             const float mn = fmaxf(M[nt][c], mc[c]);
             sc[c] = M[nt][c] == -INFINITY ? 0.f : ex2_approx(M[nt][c] - mn);
             w[c] = mc[c] == -INFINITY ? 0.f : ex2_approx(mc[c] - mn);
@@ -883,24 +893,28 @@ __global__ void __launch_bounds__(Q4Cfg<D, R4>::THREADS, Q4Cfg<D, R4>::MINB)
             L[nt][c] = fmaf(w[c], lc[c], L[nt][c] * sc[c]);
           }
 #pragma unroll
-          for (int k = 0; k < C::OW; ++k) {
+          for (int k = 0; k < OV; ++k) {
             const uint32_t v[4] = {ov[u][k].x, ov[u][k].y, ov[u][k].z, ov[u][k].w};
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-              own[nt][k][c] = fmaf(w[c & 1], __uint_as_float(~v[c]), own[nt][k][c] * sc[c & 1]);
+            for (int j = 0; j < 4; ++j) {
+              if (NC == 1 && 2 * k + j / 2 >= C::OW) continue;
+              const int c = NC == 1 ? 0 : j & 1;
+              value(nt, k, j) = fmaf(w[c], __uint_as_float(~v[j]), value(nt, k, j) * sc[c]);
+            }
           }
           if (have) {
-            st_relaxed_gpu(ml_at(cta + i + u, nt), make_uint4(0, 0, 0, 0));
+            if (g == 0) st_relaxed_gpu(ml_at(cta + i + u, nt), make_uint4(0, 0, 0, 0));
 #pragma unroll
-            for (int k = 0; k < C::OW; ++k) st_relaxed_gpu(o_at(cta + i + u, nt, k), make_uint4(0, 0, 0, 0));
+            for (int k = 0; k < OV; ++k) st_relaxed_gpu(o_at(cta + i + u, nt, k), make_uint4(0, 0, 0, 0));
           }
         }
       }
       return true;
     };
+    constexpr int N = 4;
     int i = 1;
     bool got = true;
-    for (; got && i + 3 < si.np; i += 4) got = fold(i, std::integral_constant<int, 4>{});
+    for (; got && i + N - 1 < si.np; i += N) got = fold(i, std::integral_constant<int, N>{});
     for (; got && i < si.np; ++i) got = fold(i, std::integral_constant<int, 1>{});
     if (got) write_out();
   }
@@ -925,18 +939,28 @@ cudaError_t launch_one(const DecodeQ4Launch& p) {
   return cudaGetLastError();
 }
 
+// Query rows a CTA serves: 4, 8, or 16 (kWideTiles).
+int rows_per_cta(const DecodeQ4Launch& p) {
+  const int rows = (p.Hq / p.Hkv) * p.Lq;
+  if (rows <= 8) return rows <= 4 ? 4 : 8;
+  const long long tiles = (long long)p.max_pages * (p.page_size / kTileKeys) * p.B * p.Hkv * ((rows + 15) / 16);
+  return tiles >= kWideTiles * Q4Cfg<128, 4>::MINB * p.num_sms ? 16 : 8;
+}
+
 template <int D, bool WIDE>
 cudaError_t launch_rows(const DecodeQ4Launch& p) {
-  const int rows = (p.Hq / p.Hkv) * p.Lq;
-  return rows <= 4 ? launch_one<D, 1, WIDE>(p) : rows <= 8 ? launch_one<D, 2, WIDE>(p) : launch_one<D, 4, WIDE>(p);
+  switch (rows_per_cta(p)) {
+    case 4: return launch_one<D, 1, WIDE>(p);
+    case 8: return launch_one<D, 2, WIDE>(p);
+    default: return launch_one<D, 4, WIDE>(p);
+  }
 }
 
 }  // namespace
 
-int decode_q4_cols(int rows) { return rows <= 8 ? 8 : 16; }
-
-int decode_q4_grid(int num_sms, int rows) {
-  return (rows <= 8 ? Q4Cfg<128, 2>::MINB : Q4Cfg<128, 4>::MINB) * (num_sms > 0 ? num_sms : 152);
+size_t decode_q4_partials(int num_sms) {
+  const int sms = num_sms > 0 ? num_sms : 152;
+  return (size_t)sms * std::max(8 * Q4Cfg<128, 2>::MINB, 16 * Q4Cfg<128, 4>::MINB);
 }
 
 cudaError_t launch_decode_q4(const DecodeQ4Launch& p) {

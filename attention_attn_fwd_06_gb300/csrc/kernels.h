@@ -184,9 +184,9 @@ struct DecodeQ4Launch {
   void* out;               // [B, Hq, Lq, D], bf16 or fp32
   float* lse;              // [B, Hq, Lq] or null
   float* part_o;           // fp32 [grid][cols * D], in the order of the warps' accumulators; zero between calls
-  float* part_ml;          // fp32 [grid][4 warps][cols / 8][32 lanes][4]; zero between calls
+  float* part_ml;          // fp32 [grid][4 warps][cols][2]; zero between calls
   int B, Hq, Hkv, Lq, D, page_size, max_pages, num_pages;
-  int min_tiles;           // smallest slice of the tiles one CTA takes (>= 1)
+  int min_tiles;           // smallest slice of the tiles one CTA takes (0: chosen from the lengths)
   float scale;
   int out_f32;
   int num_sms;
@@ -195,9 +195,8 @@ struct DecodeQ4Launch {
   cudaStream_t stream;
 };
 constexpr int kDecodeQ4Owners = 4;  // warps of a CTA that hold its partial
-// Query rows one CTA serves, and the CTAs of the persistent launch, for `rows` = (Hq / Hkv) * Lq.
-int decode_q4_cols(int rows);
-int decode_q4_grid(int num_sms, int rows);
+// Columns (of D sums, and a maximum and a sum for every owner) that all CTAs' partials take in any variant.
+size_t decode_q4_partials(int num_sms);
 cudaError_t launch_decode_q4(const DecodeQ4Launch& p);
 
 // One thread waits on a barrier nothing arrives on, with the kernels' bounded wait and a limit of limit_ns.

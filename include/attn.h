@@ -538,7 +538,7 @@ typedef struct attn_decode_q4_params {
 int attn_decode_q4(const attn_decode_q4_params* p);
 
 /* attn_decode_q4_workspace_bytes -- bytes a workspace of attn_decode_q4 needs on the current device (0 on invalid
- * sizes; 152 SMs assumed when no device is visible).  It depends on (Hq / Hkv) * Lq and D only. */
+ * sizes; 152 SMs assumed when no device is visible).  It depends on D and the device only. */
 unsigned long long attn_decode_q4_workspace_bytes(int Hq, int Hkv, int Lq, int D);
 
 /*
