@@ -509,8 +509,10 @@ def attn_decode_noalloc(q, kcache, vcache, kv_lens, out, lse=None, scale=None, c
     return out, lse
 
 
-# The raw handle of a device's current stream without building a Stream object (2 us of a small call on the host).
+# The raw handle of a device's current stream without building a Stream object (2 us of a small call on the host), and
+# the current device without asking whether CUDA is set up (the arguments are CUDA tensors).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream_of(stream, index):
@@ -521,7 +523,7 @@ def _stream_of(stream, index):
 
 def _call(fn, p, index, where):
     """Run one entry point with device `index` current."""
-    if index == torch.cuda.current_device():
+    if index == _current_device():
         status = fn(ctypes.byref(p))
     else:
         with torch.cuda.device(index):
@@ -533,11 +535,13 @@ def _call(fn, p, index, where):
 def _fit(t, name, dtype, shape, index):
     """The address of a contiguous tensor of just this type and shape on device `index` (_need, told shortly: a decode
     step's calls take microseconds, and so may their checks)."""
-    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and t.get_device() == index >= 0
-            and t.is_contiguous()):
-        _need(t, name, dtype, len(shape), shape, torch.device("cuda", max(index, 0)))
-        raise ValueError(f"{name}: not a contiguous CUDA tensor of shape {tuple(shape)}")
-    return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == index >= 0 and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:  # not a tensor: told below
+        pass
+    _need(t, name, dtype, len(shape), shape, torch.device("cuda", max(index, 0)))
+    raise ValueError(f"{name}: not a contiguous CUDA tensor of shape {tuple(shape)}")
 
 
 def _rows(t, name, ndim, index=None):
