@@ -34,4 +34,25 @@ __host__ __device__ inline float to_f32(long long x) {
   return (float)(unsigned)(u >> 32) * 4294967296.0f + (float)(unsigned)(u & 0xffffffffu);
 }
 
+// Division of n in [0, 2^31) by a fixed d in [1, 2^31) as a product's high half and a shift.  With s = ceil(log2 d) and
+// mul = ceil(2^(31 + s) / d) the product n mul exceeds n 2^(31 + s) / d by n e / d with e = mul d - 2^(31 + s) < d <= 2^s,
+// less than 2^(31 + s) / d together with any remainder (Granlund and Montgomery, 1994), so the quotient is exact.
+struct FastDiv {
+  unsigned d, mul, shift;
+  __host__ __device__ unsigned div(unsigned n) const {
+    if (d == 1) return n;
+    return (unsigned)(((unsigned long long)n * mul) >> 32) >> shift;
+  }
+};
+
+inline FastDiv make_fast_div(unsigned d) {
+  unsigned s = 0;
+  while ((1ull << s) < d) ++s;
+  FastDiv f;
+  f.d = d;
+  f.shift = s > 0 ? s - 1 : 0;
+  f.mul = d == 1 ? 0u : (unsigned)(((1ull << (31 + s)) + d - 1) / d);
+  return f;
+}
+
 }  // namespace attn

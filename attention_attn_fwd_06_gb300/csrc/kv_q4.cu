@@ -6,16 +6,17 @@
 // the four bits themselves cost.  NaN is stored as 0, values beyond fp16's range as its largest.
 //
 // What bounds both: HBM, once the arithmetic is short.  Writing takes 2 bytes in and 0.5625 out per element, reading
-// back the reverse.  A lane takes 16 dims (32 bytes of bf16, 8 bytes of codes), so four lanes hold a group and its
-// extremes take two shuffles.  One such piece of work a lane and as many warps as fit: 70k tokens of 8 heads at D = 128
-// take 89 us to write and 72 us to read back (a plain fill of as many bytes takes 75 us), against 113 and 79 us with a warp for each token and two rounds of its heads
-// in flight, 124 and 111 us with one wave of warps that walk runs of tokens.
+// back the reverse.  A lane takes 16 dims (32 bytes of bf16, 8 bytes of codes) of one head's key and of its value, so four
+// lanes hold a group, its extremes take two shuffles and the row's place is looked up once for both; as many warps as fit.
+// 70k tokens of 8 heads at D = 128 take 67 us to write (5.5 TB/s) and 72 us to read back (a plain fill of as many bytes
+// takes 75 us); a key's or a value's dims a lane: 89 us to write; a warp for each token and two rounds of its heads in flight
+// (with the slower codes of that day): 113 and 79 us; one wave of warps that walk runs of tokens: 124 and 111 us.
 //
 // Writing: extremes by packed bf16 min and max that pass NaN on; quotients correctly rounded, by a product with the
 // rounded reciprocal and its residual's share (Markstein's theorem), so that a tie between two codes is seen as one; their
 // rounding is that of an add of 1.5 2^23, whose low bits are the code (a conversion instruction runs at an eighth of the
-// rate); all of it in packed pairs.  Issue-bound before (floor, conversions and a decision by residual: 166 us, 112 us with
-// the residual only checked, which bf16's coarse values tie too often for).  A group whose codes or values leave
+// rate); all of it in packed pairs.  Issue-bound with floor, conversions and a decision by residual: 166 us, and 112 us with
+// the residual only checked, which bf16's coarse values tie too often for.  A group whose codes or values leave
 // their range (NaN, infinities, a scale of 0, a minimum that fp16 rounds) is decided code by code.
 // Reading: a code masked in place in a 16-bit half is, as fp16, the subnormal u 2^-24 or u 2^-20, so the conversion to
 // fp32 and one fused multiply-add with the scale make the value.
@@ -23,6 +24,7 @@
 #include <cuda_fp16.h>
 
 #include "common.cuh"
+#include "intdiv.h"
 #include "kernels.h"
 #include "kv_q4.h"
 #include "rope.cuh"
@@ -70,22 +72,13 @@ __device__ __noinline__ float2 extremes_slow(uint4 w0, uint4 w1) {
 __device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t w) { return *reinterpret_cast<__nv_bfloat162*>(&w); }
 __device__ __forceinline__ uint32_t bits_of(__nv_bfloat162 v) { return *reinterpret_cast<uint32_t*>(&v); }
 
-template <int D>
-__global__ void __launch_bounds__(kKvThreads) kv_append_q4_kernel(const KvAppendQ4Launch p, const unsigned nrows) {
-  constexpr int G = D / 64, TPR = D / 16;  // groups and lanes of a row
-  const unsigned row = blockIdx.x * (kKvThreads / TPR) + threadIdx.x / TPR;  // (token, K's heads then V's)
-  if (row >= nrows) return;  // whole groups of lanes
-  const int sub = threadIdx.x % TPR;
-  const unsigned tok = row / (2u * p.Hkv);
-  const int hh = (int)(row - tok * (2u * p.Hkv));
-  const bool is_v = hh >= p.Hkv;
-  const int h = is_v ? hh - p.Hkv : hh;
-  const uint4* src = reinterpret_cast<const uint4*>(
-      is_v ? reinterpret_cast<const __nv_bfloat16*>(p.v) + (long long)tok * p.vs[0] + h * p.vs[1] + 16 * sub
-           : reinterpret_cast<const __nv_bfloat16*>(p.k) + (long long)tok * p.ks[0] + h * p.ks[1] + 16 * sub);
-  const int slot = p.slots[tok];
-  const uint4 wa = src[0], wb = src[1];
-  const unsigned team = 0xfu << (threadIdx.x & 28);  // the group's four lanes
+struct Quantised {
+  uint2 code;
+  __half2 pair;  // scale, minimum
+};
+
+// One lane's 16 dims wa, wb of a group that the lanes of `team` hold.
+__device__ __forceinline__ Quantised quantise(uint4 wa, uint4 wb, unsigned team) {
   const uint32_t q[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
   __nv_bfloat162 mn = as_bf162(q[0]), mx = mn;
 #pragma unroll
@@ -111,10 +104,6 @@ __global__ void __launch_bounds__(kKvThreads) kv_append_q4_kernel(const KvAppend
     }
     lo = ex.x;
     hi = ex.y;
-  }
-  if (slot < 0 || slot >= p.num_pages * p.page_size) {  // -1: not written; anything else is an error
-    if (slot != -1 && sub == 0) record_status(p.status, ATTN_ERR_DEVICE_BOUNDS);
-    return;
   }
   // (hi - lo) / 15: a product, and its residual's share added (correctly rounded, as by Markstein's theorem)
   const float d = hi - lo;
@@ -142,14 +131,42 @@ __global__ void __launch_bounds__(kKvThreads) kv_append_q4_kernel(const KvAppend
                              (0x4b400000u << 16) + (0x4b400000u << 20) + (0x4b400000u << 24) + (0x4b400000u << 28);
   uint2 code = make_uint2(c[0] - kBias, c[1] - kBias);
   if (odd) code = quantise_slow(wa, wb, s, m);
-  const int page = slot / p.page_size, in_page = slot - page * p.page_size;
-  const int tile = in_page / kTileKeys, key = in_page % kTileKeys;
-  uint8_t* dst = reinterpret_cast<uint8_t*>(p.pool) + kv_q4_tile_at(page, h, tile, p.Hkv, p.page_size / kTileKeys, D);
-  const int g = sub / 4;
-  *reinterpret_cast<uint2*>(dst + (is_v ? kv_q4_v_off(D) : 0) + (g * kTileKeys + key) * 32 + (sub % 4) * 8) = code;
-  if (sub % 4 == 0)
-    *reinterpret_cast<__half2*>(dst + (is_v ? kv_q4_vp_off(D) : kv_q4_kp_off(D)) + (key * G + g) * 4) =
-        __halves2half2(sh, mh);
+  return {code, __halves2half2(sh, mh)};
+}
+
+// A lane: 16 dims of one (token, head)'s key and of its value.
+template <int D>
+__global__ void __launch_bounds__(kKvThreads) kv_append_q4_kernel(const KvAppendQ4Launch p, const unsigned nrows,
+                                                                  const FastDiv heads, const FastDiv page_keys) {
+  constexpr int G = D / 64, TPR = D / 16;  // groups and lanes of a row
+  const unsigned row = blockIdx.x * (kKvThreads / TPR) + threadIdx.x / TPR;  // (token, head)
+  if (row >= nrows) return;  // whole groups of lanes
+  const int sub = threadIdx.x % TPR;
+  const unsigned tok = heads.div(row);
+  const int h = (int)(row - tok * heads.d);
+  const int slot = p.slots[tok];
+  const uint4* ksrc = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.k) +
+                                                     (long long)tok * p.ks[0] + h * p.ks[1] + 16 * sub);
+  const uint4* vsrc = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.v) +
+                                                     (long long)tok * p.vs[0] + h * p.vs[1] + 16 * sub);
+  const uint4 ka = ksrc[0], kb = ksrc[1], va = vsrc[0], vb = vsrc[1];
+  const unsigned team = 0xfu << (threadIdx.x & 28);  // the group's four lanes
+  const Quantised qk = quantise(ka, kb, team), qv = quantise(va, vb, team);
+  if (slot < 0 || slot >= p.num_pages * p.page_size) {  // -1: not written; anything else is an error
+    if (slot != -1 && sub == 0) record_status(p.status, ATTN_ERR_DEVICE_BOUNDS);
+    return;
+  }
+  const int page = (int)page_keys.div((unsigned)slot), in_page = slot - page * p.page_size;
+  const int tile = in_page / kTileKeys, key = in_page % kTileKeys, g = sub / 4;
+  uint8_t* const dst = reinterpret_cast<uint8_t*>(p.pool) + kv_q4_tile_at(page, h, tile, p.Hkv, p.page_size / kTileKeys, D);
+  uint8_t* const code = dst + (g * kTileKeys + key) * 32 + (sub % 4) * 8;
+  *reinterpret_cast<uint2*>(code) = qk.code;
+  *reinterpret_cast<uint2*>(code + kv_q4_v_off(D)) = qv.code;
+  if (sub % 4 == 0) {
+    uint8_t* const pair = dst + kv_q4_kp_off(D) + (key * G + g) * 4;
+    *reinterpret_cast<__half2*>(pair) = qk.pair;
+    *reinterpret_cast<__half2*>(pair + kv_q4_vp_off(D) - kv_q4_kp_off(D)) = qv.pair;
+  }
 }
 
 __device__ __forceinline__ void codes_to_bf16(uint2 w, uint32_t pair, __nv_bfloat16* dst) {
@@ -171,13 +188,14 @@ __device__ __forceinline__ void codes_to_bf16(uint2 w, uint32_t pair, __nv_bfloa
 }
 
 template <int D>
-__global__ void __launch_bounds__(kKvThreads) kv_gather_q4_kernel(const KvGatherQ4Launch p, const unsigned nrows) {
+__global__ void __launch_bounds__(kKvThreads) kv_gather_q4_kernel(const KvGatherQ4Launch p, const unsigned nrows,
+                                                                  const FastDiv heads, const FastDiv page_keys) {
   constexpr int G = D / 64, TPR = D / 16;
   const unsigned row = blockIdx.x * (kKvThreads / TPR) + threadIdx.x / TPR;  // (token, head)
   if (row >= nrows) return;
   const int sub = threadIdx.x % TPR;
-  const int tok = (int)(row / (unsigned)p.Hkv);
-  const int h = (int)(row - (unsigned)tok * p.Hkv);
+  const int tok = (int)heads.div(row);
+  const int h = (int)(row - (unsigned)tok * heads.d);
   int seq = 0;
   for (int n = p.B; n > 1;) {  // the last of the sequences that start at or before tok
     const int half = n / 2;
@@ -191,7 +209,7 @@ __global__ void __launch_bounds__(kKvThreads) kv_gather_q4_kernel(const KvGather
   const int first = p.cu_k[seq];
   if (tok < first || tok >= p.cu_k[seq + 1]) return;  // rows of no sequence stay as they were
   const long long pos = (long long)tok - first + (p.kv_starts != nullptr ? p.kv_starts[seq] : 0);
-  const int pg = pos >= 0 && pos <= 0x7fffffffLL ? (int)pos / p.page_size : -1;
+  const int pg = pos >= 0 && pos <= 0x7fffffffLL ? (int)page_keys.div((unsigned)pos) : -1;
   int page = -1;
   if (pg >= 0 && pg < p.max_pages) page = p.block_table[(size_t)seq * p.max_pages + pg];
   if (page < 0 || page >= p.num_pages) {  // the row stays as it was
@@ -224,14 +242,15 @@ cudaError_t kv_blocks(long long rows, int D, unsigned& blocks) {
 }  // namespace
 
 cudaError_t launch_kv_append_q4(const KvAppendQ4Launch& p) {
-  const long long rows = 2ll * p.T * p.Hkv;
+  const long long rows = (long long)p.T * p.Hkv;
   unsigned blocks;
   const cudaError_t e = kv_blocks(rows, p.D, blocks);
   if (e != cudaSuccess || blocks == 0) return e;
+  const FastDiv heads = make_fast_div((unsigned)p.Hkv), page_keys = make_fast_div((unsigned)p.page_size);
   if (p.D == 64)
-    kv_append_q4_kernel<64><<<blocks, kKvThreads, 0, p.stream>>>(p, (unsigned)rows);
+    kv_append_q4_kernel<64><<<blocks, kKvThreads, 0, p.stream>>>(p, (unsigned)rows, heads, page_keys);
   else
-    kv_append_q4_kernel<128><<<blocks, kKvThreads, 0, p.stream>>>(p, (unsigned)rows);
+    kv_append_q4_kernel<128><<<blocks, kKvThreads, 0, p.stream>>>(p, (unsigned)rows, heads, page_keys);
   return cudaGetLastError();
 }
 
@@ -240,10 +259,11 @@ cudaError_t launch_kv_gather_q4(const KvGatherQ4Launch& p) {
   unsigned blocks;
   const cudaError_t e = kv_blocks(rows, p.D, blocks);
   if (e != cudaSuccess || blocks == 0) return e;
+  const FastDiv heads = make_fast_div((unsigned)p.Hkv), page_keys = make_fast_div((unsigned)p.page_size);
   if (p.D == 64)
-    kv_gather_q4_kernel<64><<<blocks, kKvThreads, 0, p.stream>>>(p, (unsigned)rows);
+    kv_gather_q4_kernel<64><<<blocks, kKvThreads, 0, p.stream>>>(p, (unsigned)rows, heads, page_keys);
   else
-    kv_gather_q4_kernel<128><<<blocks, kKvThreads, 0, p.stream>>>(p, (unsigned)rows);
+    kv_gather_q4_kernel<128><<<blocks, kKvThreads, 0, p.stream>>>(p, (unsigned)rows, heads, page_keys);
   return cudaGetLastError();
 }
 
