@@ -889,7 +889,9 @@ int attn_decode_q4(const attn_decode_q4_params* p) {
   const DecodeQ4Shape sh = decode_q4_shape(p->D, s->num_sms);
   char* ws = static_cast<char*>(p->workspace);
   if (ws == nullptr) {
-    st = ensure_buffer_locked(s->ws_q4, s->ws_q4_bytes, sh.bytes, sh.bytes, stream);
+    // made for the larger D, so that it never has to grow under a graph that was captured with it
+    const size_t bytes = decode_q4_shape(128, s->num_sms).bytes;
+    st = ensure_buffer_locked(s->ws_q4, s->ws_q4_bytes, bytes, bytes, stream);
     if (st != ATTN_OK) return st;
     ws = static_cast<char*>(s->ws_q4);
   } else if (p->workspace_bytes < sh.bytes) {

@@ -12,21 +12,35 @@
 // exceed its fp32 units.  So products run on the tensor cores -- mma.sync m16n8k16 in fp16, whose A operand
 // comes straight from registers: K^T and V^T tiles are 16 keys (dims) by 16, the 8 columns are the query rows of one
 // kv head.  A tcgen05 product would need the unpacked tile written to shared or tensor memory first, four times the
-// bytes of the codes, for an N of 8.
+// bytes of the codes, for an N of 8; mma.sync on 8-bit floats (codes are e4m3 as they are, q two terms) runs at fp16's
+// rate and converts its operands on the way (72 against 65 us at 131k keys).
 //  * Unpacking costs one mask per two elements: (w & 0x000f000f) is, as a pair of fp16, the subnormals u 2^-24, and
 //    (w & 0x00f000f0) is u 2^-20, both exact; the factors go into q (2^10 and 2^6, q first scaled by a power of two
 //    to a largest element in [16, 32), which is exact) and, for V, into the output.  One shift by 8 gives the
 //    other two pairs of a word.  For V, whose pairs run along keys, a byte permute first joins two keys' halves.
-//  * Scores come as S^T (keys by query rows), so a column's maximum is two registers and three shuffles for 32 keys,
-//    and the weights turn into the second product's B operand by two 8x8 transposes (movmatrix).
+//  * Scores come as S^T (keys by query rows), so a row's maximum is two registers and three shuffles for 32 keys,
+//    and the weights turn into the second product's B operand by two 8x8 transposes (movmatrix).  With up to four query
+//    rows each has two of the eight columns and a lane keeps one: half the softmax work of four columns left empty.
 //  * Weights are p s_v 2^x rounded to fp16 (2^-12 relative, against 2^-9 of a bf16 output), x kept such that they stay
 //    below 2^15 and the largest near 2^12; a call with fp32 output carries them as two fp16 terms.  Maxima, sums,
 //    the term in m_v and all accumulators are fp32.
+// At long contexts the instructions bound it: some 270 a tile of 16 keys at D = 128, 40 of them masks and shifts for K,
+// 48 with the byte permutes for V, at two clocks each (dropping either product's unpacking and matrix products reaches the
+// 60 us that the copies alone take of the 65); over short ones the chain of a launch: lengths, split, block table and first
+// copies (1.6 us), first data (4 us), a row's stages at 0.6 us each, exchange and merge (2 to 3 us).
+// Measured (CUDA-graph replays over rotating pools, 32 query and 8 kv heads, D = 128): 4 sequences of 32k to 131k keys 64.6 us
+// (5.6 TB/s, 0.82 of the copy bandwidth), 8 of 512 to 4096 keys 13.8 us, one of 4096 keys 11.7 us; 64 of up to 700 keys with
+// 16 heads of D = 64 16.0 us; 8 tokens each over 8 x 4096 keys 29.2 us.  Two CTAs of seven consumer warps an SM: 70.3 /
+// 15.0 / - / 22.0 us against 70.8 / 14.3 / - / 16.6 us that day; four tiles a warp and stage 70.5 / 16.7 / - / 19.1 us;
+// four CTAs at 96 registers 86 / 18.9 us (spills).
 // The split is decode.cu's: persistent CTAs take equal slices of the tiles of all (sequence, kv head, row chunk) rows, a
 // producer warp streams them with bulk copies (one copy per page and stage) into a shared-memory ring.  At a piece's
 // end each warp sums a quarter of the accumulators over the warps; a row split between CTAs is merged by the CTA that
-// holds its first piece, which reads the others' partials as they arrive.  CTAs start in order, and what a CTA waits
-// for no other CTA's wait holds up (it is the first thing that CTA does), so the wait ends with any number of CTAs resident.
+// holds its first piece, which reads the others' partials as they arrive.  CTAs start in order, and a CTA publishes
+// before it waits, so of all resident CTAs only the last one's row can wait for one that is not, and that one starts as soon
+// as any other ends; like every wait here this one gives up after a second.  (One count a row and a fence for it: 21.4
+// against 16.1 us over the 64 short sequences; one flag a warp, released and acquired: 17.0 us, 16.0 against 14.4 us over
+// the 8: a release waits 2 to 4 us for its stores while the cache streams.)
 #include <cfloat>
 #include <algorithm>
 #include <cmath>
@@ -68,7 +82,7 @@ struct Q4Cfg {
   static constexpr int MINB = NT == 1 ? 3 : 2;          // resident CTAs per SM
   static constexpr int NS = D == 128 ? 4 : 8;           // ring stages
   static constexpr int THREADS = 32 * (NW + 1);
-  static constexpr int LENS_CACHE = 128;                // kv_lens kept in shared memory for the walk
+  static constexpr int LENS_CACHE = 512;                // kv_lens kept in shared memory for the walk
   static constexpr int OWN = kDecodeQ4Owners;           // warps that gather the accumulators at a piece's end,
   static constexpr int OW = 4 * G / OWN;                // each this many of a column group
   static constexpr int SCR_BYTES = OWN * (NW - 1) * NT * OW * 512;  // [owner][other warps][NT][OW][lane] float4
@@ -291,8 +305,10 @@ __global__ void __launch_bounds__(Q4Cfg<D, R4>::THREADS, Q4Cfg<D, R4>::MINB)
       // the row whose cost interval holds position lo: sequences 32 at a time
       long long acc = 0;  // first cost position of sequence b
       int b = 0, nt = 0;
+      int next_nt = lane < p.B ? seq_tiles(lane) : 0;
       for (int b32 = 0;; b32 += 32) {
-        const int my_nt = b32 + lane < p.B ? seq_tiles(b32 + lane) : 0;
+        const int my_nt = next_nt;
+        next_nt = b32 + 32 + lane < p.B ? seq_tiles(b32 + 32 + lane) : 0;  // (on its way, past the lengths kept here)
         const long long mine = my_nt > 0 ? Hg * ((long long)my_nt + kRowCostTiles) : 0;
         long long upto = mine;
 #pragma unroll

@@ -374,7 +374,8 @@ unsigned long long attn_decode_workspace_bytes(int B, int Hq, int Hkv, int Lmax,
  * count) leave lengths, table and stack as they were; every slot and position is
  * then -1 and cu_new 0.  A page id out of [0, num_pages) met on the way is flagged
  * ATTN_ERR_DEVICE_BOUNDS and its tokens' slots are -1.  The buffers must not
- * overlap, except that an input not written may be passed twice.
+ * overlap, except that an input not written may be passed twice; a page stands in
+ * one row at most.  B == 0: nothing is done.
  *
  * B at most 8192; num_pages * page_size, B * max_pages and max_pages * page_size
  * below 2^31 (ATTN_ERR_UNSUPPORTED otherwise).  int32 pointers are 4-byte aligned
@@ -506,11 +507,11 @@ int attn_kv_gather_q4(const attn_kv_gather_q4_params* p);
  *   out, lse     as attn_decode_multi
  *   chunk        0 = default; otherwise the smallest number of keys of one CTA's slice,
  *                in [1, 1048576]
- *   workspace    NULL: a workspace of the library (its own, apart from attn_decode's, with
- *                the same rules: grown on demand but not during capture, calls that can
- *                overlap on the GPU race on it, and growing it invalidates graphs captured
- *                with the smaller one).  Otherwise a DEVICE buffer of workspace_bytes (at
- *                least attn_decode_q4_workspace_bytes; ATTN_ERR_SCRATCH_TOO_SMALL if not),
+ *   workspace    NULL: a workspace of the library, its own, apart from attn_decode's: made
+ *                by the first call on a device, which must not be one that is captured, and
+ *                kept until attn_release_workspace; calls that can overlap on the GPU race
+ *                on it.  Otherwise a DEVICE buffer of workspace_bytes (at least
+ *                attn_decode_q4_workspace_bytes; ATTN_ERR_SCRATCH_TOO_SMALL if not),
  *                16-byte aligned, all zeros before its first call; the calls leave it so.
  *                Calls that can overlap, and graphs that can be replayed at once, each take
  *                a buffer of their own.  After ATTN_ERR_DEVICE_TIMEOUT the caller zeroes it

@@ -374,7 +374,7 @@ def test_decode_q4_values_of_unlike_sizes():
             assert_within(ls[:, :, None], lse, bL)
 
 
-@pytest.mark.parametrize("B,Hq,Hkv", [(40, 16, 4), (400, 4, 2)])
+@pytest.mark.parametrize("B,Hq,Hkv", [(40, 16, 4), (400, 4, 2), (1100, 2, 1)])
 def test_decode_q4_many_sequences(B, Hq, Hkv):
     g = np.random.default_rng(B)
     lens = [int(x) for x in g.integers(0, 60, B)]
@@ -540,6 +540,52 @@ def test_two_captured_steps_replayed_at_once():
         assert e.lens.tolist() == [3030, 2530]
         e.check(e.q[:2])
     assert AB.attn_get_device_status() == AB.ATTN_OK
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_pool_offsets_past_32_bits(D):
+    """The last pages of a pool of over 4 GiB: written, read back and attended to like the first ones of a small one."""
+    Hkv, page, n = 4, 64, 300
+    page_bytes = AB.attn_kv_q4_page_bytes(page, Hkv, D)
+    num_pages = (5 << 30) // page_bytes
+    need = -(-n // page)
+    assert (num_pages - need) * page_bytes > 1 << 32
+    g = torch.Generator().manual_seed(D)
+    k, v = dev(torch.randn(2, n, Hkv, D, generator=g).to(torch.bfloat16))
+    q = dev(torch.randn(1, 8, D, generator=g).to(torch.bfloat16))
+    got = []
+    for pages in (need, num_pages):
+        pool = AB.attn_kv_q4_pool(pages, Hkv, page, D, DEV)
+        table = torch.arange(pages - need, pages, dtype=torch.int32, device=DEV)[None]
+        pos = torch.arange(n, device=DEV)
+        slots = table[0, pos // page] * page + (pos % page).to(torch.int32)
+        AB.attn_kv_append_q4(k, v, pool, slots)
+        got.append((*AB.attn_kv_gather_q4(pool, table, i32([0, n]), n), *AB.attn_decode_q4(q, pool, table, i32([n]))))
+        assert AB.attn_get_device_status() == AB.ATTN_OK
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
+def test_norm_without_rotation_or_positions():
+    q = dev(torch.randn(5, 3, 64).to(torch.bfloat16))
+    qo, ko = AB.attn_qk_norm_rope(q, None)
+    assert ko is None
+    ref, bound = norm_ref(oracle.to_f64(q), None, np.zeros(5, int), None, 1e-6, np.ones(5, bool))
+    assert_within(qo, ref, bound)
+
+
+def test_decode_q4_rows_of_every_width_over_a_long_capacity():
+    """16 query rows a CTA: taken from the block table's capacity, whatever the lengths."""
+    lens, page = [70, 0, 33], 16
+    pool = make_pool(10, 2, page, 64, 8)
+    table, _ = make_table(lens, page, 10, 8, width=120000)
+    for Hq, Lq in ((24, 1), (8, 5), (2, 16)):
+        q = torch.randn(3, Hq, Lq, 64, generator=torch.Generator().manual_seed(Hq)).to(torch.bfloat16)
+        for f32 in (False, True):
+            O, lse, bO, bL = decode_bound(q, pool, table, lens, 0.125, f32)
+            out, ls = run_decode(q, pool, table, lens, 0.125, out_dtype=torch.float32 if f32 else torch.bfloat16)
+            assert_within(out, O, bO)
+            assert_within(ls, lse, bL)
 
 
 def test_side_stream_gives_the_same_bits():
