@@ -32,7 +32,8 @@
 // (5.6 TB/s, 0.82 of the copy bandwidth), 8 of 512 to 4096 keys 13.8 us, one of 4096 keys 11.7 us; 64 of up to 700 keys with
 // 16 heads of D = 64 16.0 us; 8 tokens each over 8 x 4096 keys 29.2 us.  Two CTAs of seven consumer warps an SM: 70.3 /
 // 15.0 / - / 22.0 us against 70.8 / 14.3 / - / 16.6 us that day; four tiles a warp and stage 70.5 / 16.7 / - / 19.1 us;
-// four CTAs at 96 registers 86 / 18.9 us (spills).
+// four CTAs at 96 registers 86 / 18.9 us (spills).  At D = 64 two, three, four tiles a warp and stage: 16 heads over 4 x 16k to
+// 64k keys 45.1, 37.9, 36.2 us, the 64 short sequences 16.0, 16.1, 18.3 us.
 // The split is decode.cu's: persistent CTAs take equal slices of the tiles of all (sequence, kv head, row chunk) rows, a
 // producer warp streams them with bulk copies (one copy per page and stage) into a shared-memory ring.  At a piece's
 // end each warp sums a quarter of the accumulators over the warps; a row split between CTAs is merged by the CTA that
@@ -75,12 +76,12 @@ struct Q4Cfg {
   static constexpr int NT = (R4 + 1) / 2;               // column tiles of the second product
   static constexpr int NC = R4 == 1 ? 1 : 2;            // query rows a lane keeps of each
   static constexpr int NW = 4;                          // consumer warps
-  static constexpr int KT = 2;                          // tiles of a stage per consumer warp
+  static constexpr int KT = D == 64 ? 3 : 2;            // tiles of a stage per consumer warp
   static constexpr int ST = NW * KT;                    // tiles per stage
   static constexpr int TILE = kv_q4_tile_bytes(D);
   static constexpr int STAGE = ST * TILE;
   static constexpr int MINB = NT == 1 ? 3 : 2;          // resident CTAs per SM
-  static constexpr int NS = D == 128 ? 4 : 8;           // ring stages
+  static constexpr int NS = D == 64 ? 5 : 4;            // ring stages
   static constexpr int THREADS = 32 * (NW + 1);
   static constexpr int LENS_CACHE = 512;                // kv_lens kept in shared memory for the walk
   static constexpr int OWN = kDecodeQ4Owners;           // warps that gather the accumulators at a piece's end,
