@@ -12,6 +12,7 @@
 // (three running sums: tokens, pages taken, pages given back), and a cluster barrier separates these reads from the
 // in-place writes, which needs no scratch memory and no second launch.
 #include "common.cuh"
+#include "intdiv.h"
 #include "kernels.h"
 
 namespace attn {
@@ -28,7 +29,11 @@ __device__ __forceinline__ void launch_barrier() {
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
-__device__ __forceinline__ int ceil_div_pos(int x, int d) { return (int)(((unsigned)x + (unsigned)d - 1u) / (unsigned)d); }
+// ceil(x / d) for x >= 0
+__device__ __forceinline__ int pages_of(int x, const FastDiv& d) {
+  const unsigned q = d.div((unsigned)x);
+  return (int)(q + (q * d.d < (unsigned)x ? 1u : 0u));
+}
 
 // The largest b with sum[b] <= i, for 0 <= i < sum[B] (rows of no items are passed over).
 __device__ __forceinline__ int row_of(const int* sum, int B, int i) {
@@ -40,7 +45,7 @@ __device__ __forceinline__ int row_of(const int* sum, int B, int i) {
   return lo;
 }
 
-__global__ void __launch_bounds__(kPageThreads) page_step_kernel(const PageStepLaunch p) {
+__global__ void __launch_bounds__(kPageThreads) page_step_kernel(const PageStepLaunch p, const FastDiv page_keys) {
   extern __shared__ int page_smem[];
   const int B = p.B, ps = p.page_size;
   int* cu = page_smem;          // [B + 1] tokens before row b
@@ -67,7 +72,7 @@ __global__ void __launch_bounds__(kPageThreads) page_step_kernel(const PageStepL
     const int n = p.new_lens != nullptr ? p.new_lens[b] : 0;
     const bool ok = a >= 0 && a <= cap && c >= 0 && c <= a && n >= 0 && n <= cap - c;
     bad |= ok ? 0 : 1;
-    const int h = ok ? ceil_div_pos(a, ps) : 0, d = ok ? ceil_div_pos(c + n, ps) : 0;
+    const int h = ok ? pages_of(a, page_keys) : 0, d = ok ? pages_of(c + n, page_keys) : 0;
     kept[b] = c;
     have[b] = h;
     need[b] = d;
@@ -183,7 +188,7 @@ __global__ void __launch_bounds__(kPageThreads) page_step_kernel(const PageStepL
       if (i < total) {
         while (cu[b + 1] <= (int)i) ++b;
         const int pos = kept[b] + ((int)i - cu[b]);
-        const int q = (int)((unsigned)pos / (unsigned)ps);
+        const int q = (int)page_keys.div((unsigned)pos);
         if (q != pg || b != pgb) {
           pg = q;
           pgb = b;
@@ -245,7 +250,7 @@ cudaError_t launch_page_step(const PageStepLaunch& p) {
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = many ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, page_step_kernel, p);
+  return cudaLaunchKernelEx(&cfg, page_step_kernel, p, make_fast_div((unsigned)p.page_size));
 }
 
 }  // namespace attn
