@@ -26,11 +26,11 @@
 //    the term in m_v and all accumulators are fp32.
 // At long contexts the instructions bound it: some 270 a tile of 16 keys at D = 128, 40 of them masks and shifts for K,
 // 48 with the byte permutes for V, at two clocks each (dropping either product's unpacking and matrix products reaches the
-// 60 us that the copies alone take of the 65); over short ones the chain of a launch: lengths, split, block table and first
+// 60 us that the copies alone take of the 64); over short ones the chain of a launch: lengths, split, block table and first
 // copies (1.6 us), first data (4 us), a row's stages at 0.6 us each, exchange and merge (2 to 3 us).
-// Measured (CUDA-graph replays over rotating pools, 32 query and 8 kv heads, D = 128): 4 sequences of 32k to 131k keys 64.6 us
-// (5.6 TB/s, 0.82 of the copy bandwidth), 8 of 512 to 4096 keys 13.8 us, one of 4096 keys 11.7 us; 64 of up to 700 keys with
-// 16 heads of D = 64 16.0 us; 8 tokens each over 8 x 4096 keys 29.2 us.  Two CTAs of seven consumer warps an SM: 70.3 /
+// Measured (CUDA-graph replays over rotating pools, 32 query and 8 kv heads, D = 128): 4 sequences of 32k to 131k keys 63.6 us
+// (5.7 TB/s, 0.84 of the copy bandwidth), 8 of 512 to 4096 keys 13.6 us, one of 4096 keys 11.5 us; 64 of up to 700 keys with
+// 16 heads of D = 64 16.0 us; 8 tokens each over 8 x 4096 keys 29.6 us.  Two CTAs of seven consumer warps an SM: 70.3 /
 // 15.0 / - / 22.0 us against 70.8 / 14.3 / - / 16.6 us that day; four tiles a warp and stage 70.5 / 16.7 / - / 19.1 us;
 // four CTAs at 96 registers 86 / 18.9 us (spills).  At D = 64 two, three, four tiles a warp and stage: 16 heads over 4 x 16k to
 // 64k keys 45.1, 37.9, 36.2 us, the 64 short sequences 16.0, 16.1, 18.3 us.
@@ -482,44 +482,61 @@ __global__ void __launch_bounds__(Q4Cfg<D, R4>::THREADS, Q4Cfg<D, R4>::MINB)
     }
     const int all_see = len - p.Lq + 1;  // keys below it are seen by every column
 
+    // The (scale, minimum) pairs of score rows g and g + 8, from the tile's pairs at `par`.
+    auto load_pairs = [&](const uint8_t* par, uint32_t (&ra)[G], uint32_t (&rb)[G]) {
+      if constexpr (G == 2) {
+        const uint2 a = *reinterpret_cast<const uint2*>(par + kg * 8), b = *reinterpret_cast<const uint2*>(par + (kg + 8) * 8);
+        ra[0] = a.x, ra[G - 1] = a.y, rb[0] = b.x, rb[G - 1] = b.y;
+      } else {
+        ra[0] = *reinterpret_cast<const uint32_t*>(par + kg * 4);
+        rb[0] = *reinterpret_cast<const uint32_t*>(par + (kg + 8) * 4);
+      }
+    };
     // N tiles at `tp`, the first of which is tile `tile` of the sequence; EDGE: some column does not see all their keys.
     auto process = [&](const uint8_t* tp, int tile, auto n_c, auto edge_c) {
       constexpr int N = decltype(n_c)::value;
       constexpr bool EDGE = decltype(edge_c)::value;
       const int key0 = tile * kTileKeys;
       float x[N][NT][4];
+      // scores; the products that wait on one another's sums alternate between the groups
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const uint8_t* tb = tp + i * C::TILE;
+        uint2 wa[G], wb[G];
+        float acc[G][NT][4];
 #pragma unroll
         for (int gg = 0; gg < G; ++gg) {
-          const uint2 wa = *reinterpret_cast<const uint2*>(tb + gg * 512 + kg * 32 + t4 * 8);
-          const uint2 wb = *reinterpret_cast<const uint2*>(tb + gg * 512 + (kg + 8) * 32 + t4 * 8);
-          float acc[NT][4];
+          wa[gg] = *reinterpret_cast<const uint2*>(tb + gg * 512 + kg * 32 + t4 * 8);
+          wb[gg] = *reinterpret_cast<const uint2*>(tb + gg * 512 + (kg + 8) * 32 + t4 * 8);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
+          for (int nt = 0; nt < NT; ++nt) acc[gg][nt][0] = acc[gg][nt][1] = acc[gg][nt][2] = acc[gg][nt][3] = 0.f;
+        }
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const uint32_t a = j ? wa.y : wa.x, b = j ? wb.y : wb.x;
-            const uint32_t a8 = a >> 8, b8 = b >> 8;
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              mma_16816(acc[nt], a & kLowNibble, b & kLowNibble, a & kHighNibble, b & kHighNibble,
-                        qf[nt][4 * gg + 2 * j][0], qf[nt][4 * gg + 2 * j][1]);
-              mma_16816(acc[nt], a8 & kLowNibble, b8 & kLowNibble, a8 & kHighNibble, b8 & kHighNibble,
-                        qf[nt][4 * gg + 2 * j + 1][0], qf[nt][4 * gg + 2 * j + 1][1]);
+          for (int gg = 0; gg < G; ++gg) {
+            uint32_t a = j / 2 ? wa[gg].y : wa[gg].x, b = j / 2 ? wb[gg].y : wb[gg].x;
+            if (j % 2) {
+              a >>= 8;
+              b >>= 8;
             }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma_16816(acc[gg][nt], a & kLowNibble, b & kLowNibble, a & kHighNibble, b & kHighNibble,
+                        qf[nt][4 * gg + j][0], qf[nt][4 * gg + j][1]);
           }
-          const float2 pa = half2_floats(*reinterpret_cast<const uint32_t*>(tb + kv_q4_kp_off(D) + (kg * G + gg) * 4));
-          const float2 pb =
-              half2_floats(*reinterpret_cast<const uint32_t*>(tb + kv_q4_kp_off(D) + ((kg + 8) * G + gg) * 4));
+        uint32_t ra[G], rb[G];
+        load_pairs(tb + kv_q4_kp_off(D), ra, rb);
+#pragma unroll
+        for (int gg = 0; gg < G; ++gg) {
+          const float2 pa = half2_floats(ra[gg]), pb = half2_floats(rb[gg]);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
               const float q = qs[nt][gg][c];
-              x[i][nt][c] = fmaf(pa.x, acc[nt][c], gg ? fmaf(pa.y, q, x[i][nt][c]) : pa.y * q);
-              x[i][nt][2 + c] = fmaf(pb.x, acc[nt][2 + c], gg ? fmaf(pb.y, q, x[i][nt][2 + c]) : pb.y * q);
+              x[i][nt][c] = fmaf(pa.x, acc[gg][nt][c], gg ? fmaf(pa.y, q, x[i][nt][c]) : pa.y * q);
+              x[i][nt][2 + c] = fmaf(pb.x, acc[gg][nt][2 + c], gg ? fmaf(pb.y, q, x[i][nt][2 + c]) : pb.y * q);
             }
         }
       }
@@ -528,12 +545,10 @@ __global__ void __launch_bounds__(Q4Cfg<D, R4>::THREADS, Q4Cfg<D, R4>::MINB)
       uint32_t va[N][G], vb[N][G];
       uint32_t all = 0;
 #pragma unroll
-      for (int i = 0; i < N; ++i)
+      for (int i = 0; i < N; ++i) {
+        load_pairs(tp + i * C::TILE + kv_q4_vp_off(D), va[i], vb[i]);
 #pragma unroll
         for (int gg = 0; gg < G; ++gg) {
-          const uint8_t* tb = tp + i * C::TILE + kv_q4_vp_off(D) + gg * 4;
-          va[i][gg] = *reinterpret_cast<const uint32_t*>(tb + kg * G * 4);
-          vb[i][gg] = *reinterpret_cast<const uint32_t*>(tb + (kg + 8) * G * 4);
           if constexpr (EDGE) {
             const int k = key0 + i * kTileKeys + kg;
             if (k >= len) va[i][gg] = 0;
@@ -541,6 +556,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, R4>::THREADS, Q4Cfg<D, R4>::MINB)
           }
           all |= va[i][gg] | vb[i][gg];
         }
+      }
       // row maxima (of x, or at an edge of the masked logits f x)
       float mx[NT][NC];
       bool change = (all & 0x7fffu) > wlimit;
