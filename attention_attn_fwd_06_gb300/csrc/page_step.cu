@@ -151,7 +151,9 @@ __global__ void __launch_bounds__(kPageThreads) page_step_kernel(const PageStepL
   for (int r = gtid; r < ngiven; r += gthreads) {
     const int b = row_of(given, B, r);
     int* entry = p.block_table + (size_t)b * p.max_pages + need[b] + (r - given[b]);
-    p.free_pages[count + ngiven - 1 - r] = *entry;
+    const int id = *entry;
+    if (id < 0 || id >= p.num_pages) record_status(p.status, ATTN_ERR_DEVICE_BOUNDS);
+    p.free_pages[count + ngiven - 1 - r] = id;
     *entry = -1;
   }
   if (ngiven > 0) launch_barrier();  // (the same in every CTA) pages just given back can be taken below

@@ -372,8 +372,8 @@ unsigned long long attn_decode_workspace_bytes(int B, int Hq, int Hkv, int Lmax,
  * max_tokens tokens while slots or positions is given (ATTN_ERR_DEVICE_BOUNDS), or
  * too few free pages (ATTN_ERR_DEVICE_POOL; pages given back by the same step
  * count) leave lengths, table and stack as they were; every slot and position is
- * then -1 and cu_new 0.  A page id out of [0, num_pages) met on the way is flagged
- * ATTN_ERR_DEVICE_BOUNDS and its tokens' slots are -1.  The buffers must not
+ * then -1 and cu_new 0.  A page id out of [0, num_pages) met on the way, taken, kept or
+ * given back, is flagged ATTN_ERR_DEVICE_BOUNDS, and its tokens' slots are -1.  The buffers must not
  * overlap, except that an input not written may be passed twice; a page stands in
  * one row at most.  B == 0: nothing is done.
  *
