@@ -646,6 +646,8 @@ def attn_qk_norm_rope(q, k, q_weight=None, k_weight=None, rope=None, positions=N
         if style not in _ROPE_STYLES:
             raise ValueError("rope style must be 'half' or 'interleaved'")
         tab = (cos.shape[0] if isinstance(cos, torch.Tensor) and cos.dim() else 0, D // 2)
+        if tab[0] == 0:
+            raise ValueError("rope tables must have rows")
         r = (_fit(cos, "rope cos", torch.float32, tab, at), _fit(sin, "rope sin", torch.float32, tab, at), tab[0],
              _ROPE_STYLES[style], None)
     p = attn_qk_norm_rope_params(

@@ -112,6 +112,10 @@ def test_page_step_bad_page_ids_are_flagged():
     AB.attn_page_step(P.d_lens, P.d_table, P.d_free, P.d_count, 16, new_lens=i32([1]), slots=slots)
     assert AB.attn_get_device_status() == AB.ATTN_ERR_DEVICE_BOUNDS and slots.tolist() == [-1]
     assert P.d_lens.tolist() == [21]
+    AB.attn_page_step(P.d_lens, P.d_table, P.d_free, P.d_count, 16, keep_lens=i32([16]))  # and when it goes back
+    assert AB.attn_get_device_status() == AB.ATTN_ERR_DEVICE_BOUNDS and P.d_lens.tolist() == [16]
+    AB.attn_page_step(P.d_lens, P.d_table, P.d_free, P.d_count, 16, new_lens=i32([1]), slots=slots)  # and is taken
+    assert AB.attn_get_device_status() == AB.ATTN_ERR_DEVICE_BOUNDS and slots.tolist() == [-1]
 
 
 def test_page_step_without_lists():
@@ -189,6 +193,27 @@ def test_qk_norm_rope_dense_layout(D):
         flat = x.transpose(1, 2).reshape(B * L, -1, D)
         ref, bound = norm_ref(oracle.to_f64(flat), None, p, rope, 1e-6, np.ones(B * L, bool))
         assert_within(out.transpose(1, 2).reshape(B * L, -1, D), ref, bound)
+
+
+def test_qk_norm_rope_refuses_what_it_would_misread():
+    q = dev(torch.randn(4, 2, 64).to(torch.bfloat16))
+    cos = torch.zeros(8, 32, device=DEV)
+    for rope in ((cos[:0], cos[:0], "half"), (cos, cos[:4], "half"), (cos, cos.double(), "half"), (cos, cos, "both"),
+                 (cos, cos, "half", q)):
+        with pytest.raises((ValueError, TypeError)):
+            AB.attn_qk_norm_rope(q, None, rope=rope, positions=i32([0, 1, 2, 3]))
+    with pytest.raises(ValueError):
+        AB.attn_qk_norm_rope(q, None, positions=i32([0, 1, 2]))
+    with pytest.raises(ValueError):
+        AB.attn_qk_norm_rope(q, q[:3])
+    with pytest.raises(ValueError, match="overlap"):
+        AB.attn_qk_norm_rope(q, None, q_out=q[:1].expand(4, 2, 64))
+    with pytest.raises(AB.AttnError) as e:  # a view that does not start on 16 bytes
+        AB.attn_qk_norm_rope(torch.zeros(4 * 128 + 4, dtype=torch.bfloat16, device=DEV)[4:].view(4, 2, 64), None)
+    assert e.value.status == AB.ATTN_ERR_ALIGNMENT
+    with pytest.raises(AB.AttnError) as e:  # rotation without positions
+        AB.attn_qk_norm_rope(q, None, rope=(cos, cos, "half"))
+    assert e.value.status == AB.ATTN_ERR_INVALID_ARG
 
 
 def test_qk_norm_rope_positions_out_of_range_are_flagged():
@@ -419,6 +444,30 @@ def test_decode_q4_timeout_is_reported_and_the_next_call_is_right(monkeypatch):
     monkeypatch.delenv("ATTN_FAULT_INJECT")
     b = run_decode(q, pool, table, [16000, 15000], 0.09, chunk=1 << 14)
     assert torch.equal(a[0], b[0])
+
+
+def test_cache_calls_refuse_what_they_would_misread():
+    pool = dev(make_pool(4, 2, 16, 64, 4))
+    q, table, lens = dev(torch.randn(1, 4, 64).to(torch.bfloat16)), i32([0, 1])[None], i32([20])
+    k = dev(torch.randn(3, 2, 64).to(torch.bfloat16))
+    for args in ((k, k, pool, i32([0, 1])), (k, k[:2], pool, i32([0, 1, 2])), (k[:, :1], k[:, :1], pool, i32([0, 1, 2])),
+                 (k, k, pool[..., :1000], i32([0, 1, 2])), (k, k.transpose(1, 2), pool, i32([0, 1, 2])),
+                 (k, k, pool, i32([0, 1, 2]).long()), (k.float(), k, pool, i32([0, 1, 2]))):
+        with pytest.raises((ValueError, TypeError)):
+            AB.attn_kv_append_q4(*args)
+    for kw in (dict(cu_k=i32([0, 3, 4])), dict(kv_starts=i32([0, 0])), dict(total_k=4, k_out=k), dict(block_table=table[0])):
+        with pytest.raises((ValueError, TypeError)):
+            AB.attn_kv_gather_q4(**{**dict(pool=pool, block_table=table, cu_k=i32([0, 3]), total_k=3), **kw})
+    for kw in (dict(q=q.float()), dict(q=q.cpu()), dict(kv_lens=lens.long()), dict(kv_lens=i32([1, 2])),
+               dict(block_table=table[0]), dict(out=torch.empty(1, 4, 128, dtype=torch.bfloat16, device=DEV)),
+               dict(lse=torch.empty(4, device=DEV)), dict(out_dtype=torch.float16), dict(pool=pool.view(4, 2, -1)),
+               dict(workspace=torch.zeros(8, device=DEV))):
+        with pytest.raises((ValueError, TypeError)):
+            AB.attn_decode_q4(**{**dict(q=q, pool=pool, block_table=table, kv_lens=lens), **kw})
+    with pytest.raises(AB.AttnError) as e:
+        AB.attn_decode_q4(q[:, :3].contiguous(), pool, table, lens)  # 3 query heads over 2
+    assert e.value.status == AB.ATTN_ERR_INVALID_ARG
+    assert AB.attn_get_device_status() == AB.ATTN_OK
 
 
 def test_decode_q4_workspace_too_small_is_refused():
