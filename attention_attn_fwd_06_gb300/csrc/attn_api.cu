@@ -97,7 +97,8 @@ int map_cuda(cudaError_t e) {
   return ATTN_ERR_CUDA;
 }
 
-// Ensures the workspace (ws, ws_bytes) holds `bytes`, its first `zeroed` bytes zero when it is made.  Refuses to
+// Ensures the workspace (ws, ws_bytes) holds `bytes`, its first `zeroed` bytes zero when it is made (on `stream`, whose
+// next kernel uses it: streams made not to wait for the default stream would not wait for a memset there).  Refuses to
 // allocate while the stream is being captured into a CUDA graph.  Caller holds g_mu.
 int ensure_buffer_locked(void*& ws, size_t& ws_bytes, size_t bytes, size_t zeroed, cudaStream_t stream) {
   if (bytes <= ws_bytes) return ATTN_OK;
@@ -117,7 +118,7 @@ int ensure_buffer_locked(void*& ws, size_t& ws_bytes, size_t bytes, size_t zeroe
     ws = nullptr;
     return ATTN_ERR_CUDA;
   }
-  if (cudaMemset(ws, 0, zeroed) != cudaSuccess) {
+  if (cudaMemsetAsync(ws, 0, zeroed, stream) != cudaSuccess) {
     cudaGetLastError();
     cudaFree(ws);
     ws = nullptr;

@@ -470,6 +470,43 @@ def test_cache_calls_refuse_what_they_would_misread():
     assert AB.attn_get_device_status() == AB.ATTN_OK
 
 
+def test_decode_q4_workspace_is_zeroed_on_the_calls_stream():
+    # the library's workspace is made by a call on a side stream, while the default stream is busy
+    pool, q = dev(make_pool(64, 1, 16, 64, 7)), dev(torch.randn(1, 4, 64).to(torch.bfloat16))
+    args = (q, pool, i32(range(64))[None], i32([1024]))
+    want = AB.attn_decode_q4(*args, workspace=AB.attn_decode_q4_workspace(4, 1, 64))
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    AB.attn_release_workspace()
+    torch.cuda._sleep(100_000_000)
+    with torch.cuda.stream(side):
+        for _ in range(3):
+            got = AB.attn_decode_q4(*args)
+            side.synchronize()
+            assert torch.equal(want[0].cpu(), got[0].cpu()) and torch.equal(want[1].cpu(), got[1].cpu())
+    torch.cuda.synchronize()
+    assert AB.attn_get_device_status() == AB.ATTN_OK
+
+
+def test_decode_q4_does_not_make_its_workspace_inside_a_capture():
+    pool, q = dev(make_pool(1, 1, 16, 64, 4)), dev(torch.randn(1, 1, 64).to(torch.bfloat16))
+    args = (q, pool, i32([0])[None], i32([5]))
+    want = AB.attn_decode_q4(*args)
+    out, lse = torch.empty_like(want[0]), torch.empty_like(want[1])
+    torch.cuda.synchronize()
+    AB.attn_release_workspace()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(AB.AttnError) as e:
+            AB.attn_decode_q4(*args, out=out, lse=lse)
+        out.fill_(3)
+    assert e.value.status == AB.ATTN_ERR_INVALID_ARG
+    graph.replay()  # the capture itself was left intact
+    torch.cuda.synchronize()
+    assert (out == 3).all()
+    assert torch.equal(AB.attn_decode_q4(*args)[0], want[0])
+
+
 def test_decode_q4_workspace_too_small_is_refused():
     pool, q = dev(make_pool(1, 1, 16, 64, 4)), dev(torch.randn(1, 1, 64).to(torch.bfloat16))
     ws = torch.zeros(1024, dtype=torch.uint8, device=DEV)
