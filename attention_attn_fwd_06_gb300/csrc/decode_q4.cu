@@ -95,7 +95,7 @@ struct Q4Cfg {
   static constexpr int OFF_LENS = OFF_ML + NW * 8 * NT * 8;
   static constexpr int OFF_MISC = OFF_LENS + LENS_CACHE * 4;
   static constexpr int SMEM = OFF_MISC + 16;
-  static_assert(OWN <= NW && 4 * G % OWN == 0, "every owner has as many accumulators");
+  static_assert(OWN == NW && 4 * G % OWN == 0, "every warp owns as many accumulators");
   static_assert(OFF_BAR % 16 == 0 && OFF_ML % 8 == 0, "aligned regions");
   static_assert(MINB * (SMEM + 1024) <= 228 * 1024, "MINB CTAs per SM");
   static_assert(ST <= 32, "a stage spans at most one page per lane");
@@ -772,10 +772,6 @@ __global__ void __launch_bounds__(Q4Cfg<D, R4>::THREADS, Q4Cfg<D, R4>::MINB)
       }
     }
     named_bar_sync(1, nct);
-    if (C::NW > C::OWN && warp >= C::OWN) {
-      release();
-      continue;
-    }
     float M[NT][2], L[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -827,7 +823,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, R4>::THREADS, Q4Cfg<D, R4>::MINB)
         for (int c = 0; c < NC; ++c) {
           const int row = 8 * nt + 4 * c + t4;
           if (row0 + row >= rows) continue;
-          const bool none = M[nt][c] == -INFINITY;  // a row that sees no key: O = 0, lse = -inf
+          const bool none = L[nt][c] == 0.f;  // a row that sees no key: O = 0, lse = -inf (a NaN query: L and O are NaN)
           const float inv = none ? 0.f : 1.f / L[nt][c];
           const size_t at = (orow0 + row) * D;
 #pragma unroll

@@ -421,6 +421,20 @@ def test_decode_q4_is_reproducible_and_agrees_across_lq():
     assert torch.equal(a[0], c[0][:, :, 0]) and torch.equal(a[1], c[1][:, :, 0])
 
 
+@pytest.mark.parametrize("Lq,n", [(1, 20), (1, 3000), (2, 40), (4, 3000)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_decode_q4_nan_queries_stay_in_their_rows(Lq, n, bad):
+    pool, (table, _) = make_pool(200, 2, 16, 64, 4), make_table([n], 16, 200, 4)
+    q = torch.randn(1, 8, Lq, 64, generator=torch.Generator().manual_seed(n)).to(torch.bfloat16)
+    hurt = q.clone()
+    hurt[0, 3, 0, 5] = bad
+    O, lse = run_decode(q, pool, table, [n], 0.125)
+    o, ls = run_decode(hurt, pool, table, [n], 0.125)
+    assert o[0, 3, 0].isnan().all() and ls[0, 3, 0].isnan()
+    o[0, 3, 0], ls[0, 3, 0] = O[0, 3, 0], lse[0, 3, 0]
+    assert torch.equal(o, O) and torch.equal(ls, lse)
+
+
 def test_decode_q4_bad_lengths_and_pages_are_flagged():
     pool = dev(make_pool(4, 2, 16, 64, 4))
     q = dev(torch.randn(2, 4, 64).to(torch.bfloat16))
