@@ -406,14 +406,15 @@ int attn_page_step(const attn_page_step_params* p);
  * and either [B, H, L, D] or [B, L, H, D]; a row's D elements are contiguous.
  *
  *   q, k          bf16, B sequences of L tokens with Hq (Hkv) heads; Hkv = 0: no k
- *   q_out, k_out  bf16; either apart from every input, or exactly an input's rows
- *                 (same pointer and strides: in place)
+ *   q_out, k_out  bf16; either apart from every input, or exactly the rows of q (of k)
+ *                 itself (same pointer and strides: in place)
  *   q_weight, k_weight  bf16 [D], or NULL for ones
  *   positions     int32 [B, L]; -1 marks a padded row, which is left as it was.  Any
  *                 other value outside [0, max_pos) is flagged and its row left as it
  *                 was.  May be NULL without rotation.
  *   rope          tables and style (k_out unused); ATTN_ROPE_NONE: norm only
  *   eps           finite, >= 0 (a row of zeros with eps = 0 is 0 * inf = NaN)
+ * (In fp32 the squares of elements beyond some 10^18 overflow, and such a row is 0.)
  * Pointers are 16-byte aligned, strides multiples of 8 elements.
  */
 typedef struct attn_qk_norm_rope_params {
@@ -457,6 +458,7 @@ unsigned long long attn_kv_q4_page_bytes(int page_size, int Hkv, int D);
  *   slots  int32 [T]; -1: the row is not written.  Any other slot outside the pool is
  *          flagged and not written.  The slots of one call must differ: rows of the same
  *          slot would be written over each other in no order.
+ * T * Hkv below 2^31 (ATTN_ERR_UNSUPPORTED otherwise).
  */
 typedef struct attn_kv_append_q4_params {
   const void* k;
@@ -480,6 +482,7 @@ int attn_kv_append_q4(const attn_kv_append_q4_params* p);
  *   kv_starts    int32 [B], or NULL for zeros
  *   k, v         bf16 [total_k, Hkv, D]; rows at and past cu_k[B] stay as they were, and
  *                so do rows of positions or pages out of range, which are flagged
+ * total_k * Hkv below 2^31 (ATTN_ERR_UNSUPPORTED otherwise).
  */
 typedef struct attn_kv_gather_q4_params {
   const void* pool;
