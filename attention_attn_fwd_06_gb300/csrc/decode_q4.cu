@@ -12,8 +12,9 @@
 // exceed its fp32 units.  So products run on the tensor cores -- mma.sync m16n8k16 in fp16, whose A operand
 // comes straight from registers: K^T and V^T tiles are 16 keys (dims) by 16, the 8 columns are the query rows of one
 // kv head.  A tcgen05 product would need the unpacked tile written to shared or tensor memory first, four times the
-// bytes of the codes, for an N of 8; mma.sync on 8-bit floats (codes are e4m3 as they are, q two terms) runs at fp16's
-// rate and converts its operands on the way (72 against 65 us at 131k keys).
+// bytes of the codes, for an N of 8 (for 32 query rows over 131k keys it takes 179 against 214 us, over 8 x 4096 37 against 30);
+// mma.sync on 8-bit floats (codes are e4m3 as they are, q two terms) runs at fp16's rate and converts its operands on the
+// way (72 against 65 us at 131k keys).
 //  * Unpacking costs one mask per two elements: (w & 0x000f000f) is, as a pair of fp16, the subnormals u 2^-24, and
 //    (w & 0x00f000f0) is u 2^-20, both exact; the factors go into q (2^10 and 2^6, q first scaled by a power of two
 //    to a largest element in [16, 32), which is exact) and, for V, into the output.  One shift by 8 gives the
