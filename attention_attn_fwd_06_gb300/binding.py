@@ -684,11 +684,15 @@ _NO_ROPE = (0, 0, 0, ATTN_ROPE_NONE, 0)
 
 def _out_rows(out, name, like, ndim, at):
     """The strides of an output shaped like `like` whose rows are written once each."""
+    try:
+        if out.dtype is torch.bfloat16 and out.shape == like.shape and out.get_device() == at and out.is_contiguous():
+            return out.stride()
+    except AttributeError:  # not a tensor: told below
+        pass
     st = _rows(out, name, ndim, at)
     if out.shape != like.shape:
         raise ValueError(f"{name} must have shape {tuple(like.shape)}, got {tuple(out.shape)}")
-    if not out.is_contiguous():
-        _written_once(out, name)
+    _written_once(out, name)
     return st
 
 
