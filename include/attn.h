@@ -54,7 +54,7 @@ typedef enum attn_status {
   ATTN_ERR_ALIGNMENT = 3,       /* a pointer is not 16-byte aligned                    */
   ATTN_ERR_CUDA = 4,            /* a CUDA runtime call or launch failed                */
   ATTN_ERR_DEVICE_TIMEOUT = 5,  /* device status: a bounded pipeline wait expired      */
-  ATTN_ERR_DEVICE_BOUNDS = 6,   /* device status: a kv_len was outside [0, Lmax]       */
+  ATTN_ERR_DEVICE_BOUNDS = 6,   /* device status: a length, position, slot or page id was out of range */
   ATTN_ERR_SCRATCH_TOO_SMALL = 7, /* attn_decode_noalloc: partials exceed its fixed buffer; a caller's workspace is too small */
   ATTN_ERR_DEVICE_POOL = 8      /* device status: attn_page_step found too few free pages  */
 } attn_status;
@@ -373,9 +373,9 @@ unsigned long long attn_decode_workspace_bytes(int B, int Hq, int Hkv, int Lmax,
  * too few free pages (ATTN_ERR_DEVICE_POOL; pages given back by the same step
  * count) leave lengths, table and stack as they were; every slot and position is
  * then -1 and cu_new 0.  A page id out of [0, num_pages) met on the way, taken, kept or
- * given back, is flagged ATTN_ERR_DEVICE_BOUNDS, and its tokens' slots are -1.  The buffers must not
- * overlap, except that an input not written may be passed twice; a page stands in
- * one row at most.  B == 0: nothing is done.
+ * given back, is flagged ATTN_ERR_DEVICE_BOUNDS, and its tokens' slots are -1.  The
+ * buffers must not overlap, except that an input not written may be passed twice; a
+ * page stands in one row at most.  B == 0: nothing is done.
  *
  * B at most 8192; num_pages * page_size, B * max_pages and max_pages * page_size
  * below 2^31 (ATTN_ERR_UNSUPPORTED otherwise).  int32 pointers are 4-byte aligned
@@ -507,7 +507,7 @@ int attn_kv_gather_q4(const attn_kv_gather_q4_params* p);
  *                most max_pages * page_size (clamped and flagged otherwise).  Only
  *                entries of pages that hold keys are read; a page id outside the pool
  *                is flagged and page 0 read instead.
- *   out, lse     as attn_decode_multi
+ *   out, lse     as attn_decode_multi, apart from every input
  *   chunk        0 = default; otherwise the smallest number of keys of one CTA's slice,
  *                in [1, 1048576]
  *   workspace    NULL: a workspace of the library, its own, apart from attn_decode's: made

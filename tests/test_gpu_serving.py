@@ -3,6 +3,10 @@ reading, decode over it, and a step of all of them together.
 
 Page bookkeeping and the cache's bytes are compared for equality; computed values against fp64 with bounds counted
 in roundings (tests/_serving.py, and beside each test)."""
+import pathlib
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -699,3 +703,42 @@ def test_side_stream_gives_the_same_bits():
     b = AB.attn_decode_q4(q, pool, table, lens, stream=st)
     st.synchronize()
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+FIRST_CALLS = """
+import torch
+from attention_attn_fwd_06_gb300 import binding as AB
+i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+lens, table, free, count, new = i32([0] * 3), i32([[-1, -1]] * 3), i32(range(8)), i32([8]), i32([5, 17, 0])
+slots, pos, cu = i32([0] * 22), i32([0] * 22), i32([0] * 4)
+x = torch.randn(22, 2, 64, device="cuda").to(torch.bfloat16)
+pool = torch.zeros(8, 2, 1, 18 * 64, dtype=torch.uint8, device="cuda")
+cos = torch.randn(32, 32, device="cuda")
+q, k, v, out, lse = torch.empty_like(x), torch.empty_like(x), torch.empty_like(x), torch.empty_like(x[:3]), torch.empty(3, 2, device="cuda")
+ws = AB.attn_decode_q4_workspace(2, 2, 64)  # (a size only: nothing has run)
+
+def step():
+    AB.attn_page_step(lens, table, free, count, 16, new_lens=new, slots=slots, positions=pos, cu_new=cu)
+    AB.attn_qk_norm_rope(x, None, rope=(cos, cos, "half"), positions=pos, q_out=q)
+    AB.attn_kv_append_q4(q, x, pool, slots)
+    AB.attn_kv_gather_q4(pool, table, cu, 22, k_out=k, v_out=v)
+    AB.attn_decode_q4(q[:3], pool, table, lens, out=out, lse=lse, workspace=ws)
+
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    step()
+graph.replay()
+got = [t.clone() for t in (lens, table, slots, pos, cu, q, k, v, out, lse)]
+lens.zero_(), table.fill_(-1), free.copy_(i32(range(8))), count.fill_(8), pool.zero_()
+step()
+assert AB.attn_get_device_status() == AB.ATTN_OK
+assert all(torch.equal(a, b) for a, b in zip(got, (lens, table, slots, pos, cu, q, k, v, out, lse)))
+assert lens.tolist() == [5, 17, 0] and lse[2].isneginf().all()
+"""
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], capture_output=True, text=True, timeout=120,
+                       cwd=pathlib.Path(__file__).parents[1])
+    assert r.returncode == 0, r.stderr
