@@ -134,8 +134,8 @@ __device__ __forceinline__ Quantised quantise(uint4 wa, uint4 wb, unsigned team)
   return {code, __halves2half2(sh, mh)};
 }
 
-// A lane: 16 dims of one (token, head)'s key and of its value.
-template <int D>
+// A lane: 16 dims of one (token, head)'s key and of its value.  WIDE: rows start on 32 bytes.
+template <int D, bool WIDE>
 __global__ void __launch_bounds__(kKvThreads) kv_append_q4_kernel(const KvAppendQ4Launch p, const unsigned nrows,
                                                                   const FastDiv heads, const FastDiv page_keys) {
   constexpr int G = D / 64, TPR = D / 16;  // groups and lanes of a row
@@ -149,7 +149,13 @@ __global__ void __launch_bounds__(kKvThreads) kv_append_q4_kernel(const KvAppend
                                                      (long long)tok * p.ks[0] + h * p.ks[1] + 16 * sub);
   const uint4* vsrc = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.v) +
                                                      (long long)tok * p.vs[0] + h * p.vs[1] + 16 * sub);
-  const uint4 ka = ksrc[0], kb = ksrc[1], va = vsrc[0], vb = vsrc[1];
+  uint4 ka, kb, va, vb;
+  if constexpr (WIDE) {
+    ldg256(ksrc, ka, kb);
+    ldg256(vsrc, va, vb);
+  } else {
+    ka = ksrc[0], kb = ksrc[1], va = vsrc[0], vb = vsrc[1];
+  }
   const unsigned team = 0xfu << (threadIdx.x & 28);  // the group's four lanes
   const Quantised qk = quantise(ka, kb, team), qv = quantise(va, vb, team);
   if (slot < 0 || slot >= p.num_pages * p.page_size) {  // -1: not written; anything else is an error
@@ -169,9 +175,11 @@ __global__ void __launch_bounds__(kKvThreads) kv_append_q4_kernel(const KvAppend
   }
 }
 
+template <bool WIDE>
 __device__ __forceinline__ void codes_to_bf16(uint2 w, uint32_t pair, __nv_bfloat16* dst) {
   const float2 sm = __half22float2(*reinterpret_cast<__half2*>(&pair));
   const float s24 = sm.x * 16777216.f, s20 = sm.x * 1048576.f;
+  uint4 out[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const uint32_t v = i ? w.y : w.x;
@@ -183,11 +191,18 @@ __device__ __forceinline__ void codes_to_bf16(uint2 w, uint32_t pair, __nv_bfloa
       x[n] = fmaf(f.x, n % 2 ? s20 : s24, sm.y);
       x[n + 4] = fmaf(f.y, n % 2 ? s20 : s24, sm.y);
     }
-    *reinterpret_cast<uint4*>(dst + 8 * i) = pack8(x);
+    out[i] = pack8(x);
+  }
+  if constexpr (WIDE) {
+    stg256(dst, out[0], out[1]);
+  } else {
+    *reinterpret_cast<uint4*>(dst) = out[0];
+    *reinterpret_cast<uint4*>(dst + 8) = out[1];
   }
 }
 
-template <int D>
+// WIDE: k and v start on 32 bytes.
+template <int D, bool WIDE>
 __global__ void __launch_bounds__(kKvThreads) kv_gather_q4_kernel(const KvGatherQ4Launch p, const unsigned nrows,
                                                                   const FastDiv heads, const FastDiv page_keys) {
   constexpr int G = D / 64, TPR = D / 16;
@@ -227,8 +242,8 @@ __global__ void __launch_bounds__(kKvThreads) kv_gather_q4_kernel(const KvGather
   const uint32_t pk = *reinterpret_cast<const uint32_t*>(src + kv_q4_kp_off(D) + par);
   const uint32_t pv = *reinterpret_cast<const uint32_t*>(src + kv_q4_vp_off(D) + par);
   const size_t at = (size_t)row * D + 16 * sub;
-  codes_to_bf16(wk, pk, reinterpret_cast<__nv_bfloat16*>(p.k) + at);
-  codes_to_bf16(wv, pv, reinterpret_cast<__nv_bfloat16*>(p.v) + at);
+  codes_to_bf16<WIDE>(wk, pk, reinterpret_cast<__nv_bfloat16*>(p.k) + at);
+  codes_to_bf16<WIDE>(wv, pv, reinterpret_cast<__nv_bfloat16*>(p.v) + at);
 }
 
 // Blocks for `rows` rows of D elements; cudaErrorNotSupported past 2^31 rows (more than any GPU's memory).
@@ -241,16 +256,40 @@ cudaError_t kv_blocks(long long rows, int D, unsigned& blocks) {
 
 }  // namespace
 
+namespace {
+
+bool on32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31) == 0; }
+
+template <int D>
+void append(const KvAppendQ4Launch& p, unsigned rows, unsigned blocks) {
+  const FastDiv heads = make_fast_div((unsigned)p.Hkv), page_keys = make_fast_div((unsigned)p.page_size);
+  const bool wide = on32(p.k) && on32(p.v) && (p.ks[0] | p.ks[1] | p.vs[0] | p.vs[1]) % 16 == 0;
+  if (wide)
+    kv_append_q4_kernel<D, true><<<blocks, kKvThreads, 0, p.stream>>>(p, rows, heads, page_keys);
+  else
+    kv_append_q4_kernel<D, false><<<blocks, kKvThreads, 0, p.stream>>>(p, rows, heads, page_keys);
+}
+
+template <int D>
+void gather(const KvGatherQ4Launch& p, unsigned rows, unsigned blocks) {
+  const FastDiv heads = make_fast_div((unsigned)p.Hkv), page_keys = make_fast_div((unsigned)p.page_size);
+  if (on32(p.k) && on32(p.v))
+    kv_gather_q4_kernel<D, true><<<blocks, kKvThreads, 0, p.stream>>>(p, rows, heads, page_keys);
+  else
+    kv_gather_q4_kernel<D, false><<<blocks, kKvThreads, 0, p.stream>>>(p, rows, heads, page_keys);
+}
+
+}  // namespace
+
 cudaError_t launch_kv_append_q4(const KvAppendQ4Launch& p) {
   const long long rows = (long long)p.T * p.Hkv;
   unsigned blocks;
   const cudaError_t e = kv_blocks(rows, p.D, blocks);
   if (e != cudaSuccess || blocks == 0) return e;
-  const FastDiv heads = make_fast_div((unsigned)p.Hkv), page_keys = make_fast_div((unsigned)p.page_size);
   if (p.D == 64)
-    kv_append_q4_kernel<64><<<blocks, kKvThreads, 0, p.stream>>>(p, (unsigned)rows, heads, page_keys);
+    append<64>(p, (unsigned)rows, blocks);
   else
-    kv_append_q4_kernel<128><<<blocks, kKvThreads, 0, p.stream>>>(p, (unsigned)rows, heads, page_keys);
+    append<128>(p, (unsigned)rows, blocks);
   return cudaGetLastError();
 }
 
@@ -259,11 +298,10 @@ cudaError_t launch_kv_gather_q4(const KvGatherQ4Launch& p) {
   unsigned blocks;
   const cudaError_t e = kv_blocks(rows, p.D, blocks);
   if (e != cudaSuccess || blocks == 0) return e;
-  const FastDiv heads = make_fast_div((unsigned)p.Hkv), page_keys = make_fast_div((unsigned)p.page_size);
   if (p.D == 64)
-    kv_gather_q4_kernel<64><<<blocks, kKvThreads, 0, p.stream>>>(p, (unsigned)rows, heads, page_keys);
+    gather<64>(p, (unsigned)rows, blocks);
   else
-    kv_gather_q4_kernel<128><<<blocks, kKvThreads, 0, p.stream>>>(p, (unsigned)rows, heads, page_keys);
+    gather<128>(p, (unsigned)rows, blocks);
   return cudaGetLastError();
 }
 

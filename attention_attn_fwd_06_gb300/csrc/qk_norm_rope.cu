@@ -38,7 +38,7 @@ __global__ void __launch_bounds__(32 * kNormWarps, kNormBlocks)
   constexpr int TPR = D / 16;    // lanes per head
   constexpr int HPW = 32 / TPR;  // heads per round
   constexpr int U = 2;           // rounds in flight
-  constexpr int OFF_B = STYLE == 1 ? D / 2 : 8;  // from a lane's first 8 elements to its other 8
+  constexpr int OFF_B = D / 2;   // from a lane's first 8 elements to its other 8 (whole sectors for a warp's accesses)
   __shared__ __align__(16) float tables[kNormWarps][2][STYLE != 0 ? D : 4];  // cos row, sin row of two tokens
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long job = (long long)blockIdx.x * kNormWarps + warp;
@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(32 * kNormWarps, kNormBlocks)
   if (left <= 0) return;
   const int ntok = left < share.tokens ? (int)left : share.tokens;
   const int sub = lane % TPR;
-  const int d0 = STYLE == 1 ? 8 * sub : 16 * sub;  // the lane's first element
+  const int d0 = 8 * sub;  // the lane's first element
   const int H = p.Hq + p.Hkv;
   const int rbase = share.chunks == 1 ? 0 : (int)(job - t0 * share.chunks) * share.rounds;
   const int h0 = rbase * HPW + lane / TPR;
@@ -101,11 +101,13 @@ __global__ void __launch_bounds__(32 * kNormWarps, kNormBlocks)
       fetch_tables(tk + 1);
       cp_async_wait<1>();
       __syncwarp();
-      const float4* tab = reinterpret_cast<const float4*>(tables[warp][tk & 1] + 8 * sub);
+      // the lane's eight pairs: 8 sub .., or four from each of its runs of elements
+      constexpr int NEXT = STYLE == 1 ? 1 : D / 16;
+      const float4* tab = reinterpret_cast<const float4*>(tables[warp][tk & 1] + (STYLE == 1 ? 8 : 4) * sub);
       *reinterpret_cast<float4*>(c) = tab[0];
-      *reinterpret_cast<float4*>(c + 4) = tab[1];
+      *reinterpret_cast<float4*>(c + 4) = tab[NEXT];
       *reinterpret_cast<float4*>(s) = tab[D / 8];
-      *reinterpret_cast<float4*>(s + 4) = tab[D / 8 + 1];
+      *reinterpret_cast<float4*>(s + 4) = tab[D / 8 + NEXT];
     }
     for (int r0 = 0; r0 < rounds; r0 += U) {
 #pragma unroll
