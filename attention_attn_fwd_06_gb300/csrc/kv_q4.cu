@@ -8,9 +8,11 @@
 // What bounds both: HBM, once the arithmetic is short.  Writing takes 2 bytes in and 0.5625 out per element, reading
 // back the reverse.  A lane takes 16 dims (32 bytes of bf16, 8 bytes of codes) of one head's key and of its value, so four
 // lanes hold a group, its extremes take two shuffles and the row's place is looked up once for both; as many warps as fit.
-// 70k tokens of 8 heads at D = 128 take 67 us to write (5.5 TB/s) and 72 us to read back (a plain fill of as many bytes
-// takes 75 us); a key's or a value's dims a lane: 89 us to write; a warp for each token and two rounds of its heads in flight
-// (with the slower codes of that day): 113 and 79 us; one wave of warps that walk runs of tokens: 124 and 111 us.
+// 70k tokens of 8 heads at D = 128 take 64 us to write (5.8 TB/s) and 60 us to read back (6.2 TB/s).  Each lane's 32 bytes are
+// one access where rows start on 32 bytes: as two of 16, each store fills half a sector, and reading back takes 73 us (a fill
+// of 290 MB that way 76 against 42 us), writing 67.  A key's or a value's dims a lane: 89 us to write; a warp for each token
+// and two rounds of its heads in flight (with the slower codes of that day): 113 and 79 us; one wave of warps that walk runs of
+// tokens: 124 and 111 us; warps of four tokens of one head: 65.7 and 59.4 us.
 //
 // Writing: extremes by packed bf16 min and max that pass NaN on; quotients correctly rounded, by a product with the
 // rounded reciprocal and its residual's share (Markstein's theorem), so that a tie between two codes is seen as one; their

@@ -303,6 +303,32 @@ def test_gather_reads_the_oracle_values(B, Hkv, D, page, hi):
         assert torch.equal(out.cpu()[:int(cu[-1])], ref) and (out[int(cu[-1]):] == 7).all()
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_rows_that_start_on_16_bytes(D):
+    """The same bytes whether rows start on 32 bytes or only on 16: by their base, by a stride, and on the way back."""
+    T, Hkv, page = 45, 3, 16
+    x = dev(torch.randn(2, T, Hkv, D, generator=torch.Generator().manual_seed(D)).to(torch.bfloat16))
+    slots, table, cu = i32(range(T)), i32(range(3))[None], i32([0, T])
+
+    def shifted(rows=None):
+        t = torch.empty(T * Hkv * D + 8, dtype=torch.bfloat16, device=DEV)[8:].view(T, Hkv, D)
+        return t if rows is None else t.copy_(rows)
+
+    def strided(rows):
+        return torch.empty(T, Hkv, D + 8, dtype=torch.bfloat16, device=DEV)[..., :D].copy_(rows)
+
+    pools = []
+    for k, v in ((x[0], x[1]), (shifted(x[0]), x[1]), (x[0], shifted(x[1])), (strided(x[0]), x[1]), (x[0], strided(x[1]))):
+        pools.append(AB.attn_kv_q4_pool(3, Hkv, page, D, DEV))
+        AB.attn_kv_append_q4(k, v, pools[-1], slots)
+    assert all(torch.equal(p, pools[0]) for p in pools)
+    want = AB.attn_kv_gather_q4(pools[0], table, cu, T)
+    for k, v in ((shifted(), None), (None, shifted())):
+        got = AB.attn_kv_gather_q4(pools[0], table, cu, T, k_out=k, v_out=v)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert AB.attn_get_device_status() == AB.ATTN_OK
+
+
 def test_gather_out_of_range_rows_are_flagged_and_left():
     pool = dev(make_pool(3, 1, 16, 64, 2))
     for table, start in (([[0, 7]], 0), ([[0, -1]], 0), ([[0, 1]], 20), ([[0, 1]], -3)):
