@@ -24,7 +24,10 @@
 //    rows each has two of the eight columns and a lane keeps one: half the softmax work of four columns left empty.
 //  * Weights are p s_v 2^x rounded to fp16 (2^-12 relative, against 2^-9 of a bf16 output), x kept such that they stay
 //    below 2^15 and the largest near 2^12; a call with fp32 output carries them as two fp16 terms.  Maxima, sums,
-//    the term in m_v and all accumulators are fp32.
+//    the term in m_v and all accumulators are fp32.  The matrix unit truncates as it adds to an accumulator, one add for 16
+//    keys: over a slice of 131,072 keys, 2048 adds a warp, that biases O by some 2^-13 of its terms' sum, below the 2^-11
+//    that a weight's rounding is off by at most.  With fp32 output each tile's products start from zero and are added with
+//    rounding (131k keys 71.1 against 66.3 us, 8 x 4096 14.3 against 13.9 us; 32 query rows over 131k 317 against 300 us).
 // At long contexts the instructions bound it: some 270 a tile of 16 keys at D = 128, 40 of them masks and shifts for K,
 // 48 with the byte permutes for V, at two clocks each (dropping either product's unpacking and matrix products reaches the
 // 60 us that the copies alone take of the 64); over short ones the chain of a launch: lengths, split, block table and first
@@ -676,11 +679,17 @@ __global__ void __launch_bounds__(Q4Cfg<D, R4>::THREADS, Q4Cfg<D, R4>::MINB)
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              mma_16816(o[4 * gg + mt][nt], a & kLowNibble, a & kHighNibble, b & kLowNibble, b & kHighNibble, b0[nt],
-                        b1[nt]);
-              if constexpr (WIDE && NC == 2)
-                mma_16816(o[4 * gg + mt][nt], a & kLowNibble, a & kHighNibble, b & kLowNibble, b & kHighNibble, c0[nt],
-                          c1[nt]);
+              float(&oo)[4] = o[4 * gg + mt][nt];
+              if constexpr (WIDE) {  // a tile's products apart, then rounded adds (the matrix unit's own adds truncate)
+                float part[4] = {0.f, 0.f, 0.f, 0.f};
+                mma_16816(part, a & kLowNibble, a & kHighNibble, b & kLowNibble, b & kHighNibble, b0[nt], b1[nt]);
+                if constexpr (NC == 2)
+                  mma_16816(part, a & kLowNibble, a & kHighNibble, b & kLowNibble, b & kHighNibble, c0[nt], c1[nt]);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) oo[c] += part[c];
+              } else {
+                mma_16816(oo, a & kLowNibble, a & kHighNibble, b & kLowNibble, b & kHighNibble, b0[nt], b1[nt]);
+              }
             }
           }
         }

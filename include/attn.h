@@ -519,8 +519,9 @@ int attn_kv_gather_q4(const attn_kv_gather_q4_params* p);
  *                Calls that can overlap, and graphs that can be replayed at once, each take
  *                a buffer of their own.  After ATTN_ERR_DEVICE_TIMEOUT the caller zeroes it
  *                again.
- * (Hq / Hkv) * Lq at most 128.  Weights are rounded to fp16 before the second product;
- * with out_dtype = ATTN_DTYPE_F32 they are carried in two fp16 terms.
+ * (Hq / Hkv) * Lq at most 128.  Weights are rounded to fp16 before the second product,
+ * whose sums are fp32 with truncated adds; with out_dtype = ATTN_DTYPE_F32 they are carried
+ * in two fp16 terms and the adds are rounded.
  */
 typedef struct attn_decode_q4_params {
   const void* q;

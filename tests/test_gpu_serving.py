@@ -429,6 +429,39 @@ def test_decode_q4_values_of_unlike_sizes():
             assert_within(ls[:, :, None], lse, bL)
 
 
+def check_first_key_leads(n, D, Hq, scales, types, odd_key=None, odd_scale=None):
+    """A row in one slice whose first key's weight is 2^21 times the others', V's scales drawn from an interval; one other
+    key may have a scale of its own, and a logit 60 below the rest if that scale is large."""
+    g, page = np.random.default_rng(n), 64
+    num = n // page
+    pool = make_pool(num, 1, page, D, 3)
+    pairs = np.empty((num, 1, page // 16, 2, 16, D // 64, 2), np.float16)
+    k, v = np.moveaxis(pairs, 3, 0)  # [page, head, tile, key, group, (scale, minimum)]
+    k[...] = 0
+    k[0, 0, 0, 0, :, 1] = 21 * np.log(2) / D
+    v[..., 0] = g.uniform(*scales, v.shape[:-1])
+    if odd_key is not None:
+        at = (odd_key // page, 0, odd_key % page // 16, odd_key % 16)
+        v[at][0, 0] = odd_scale
+        if odd_scale > 100:
+            k[at][:, 1] = -60 / D
+    v[..., 1] = -7.5 * v[..., 0]
+    pool[..., 16 * D:] = pairs.reshape(num, 1, page // 16, -1).view(np.uint8)
+    table = np.arange(num, dtype=np.int32)[None]
+    q = torch.ones(1, Hq, 1, D, dtype=torch.bfloat16)
+    for out_dtype in types:
+        O, lse, bO, bL = decode_bound(q, pool, table, [n], 1.0, out_dtype == torch.float32)
+        out, ls = run_decode(q[:, :, 0].contiguous(), pool, table, [n], 1.0, chunk=1 << 20, out_dtype=out_dtype)
+        assert_within(out[:, :, None], O, bO, f"O {out_dtype}")
+        assert_within(ls[:, :, None], lse, bL, f"lse {out_dtype}")
+
+
+@pytest.mark.parametrize("D,Hq", [(64, 1), (64, 8), (128, 1), (128, 8), (128, 16)])
+def test_decode_q4_long_slices_in_fp32(D, Hq):
+    """131072 keys added to one accumulator: terms 2^-23 of the first one's size each, thousands of sums."""
+    check_first_key_leads(131072, D, Hq, (0.2, 0.6), [torch.float32])
+
+
 @pytest.mark.parametrize("B,Hq,Hkv", [(40, 16, 4), (400, 4, 2), (1100, 2, 1)])
 def test_decode_q4_many_sequences(B, Hq, Hkv):
     g = np.random.default_rng(B)
