@@ -22,8 +22,12 @@
 //  * Scores come as S^T (keys by query rows), so a row's maximum is two registers and three shuffles for 32 keys,
 //    and the weights turn into the second product's B operand by two 8x8 transposes (movmatrix).  With up to four query
 //    rows each has two of the eight columns and a lane keeps one: half the softmax work of four columns left empty.
-//  * Weights are p s_v 2^x rounded to fp16 (2^-12 relative, against 2^-9 of a bf16 output), x kept such that they stay
-//    below 2^15 and the largest near 2^12; a call with fp32 output carries them as two fp16 terms.  Maxima, sums,
+//  * Weights are p s_v 2^x rounded to fp16, each off by at most 2^-11 of itself: 2^-11 of the sum of |p s u| for O, in which
+//    these terms and the p m cancel, against the output's own rounding, 2^-8 of what is left.  Each warp chooses x by the
+//    largest scale s of the keys of a step (32, or 48 at D = 64): a weight stays below 2^15, and that scale times 2^x at 2^9 or
+//    above, so that what falls below fp16's normal range is off by 2^-34 of that scale at most.  (Scales or-ed together in
+//    place of their maximum gave x up to 14 too low, and 68.9 us over 131k keys with scales on both sides of 2, now 64.0.)
+//    A call with fp32 output carries weights as two fp16 terms.  Maxima, sums,
 //    the term in m_v and all accumulators are fp32.  The matrix unit truncates as it adds to an accumulator, one add for 16
 //    keys: over a slice of 131,072 keys, 2048 adds a warp, that biases O by some 2^-13 of its terms' sum, below the 2^-11
 //    that a weight's rounding is off by at most.  With fp32 output each tile's products start from zero and are added with
@@ -137,9 +141,9 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-__device__ __forceinline__ float2 half2_floats(uint32_t w) {
-  return __half22float2(*reinterpret_cast<const __half2*>(&w));
-}
+__device__ __forceinline__ __half2 as_half2(uint32_t w) { return *reinterpret_cast<const __half2*>(&w); }
+__device__ __forceinline__ uint32_t half2_word(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
+__device__ __forceinline__ float2 half2_floats(uint32_t w) { return __half22float2(as_half2(w)); }
 
 constexpr uint32_t kLowNibble = 0x000f000fu, kHighNibble = 0x00f000f0u;
 
@@ -464,13 +468,15 @@ __global__ void __launch_bounds__(Q4Cfg<D, R4>::THREADS, Q4Cfg<D, R4>::MINB)
     float m[NT][NC], l[NT][NC];
     // Weights, their sums l and z, and O all carry the factor 2^wexp (2^30 until the first scales are seen).
     float wexp = 30.f;
-    uint32_t wlimit;         // the largest scale, as fp16 bits, that wexp allows: 2^(15 - wexp) or less
+    uint32_t wlimit, wlow;   // as fp16 bits: the largest scale that wexp allows, 2^(15 - wexp) or less, and the least
+                             // largest scale of a step that it serves, 2^(9 - wexp) (weights below 2^9 in it rise again)
     float sub[NT][NC];       // wexp - max of a row
-    auto set_wlimit = [&]() {
-      const __half h = __float2half_rz(ex2_approx(15.f - wexp) * 0.9990234375f);
-      wlimit = *reinterpret_cast<const uint16_t*>(&h);
+    auto set_wlimits = [&]() {
+      const __half hi = __float2half_rz(ex2_approx(15.f - wexp) * 0.9990234375f), lo = __float2half_rz(ex2_approx(9.f - wexp));
+      wlimit = *reinterpret_cast<const uint16_t*>(&hi);
+      wlow = *reinterpret_cast<const uint16_t*>(&lo);
     };
-    set_wlimit();
+    set_wlimits();
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -544,10 +550,9 @@ __global__ void __launch_bounds__(Q4Cfg<D, R4>::THREADS, Q4Cfg<D, R4>::MINB)
             }
         }
       }
-      // V's pairs (those of keys past the sequence's end are no data).  All scales or-ed together lie above the largest
-      // (by less than a factor of 2 unless the or-ed exponents make infinity or NaN, which count as 65504).
+      // V's pairs (those of keys past the sequence's end are no data), and the lane's largest scale (the low halves).
       uint32_t va[N][G], vb[N][G];
-      uint32_t all = 0;
+      __half2 tops = __halves2half2(__half(0.f), __half(0.f));
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         load_pairs(tp + i * C::TILE + kv_q4_vp_off(D), va[i], vb[i]);
@@ -558,12 +563,14 @@ __global__ void __launch_bounds__(Q4Cfg<D, R4>::THREADS, Q4Cfg<D, R4>::MINB)
             if (k >= len) va[i][gg] = 0;
             if (k + 8 >= len) vb[i][gg] = 0;
           }
-          all |= va[i][gg] | vb[i][gg];
+          tops = __hmax2(tops, __hmax2(__habs2(as_half2(va[i][gg])), __habs2(as_half2(vb[i][gg]))));
         }
       }
+      uint32_t top = half2_word(tops) & 0x7fffu;  // (as fp16 bits, which order as the scales do)
       // row maxima (of x, or at an edge of the masked logits f x)
       float mx[NT][NC];
-      bool change = (all & 0x7fffu) > wlimit;
+      const bool low = !__any_sync(0xffffffffu, top >= wlow);  // (the vote is every lane's, so apart from the next line)
+      bool change = low | (top > wlimit);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -583,17 +590,15 @@ __global__ void __launch_bounds__(Q4Cfg<D, R4>::THREADS, Q4Cfg<D, R4>::MINB)
           mx[nt][c] = EDGE ? v : v * f[nt][c];
           change |= mx[nt][c] > m[nt][c];
         }
-      // A maximum rises, or the weights' factor has to fall (then its bound is met for a long time): rescale what is there.
+      // A maximum rises, or the weights' factor has to fall or may rise: rescale what is there.
       if (__any_sync(0xffffffffu, change)) {
-        uint32_t top = all & 0x7fffu;
-#pragma unroll
-        for (int mask = 1; mask < 32; mask <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, mask));
+        top = __reduce_max_sync(0xffffffffu, top);
         float ratio = 1.f;
-        if (top > wlimit) {  // 2^wexp times the largest scale (below 2^16) is to lie in [2^11, 2^13)
+        if (top > wlimit || (top < wlow && top > 0)) {  // 2^wexp times the largest scale (below 2^16): into [2^12, 2^13)
           const float we = (float)(12 - ((int)(__float_as_uint(fminf(half2_floats(top).x, 65504.f)) >> 23) - 127));
           ratio = ex2_approx(we - wexp);
           wexp = we;
-          set_wlimit();
+          set_wlimits();
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)

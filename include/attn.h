@@ -522,6 +522,9 @@ int attn_kv_gather_q4(const attn_kv_gather_q4_params* p);
  * (Hq / Hkv) * Lq at most 128.  Weights are rounded to fp16 before the second product,
  * whose sums are fp32 with truncated adds; with out_dtype = ATTN_DTYPE_F32 they are carried
  * in two fp16 terms and the adds are rounded.
+ * A weight is its softmax numerator times V's scale; it is off by 2^-11 (2^-22) of itself,
+ * or by 2^-34 of the largest scale among the keys it is taken with (up to 48 neighbours,
+ * both groups of 64 dims), whichever is more.
  */
 typedef struct attn_decode_q4_params {
   const void* q;

@@ -462,6 +462,18 @@ def test_decode_q4_long_slices_in_fp32(D, Hq):
     check_first_key_leads(131072, D, Hq, (0.2, 0.6), [torch.float32])
 
 
+@pytest.mark.parametrize("n,odd_key,odd_scale,scales", [
+    (131072, 0, 2.5, (0.2, 0.6)),        # one scale a few times the others'
+    (16384, 8000, 2.5, (0.2, 0.6)),
+    (16384, None, None, (1.5, 2.5)),     # scales on both sides of a power of two
+    (131072, 500, 8000.0, (2e-4, 4e-4)),   # a scale far above all others, of a key that hardly counts
+    (16384, 9001, 8000.0, (2e-4, 4e-4)),
+])
+@pytest.mark.parametrize("D,Hq", [(64, 1), (128, 8)])
+def test_decode_q4_scales_of_v_that_differ(n, odd_key, odd_scale, scales, D, Hq):
+    check_first_key_leads(n, D, Hq, scales, [torch.bfloat16, torch.float32], odd_key, odd_scale)
+
+
 @pytest.mark.parametrize("B,Hq,Hkv", [(40, 16, 4), (400, 4, 2), (1100, 2, 1)])
 def test_decode_q4_many_sequences(B, Hq, Hkv):
     g = np.random.default_rng(B)
