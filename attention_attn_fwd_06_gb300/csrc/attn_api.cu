@@ -939,9 +939,11 @@ int attn_get_device_status(void* stream) {
   const unsigned zero = 0;
   if (cudaMemcpy(s->status, &zero, sizeof(zero), cudaMemcpyHostToDevice) != cudaSuccess) return ATTN_ERR_CUDA;
   if (v == ATTN_ERR_DEVICE_TIMEOUT) {
-    // A decode that gave up part-way may have left its work counters armed, or partials unread: clear them.
+    // A decode that gave up part-way may have left its work counters armed, or partials unread: clear them, with no
+    // decode of another stream on the device.
     int dev = -1;
     cudaGetDevice(&dev);
+    cudaDeviceSynchronize();
     if (s->ws != nullptr) cudaMemset(s->ws, 0, kCounterBytes);
     if (s->ws_q4 != nullptr) cudaMemset(s->ws_q4, 0, s->ws_q4_bytes);
     if (dev >= 0 && dev < kMaxDevices && g_noalloc_ptr[dev] != nullptr) cudaMemset(g_noalloc_ptr[dev], 0, kCounterBytes);

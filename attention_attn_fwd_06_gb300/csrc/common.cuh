@@ -27,9 +27,13 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
   return t;
 }
 
-// First error wins; later ones are dropped (the host reads one code).
+// The host reads one code: the first error, but a timeout replaces any other, since workspaces are to be zeroed after it.
 __device__ __forceinline__ void record_status(unsigned* status, unsigned code) {
-  if (status != nullptr) atomicCAS(status, 0u, code);
+  if (status == nullptr) return;
+  if (code == ATTN_ERR_DEVICE_TIMEOUT)
+    atomicExch(status, code);
+  else
+    atomicCAS(status, 0u, code);
 }
 
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {

@@ -552,7 +552,12 @@ unsigned long long attn_decode_q4_workspace_bytes(int Hq, int Hkv, int Lq, int D
 /*
  * attn_get_device_status -- synchronises `stream`, then returns and clears the
  * current device's status word (ATTN_OK if no kernel flagged a problem since
- * the last read).  Returns ATTN_ERR_CUDA if the synchronisation fails.
+ * the last read).  Of several problems it holds the first, but
+ * ATTN_ERR_DEVICE_TIMEOUT takes the place of any other: a decode that gave up may
+ * leave partial results in its workspace, so the outputs of every call since the
+ * last read are to be taken as wrong.  Reading it synchronises the device and
+ * zeroes the library's workspaces; a caller's own are the caller's to zero.
+ * Returns ATTN_ERR_CUDA if the synchronisation fails.
  */
 int attn_get_device_status(void* stream);
 

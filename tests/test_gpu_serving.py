@@ -535,6 +535,25 @@ def test_decode_q4_timeout_is_reported_and_the_next_call_is_right(monkeypatch):
     assert torch.equal(a[0], b[0])
 
 
+@pytest.mark.parametrize("first", [AB.ATTN_ERR_DEVICE_POOL, AB.ATTN_ERR_DEVICE_BOUNDS])
+def test_a_timeout_is_told_whatever_was_recorded_before(monkeypatch, first):
+    # An unread status of another kind, a decode that gives up over rows split between CTAs, and one that follows.
+    pool, (table, _) = make_pool(1000, 1, 16, 128, 4), make_table([16000], 16, 1000, 5)
+    args = (torch.randn(1, 4, 128, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16), pool, table, [16000], 0.09)
+    a = run_decode(*args, chunk=1 << 12)
+    d_args = dev(args[0]), dev(pool), dev(table), i32([16000])
+    new = i32([1 if first == AB.ATTN_ERR_DEVICE_POOL else -1])
+    AB.attn_page_step(i32([0]), i32([-1])[None], i32([0]), i32([0]), 16, new_lens=new)
+    monkeypatch.setenv("ATTN_FAULT_INJECT", "skip_arrive")
+    AB.attn_decode_q4(*d_args, scale=0.09, chunk=1 << 12)
+    monkeypatch.delenv("ATTN_FAULT_INJECT")
+    AB.attn_page_step(i32([0]), i32([-1])[None], i32([0]), i32([0]), 16, new_lens=new)
+    assert AB.attn_get_device_status() == AB.ATTN_ERR_DEVICE_TIMEOUT
+    for _ in range(2):
+        b = run_decode(*args, chunk=1 << 12)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 def test_cache_calls_refuse_what_they_would_misread():
     pool = dev(make_pool(4, 2, 16, 64, 4))
     q, table, lens = dev(torch.randn(1, 4, 64).to(torch.bfloat16)), i32([0, 1])[None], i32([20])
