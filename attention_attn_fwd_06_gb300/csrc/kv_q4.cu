@@ -8,9 +8,9 @@
 // What bounds both: HBM, once the arithmetic is short.  Writing takes 2 bytes in and 0.5625 out per element, reading
 // back the reverse.  A lane takes 16 dims (32 bytes of bf16, 8 bytes of codes) of one head's key and of its value, so four
 // lanes hold a group, its extremes take two shuffles and the row's place is looked up once for both; as many warps as fit.
-// 70k tokens of 8 heads at D = 128 take 64 us to write (5.8 TB/s) and 60 us to read back (6.2 TB/s).  Each lane's 32 bytes are
+// 70k tokens of 8 heads at D = 128 take 66 us to write (5.6 TB/s) and 60 us to read back (6.2 TB/s).  Each lane's 32 bytes are
 // one access where rows start on 32 bytes: as two of 16, each store fills half a sector, and reading back takes 73 us (a fill
-// of 290 MB that way 76 against 42 us), writing 67.  A key's or a value's dims a lane: 89 us to write; a warp for each token
+// of 290 MB that way 76 against 42 us), writing 67 against 64 that day.  A key's or a value's dims a lane: 89 us to write; a warp for each token
 // and two rounds of its heads in flight (with the slower codes of that day): 113 and 79 us; one wave of warps that walk runs of
 // tokens: 124 and 111 us; warps of four tokens of one head: 65.7 and 59.4 us.
 //
@@ -48,10 +48,12 @@ __device__ __noinline__ uint2 quantise_slow(uint4 w0, uint4 w1, float s, float m
   for (int j = 0; j < 16; ++j) {
     const float v = x[j] == x[j] ? fminf(fmaxf(x[j], -kF16Max), kF16Max) : 0.f;
     const float t = v - m;
+    const float b = t - v, rest = (v - (t - b)) + (-m - b);  // v - m = t + rest exactly (Knuth's two-sum)
     const float k = fminf(fmaxf(floorf(t / s), 0.f), 14.f);
-    const float e = fmaf(-(k + 0.5f), s, t);  // its sign is exact
-    const int ki = (int)k;
-    out[j / 8] |= (unsigned)(ki + ((e > 0.f || (e == 0.f && (ki & 1))) ? 1 : 0)) << (4 * (j % 8));
+    const float e = fmaf(-(k + 0.5f), s, t);  // above or below the border (16 bits, so t is not rounded across it), or on it:
+    const int ki = (int)k;                    // then the rest decides, and where there is none the tie goes to the even code
+    const bool up = e > 0.f || (e == 0.f && (rest > 0.f || (rest == 0.f && (ki & 1))));
+    out[j / 8] |= (unsigned)(ki + (up ? 1 : 0)) << (4 * (j % 8));
   }
   return make_uint2(out[0], out[1]);
 }
@@ -116,6 +118,19 @@ __device__ __forceinline__ Quantised quantise(uint4 wa, uint4 wb, unsigned team)
   // all quotients lie between those of lo and hi (infinite or NaN where s is 0)
   odd |= !((lo - m) * inv > -0.25f) || !((hi - m) * inv < 15.25f);
   constexpr float kMagic = 12582912.f;  // 1.5 2^23: adding it rounds to an integer, ties to even
+  // x - m is rounded where |x| is below 2^-16 or |m| below 2^-12 of it, and may then seem to lie on a border (k + 0.5) s that
+  // it only comes near: with a small x if -m / s is within 2^-12 of k + 0.5, with a small m if that is below 2^-8 s.  m / s in
+  // units of 2^-10, as the low bits of a sum, tells both; only then (a group in 1000) are the dims looked through.  (All such
+  // groups decided code by code: 78 us; the question not asked: 64.3 us, not 65.7.)
+  constexpr uint32_t kZero = 0x46400000u;  // 1.5 2^13
+  const uint32_t z = __float_as_uint(fmaf(m, inv, __uint_as_float(kZero)));
+  if ((z & 0x3ffu) == 0x200u || z - kZero + 4u <= 8u) {
+    odd |= m != 0.f && z - kZero + 4u <= 8u;
+    const uint32_t small = __float_as_uint(fabsf(m) * 0x1p-15f) >> 16;  // as bf16 bits
+#pragma unroll
+    for (int j = 0; j < 8; ++j)  // 0 itself is exact
+      odd |= (q[j] & 0x7fffu) - 1u < small || (q[j] >> 16 & 0x7fffu) - 1u < small;
+  }
   const float2 m2 = make_float2(-m, -m), i2 = make_float2(inv, inv), s2 = make_float2(-s, -s);
   const float2 up = make_float2(kMagic, kMagic);
   uint32_t c[2] = {0, 0};

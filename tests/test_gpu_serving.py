@@ -6,6 +6,7 @@ in roundings (tests/_serving.py, and beside each test)."""
 import pathlib
 import subprocess
 import sys
+from fractions import Fraction
 
 import numpy as np
 import pytest
@@ -272,6 +273,41 @@ def test_append_ties_and_borders_match_exact_decisions():
         AB.attn_kv_append_q4(dev(kk), dev(kk), got, i32(range(4)))
         oracle.write_q4(pool, kk, kk, range(4))
         assert np.array_equal(got.cpu().numpy(), pool)
+
+
+def test_append_values_a_hair_beside_a_border():
+    """x - minimum is a border between two codes but for a part too small for fp32: by the definition that part decides.
+    Expected codes by rational arithmetic."""
+    rows = []
+    for s, k in ((1.0, 0), (1.0, 1), (2.0 ** -3, 6), (2.0 ** -3, 7), (3.0, 10), (0.34375, 13), (2.0 ** -5, 14)):
+        border = (k + 0.5) * s
+        x = torch.zeros(64, dtype=torch.float64)  # small values over a minimum of minus the border, 0 among them
+        x[0], x[1] = -border, 15 * s - border
+        x[2:34] = 2.0 ** -torch.arange(18, 50, dtype=torch.float64) * border
+        x[34:60] = -(2.0 ** -torch.arange(18, 122, 4, dtype=torch.float64)) * border
+        x[60] = 2.0 ** -126
+        rows.append(x)
+        for m in (2.0 ** -24, -(2.0 ** -24), 3 * 2.0 ** -20, -(2.0 ** -14), -(2.0 ** -9)):
+            x = torch.full((64,), border, dtype=torch.float64)  # the border over a small minimum
+            x[0], x[1], x[2] = m, 15 * s, border * (1 + 2.0 ** -7)
+            rows.append(x)
+    k = torch.stack(rows)[:, None].to(torch.bfloat16)
+    T = k.shape[0]
+    assert T <= 48
+    pool = AB.attn_kv_q4_pool(3, 1, 16, 64, DEV)
+    AB.attn_kv_append_q4(dev(k), dev(k), pool, i32(range(T)))
+    assert AB.attn_get_device_status() == AB.ATTN_OK
+    _, s, m = oracle.quantise_q4(k)
+    got, seen = pool.cpu().numpy(), 0
+    for t in range(T):
+        scale, least = Fraction(float(s[t, 0, 0])), Fraction(float(m[t, 0, 0]))
+        want = [min(15, max(0, round((Fraction(float(x)) - least) / scale))) for x in k[t, 0].double()]  # ties to even
+        seen += sum(u != min(15, max(0, round(float(np.float32(x) - np.float32(least)) / float(scale))))
+                    for u, x in zip(want, k[t, 0].float().numpy()))
+        for codes, pairs in oracle.serving.tile_parts(got[t // 16, 0, 0], 64):
+            u = np.stack([codes[0, t % 16] & 15, codes[0, t % 16] >> 4], -1).reshape(-1)
+            assert pairs[t % 16, 0].tolist() == [float(scale), float(least)] and u.tolist() == want, t
+    assert seen > 100  # values that fp32's difference would put on the border
 
 
 def test_append_slots_out_of_the_pool_are_flagged():
