@@ -63,7 +63,8 @@ __global__ void __launch_bounds__(kPageThreads) page_step_kernel(const PageStepL
   const long long cap = (long long)p.max_pages * ps;  // below 2^31
   const int per = (B + threads - 1) / threads;
   const int b0 = min(tid * per, B), b1 = min(b0 + per, B);
-  int s0 = 0, s1 = 0, s2 = 0;            // the thread's tokens (modulo 2^32), pages taken, pages given back
+  unsigned s0 = 0;                       // the thread's tokens (modulo 2^32)
+  int s1 = 0, s2 = 0;                    // pages taken, pages given back
   unsigned n_low = 0, n_high = 0;        // tokens again, in halves that cannot overflow
   int bad = 0;
   for (int b = b0; b < b1; ++b) {
@@ -76,17 +77,18 @@ __global__ void __launch_bounds__(kPageThreads) page_step_kernel(const PageStepL
     kept[b] = c;
     have[b] = h;
     need[b] = d;
-    s0 += ok ? n : 0;
+    s0 += ok ? (unsigned)n : 0u;
     n_low += ok ? n & 0xffff : 0;
     n_high += ok ? n >> 16 : 0;
     s1 += max(d - h, 0);
     s2 += max(h - d, 0);
   }
-  int i0 = s0, i1 = s1, i2 = s2;
+  unsigned i0 = s0;
+  int i1 = s1, i2 = s2;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
-    const int t0 = __shfl_up_sync(0xffffffffu, i0, off), t1 = __shfl_up_sync(0xffffffffu, i1, off),
-              t2 = __shfl_up_sync(0xffffffffu, i2, off);
+    const unsigned t0 = __shfl_up_sync(0xffffffffu, i0, off);
+    const int t1 = __shfl_up_sync(0xffffffffu, i1, off), t2 = __shfl_up_sync(0xffffffffu, i2, off);
     if (lane >= off) {
       i0 += t0;
       i1 += t1;
@@ -111,7 +113,7 @@ __global__ void __launch_bounds__(kPageThreads) page_step_kernel(const PageStepL
   const int ntaken = (int)__reduce_add_sync(0xffffffffu, (unsigned)ws[2]);
   const int ngiven = (int)__reduce_add_sync(0xffffffffu, (unsigned)ws[3]);
   const bool before = lane < warp;
-  int e0 = (int)__reduce_add_sync(0xffffffffu, before ? ((unsigned)ws[1] << 16) + (unsigned)ws[0] : 0u) + i0 - s0;
+  unsigned e0 = __reduce_add_sync(0xffffffffu, before ? ((unsigned)ws[1] << 16) + (unsigned)ws[0] : 0u) + i0 - s0;
   int e1 = (int)__reduce_add_sync(0xffffffffu, before ? (unsigned)ws[2] : 0u) + i1 - s1;
   int e2 = (int)__reduce_add_sync(0xffffffffu, before ? (unsigned)ws[3] : 0u) + i2 - s2;
   const bool listed = p.slots != nullptr || p.positions != nullptr;
@@ -120,10 +122,10 @@ __global__ void __launch_bounds__(kPageThreads) page_step_kernel(const PageStepL
   const bool refused = wrong || count + ngiven < ntaken;
   if (!refused) {
     for (int b = b0; b < b1; ++b) {  // the row's sums again, from what it kept
-      cu[b] = e0;
+      cu[b] = (int)e0;  // (below 2^31 now, as the total is)
       taken[b] = e1;
       given[b] = e2;
-      e0 += p.new_lens != nullptr ? p.new_lens[b] : 0;
+      e0 += p.new_lens != nullptr ? (unsigned)p.new_lens[b] : 0u;
       e1 += max(need[b] - have[b], 0);
       e2 += max(have[b] - need[b], 0);
     }

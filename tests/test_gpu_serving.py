@@ -109,6 +109,17 @@ def test_page_step_refusals_leave_everything():
     assert AB.attn_get_device_status() == AB.ATTN_ERR_DEVICE_BOUNDS and slots.tolist() == [-1, -1]
 
 
+@pytest.mark.parametrize("rows", [[2 ** 30 - 1] * 8, [2 ** 30 - 1, 2 ** 30 - 1, 2], [2 ** 30] * 4, [0, 2 ** 30 - 1, 0, 2 ** 30 - 1] * 9])
+def test_page_step_token_sums_past_32_bits_are_refused(rows):
+    # every row's length is allowed, the sum is 2^31 or more (of two, four and more rows: 0 modulo 2^32 among them)
+    B, pages = len(rows), 1 << 20
+    lens, table, new = i32([0] * B), torch.full((B, pages), -1, dtype=torch.int32, device=DEV), i32(rows)
+    free, count, cu = i32(range(64)), i32([64]), i32([7] * (B + 1))
+    AB.attn_page_step(lens, table, free, count, 1024, new_lens=new, cu_new=cu)
+    assert AB.attn_get_device_status() == AB.ATTN_ERR_DEVICE_BOUNDS
+    assert lens.tolist() == [0] * B and count.item() == 64 and cu.tolist() == [0] * (B + 1) and (table == -1).all()
+
+
 def test_page_step_bad_page_ids_are_flagged():
     P = Pages(1, 16, 4, 4, seed=2)
     P.step(new=[20])
