@@ -253,16 +253,18 @@ bool strides8(const long long* s, int n) {
 bool aligned128(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 127u) == 0; }
 
 struct DecodeQ4Shape {
+  size_t count_bytes = 0;
   size_t part_o_elems = 0;
   size_t bytes = 0;
 };
 
-// The partials of any variant: sums, and for each of a CTA's warps that hold one every column's (max, sum).
+// The counts and partials of any variant: sums, and for each of a CTA's warps that hold one every column's (max, sum).
 DecodeQ4Shape decode_q4_shape(int D, int num_sms) {
   DecodeQ4Shape s;
   const size_t cols = attn::decode_q4_partials(num_sms);
+  s.count_bytes = (attn::decode_q4_counts(num_sms) * sizeof(unsigned) + 127) / 128 * 128;
   s.part_o_elems = cols * D;
-  s.bytes = cols * (D + attn::kDecodeQ4Owners * 2) * sizeof(float);
+  s.bytes = s.count_bytes + cols * (D + attn::kDecodeQ4Owners * 2) * sizeof(float);
   return s;
 }
 
@@ -905,7 +907,8 @@ int attn_decode_q4(const attn_decode_q4_params* p) {
   L.kv_lens = p->kv_lens;
   L.out = p->out;
   L.lse = p->lse;
-  L.part_o = reinterpret_cast<float*>(ws);
+  L.counts = reinterpret_cast<unsigned*>(ws);
+  L.part_o = reinterpret_cast<float*>(ws + sh.count_bytes);
   L.part_ml = L.part_o + sh.part_o_elems;
   L.B = p->B;
   L.Hq = p->Hq;

@@ -36,20 +36,21 @@
 // 48 with the byte permutes for V, at two clocks each (dropping either product's unpacking and matrix products reaches the
 // 60 us that the copies alone take of the 64); over short ones the chain of a launch: lengths, split, block table and first
 // copies (1.6 us), first data (4 us), a row's stages at 0.6 us each, exchange and merge (2 to 3 us).
-// Measured (CUDA-graph replays over rotating pools, 32 query and 8 kv heads, D = 128): 4 sequences of 32k to 131k keys 63.6 us
-// (5.7 TB/s, 0.84 of the copy bandwidth), 8 of 512 to 4096 keys 13.6 us, one of 4096 keys 11.5 us; 64 of up to 700 keys with
-// 16 heads of D = 64 16.0 us; 8 tokens each over 8 x 4096 keys 29.6 us.  Two CTAs of seven consumer warps an SM: 70.3 /
+// Measured (CUDA-graph replays over rotating pools, 32 query and 8 kv heads, D = 128): 4 sequences of 32k to 131k keys 64.3 us
+// (5.6 TB/s, 0.83 of the copy bandwidth), 8 of 512 to 4096 keys 13.9 us, one of 4096 keys 11.4 us; 64 of up to 700 keys with
+// 16 heads of D = 64 16.7 us; 8 tokens each over 8 x 4096 keys 30.2 us.  Two CTAs of seven consumer warps an SM: 70.3 /
 // 15.0 / - / 22.0 us against 70.8 / 14.3 / - / 16.6 us that day; four tiles a warp and stage 70.5 / 16.7 / - / 19.1 us;
 // four CTAs at 96 registers 86 / 18.9 us (spills).  At D = 64 two, three, four tiles a warp and stage: 16 heads over 4 x 16k to
 // 64k keys 45.1, 37.9, 36.2 us, the 64 short sequences 16.0, 16.1, 18.3 us.
 // The split is decode.cu's: persistent CTAs take equal slices of the tiles of all (sequence, kv head, row chunk) rows, a
 // producer warp streams them with bulk copies (one copy per page and stage) into a shared-memory ring.  At a piece's
-// end each warp sums a quarter of the accumulators over the warps; a row split between CTAs is merged by the CTA that
-// holds its first piece, which reads the others' partials as they arrive.  CTAs start in order, and a CTA publishes
-// before it waits, so of all resident CTAs only the last one's row can wait for one that is not, and that one starts as soon
-// as any other ends; like every wait here this one gives up after a second.  (One count a row and a fence for it: 21.4
-// against 16.1 us over the 64 short sequences; one flag a warp, released and acquired: 17.0 us, 16.0 against 14.4 us over
-// the 8: a release waits 2 to 4 us for its stores while the cache streams.)
+// end each warp sums a quarter of the accumulators over the warps; the pieces of a row split between CTAs are published and
+// counted, and who counts the last one merges them, so no CTA depends on another that may not have started.  (One count and
+// a fence for it: 21.4 against 16.1 us over the 64 short sequences; one flag a warp, released and acquired: 17.0 us, 16.0
+// against 14.4 us over the 8: a release waits 2 to 4 us for its stores while the cache streams.  The CTA of the first piece
+// waiting for the others' words, with no counts: 63.9 / 13.4 / 11.2 / 15.8 / 29.6 us for the list above, but CUDA does not
+// promise that the CTAs it waits for start; tickets that make them run, slices dealt from the back: 70.3 / 14.1 / 14.1 / 16.9 /
+// 31.8 us, a cooperative launch: 68.1 / 13.4 / 14.4 / 16.3 / 30.8 us.)
 #include <cfloat>
 #include <algorithm>
 #include <cmath>
@@ -117,7 +118,7 @@ struct Q4PieceInfo {
   int tiles;   // and their number
   int len;     // keys of the sequence
   int np;      // CTAs holding a piece of this row (0: no keys, 1: whole row here)
-  int first;   // whether this CTA holds the row's first piece (and merges the others')
+  int c_lo;    // the first of them
 };
 
 __device__ __forceinline__ int clamp_len(int len, int Lmax) { return len < 0 ? 0 : (len > Lmax ? Lmax : len); }
@@ -259,7 +260,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, R4>::THREADS, Q4Cfg<D, R4>::MINB)
       const int hkv = hg / chunks;
       const int n = te - tb;
       const int nst = n > 0 ? (n + C::ST - 1) / C::ST : 1;
-      int np = 0, first = 0;
+      int np = 0, row_lo = 0;
       for (int u = 0; u < nst; ++u, ++t) {
         const int slot_r = t % C::NS;
         if (t >= C::NS && !wait_empty(slot_r)) return false;
@@ -289,7 +290,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, R4>::THREADS, Q4Cfg<D, R4>::MINB)
             }
           }
           np = c_hi - c_lo + 1;
-          first = c_lo == cta;
+          row_lo = c_lo;
         }
         if (lane == 0) {
           if (u == 0) {
@@ -300,7 +301,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, R4>::THREADS, Q4Cfg<D, R4>::MINB)
             pi.tiles = n;
             pi.len = seq_len(b);
             pi.np = np;
-            pi.first = first;
+            pi.c_lo = row_lo;
             info[slot_r] = pi;
           }
           mbar_arrive(&told[slot_r]);  // every stage, so that its phases run with the others'
@@ -859,10 +860,11 @@ __global__ void __launch_bounds__(Q4Cfg<D, R4>::THREADS, Q4Cfg<D, R4>::MINB)
       write_out();
       continue;
     }
-    // A row split between CTAs: the CTA with its first piece -- the last of that CTA's slice -- merges, each warp its
-    // share; every other piece starts its CTA's slice, so a CTA publishes at most one partial.  A partial's words are
-    // stored complemented over zeros, and no sum has the bits ~0 (a NaN that arithmetic does not make), so a word that is
-    // not zero has arrived: no fence, no count, no second round trip.  The merging warp zeroes what it has read.
+    // A row split between CTAs: each CTA publishes its piece and counts it, each warp its share, and the warp that counts the
+    // last one merges them all: no CTA waits for another's work.  A CTA holds at most two such pieces, the first of its slice
+    // (slot 2 cta) and the last (2 cta + 1, a row's first piece).  A partial's words are stored complemented over zeros, and no
+    // sum has the bits ~0 (a NaN that arithmetic does not make), so a word that is not zero has arrived: no fence between
+    // the words and the count, only a wait for what is on its way.  The merging warp zeroes what it has read, and the count.
     // Words of four: an accumulator's two dims of two rows; with one row a lane two accumulators, and the row's (m, l).
     constexpr int OV = NC == 1 ? (C::OW + 1) / 2 : C::OW;
     uint4* const part_o = reinterpret_cast<uint4*>(p.part_o);
@@ -873,24 +875,36 @@ __global__ void __launch_bounds__(Q4Cfg<D, R4>::THREADS, Q4Cfg<D, R4>::MINB)
     auto value = [&](int nt, int k, int v) -> float& {
       return NC == 1 ? own[nt][min(2 * k + v / 2, C::OW - 1)][2 * (v & 1)] : own[nt][k][v];
     };
-    if (!si.first) {
+    const int mine = 2 * cta + (cta == si.c_lo ? 1 : 0);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        if (row0 + 8 * nt + t4 >= rows) continue;
+    for (int nt = 0; nt < NT; ++nt) {
+      if (row0 + 8 * nt + t4 >= rows) continue;
 #pragma unroll
-        for (int k = 0; k < OV; ++k)
-          st_relaxed_gpu(o_at(cta, nt, k), make_uint4(~__float_as_uint(value(nt, k, 0)), ~__float_as_uint(value(nt, k, 1)),
-                                                      ~__float_as_uint(value(nt, k, 2)), ~__float_as_uint(value(nt, k, 3))));
-        if (g == 0)
-          st_relaxed_gpu(ml_at(cta, nt), make_uint4(~__float_as_uint(M[nt][0]), ~__float_as_uint(L[nt][0]),
-                                                    ~__float_as_uint(M[nt][1]), ~__float_as_uint(L[nt][1])));
-      }
-      continue;
+      for (int k = 0; k < OV; ++k)
+        st_relaxed_gpu(o_at(mine, nt, k), make_uint4(~__float_as_uint(value(nt, k, 0)), ~__float_as_uint(value(nt, k, 1)),
+                                                     ~__float_as_uint(value(nt, k, 2)), ~__float_as_uint(value(nt, k, 3))));
+      if (g == 0)
+        st_relaxed_gpu(ml_at(mine, nt), make_uint4(~__float_as_uint(M[nt][0]), ~__float_as_uint(L[nt][0]),
+                                                   ~__float_as_uint(M[nt][1]), ~__float_as_uint(L[nt][1])));
     }
-    // Fold the others' partials in slice order with running maxima (a fixed order: bitwise reproducible), the loads of
+    unsigned* const count = p.counts + si.c_lo * C::OWN + warp;
+    unsigned before = 0;
+    __syncwarp();
+    if (lane == 0) before = atomicAdd(count, 1u);
+    if (__shfl_sync(0xffffffffu, before, 0) + 1 != (unsigned)si.np) continue;
+    if (lane == 0) *count = 0;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      M[nt][0] = M[nt][1] = -INFINITY;
+      L[nt][0] = L[nt][1] = 0.f;
+#pragma unroll
+      for (int k = 0; k < C::OW; ++k) own[nt][k][0] = own[nt][k][1] = own[nt][k][2] = own[nt][k][3] = 0.f;
+    }
+    // Fold the partials in slice order with running maxima (a fixed order: bitwise reproducible), the loads of
     // up to N in flight at a time.
     auto fold = [&](int i, auto n_c) -> bool {
       constexpr int N = decltype(n_c)::value;
+      auto slot_of = [&](int u) { return 2 * (si.c_lo + i + u) + (i + u == 0 ? 1 : 0); };
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const bool have = row0 + 8 * nt + t4 < rows;
@@ -901,11 +915,11 @@ __global__ void __launch_bounds__(Q4Cfg<D, R4>::THREADS, Q4Cfg<D, R4>::MINB)
 #pragma unroll
           for (int u = 0; u < N; ++u) {
             ml[u] = make_uint4(1, 1, 1, 1);
-            if (have) ml[u] = ld_relaxed_gpu(ml_at(cta + i + u, nt));
+            if (have) ml[u] = ld_relaxed_gpu(ml_at(slot_of(u), nt));
 #pragma unroll
             for (int k = 0; k < OV; ++k) {
               ov[u][k] = make_uint4(1, 1, 1, 1);
-              if (have) ov[u][k] = ld_relaxed_gpu(o_at(cta + i + u, nt, k));
+              if (have) ov[u][k] = ld_relaxed_gpu(o_at(slot_of(u), nt, k));
             }
           }
 #pragma unroll
@@ -947,16 +961,16 @@ __global__ void __launch_bounds__(Q4Cfg<D, R4>::THREADS, Q4Cfg<D, R4>::MINB)
             }
           }
           if (have) {
-            if (g == 0) st_relaxed_gpu(ml_at(cta + i + u, nt), make_uint4(0, 0, 0, 0));
+            if (g == 0) st_relaxed_gpu(ml_at(slot_of(u), nt), make_uint4(0, 0, 0, 0));
 #pragma unroll
-            for (int k = 0; k < OV; ++k) st_relaxed_gpu(o_at(cta + i + u, nt, k), make_uint4(0, 0, 0, 0));
+            for (int k = 0; k < OV; ++k) st_relaxed_gpu(o_at(slot_of(u), nt, k), make_uint4(0, 0, 0, 0));
           }
         }
       }
       return true;
     };
     constexpr int N = 4;
-    int i = 1;
+    int i = 0;
     bool got = true;
     for (; got && i + N - 1 < si.np; i += N) got = fold(i, std::integral_constant<int, N>{});
     for (; got && i < si.np; ++i) got = fold(i, std::integral_constant<int, 1>{});
@@ -1004,7 +1018,11 @@ cudaError_t launch_rows(const DecodeQ4Launch& p) {
 
 size_t decode_q4_partials(int num_sms) {
   const int sms = num_sms > 0 ? num_sms : 152;
-  return (size_t)sms * std::max(8 * Q4Cfg<128, 2>::MINB, 16 * Q4Cfg<128, 4>::MINB);
+  return (size_t)2 * sms * std::max(8 * Q4Cfg<128, 2>::MINB, 16 * Q4Cfg<128, 4>::MINB);
+}
+
+size_t decode_q4_counts(int num_sms) {
+  return (size_t)(num_sms > 0 ? num_sms : 152) * Q4Cfg<128, 2>::MINB * kDecodeQ4Owners;
 }
 
 cudaError_t launch_decode_q4(const DecodeQ4Launch& p) {

@@ -183,8 +183,9 @@ struct DecodeQ4Launch {
   const int* kv_lens;      // [B], the Lq new tokens' keys included
   void* out;               // [B, Hq, Lq, D], bf16 or fp32
   float* lse;              // [B, Hq, Lq] or null
-  float* part_o;           // fp32 [grid][cols * D], in the order of the warps' accumulators; zero between calls
-  float* part_ml;          // fp32 [grid][4 warps][cols][2]; zero between calls
+  unsigned* counts;        // [grid][4 warps] pieces of the row that starts in a CTA's slice and goes on; zero between calls
+  float* part_o;           // fp32 [2 grid][cols * D], in the order of the warps' accumulators; zero between calls
+  float* part_ml;          // fp32 [2 grid][4 warps][cols][2]; zero between calls
   int B, Hq, Hkv, Lq, D, page_size, max_pages, num_pages;
   int min_tiles;           // smallest slice of the tiles one CTA takes (0: chosen from the lengths)
   float scale;
@@ -197,6 +198,7 @@ struct DecodeQ4Launch {
 constexpr int kDecodeQ4Owners = 4;  // warps of a CTA that hold its partial
 // Columns (of D sums, and a maximum and a sum for every owner) that all CTAs' partials take in any variant.
 size_t decode_q4_partials(int num_sms);
+size_t decode_q4_counts(int num_sms);  // counts of all CTAs in any variant
 cudaError_t launch_decode_q4(const DecodeQ4Launch& p);
 
 // One thread waits on a barrier nothing arrives on, with the kernels' bounded wait and a limit of limit_ns.

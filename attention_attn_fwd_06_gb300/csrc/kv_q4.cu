@@ -10,9 +10,9 @@
 // lanes hold a group, its extremes take two shuffles and the row's place is looked up once for both; as many warps as fit.
 // 70k tokens of 8 heads at D = 128 take 66 us to write (5.6 TB/s) and 60 us to read back (6.2 TB/s).  Each lane's 32 bytes are
 // one access where rows start on 32 bytes: as two of 16, each store fills half a sector, and reading back takes 73 us (a fill
-// of 290 MB that way 76 against 42 us), writing 67 against 64 that day.  A key's or a value's dims a lane: 89 us to write; a warp for each token
-// and two rounds of its heads in flight (with the slower codes of that day): 113 and 79 us; one wave of warps that walk runs of
-// tokens: 124 and 111 us; warps of four tokens of one head: 65.7 and 59.4 us.
+// of 290 MB that way 76 against 42 us), writing 67 against 64 that day.  A key's or a value's dims a lane: 89 us to write; a
+// warp for each token and two rounds of its heads in flight (with the slower codes of that day): 113 and 79 us; one wave of
+// warps that walk runs of tokens: 124 and 111 us; warps of four tokens of one head: 65.7 and 59.4 us.
 //
 // Writing: extremes by packed bf16 min and max that pass NaN on; quotients correctly rounded, by a product with the
 // rounded reciprocal and its residual's share (Markstein's theorem), so that a tie between two codes is seen as one; their

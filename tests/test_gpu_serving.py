@@ -601,6 +601,20 @@ def test_a_timeout_is_told_whatever_was_recorded_before(monkeypatch, first):
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+@pytest.mark.parametrize("Hq,Hkv,Lq,D", [(8, 2, 1, 128), (8, 2, 1, 64), (16, 2, 1, 128), (32, 2, 2, 64), (24, 2, 3, 128)])
+def test_decode_q4_leaves_its_workspace_zero(Hq, Hkv, Lq, D):
+    """Rows in one CTA, in a few and in all of them, sequences without keys: whatever counts and partials a call writes it
+    takes back, and the next call starts from there."""
+    ws = AB.attn_decode_q4_workspace(Hq, Hkv, D, Lq=Lq, device=DEV)
+    pool, q = dev(make_pool(700, Hkv, 16, D, 4)), dev(torch.randn(3, Hq, Lq, D).to(torch.bfloat16))
+    for lens in ([1, 0, 16], [700, 64, 0], [5000, 3000, 1000], [9, 9000, 1]):
+        table = dev(make_table(lens, 16, 700, 5)[0])
+        for chunk in (0, 1, 600):
+            for dtype in (torch.bfloat16, torch.float32):
+                AB.attn_decode_q4(q, pool, table, i32(lens), chunk=chunk, out_dtype=dtype, workspace=ws)
+                assert AB.attn_get_device_status() == AB.ATTN_OK and (ws == 0).all(), (lens, chunk, dtype)
+
+
 def test_cache_calls_refuse_what_they_would_misread():
     pool = dev(make_pool(4, 2, 16, 64, 4))
     q, table, lens = dev(torch.randn(1, 4, 64).to(torch.bfloat16)), i32([0, 1])[None], i32([20])
