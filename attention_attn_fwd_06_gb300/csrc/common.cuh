@@ -203,5 +203,15 @@ __device__ __forceinline__ void cp_async_wait() {
 __device__ __forceinline__ void named_bar_sync(int id, int nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
+// The same, and whether x holds in any of the threads.
+__device__ __forceinline__ bool named_bar_any(int id, int nthreads, bool x) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"((uint32_t)x), "r"(id), "r"(nthreads)
+      : "memory");
+  return any != 0;
+}
 
 }  // namespace attn

@@ -398,10 +398,24 @@ __global__ void __launch_bounds__(Q4Cfg<D, R4>::THREADS, Q4Cfg<D, R4>::MINB)
     }
   };
 
+  // A wait can run out in one warp and just succeed in another (not in lanes of one warp, which test in one instruction).  So
+  // every warp takes part in two barriers for each record, the end's among them; the second tells whether any gave up.
+  auto wait = [&](uint64_t* bar) -> bool { return mbar_wait(bar, phase, p.status, abort_flag); };
+  auto leave = [&](bool gave_up) {
+    named_bar_sync(1, nct);
+    named_bar_any(1, nct, gave_up);
+  };
+
   while (true) {
-    if (!mbar_wait(&told[slot], phase, p.status, abort_flag)) break;
+    if (!wait(&told[slot])) {
+      leave(true);
+      break;
+    }
     const Q4PieceInfo si = info[slot];
-    if (si.b < 0) break;
+    if (si.b < 0) {
+      leave(false);
+      break;
+    }
     const int hkv = si.hg / chunks;
     const int row0 = (si.hg - hkv * chunks) * C::ROWS;  // first query row of the kv head this CTA serves
     const int len = si.len;
@@ -710,7 +724,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, R4>::THREADS, Q4Cfg<D, R4>::MINB)
     const int interior = whole < 0 ? 0 : whole / C::ST + 1;
     int stage = 0;
     for (; stage < interior; ++stage) {
-      if (!mbar_wait(&full[slot], phase, p.status, abort_flag)) {
+      if (!wait(&full[slot])) {
         alive = false;
         break;
       }
@@ -720,7 +734,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, R4>::THREADS, Q4Cfg<D, R4>::MINB)
       release();
     }
     for (; alive && stage <= last && !(stage == last && interior > last); ++stage) {
-      if (!mbar_wait(&full[slot], phase, p.status, abort_flag)) {
+      if (!wait(&full[slot])) {
         alive = false;
         break;
       }
@@ -732,7 +746,10 @@ __global__ void __launch_bounds__(Q4Cfg<D, R4>::THREADS, Q4Cfg<D, R4>::MINB)
       __syncwarp();
       if (stage < last) release();
     }
-    if (!alive) break;
+    if (!alive) {
+      leave(true);
+      break;
+    }
 
     // ---------------- end of a row piece: each warp gathers its share of the accumulators from all ----------------
     // Accumulators i = warp * OW .. + OW-1 of every column group are summed by `warp`, weighted by 2^(m_w - M), in warp
@@ -787,7 +804,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, R4>::THREADS, Q4Cfg<D, R4>::MINB)
           mlbuf[(warp * NT + nt) * 8 + 2 * t4 + c] = make_float2(c < NC ? m[nt][c < NC ? c : 0] : -INFINITY, ll[c]);
       }
     }
-    named_bar_sync(1, nct);
+    if (named_bar_any(1, nct, false)) break;  // the sums of a warp that gave up are missing
     float M[NT][2], L[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
