@@ -843,6 +843,28 @@ def test_decode_q4_rows_of_every_width_over_a_long_capacity():
             assert_within(ls, lse, bL)
 
 
+@pytest.mark.parametrize("Hq,Lq", [(24, 1), (18, 1), (8, 5), (2, 16), (6, 13)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_decode_q4_wide_rows_split_between_many_ctas(D, Hq, Lq):
+    """16 query rows a CTA over a long capacity, a sequence of thousands of keys split into pieces that are merged four at a
+    time and singly, beside short and empty ones; by the default split too."""
+    lens, page = [6000, 0, 33, 1, 700], 16
+    pool = make_pool(430, 2, page, D, 8)
+    table, _ = make_table(lens, page, 430, 8, width=120000)
+    q = torch.randn(5, Hq, Lq, D, generator=torch.Generator().manual_seed(Hq)).to(torch.bfloat16)
+    for dtype in (torch.bfloat16, torch.float32):
+        O, lse, bO, bL = decode_bound(q, pool, table, lens, 0.1, dtype == torch.float32)
+        seen = []
+        for chunk in (0, 256, 1000, 1 << 20):
+            out, ls = run_decode(q, pool, table, lens, 0.1, chunk=chunk, out_dtype=dtype)
+            assert_within(out, O, bO, f"O {dtype} {chunk}")
+            assert_within(ls, lse, bL, f"lse {dtype} {chunk}")
+            again = run_decode(q, pool, table, lens, 0.1, chunk=chunk, out_dtype=dtype)
+            assert torch.equal(out, again[0]) and torch.equal(ls, again[1])
+            seen.append(out)
+        assert not torch.equal(seen[1], seen[3])  # split indeed
+
+
 def test_side_stream_gives_the_same_bits():
     torch.manual_seed(3)
     pool = dev(make_pool(100, 2, 16, 64, 1))
