@@ -196,6 +196,47 @@ def test_qk_norm_rope(T, Hq, Hkv, D, style, weights):
     assert torch.equal(qkv[:, Hq + Hkv:], before[:, Hq + Hkv:])
 
 
+def long_norm_case(T, Hq, Hkv, D, style, seed):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    q = torch.randn(T, Hq, D, generator=g, device=DEV).to(torch.bfloat16)
+    k = torch.randn(T, Hkv, D, generator=g, device=DEV).to(torch.bfloat16)
+    pos = torch.randint(0, 3000, (T,), generator=g, device=DEV, dtype=torch.int32)
+    pos[torch.rand(T, generator=g, device=DEV) < 0.1] = -1  # padded rows inside the warps' runs of tokens
+    pos[T // 3:T // 3 + 70] = -1
+    return q, k, pos, tuple(x.to(DEV) for x in rope_tables(3000, D)) + (style,)
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(2, 1), (9, 2)])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("style", ["half", "interleaved"])
+def test_qk_norm_rope_runs_of_tokens(style, D, Hq, Hkv):
+    """About seven tokens a warp: the buffers of table rows are refilled, with one round of heads a token and with several."""
+    q, k, pos, rope = long_norm_case(20011, Hq, Hkv, D, style, D)
+    qo, ko = torch.full_like(q, 7.0), torch.full_like(k, 7.0)
+    AB.attn_qk_norm_rope(q, k, None, None, rope, pos, eps=1e-5, q_out=qo, k_out=ko)
+    assert AB.attn_get_device_status() == AB.ATTN_OK
+    p = pos.cpu().numpy()
+    for x, out in ((q, qo), (k, ko)):
+        ref, bound = norm_ref(oracle.to_f64(x.cpu()), None, p, rope, 1e-5, p >= 0)
+        assert_within(out, ref, bound)
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,D,style", [(70001, 32, 8, 128, "half"), (130003, 2, 1, 64, "interleaved"),
+                                              (130003, 5, 4, 128, "half"), (130003, 16, 2, 64, "half"),
+                                              (200000, 1, 1, 128, "interleaved")])
+def test_qk_norm_rope_longest_runs(T, Hq, Hkv, D, style):
+    """Tens of tokens a warp, and past 32 more warps instead: the bits of calls of a token a warp over parts of it."""
+    q, k, pos, rope = long_norm_case(T, Hq, Hkv, D, style, T)
+    qo, ko = torch.full_like(q, 7.0), torch.full_like(k, 7.0)
+    AB.attn_qk_norm_rope(q, k, None, None, rope, pos, q_out=qo, k_out=ko)
+    qs, ks = torch.full_like(q, 7.0), torch.full_like(k, 7.0)
+    for t in range(0, T, 2000):
+        at = slice(t, min(T, t + 2000))
+        AB.attn_qk_norm_rope(q[at], k[at], None, None, rope, pos[at].contiguous(), q_out=qs[at], k_out=ks[at])
+    assert AB.attn_get_device_status() == AB.ATTN_OK
+    assert torch.equal(qo, qs) and torch.equal(ko, ks)
+
+
 @pytest.mark.parametrize("D", [64, 128])
 def test_qk_norm_rope_dense_layout(D):
     B, Hq, Hkv, L = 3, 6, 2, 37
