@@ -838,6 +838,82 @@ def test_two_captured_steps_replayed_at_once():
     assert AB.attn_get_device_status() == AB.ATTN_OK
 
 
+@pytest.mark.parametrize("Hq,Hkv,D,Lq,style", [(8, 2, 128, 4, "half"), (4, 4, 64, 3, "interleaved"), (16, 2, 128, 5, "half")])
+def test_draft_steps_in_a_graph(Hq, Hkv, D, Lq, style):
+    """Steps of Lq draft tokens a request, some of them refused: pages, norm into the decode's layout, rows into the cache,
+    decode of all drafts at once, captured as one step; every output against fp64 over the values in the cache."""
+    B, page = 3, 16
+    g = torch.Generator(device=DEV).manual_seed(Lq)
+    lens, keep, new = i32([0] * B), i32([0] * B), i32([Lq] * B)
+    table, free, count = torch.full((B, 9), -1, dtype=torch.int32, device=DEV), i32(range(30)), i32([30])
+    slots, pos = i32([0] * (B * Lq)), i32([0] * (B * Lq))
+    pool = AB.attn_kv_q4_pool(30, Hkv, page, D, DEV)
+    rope = tuple(x.to(DEV) for x in rope_tables(9 * page, D)) + (style,)
+    w = (1 + 0.1 * torch.randn(2, D, generator=g, device=DEV)).to(torch.bfloat16)
+    qkv = torch.zeros(B, Lq, Hq + 2 * Hkv, D, dtype=torch.bfloat16, device=DEV)
+    q, k = torch.empty(B, Hq, Lq, D, dtype=torch.bfloat16, device=DEV), torch.empty(B, Lq, Hkv, D, dtype=torch.bfloat16, device=DEV)
+    out, lse = torch.empty_like(q), torch.empty(B, Hq, Lq, device=DEV)
+    ws = AB.attn_decode_q4_workspace(Hq, Hkv, D, Lq=Lq, device=DEV)
+
+    def step():
+        x = qkv.transpose(1, 2)  # [B, heads, Lq, D]
+        AB.attn_page_step(lens, table, free, count, page, new_lens=new, keep_lens=keep, slots=slots, positions=pos)
+        AB.attn_qk_norm_rope(x[:, :Hq], x[:, Hq:Hq + Hkv], w[0], w[1], rope, pos.view(B, Lq), q_out=q, k_out=k.transpose(1, 2))
+        AB.attn_kv_append_q4(k.flatten(0, 1), qkv[:, :, Hq + Hkv:].flatten(0, 1), pool, slots)
+        AB.attn_decode_q4(q, pool, table, lens, out=out, lse=lse, workspace=ws)
+
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    held = [0] * B
+    for i in range(12):
+        taken = [h if i == 0 else h - Lq + (i * (b + 1)) % (Lq + 1) for b, h in enumerate(held)]  # 0 to Lq drafts kept
+        keep.copy_(i32(taken))
+        qkv.normal_(generator=g)
+        graph.replay()
+        held = [n + Lq for n in taken]
+        assert AB.attn_get_device_status() == AB.ATTN_OK and lens.tolist() == held
+        assert pos.view(B, Lq).tolist() == [list(range(n, n + Lq)) for n in taken]
+        flat = qkv[:, :, :Hq].reshape(B * Lq, Hq, D)
+        ref, bound = norm_ref(oracle.to_f64(flat.cpu()), w[0].cpu(), pos.cpu().numpy(), rope, 1e-6, np.ones(B * Lq, bool))
+        assert_within(q.transpose(1, 2).reshape(B * Lq, Hq, D), ref, bound)
+        cached, _ = AB.attn_kv_gather_q4(pool, table, i32(range(0, B * Lq + 1, Lq)), B * Lq, kv_starts=i32(taken))
+        u, s, m = oracle.quantise_q4(k.flatten(0, 1).cpu())
+        assert torch.equal(cached.cpu(), torch.from_numpy(oracle.values_q4(u, s, m)).float().to(torch.bfloat16))
+        O, L, bO, bL = decode_bound(q.cpu(), pool.cpu().numpy(), table.cpu().numpy(), held, D ** -0.5, False)
+        assert_within(out, O, bO)
+        assert_within(lse, L, bL)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 2, 128), (4, 4, 64)])
+def test_prefill_of_chunks_over_a_cached_prefix(Hq, Hkv, D):
+    """Prompts in chunks: each chunk's rows go into the cache, all keys so far are read back, and the packed prefill runs the
+    chunk's queries over them (more keys than queries, a request without new tokens among them)."""
+    e = Engine(4, Hq, Hkv, D, 16, 80, 30, 600)
+    held = [0] * 4
+    for new in ([130, 0, 65, 16], [200, 33, 0, 1], [7, 200, 64, 100]):
+        e.new.copy_(i32(new))
+        e.qkv.normal_()
+        e.prefix()
+        held = [a + b for a, b in zip(held, new)]
+        cu_q, cu_k = e.cu, i32(np.concatenate([[0], np.cumsum(held)]))
+        k, v = AB.attn_kv_gather_q4(e.pool, e.table, cu_k, sum(held))
+        n = sum(new)
+        out, lse = AB.attn_fwd_varlen(e.q[:n], k, v, cu_q, cu_k, max(new), max(held))
+        assert AB.attn_get_device_status() == AB.ATTN_OK
+        for b in range(4):
+            if new[b] == 0:
+                continue
+            rows, keys = slice(int(cu_q[b]), int(cu_q[b + 1])), slice(sum(held[:b]), sum(held[:b + 1]))
+            kk, vv, _, _ = oracle.read_q4(e.pool.cpu().numpy(), e.table[b].cpu().numpy(), 0, held[b])
+            for x, got in ((kk, k[keys]), (vv, v[keys])):  # what the cache holds, rounded once
+                assert torch.equal(got.cpu(), torch.from_numpy(x).float().to(torch.bfloat16))
+            for h in range(Hq):
+                o, _ = oracle.attention_head(oracle.to_f64(e.q[rows, h].cpu()), oracle.to_f64(k[keys, h // (Hq // Hkv)].cpu()),
+                                             oracle.to_f64(v[keys, h // (Hq // Hkv)].cpu()), D ** -0.5, causal=True)
+                assert np.abs(out[rows, h].double().cpu().numpy() - o).max() < 2e-2  # the prefill kernel's own bar
+
+
 @pytest.mark.parametrize("D", [64, 128])
 def test_pool_offsets_past_32_bits(D):
     """The last pages of a pool of over 4 GiB: written, read back and attended to like the first ones of a small one."""
