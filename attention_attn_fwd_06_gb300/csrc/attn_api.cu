@@ -243,11 +243,14 @@ int validate_pool_q4(int Hkv, int D, int page_size, int num_pages) {
   return ATTN_OK;
 }
 
-// Strides in elements of rows read or written 16 bytes at a time.
-bool strides8(const long long* s, int n) {
-  for (int i = 0; i < n; ++i)
-    if (s[i] % 8 != 0) return false;
-  return true;
+// Strides in elements of rows read or written 16 bytes at a time; that of an axis of one element says nothing and becomes 0.
+bool take_strides8(const long long* stride, const int* extent, int n, long long* out) {
+  bool ok = true;
+  for (int i = 0; i < n; ++i) {
+    out[i] = extent[i] > 1 ? stride[i] : 0;
+    ok = ok && out[i] % 8 == 0;
+  }
+  return ok;
 }
 
 bool aligned128(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 127u) == 0; }
@@ -750,17 +753,19 @@ int attn_qk_norm_rope(const attn_qk_norm_rope_params* p) {
   if (p->q == nullptr || p->q_out == nullptr || (p->Hkv > 0 && (p->k == nullptr || p->k_out == nullptr)) ||
       (rope_on && p->positions == nullptr))
     return ATTN_ERR_INVALID_ARG;
+  attn::QkNormRopeLaunch L{};
+  const int q_extent[3] = {p->B, p->L, p->Hq}, k_extent[3] = {p->B, p->L, p->Hkv};
   if (!aligned16(p->q) || !aligned16(p->q_out) || !aligned16(p->q_weight) || !aligned16(p->k_weight) ||
-      !aligned4(p->positions) || !strides8(p->q_stride, 3) || !strides8(p->q_out_stride, 3))
+      !aligned4(p->positions) || !take_strides8(p->q_stride, q_extent, 3, L.qs) ||
+      !take_strides8(p->q_out_stride, q_extent, 3, L.qos))
     return ATTN_ERR_ALIGNMENT;
-  if (p->Hkv > 0 &&
-      (!aligned16(p->k) || !aligned16(p->k_out) || !strides8(p->k_stride, 3) || !strides8(p->k_out_stride, 3)))
+  if (p->Hkv > 0 && (!aligned16(p->k) || !aligned16(p->k_out) || !take_strides8(p->k_stride, k_extent, 3, L.ks) ||
+                     !take_strides8(p->k_out_stride, k_extent, 3, L.kos)))
     return ATTN_ERR_ALIGNMENT;
   if ((long long)p->B * p->L > kIntMax || (long long)p->Hq + p->Hkv > 65535) return ATTN_ERR_UNSUPPORTED;
   DeviceState* s = nullptr;
   st = device_state(&s);
   if (st != ATTN_OK) return st;
-  attn::QkNormRopeLaunch L{};
   L.q = p->q;
   L.k = p->k;
   L.q_out = p->q_out;
@@ -774,12 +779,6 @@ int attn_qk_norm_rope(const attn_qk_norm_rope_params* p) {
   L.Hkv = p->Hkv;
   L.D = p->D;
   L.eps = p->eps;
-  for (int i = 0; i < 3; ++i) {
-    L.qs[i] = p->q_stride[i];
-    L.ks[i] = p->k_stride[i];
-    L.qos[i] = p->q_out_stride[i];
-    L.kos[i] = p->k_out_stride[i];
-  }
   L.rope = rope_args(p->rope);
   L.status = s->status;
   L.stream = static_cast<cudaStream_t>(p->stream);
@@ -799,13 +798,14 @@ int attn_kv_append_q4(const attn_kv_append_q4_params* p) {
   if (p->T < 0) return ATTN_ERR_INVALID_ARG;
   if (p->T == 0) return ATTN_OK;
   if (p->k == nullptr || p->v == nullptr || p->pool == nullptr || p->slots == nullptr) return ATTN_ERR_INVALID_ARG;
+  attn::KvAppendQ4Launch L{};
+  const int extent[2] = {p->T, p->Hkv};
   if (!aligned16(p->k) || !aligned16(p->v) || !aligned128(p->pool) || !aligned4(p->slots) ||
-      !strides8(p->k_stride, 2) || !strides8(p->v_stride, 2))
+      !take_strides8(p->k_stride, extent, 2, L.ks) || !take_strides8(p->v_stride, extent, 2, L.vs))
     return ATTN_ERR_ALIGNMENT;
   DeviceState* s = nullptr;
   st = device_state(&s);
   if (st != ATTN_OK) return st;
-  attn::KvAppendQ4Launch L{};
   L.k = p->k;
   L.v = p->v;
   L.pool = p->pool;
@@ -815,10 +815,6 @@ int attn_kv_append_q4(const attn_kv_append_q4_params* p) {
   L.D = p->D;
   L.page_size = p->page_size;
   L.num_pages = p->num_pages;
-  for (int i = 0; i < 2; ++i) {
-    L.ks[i] = p->k_stride[i];
-    L.vs[i] = p->v_stride[i];
-  }
   L.status = s->status;
   L.stream = static_cast<cudaStream_t>(p->stream);
   return map_cuda(attn::launch_kv_append_q4(L));

@@ -415,7 +415,8 @@ int attn_page_step(const attn_page_step_params* p);
  *   rope          tables and style (k_out unused); ATTN_ROPE_NONE: norm only
  *   eps           finite, >= 0 (a row of zeros with eps = 0 is 0 * inf = NaN)
  * (In fp32 the squares of elements beyond some 10^18 overflow, and such a row is 0.)
- * Pointers are 16-byte aligned, strides multiples of 8 elements.
+ * Pointers are 16-byte aligned, strides multiples of 8 elements (that of an axis of one
+ * element may be anything).
  */
 typedef struct attn_qk_norm_rope_params {
   const void* q;
@@ -454,7 +455,8 @@ unsigned long long attn_kv_q4_page_bytes(int page_size, int Hkv, int D);
  * counts as 0, values beyond +-65504 as that.
  *
  *   k, v   bf16 [T, Hkv, D] with strides of token and head in elements (multiples of
- *          8; D contiguous; 16-byte aligned): views of a projection's output will do
+ *          8, unless there is one; D contiguous; 16-byte aligned): views of a
+ *          projection's output will do
  *   slots  int32 [T]; -1: the row is not written.  Any other slot outside the pool is
  *          flagged and not written.  The slots of one call must differ: rows of the same
  *          slot would be written over each other in no order.

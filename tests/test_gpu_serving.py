@@ -252,6 +252,22 @@ def test_qk_norm_rope_dense_layout(D):
         assert_within(out.transpose(1, 2).reshape(B * L, -1, D), ref, bound)
 
 
+def test_one_token_of_any_stride():
+    """A single token's (head's) row may come with any stride: the same bits as from a contiguous tensor."""
+    g = torch.Generator().manual_seed(1)
+    q, k = dev(torch.randn(1, 4, 64, generator=g).to(torch.bfloat16)), dev(torch.randn(1, 1, 64, generator=g).to(torch.bfloat16))
+    odd_q, odd_k = q.as_strided(q.shape, (3, 64, 1)), k.as_strided(k.shape, (1, 5, 1))
+    want, got = AB.attn_qk_norm_rope(q, k), AB.attn_qk_norm_rope(odd_q, odd_k)
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+    out = torch.empty_like(q), torch.empty_like(k)
+    AB.attn_qk_norm_rope(q, k, q_out=out[0].as_strided(q.shape, (3, 64, 1)), k_out=out[1].as_strided(k.shape, (1, 5, 1)))
+    assert torch.equal(want[0], out[0]) and torch.equal(want[1], out[1])
+    pools = [AB.attn_kv_q4_pool(1, 1, 16, 64, DEV) for _ in range(2)]
+    AB.attn_kv_append_q4(k, k, pools[0], i32([5]))
+    AB.attn_kv_append_q4(odd_k, odd_k, pools[1], i32([5]))
+    assert torch.equal(*pools) and AB.attn_get_device_status() == AB.ATTN_OK
+
+
 def test_qk_norm_rope_refuses_what_it_would_misread():
     q = dev(torch.randn(4, 2, 64).to(torch.bfloat16))
     cos = torch.zeros(8, 32, device=DEV)

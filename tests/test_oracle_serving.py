@@ -206,6 +206,26 @@ def test_decode_q4_refusals(lib, kw, code):
     assert lib.attn_decode_q4(params(B.attn_decode_q4_params, **{**DECODE, **kw})) == code
 
 
+def test_strides_of_axes_of_one_element_are_not_looked_at(lib):
+    """Whether a call is refused before it looks for a device."""
+    def refused(fn, cls, base, **kw):
+        return fn(params(cls, **{**base, **kw})) == B.ATTN_ERR_ALIGNMENT
+
+    norm = lib.attn_qk_norm_rope, B.attn_qk_norm_rope_params, {**NORM, "B": 1, "L": 1}
+    append = lib.attn_kv_append_q4, B.attn_kv_append_q4_params, {**APPEND, "T": 1}
+    if torch.cuda.is_available():
+        pytest.skip("the addresses are not memory")
+    for t in ("q", "k", "q_out", "k_out"):
+        assert not refused(*norm, **{f"{t}_token_stride": 3, f"{t}_sequence_stride": 1})
+        assert refused(*norm, L=2, **{f"{t}_token_stride": 3})
+        assert refused(*norm, B=2, **{f"{t}_sequence_stride": 3})
+        assert refused(*norm, Hq=2, Hkv=2, **{f"{t}_head_stride": 3})
+    for t in ("k", "v"):
+        assert not refused(*append, **{f"{t}_token_stride": 3})
+        assert refused(*append, T=2, **{f"{t}_token_stride": 3})
+        assert not refused(*append, Hkv=1, **{f"{t}_head_stride": 3})
+
+
 def test_empty_calls_succeed_without_a_device(lib):
     assert lib.attn_page_step(params(B.attn_page_step_params, **{**PAGE, "B": 0})) == B.ATTN_OK
     assert lib.attn_qk_norm_rope(params(B.attn_qk_norm_rope_params, **{**NORM, "L": 0})) == B.ATTN_OK
