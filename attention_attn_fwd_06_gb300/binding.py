@@ -616,8 +616,9 @@ def attn_page_step(kv_lens, block_table, free_pages, free_count, page_size, new_
           _fit(free_pages, "free_pages", i32, (pages,), at),
           _fit(free_count, "free_count", i32, (1,), at),
           0 if cu_new is None else _fit(cu_new, "cu_new", i32, (B + 1,), at),
-          0 if slots is None else _fit(slots, "slots", i32, (room,), at),
-          0 if positions is None else _fit(positions, "positions", i32, (room,), at),
+          # (a list without room has no address of its own, and is none the less a list: any other stands for it)
+          0 if slots is None else _fit(slots, "slots", i32, (room,), at) or kv_lens.data_ptr(),
+          0 if positions is None else _fit(positions, "positions", i32, (room,), at) or kv_lens.data_ptr(),
           B, int(page_size), width, pages, room, _stream_of(stream, at))
     return slots, positions, cu_new
 

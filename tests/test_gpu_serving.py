@@ -120,6 +120,18 @@ def test_page_step_token_sums_past_32_bits_are_refused(rows):
     assert lens.tolist() == [0] * B and count.item() == 64 and cu.tolist() == [0] * (B + 1) and (table == -1).all()
 
 
+def test_page_step_lists_without_room():
+    """An empty list is a list: tokens it has no room for are refused, a step without tokens is not."""
+    for name in ("slots", "positions"):
+        P = Pages(2, 16, 4, 8, seed=1)
+        empty = {name: torch.empty(0, dtype=torch.int32, device=DEV)}
+        AB.attn_page_step(P.d_lens, P.d_table, P.d_free, P.d_count, 16, new_lens=i32([1, 0]), **empty)
+        assert AB.attn_get_device_status() == AB.ATTN_ERR_DEVICE_BOUNDS
+        assert P.d_lens.tolist() == [0, 0] and P.d_count.item() == 8
+        AB.attn_page_step(P.d_lens, P.d_table, P.d_free, P.d_count, 16, new_lens=i32([0, 0]), **empty)
+        assert AB.attn_get_device_status() == AB.ATTN_OK and P.d_lens.tolist() == [0, 0]
+
+
 def test_page_step_bad_page_ids_are_flagged():
     P = Pages(1, 16, 4, 4, seed=2)
     P.step(new=[20])
