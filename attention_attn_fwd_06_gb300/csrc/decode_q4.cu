@@ -12,9 +12,11 @@
 // exceed its fp32 units.  So products run on the tensor cores -- mma.sync m16n8k16 in fp16, whose A operand
 // comes straight from registers: K^T and V^T tiles are 16 keys (dims) by 16, the 8 columns are the query rows of one
 // kv head.  A tcgen05 product would need the unpacked tile written to shared or tensor memory first, four times the
-// bytes of the codes, for an N of 8 (for 32 query rows over 131k keys it takes 179 against 214 us, over 8 x 4096 37 against 30);
-// mma.sync on 8-bit floats (codes are e4m3 as they are, q two terms) runs at fp16's rate and converts its operands on the
-// way (72 against 65 us at 131k keys).
+// bytes of the codes, for an N of 8: 37 against 30 us for 32 query rows over 8 x 4096 keys.  (Over long caches those rows
+// would gain by it, 179 against 214 us at 131k keys; this kernel has no such variant, and with 32 rows it takes longer than
+// bf16 does: 218 us for 313,590 keys, attn_decode_multi 199.8 us for 327,680 of 3.6 times the bytes.)  mma.sync on 8-bit
+// floats (codes are e4m3 as they are, q two terms) runs at fp16's rate and converts its operands on the way (72 against
+// 65 us at 131k keys).
 //  * Unpacking costs one mask per two elements: (w & 0x000f000f) is, as a pair of fp16, the subnormals u 2^-24, and
 //    (w & 0x00f000f0) is u 2^-20, both exact; the factors go into q (2^10 and 2^6, q first scaled by a power of two
 //    to a largest element in [16, 32), which is exact) and, for V, into the output.  One shift by 8 gives the
@@ -32,13 +34,14 @@
 //    keys: over a slice of 131,072 keys, 2048 adds a warp, that biases O by some 2^-13 of its terms' sum, below the 2^-11
 //    that a weight's rounding is off by at most.  With fp32 output each tile's products start from zero and are added with
 //    rounding (131k keys 71.1 against 66.3 us, 8 x 4096 14.3 against 13.9 us; 32 query rows over 131k 317 against 300 us).
-// At long contexts the instructions bound it: some 270 a tile of 16 keys at D = 128, 40 of them masks and shifts for K,
-// 48 with the byte permutes for V, at two clocks each (dropping either product's unpacking and matrix products reaches the
-// 60 us that the copies alone take of the 64); over short ones the chain of a launch: lengths, split, block table and first
+// At long contexts the instructions bound it: 243 a tile of 16 keys at D = 128 (all that a launch executes over its tiles), 40
+// of them masks and shifts for K, 48 with the byte permutes for V, at two clocks each (dropping either product's unpacking
+// and matrix products reaches the 60 us that the copies alone take of the 64); over short ones the chain of a launch:
+// lengths, split, block table and first
 // copies (1.6 us), first data (4 us), a row's stages at 0.6 us each, exchange and merge (2 to 3 us).
-// Measured (CUDA-graph replays over rotating pools, 32 query and 8 kv heads, D = 128): 4 sequences of 32k to 131k keys 64.3 us
-// (5.6 TB/s, 0.83 of the copy bandwidth), 8 of 512 to 4096 keys 13.9 us, one of 4096 keys 11.4 us; 64 of up to 700 keys with
-// 16 heads of D = 64 16.7 us; 8 tokens each over 8 x 4096 keys 30.2 us.  Two CTAs of seven consumer warps an SM: 70.3 /
+// Measured (CUDA-graph replays over rotating pools, 32 query and 8 kv heads, D = 128): 4 sequences of 32k to 131k keys 64.1 us
+// (5.6 TB/s, 0.83 of the copy bandwidth), 8 of 512 to 4096 keys 14.0 us, one of 4096 keys 11.4 us; 64 of up to 700 keys with
+// 16 heads of D = 64 16.9 us; 8 tokens each over 8 x 4096 keys 30.3 us.  Two CTAs of seven consumer warps an SM: 70.3 /
 // 15.0 / - / 22.0 us against 70.8 / 14.3 / - / 16.6 us that day; four tiles a warp and stage 70.5 / 16.7 / - / 19.1 us;
 // four CTAs at 96 registers 86 / 18.9 us (spills).  At D = 64 two, three, four tiles a warp and stage: 16 heads over 4 x 16k to
 // 64k keys 45.1, 37.9, 36.2 us, the 64 short sequences 16.0, 16.1, 18.3 us.
@@ -74,7 +77,9 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kRowCostTiles = 16;
 // From this many tiles a CTA at the caches' capacity on, 16 query rows a CTA (two CTAs an SM, each tile unpacked once for
 // all 16) beat 8 (three): 32 rows over 131k keys 213 against 252 us; below, 8 rows win by their cheaper piece ends: 32
-// rows over 8 x 4096 keys 29.4 against 31.1 us, 16 rows 18.7 against 24.3 us.
+// rows over 8 x 4096 keys 29.4 against 31.1 us, 16 rows 18.7 against 24.3 us.  The lengths are on the device, so this reads the
+// tables' width: over tables 32 times wider than 8 requests of 512 to 4096 keys need, 16 rows take 26.9 us (19.8 over tight
+// ones), 32 rows 32.9 (28.8).
 constexpr long long kWideTiles = 256;
 
 // R4: groups of 4 query rows a CTA serves (1, 2 or 4).

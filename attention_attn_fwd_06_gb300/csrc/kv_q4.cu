@@ -2,8 +2,10 @@
 //
 // A group is 64 consecutive dims of one key's (value's) row.  With m = fp16(min x) and s = fp16((max x - min x) / 15)
 // its codes are u = clamp(round((x - m) / s), 0, 15), ties to even, and a code reads back as s * u + m.  Scale and
-// minimum are held in fp16: eleven bits, so that a code's step is off by 2^-12 at most against the step's half that
-// the four bits themselves cost.  NaN is stored as 0, values beyond fp16's range as its largest.
+// minimum are held in fp16: eleven bits, so that each is off by 2^-11 of itself at most, against the half of a step that the
+// four bits themselves cost.  Below 2^-14 fp16 has fewer bits: the scale of a group whose range is below 9.2e-4 is a multiple
+// of 2^-24, and with a range below 4.5e-7 it is 0 and the minimum stands for all.  NaN is stored as 0, values beyond fp16's
+// range as its largest.
 //
 // What bounds both: HBM, once the arithmetic is short.  Writing takes 2 bytes in and 0.5625 out per element, reading
 // back the reverse.  A lane takes 16 dims (32 bytes of bf16, 8 bytes of codes) of one head's key and of its value, so four

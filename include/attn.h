@@ -414,7 +414,8 @@ int attn_page_step(const attn_page_step_params* p);
  *                 was.  May be NULL without rotation.
  *   rope          tables and style (k_out unused); ATTN_ROPE_NONE: norm only
  *   eps           finite, >= 0 (a row of zeros with eps = 0 is 0 * inf = NaN)
- * (In fp32 the squares of elements beyond some 10^18 overflow, and such a row is 0.)
+ * (In fp32 the squares of elements beyond some 10^18 overflow, and such a row is 0; those
+ * of elements below some 10^-19 count as 0, which matters where eps does not cover them.)
  * Pointers are 16-byte aligned, strides multiples of 8 elements (that of an axis of one
  * element may be anything).
  */
