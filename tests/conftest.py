@@ -1,3 +1,4 @@
+import gc
 import os
 import sys
 
@@ -25,3 +26,12 @@ def pytest_collection_modifyitems(config, items):
     for item in items:
         if "gpu" in item.keywords:
             item.add_marker(skip)
+
+
+@pytest.fixture(autouse=True)
+def _no_collection_inside_a_test():
+    """A CUDA graph that an earlier test left in a reference cycle must not be destroyed while a test captures another:
+    that invalidates the capture.  Cycles are collected between tests."""
+    gc.disable()
+    yield
+    gc.enable()
