@@ -1023,6 +1023,33 @@ def test_side_stream_gives_the_same_bits():
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+def test_decodes_of_several_streams_at_once():
+    """Four streams' decodes of different shapes, each with a workspace of its own, beside a prefill that holds SMs: whichever
+    CTAs start first, the bits are those of the calls one after another."""
+    cases = []
+    for i, (B, Hq, Hkv, Lq, D, hi) in enumerate([(1, 32, 8, 1, 128, 9000), (6, 16, 16, 1, 64, 1500), (3, 8, 2, 4, 128, 4000),
+                                                  (40, 8, 2, 1, 64, 300)]):
+        g = np.random.default_rng(i)
+        lens = [int(x) for x in g.integers(0, hi + 1, B - 1)] + [hi]
+        num = sum(-(-n // 16) for n in lens)
+        pool, table = dev(make_pool(num, Hkv, 16, D, i)), dev(make_table(lens, 16, num, i)[0])
+        q = dev(torch.randn(B, Hq, Lq, D, generator=torch.Generator().manual_seed(i)).to(torch.bfloat16))
+        cases.append((q, pool, table, i32(lens), AB.attn_decode_q4_workspace(Hq, Hkv, D, Lq=Lq, device=DEV), torch.cuda.Stream()))
+    want = [AB.attn_decode_q4(*c[:4], workspace=c[4]) for c in cases]
+    x = dev(torch.randn(3, 2, 8, 2048, 128).to(torch.bfloat16))
+    side = torch.cuda.Stream()
+    outs = [[(torch.empty_like(w[0]), torch.empty_like(w[1])) for _ in range(25)] for w in want]
+    torch.cuda.synchronize()
+    for n in range(25):
+        AB.attn_fwd(x[0], x[1], x[2], stream=side)
+        for c, w in zip(cases, outs):
+            AB.attn_decode_q4(*c[:4], out=w[n][0], lse=w[n][1], workspace=c[4], stream=c[5])
+    torch.cuda.synchronize()
+    assert AB.attn_get_device_status() == AB.ATTN_OK
+    for w, got in zip(want, outs):
+        assert all(torch.equal(o, w[0]) and torch.equal(ls, w[1]) for o, ls in got)
+
+
 FIRST_CALLS = """
 import torch
 from attention_attn_fwd_06_gb300 import binding as AB
