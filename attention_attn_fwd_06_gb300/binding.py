@@ -49,6 +49,11 @@ EXPORTED = (
     "attn_kv_gather_q4",
     "attn_decode_q4",
     "attn_decode_q4_workspace_bytes",
+    "attn_rope_tables",
+    "attn_kv_append_paged",
+    "attn_decode_multi_paged",
+    "attn_decode_multi_paged_workspace_bytes",
+    "attn_verify_drafts",
     "attn_get_device_status",
     "attn_status_string",
     "attn_release_workspace",
@@ -61,6 +66,11 @@ ATTN_ROPE_NONE = 0
 ATTN_ROPE_HALF = 1
 ATTN_ROPE_INTERLEAVED = 2
 _ROPE_STYLES = {"half": ATTN_ROPE_HALF, "interleaved": ATTN_ROPE_INTERLEAVED}
+ATTN_ROPE_SCALE_NONE = 0
+ATTN_ROPE_SCALE_LINEAR = 1
+ATTN_ROPE_SCALE_BASE = 2
+ATTN_ROPE_SCALE_TURNS = 3
+ATTN_ROPE_SCALE_INDEX = 4
 
 
 class attn_rope(ctypes.Structure):
@@ -184,6 +194,56 @@ class attn_decode_q4_params(ctypes.Structure):
     ]
 
 
+class attn_rope_tables_params(ctypes.Structure):
+    _fields_ = [
+        ("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p),
+        ("rows", ctypes.c_int), ("start", ctypes.c_int), ("rotary_dim", ctypes.c_int), ("scaling", ctypes.c_int),
+        ("base", ctypes.c_double), ("factor", ctypes.c_double), ("context", ctypes.c_double), ("low", ctypes.c_double),
+        ("high", ctypes.c_double), ("amplitude", ctypes.c_double),
+        ("stream", ctypes.c_void_p),
+    ]
+
+
+class attn_kv_append_paged_params(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("kpages", ctypes.c_void_p), ("vpages", ctypes.c_void_p),
+        ("slots", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("q", ctypes.c_void_p), ("q_out", ctypes.c_void_p),
+        ("k_out", ctypes.c_void_p),
+        ("T", ctypes.c_int), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int), ("D", ctypes.c_int),
+        ("page_size", ctypes.c_int), ("num_pages", ctypes.c_int), ("rotary_dim", ctypes.c_int),
+        *((f"{t}_{axis}_stride", ctypes.c_longlong) for t in ("k", "v", "q", "q_out", "k_out")
+          for axis in ("token", "head")),
+        ("rope_cos", ctypes.c_void_p), ("rope_sin", ctypes.c_void_p), ("rope_max_pos", ctypes.c_int),
+        ("rope_style", ctypes.c_int), ("rope_k_out", ctypes.c_void_p),
+        ("stream", ctypes.c_void_p),
+    ]
+
+
+class attn_decode_multi_paged_params(ctypes.Structure):
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("kpages", ctypes.c_void_p), ("vpages", ctypes.c_void_p),
+        ("block_table", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p), ("cu_new", ctypes.c_void_p),
+        ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+        ("B", ctypes.c_int), ("T", ctypes.c_int), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int), ("D", ctypes.c_int),
+        ("max_new", ctypes.c_int), ("page_size", ctypes.c_int), ("max_pages", ctypes.c_int),
+        ("num_pages", ctypes.c_int), ("scale", ctypes.c_float), ("out_dtype", ctypes.c_int),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_ulonglong),
+        ("stream", ctypes.c_void_p),
+    ]
+
+
+class attn_verify_drafts_params(ctypes.Structure):
+    _fields_ = [
+        ("draft_tokens", ctypes.c_void_p), ("target_probs", ctypes.c_void_p), ("draft_probs", ctypes.c_void_p),
+        ("uniforms", ctypes.c_void_p), ("cu_target", ctypes.c_void_p), ("draft_lens", ctypes.c_void_p),
+        ("kv_lens", ctypes.c_void_p), ("tokens", ctypes.c_void_p), ("accepted", ctypes.c_void_p),
+        ("keep_lens", ctypes.c_void_p),
+        ("B", ctypes.c_int), ("K", ctypes.c_int), ("V", ctypes.c_int), ("total", ctypes.c_int), ("dtype", ctypes.c_int),
+        *((f"{t}_{axis}_stride", ctypes.c_longlong) for t in ("target", "draft") for axis in ("sequence", "row")),
+        ("stream", ctypes.c_void_p),
+    ]
+
+
 _lib = None
 _lock = threading.Lock()
 
@@ -230,6 +290,14 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.attn_decode_q4.restype = I
         lib.attn_decode_q4_workspace_bytes.argtypes = [I, I, I, I]
         lib.attn_decode_q4_workspace_bytes.restype = ctypes.c_ulonglong
+        for name, cls in (("attn_rope_tables", attn_rope_tables_params),
+                          ("attn_kv_append_paged", attn_kv_append_paged_params),
+                          ("attn_decode_multi_paged", attn_decode_multi_paged_params),
+                          ("attn_verify_drafts", attn_verify_drafts_params)):
+            lib[name].argtypes, lib[name].restype = [ctypes.POINTER(cls)], I
+            setattr(lib, name, lib[name])
+        lib.attn_decode_multi_paged_workspace_bytes.argtypes = [I, I, I, I]
+        lib.attn_decode_multi_paged_workspace_bytes.restype = ctypes.c_ulonglong
         lib.attn_get_device_status.argtypes = [P]
         lib.attn_get_device_status.restype = I
         lib.attn_status_string.argtypes = [I]
@@ -522,7 +590,8 @@ def _stream_of(stream, index):
     return _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
 
 
-_CODES = {ctypes.c_void_p: "P", ctypes.c_int: "i", ctypes.c_longlong: "q", ctypes.c_ulonglong: "Q", ctypes.c_float: "f"}
+_CODES = {ctypes.c_void_p: "P", ctypes.c_int: "i", ctypes.c_longlong: "q", ctypes.c_ulonglong: "Q", ctypes.c_float: "f",
+          ctypes.c_double: "d"}
 _entries = {}
 
 
@@ -799,6 +868,213 @@ def attn_decode_q4_workspace(Hq, Hkv, D, Lq=1, device="cuda"):
         if n == 0:
             raise AttnError(ATTN_ERR_INVALID_ARG, "attn_decode_q4_workspace")
         return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+_SCALINGS = {"linear": (ATTN_ROPE_SCALE_LINEAR, 1), "base": (ATTN_ROPE_SCALE_BASE, 1), "turns": (ATTN_ROPE_SCALE_TURNS, 4),
+             "index": (ATTN_ROPE_SCALE_INDEX, 4)}
+
+
+def attn_rope_tables(rows, rotary_dim, base=10000.0, scaling=None, amplitude=1.0, start=0, cos=None, sin=None,
+                     device="cuda", stream=None):
+    """Rotary tables, fp32 [rows, rotary_dim/2] of positions start and on: amplitude times cos and sin of position times
+    base^(-2i/rotary_dim), scaled for long contexts by ``scaling``: ("linear", factor), ("base", factor),
+    ("turns", factor, context, low, high) or ("index", factor, context, low, high).  -> (cos, sin), what ``rope`` takes"""
+    kind, numbers = ATTN_ROPE_SCALE_NONE, ()
+    if scaling is not None:
+        if scaling[0] not in _SCALINGS:
+            raise ValueError(f"scaling must be one of {sorted(_SCALINGS)}, got {scaling[0]!r}")
+        kind, count = _SCALINGS[scaling[0]]
+        numbers = tuple(scaling[1:])
+        if len(numbers) != count:
+            raise ValueError(f"scaling {scaling[0]!r} takes {count} numbers, got {len(numbers)}")
+    rows, rotary_dim, start = int(rows), int(rotary_dim), int(start)
+    if rows < 0 or rotary_dim < 2 or rotary_dim % 2:
+        raise ValueError(f"rope tables of {rows} rows and {rotary_dim} dims")
+    shape = (rows, rotary_dim // 2)
+    if cos is None:
+        cos = torch.empty(shape, dtype=torch.float32, device=device if sin is None else sin.device)
+    if sin is None:
+        sin = torch.empty(shape, dtype=torch.float32, device=cos.device)
+    at = cos.get_device() if isinstance(cos, torch.Tensor) else -1
+    _call("attn_rope_tables", attn_rope_tables_params, at,
+          _fit(cos, "cos", torch.float32, shape, at), _fit(sin, "sin", torch.float32, shape, at),
+          rows, start, rotary_dim, kind, base, *(numbers + (1.0,) * (4 - len(numbers))), amplitude,
+          _stream_of(stream, at))
+    return cos, sin
+
+
+def attn_kv_append_paged(k, v, kpages, vpages, slots, rope=None, positions=None, q=None, q_out=None, k_out=None,
+                         want_k=False, stream=None):
+    """Rows k and v [T,Hkv,D] bf16 (any strides over contiguous rows) into the pages [num_pages,Hkv,page_size,D] at slots
+    int32 [T] (-1: not written; the others must differ), k rotated by rope = (cos, sin, style) with tables
+    [max_pos, R/2], R <= D, at positions int32 [T] (-1: a padded token, left out), and q [T,Hq,D], where given, rotated
+    alike.  k_out (made where ``want_k``) takes the rotated k packed.  q_out/k_out may be q/k themselves.
+    -> (q_out, k_out)"""
+    sk, at = _rows(k, "k", 3), k.get_device()
+    sv = _rows(v, "v", 3, at)
+    T, Hkv, D = k.shape
+    if v.shape != k.shape:
+        raise ValueError(f"k/v shapes {tuple(k.shape)} {tuple(v.shape)} differ")
+    if not isinstance(kpages, torch.Tensor) or kpages.dim() != 4:
+        raise ValueError("kpages must be a tensor [num_pages,Hkv,page_size,D]")
+    num_pages, _, page_size, _ = kpages.shape
+    pool = (num_pages, Hkv, page_size, D)
+    R, Hq, qp, qop, kop = 0, 0, 0, 0, 0
+    sq = sqo = sko = (0, 0)
+    r = _NO_ROPE
+    if rope is None:
+        if q is not None or q_out is not None or k_out is not None or want_k:
+            raise ValueError("q and k_out go with a rotation")
+    else:
+        if len(rope) > 3 and rope[3] is not None:
+            raise ValueError("rope k_out is taken by prefill calls only")
+        cos, sin, style = rope[:3]
+        if style not in _ROPE_STYLES:
+            raise ValueError("rope style must be 'half' or 'interleaved'")
+        tab = tuple(cos.shape) if isinstance(cos, torch.Tensor) and cos.dim() == 2 else (0, 0)
+        if tab[0] == 0 or tab[1] == 0:
+            raise ValueError("rope tables must be [max_pos, R/2] and have rows")
+        R = 2 * tab[1]
+        r = (_fit(cos, "rope cos", torch.float32, tab, at), _fit(sin, "rope sin", torch.float32, tab, at), tab[0],
+             _ROPE_STYLES[style], 0)
+        if q is not None:
+            sq = _rows(q, "q", 3, at)
+            Hq = q.shape[1]
+            if q.shape != (T, Hq, D) or Hq == 0:
+                raise ValueError(f"q shape {tuple(q.shape)} does not match k {tuple(k.shape)}")
+            if q_out is None:
+                q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+            sqo = _out_rows(q_out, "q_out", q, 3, at)
+            qp, qop = q.data_ptr(), q_out.data_ptr()
+        elif q_out is not None:
+            raise ValueError("q_out goes with q")
+        if k_out is None and want_k:
+            k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=k.device)
+        if k_out is not None:
+            sko = _out_rows(k_out, "k_out", k, 3, at)
+            kop = k_out.data_ptr()
+    _call("attn_kv_append_paged", attn_kv_append_paged_params, at,
+          k.data_ptr(), v.data_ptr(), _fit(kpages, "kpages", torch.bfloat16, pool, at),
+          _fit(vpages, "vpages", torch.bfloat16, pool, at), _fit(slots, "slots", torch.int32, (T,), at),
+          0 if positions is None else _fit(positions, "positions", torch.int32, (T,), at), qp, qop, kop,
+          T, Hq, Hkv, D, page_size, num_pages, R,
+          sk[0], sk[1], sv[0], sv[1], sq[0], sq[1], sqo[0], sqo[1], sko[0], sko[1], *r, _stream_of(stream, at))
+    return q_out, k_out
+
+
+def attn_decode_multi_paged(q, kpages, vpages, block_table, kv_lens, cu_new, max_new, out=None, lse=None, scale=None,
+                            out_dtype=torch.bfloat16, want_lse=True, workspace=None, stream=None):
+    """Decode of several new tokens of each sequence over pages [num_pages,Hkv,page_size,D] bf16: q [T,Hq,D] bf16 (already
+    rotated), packed by cu_new int32 [B+1] with at most max_new tokens a sequence; block_table int32 [B,max_pages],
+    kv_lens int32 [B] counting the new tokens' own keys.  ``workspace`` is a buffer from
+    attn_decode_multi_paged_workspace; without one the library's is used.  Rows of no sequence stay as they were.
+    -> (out [T,Hq,D], lse [T,Hq])"""
+    _need(q, "q", torch.bfloat16, 3)
+    at = q.get_device()
+    T, Hq, D = q.shape
+    if not isinstance(kpages, torch.Tensor) or kpages.dim() != 4:
+        raise ValueError("kpages must be a tensor [num_pages,Hkv,page_size,D]")
+    num_pages, Hkv, page_size, _ = kpages.shape
+    pool = (num_pages, Hkv, page_size, D)
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("out must be bf16 or fp32")
+    B = kv_lens.shape[0] if isinstance(kv_lens, torch.Tensor) and kv_lens.dim() else 0
+    width = block_table.shape[-1] if isinstance(block_table, torch.Tensor) and block_table.dim() else 0
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=out_dtype, device=q.device)
+    if lse is None and want_lse:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+    if workspace is not None:
+        _need(workspace, "workspace", torch.uint8, 1, device=q.device)
+    i32 = torch.int32
+    _call("attn_decode_multi_paged", attn_decode_multi_paged_params, at,
+          q.data_ptr(), _fit(kpages, "kpages", torch.bfloat16, pool, at),
+          _fit(vpages, "vpages", torch.bfloat16, pool, at), _fit(block_table, "block_table", i32, (B, width), at),
+          _fit(kv_lens, "kv_lens", i32, (B,), at), _fit(cu_new, "cu_new", i32, (B + 1,), at),
+          _fit(out, "out", out_dtype, (T, Hq, D), at), 0 if lse is None else _fit(lse, "lse", torch.float32, (T, Hq), at),
+          B, T, Hq, Hkv, D, int(max_new), page_size, width, num_pages, 1.0 / math.sqrt(D) if scale is None else scale,
+          ATTN_DTYPE_F32 if out_dtype == torch.float32 else ATTN_DTYPE_BF16,
+          0 if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.shape[0],
+          _stream_of(stream, at))
+    return out, lse
+
+
+def attn_decode_multi_paged_workspace_bytes(Hq, Hkv, max_new, D) -> int:
+    return int(load().attn_decode_multi_paged_workspace_bytes(Hq, Hkv, max_new, D))
+
+
+def attn_decode_multi_paged_workspace(Hq, Hkv, D, max_new, device="cuda"):
+    """A workspace of attn_decode_multi_paged of one's own (uint8, zeroed), for calls or captured graphs that may overlap
+    others on the GPU."""
+    device = torch.device(device)
+    with torch.cuda.device(device):
+        n = attn_decode_multi_paged_workspace_bytes(Hq, Hkv, max_new, D)
+        if n == 0:
+            raise AttnError(ATTN_ERR_INVALID_ARG, "attn_decode_multi_paged_workspace")
+        return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def _prob_rows(t, name, dtype, shape, at):
+    """The strides of a tensor of probabilities whose rows (the last axis) are contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != at or at < 0:
+        raise ValueError(f"{name} must be a CUDA tensor" + (f" on cuda:{at}" if at >= 0 else ""))
+    st = t.stride()
+    if st[-1] != 1 and shape[-1] > 1:
+        raise ValueError(f"{name}: the probabilities of a row must be contiguous")
+    return st
+
+
+def attn_verify_drafts(draft_tokens, target_probs, uniforms, draft_probs=None, cu_target=None, draft_lens=None,
+                       kv_lens=None, tokens=None, accepted=None, keep_lens=None, stream=None):
+    """Which of the drafts [B,K] int32 stand, and the token that follows them.  target_probs, bf16 or fp32: [total,V]
+    packed by cu_target int32 [B+1] (a sequence's drafts and one more row), or [B,K+1,V] with draft_lens int32 [B]
+    (default K); draft_probs [B,K,V] of the same type, or None for drafts that were not drawn; uniforms fp32 [B,K+1] in
+    [0, 1).  tokens [B,K+1] become the standing drafts, the next token, then -1; accepted [B] their number; keep_lens
+    [B], where kv_lens [B] is given, what attn_page_step keeps.  -> (tokens, accepted, keep_lens)"""
+    i32 = torch.int32
+    _need(draft_tokens, "draft_tokens", i32, 2)
+    at = draft_tokens.get_device()
+    B, K = draft_tokens.shape
+    dtype = target_probs.dtype if isinstance(target_probs, torch.Tensor) else None
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("target_probs must be a bf16 or fp32 tensor")
+    if target_probs.dim() == 0:
+        raise ValueError("target_probs must have rows")
+    V = target_probs.shape[-1]
+    if cu_target is not None:
+        if draft_lens is not None:
+            raise ValueError("draft_lens goes without cu_target")
+        total = target_probs.shape[0]
+        ts = (0, _prob_rows(target_probs, "target_probs", dtype, (total, V), at)[0])
+    else:
+        total = 0
+        ts = _prob_rows(target_probs, "target_probs", dtype, (B, K + 1, V), at)[:2]
+    ds = (0, 0) if draft_probs is None else _prob_rows(draft_probs, "draft_probs", dtype, (B, K, V), at)[:2]
+    if tokens is None:
+        tokens = torch.empty((B, K + 1), dtype=i32, device=draft_tokens.device)
+    if accepted is None:
+        accepted = torch.empty((B,), dtype=i32, device=draft_tokens.device)
+    if keep_lens is None and kv_lens is not None:
+        keep_lens = torch.empty((B,), dtype=i32, device=draft_tokens.device)
+    if keep_lens is not None and kv_lens is None:
+        raise ValueError("keep_lens goes with kv_lens")
+    _call("attn_verify_drafts", attn_verify_drafts_params, at,
+          draft_tokens.data_ptr(), target_probs.data_ptr(), 0 if draft_probs is None else draft_probs.data_ptr(),
+          _fit(uniforms, "uniforms", torch.float32, (B, K + 1), at),
+          0 if cu_target is None else _fit(cu_target, "cu_target", i32, (B + 1,), at),
+          0 if draft_lens is None else _fit(draft_lens, "draft_lens", i32, (B,), at),
+          0 if kv_lens is None else _fit(kv_lens, "kv_lens", i32, (B,), at),
+          _fit(tokens, "tokens", i32, (B, K + 1), at), _fit(accepted, "accepted", i32, (B,), at),
+          0 if keep_lens is None else _fit(keep_lens, "keep_lens", i32, (B,), at),
+          B, K, V, total, ATTN_DTYPE_F32 if dtype == torch.float32 else ATTN_DTYPE_BF16, *ts, *ds,
+          _stream_of(stream, at))
+    return tokens, accepted, keep_lens
 
 
 def attn_decode_workspace_bytes(B, Hq, Hkv, Lmax, D, chunk=0) -> int:

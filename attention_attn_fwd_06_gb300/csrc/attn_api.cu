@@ -36,6 +36,8 @@ struct DeviceState {
   size_t ws_bytes = 0;
   void* ws_q4 = nullptr;  // attn_decode_q4's partials: all zeros between calls
   size_t ws_q4_bytes = 0;
+  void* ws_paged = nullptr;  // attn_decode_multi_paged's counters and partials
+  size_t ws_paged_bytes = 0;
 };
 
 std::mutex g_mu;
@@ -276,6 +278,45 @@ int validate_decode_q4_heads(int Hq, int Hkv, int Lq, int D) {
   if (D != 64 && D != 128) return ATTN_ERR_UNSUPPORTED;
   if ((long long)(Hq / Hkv) * Lq > 128) return ATTN_ERR_UNSUPPORTED;
   return ATTN_OK;
+}
+
+// Counters, then two partials (rows of O, and of maximum and sum) for each CTA.
+struct DecodeMultiShape {
+  size_t part_o_elems = 0;
+  size_t bytes = 0;
+};
+DecodeMultiShape decode_multi_shape(long long rows, int D, int num_sms) {
+  DecodeMultiShape s;
+  const size_t slots = (size_t)2 * attn::decode_multi_grid(num_sms);
+  s.part_o_elems = slots * (size_t)rows * D;
+  s.bytes = kCounterBytes + (s.part_o_elems + slots * (size_t)rows * 2) * sizeof(float);
+  return s;
+}
+
+constexpr double kTwoPi = 6.283185307179586476925286766559;
+
+double rope_base(const attn_rope_tables_params& p) {
+  const double R = p.rotary_dim;
+  return p.scaling == ATTN_ROPE_SCALE_BASE ? p.base * std::pow(p.factor, R / (R - 2)) : p.base;
+}
+
+// Radians a position of pair i of a rotary table (attn_rope_tables), sizes checked.
+double rope_frequency(const attn_rope_tables_params& p, int i) {
+  const double R = p.rotary_dim, base = rope_base(p);
+  const double f = std::pow(base, -2.0 * i / R);
+  double keep = 1.0;  // the share of the pair's speed that stays as it is
+  if (p.scaling == ATTN_ROPE_SCALE_LINEAR) {
+    keep = 0.0;
+  } else if (p.scaling == ATTN_ROPE_SCALE_TURNS) {
+    keep = (p.context * f / kTwoPi - p.low) / (p.high - p.low);
+  } else if (p.scaling == ATTN_ROPE_SCALE_INDEX) {
+    const double per = R / 2 / std::log(base);
+    const double a = std::fmax(0.0, std::floor(per * std::log(p.context / (kTwoPi * p.high))));
+    const double b = std::fmin(R - 1, std::ceil(per * std::log(p.context / (kTwoPi * p.low))));
+    keep = 1.0 - (i - a) / std::fmax(b - a, 0.001);
+  }
+  keep = std::fmin(1.0, std::fmax(0.0, keep));
+  return f * keep + f * (1.0 - keep) / p.factor;
 }
 
 bool is_empty_fwd(const attn_fwd_params* p) {
@@ -541,10 +582,8 @@ int attn_decode_multi(const attn_decode_multi_params* p) {
   DeviceState* s = nullptr;
   st = device_state_locked(&s);
   if (st != ATTN_OK) return st;
-  const size_t slots = (size_t)2 * attn::decode_multi_grid(s->num_sms);
-  const size_t part_o_elems = slots * (size_t)rows * p->D;
-  const size_t part_ml_elems = slots * (size_t)rows * 2;
-  st = ensure_workspace_locked(*s, kCounterBytes + (part_o_elems + part_ml_elems) * sizeof(float), stream);
+  const DecodeMultiShape sh = decode_multi_shape(rows, p->D, s->num_sms);
+  st = ensure_workspace_locked(*s, sh.bytes, stream);
   if (st != ATTN_OK) return st;
   attn::DecodeMultiLaunch L{};
   L.q = p->q;
@@ -555,7 +594,7 @@ int attn_decode_multi(const attn_decode_multi_params* p) {
   L.lse = p->lse;
   L.counters = static_cast<unsigned*>(s->ws);
   L.part_o = reinterpret_cast<float*>(static_cast<char*>(s->ws) + kCounterBytes);
-  L.part_ml = L.part_o + part_o_elems;
+  L.part_ml = L.part_o + sh.part_o_elems;
   L.B = p->B;
   L.Hq = p->Hq;
   L.Hkv = p->Hkv;
@@ -924,6 +963,220 @@ int attn_decode_q4(const attn_decode_q4_params* p) {
   return map_cuda(attn::launch_decode_q4(L));
 }
 
+int attn_rope_tables(const attn_rope_tables_params* p) {
+  if (p == nullptr) return ATTN_ERR_INVALID_ARG;
+  if (p->rows < 0 || p->start < 0 || p->rotary_dim <= 0) return ATTN_ERR_INVALID_ARG;
+  if (p->scaling < ATTN_ROPE_SCALE_NONE || p->scaling > ATTN_ROPE_SCALE_INDEX) return ATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(p->base) || p->base <= 1.0 || !std::isfinite((float)p->amplitude)) return ATTN_ERR_INVALID_ARG;
+  if (p->scaling != ATTN_ROPE_SCALE_NONE && (!std::isfinite(p->factor) || p->factor <= 0.0)) return ATTN_ERR_INVALID_ARG;
+  if ((p->scaling == ATTN_ROPE_SCALE_TURNS || p->scaling == ATTN_ROPE_SCALE_INDEX) &&
+      !(std::isfinite(p->context) && p->context > 0.0 && p->low > 0.0 && p->high > p->low && std::isfinite(p->high)))
+    return ATTN_ERR_INVALID_ARG;
+  if (p->rotary_dim % 16 != 0 || p->rotary_dim > 2 * attn::kMaxRotaryPairs) return ATTN_ERR_UNSUPPORTED;
+  if (!std::isfinite(rope_base(*p)) || rope_base(*p) <= 1.0) return ATTN_ERR_INVALID_ARG;
+  if ((long long)p->start + p->rows > kIntMax) return ATTN_ERR_UNSUPPORTED;
+  if (p->rows == 0) return ATTN_OK;
+  if (p->cos == nullptr || p->sin == nullptr) return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(p->cos) || !aligned16(p->sin)) return ATTN_ERR_ALIGNMENT;
+  attn::RopeTablesLaunch L{};
+  L.pairs = p->rotary_dim / 2;
+  for (int i = 0; i < L.pairs; ++i) {
+    const double turn = rope_frequency(*p, i) / kTwoPi;
+    const double part = turn - std::floor(turn);  // whole turns a position say nothing (a factor below 1)
+    if (!std::isfinite(part)) return ATTN_ERR_INVALID_ARG;
+    L.turn[i] = part >= 0.5 ? (unsigned long long)((part - 0.5) * 0x1p64 + 0.5) + (1ull << 63)
+                            : (unsigned long long)(part * 0x1p64 + 0.5);
+  }
+  DeviceState* s = nullptr;
+  const int st = device_state(&s);
+  if (st != ATTN_OK) return st;
+  L.cos = p->cos;
+  L.sin = p->sin;
+  L.rows = p->rows;
+  L.start = p->start;
+  L.amplitude = (float)p->amplitude;
+  L.num_sms = s->num_sms;
+  L.stream = static_cast<cudaStream_t>(p->stream);
+  return map_cuda(attn::launch_rope_tables(L));
+}
+
+int attn_kv_append_paged(const attn_kv_append_paged_params* p) {
+  if (p == nullptr) return ATTN_ERR_INVALID_ARG;
+  if (p->T < 0 || p->Hq < 0 || p->Hkv <= 0 || p->D <= 0 || p->page_size < 1 || p->num_pages < 1)
+    return ATTN_ERR_INVALID_ARG;
+  if (p->D != 64 && p->D != 128) return ATTN_ERR_UNSUPPORTED;
+  const bool rope_on = p->rope.style != ATTN_ROPE_NONE && p->rope.cos != nullptr;
+  int st = validate_rope(p->rope, rope_on ? p->rotary_dim : p->D, 0);
+  if (st != ATTN_OK) return st;
+  if (rope_on && p->rotary_dim <= 0) return ATTN_ERR_INVALID_ARG;
+  if (rope_on && (p->rotary_dim % 16 != 0 || p->rotary_dim > p->D)) return ATTN_ERR_UNSUPPORTED;
+  if ((p->q == nullptr) != (p->q_out == nullptr) || (p->q == nullptr) != (p->Hq == 0)) {
+    if (p->T > 0) return ATTN_ERR_INVALID_ARG;
+  }
+  if (!rope_on && (p->q != nullptr || p->k_out != nullptr)) return ATTN_ERR_INVALID_ARG;
+  if ((long long)p->num_pages * p->page_size > kIntMax || (long long)p->Hq + 2ll * p->Hkv > 65535)
+    return ATTN_ERR_UNSUPPORTED;
+  if (p->T == 0) return ATTN_OK;
+  if (p->k == nullptr || p->v == nullptr || p->kpages == nullptr || p->vpages == nullptr || p->slots == nullptr ||
+      (rope_on && p->positions == nullptr))
+    return ATTN_ERR_INVALID_ARG;
+  attn::KvAppendPagedLaunch L{};
+  const int extent[2] = {p->T, p->Hkv}, q_extent[2] = {p->T, p->Hq};
+  if (!aligned16(p->k) || !aligned16(p->v) || !aligned16(p->kpages) || !aligned16(p->vpages) || !aligned16(p->q) ||
+      !aligned16(p->q_out) || !aligned16(p->k_out) || !aligned4(p->slots) || !aligned4(p->positions) ||
+      !take_strides8(p->k_stride, extent, 2, L.ks) || !take_strides8(p->v_stride, extent, 2, L.vs))
+    return ATTN_ERR_ALIGNMENT;
+  if (p->q != nullptr && (!take_strides8(p->q_stride, q_extent, 2, L.qs) || !take_strides8(p->q_out_stride, q_extent, 2, L.qos)))
+    return ATTN_ERR_ALIGNMENT;
+  if (p->k_out != nullptr && !take_strides8(p->k_out_stride, extent, 2, L.kos)) return ATTN_ERR_ALIGNMENT;
+  DeviceState* s = nullptr;
+  st = device_state(&s);
+  if (st != ATTN_OK) return st;
+  L.k = p->k;
+  L.v = p->v;
+  L.q = p->q;
+  L.kpages = p->kpages;
+  L.vpages = p->vpages;
+  L.q_out = p->q_out;
+  L.k_out = p->k_out;
+  L.slots = p->slots;
+  L.positions = p->positions;
+  L.T = p->T;
+  L.Hq = p->Hq;
+  L.Hkv = p->Hkv;
+  L.D = p->D;
+  L.page_size = p->page_size;
+  L.num_pages = p->num_pages;
+  L.rotary = rope_on ? p->rotary_dim : 0;
+  L.rope = rope_args(p->rope);
+  L.num_sms = s->num_sms;
+  L.status = s->status;
+  L.stream = static_cast<cudaStream_t>(p->stream);
+  return map_cuda(attn::launch_kv_append_paged(L));
+}
+
+unsigned long long attn_decode_multi_paged_workspace_bytes(int Hq, int Hkv, int max_new, int D) {
+  if (validate_decode_q4_heads(Hq, Hkv, max_new, D) != ATTN_OK) return 0;
+  DeviceState* s = nullptr;
+  const int sms = device_state(&s) == ATTN_OK ? s->num_sms : 0;
+  return decode_multi_shape((long long)(Hq / Hkv) * max_new, D, sms).bytes;
+}
+
+int attn_decode_multi_paged(const attn_decode_multi_paged_params* p) {
+  if (p == nullptr) return ATTN_ERR_INVALID_ARG;
+  int st = validate_decode_q4_heads(p->Hq, p->Hkv, p->max_new, p->D);  // (the same limits: 128 query rows a kv head)
+  if (st != ATTN_OK) return st;
+  if (p->B < 0 || p->T < 0 || p->page_size < 8 || p->page_size > 65536 || p->max_pages < 1 || p->num_pages < 1)
+    return ATTN_ERR_INVALID_ARG;
+  if (p->out_dtype != ATTN_DTYPE_BF16 && p->out_dtype != ATTN_DTYPE_F32) return ATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(p->scale)) return ATTN_ERR_INVALID_ARG;
+  if (p->page_size % 8 != 0) return ATTN_ERR_UNSUPPORTED;
+  // (a tile's keys past the last one stay countable: up to 127 more)
+  if ((long long)p->max_pages * p->page_size > kIntMax - 128 || (long long)p->num_pages * p->Hkv > kIntMax ||
+      (long long)p->T * p->Hq > kIntMax)
+    return ATTN_ERR_UNSUPPORTED;
+  if (p->B == 0 || p->T == 0) return ATTN_OK;
+  if (p->q == nullptr || p->kpages == nullptr || p->vpages == nullptr || p->block_table == nullptr ||
+      p->kv_lens == nullptr || p->cu_new == nullptr || p->out == nullptr)
+    return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(p->q) || !aligned16(p->kpages) || !aligned16(p->vpages) || !aligned16(p->out) ||
+      !aligned16(p->workspace) || !aligned4(p->block_table) || !aligned4(p->kv_lens) || !aligned4(p->cu_new) ||
+      !aligned4(p->lse))
+    return ATTN_ERR_ALIGNMENT;
+  if (2 + (long long)p->B * p->Hkv > attn::kDecodeCounterSlots) return ATTN_ERR_UNSUPPORTED;
+  cudaStream_t stream = static_cast<cudaStream_t>(p->stream);
+  std::lock_guard<std::mutex> lock(g_mu);
+  DeviceState* s = nullptr;
+  st = device_state_locked(&s);
+  if (st != ATTN_OK) return st;
+  const DecodeMultiShape sh = decode_multi_shape((long long)(p->Hq / p->Hkv) * p->max_new, p->D, s->num_sms);
+  char* ws = static_cast<char*>(p->workspace);
+  if (ws == nullptr) {
+    // made for the largest call, so that it never has to grow under a graph that was captured with it
+    st = ensure_buffer_locked(s->ws_paged, s->ws_paged_bytes, decode_multi_shape(128, 128, s->num_sms).bytes, kCounterBytes,
+                              stream);
+    if (st != ATTN_OK) return st;
+    ws = static_cast<char*>(s->ws_paged);
+  } else if (p->workspace_bytes < sh.bytes) {
+    return ATTN_ERR_SCRATCH_TOO_SMALL;
+  }
+  attn::DecodeMultiLaunch L{};
+  L.q = p->q;
+  L.kcache = p->kpages;
+  L.vcache = p->vpages;
+  L.block_table = p->block_table;
+  L.cu_new = p->cu_new;
+  L.T = p->T;
+  L.page_size = p->page_size;
+  L.max_pages = p->max_pages;
+  L.num_pages = p->num_pages;
+  L.kv_lens = p->kv_lens;
+  L.out = p->out;
+  L.lse = p->lse;
+  L.counters = reinterpret_cast<unsigned*>(ws);
+  L.part_o = reinterpret_cast<float*>(ws + kCounterBytes);
+  L.part_ml = L.part_o + sh.part_o_elems;
+  L.B = p->B;
+  L.Hq = p->Hq;
+  L.Hkv = p->Hkv;
+  L.Lq = p->max_new;
+  L.Lmax = p->max_pages * p->page_size;
+  L.D = p->D;
+  L.scale = p->scale;
+  L.out_f32 = p->out_dtype == ATTN_DTYPE_F32;
+  L.num_sms = s->num_sms;
+  L.status = s->status;
+  L.fault_skip_arrive = fault_skip_arrive();
+  L.stream = stream;
+  return map_cuda(attn::launch_decode_multi(L));
+}
+
+int attn_verify_drafts(const attn_verify_drafts_params* p) {
+  if (p == nullptr) return ATTN_ERR_INVALID_ARG;
+  if (p->B < 0 || p->K < 0 || p->V < 1 || (p->cu_target != nullptr && p->total < 0)) return ATTN_ERR_INVALID_ARG;
+  if (p->dtype != ATTN_DTYPE_BF16 && p->dtype != ATTN_DTYPE_F32) return ATTN_ERR_INVALID_ARG;
+  if (p->K >= (1 << 20) || p->V >= (1 << 30) || (long long)p->B * (p->K + 1) >= (1 << 28)) return ATTN_ERR_UNSUPPORTED;
+  if (p->B == 0) return ATTN_OK;
+  // (with cu_target and no rows at all no sequence has any, and the probabilities are never read)
+  if ((p->target_probs == nullptr && (p->cu_target == nullptr || p->total > 0)) || p->uniforms == nullptr ||
+      p->tokens == nullptr || p->accepted == nullptr || (p->K > 0 && p->draft_tokens == nullptr) ||
+      (p->kv_lens == nullptr) != (p->keep_lens == nullptr))
+    return ATTN_ERR_INVALID_ARG;
+  const unsigned mask = p->dtype == ATTN_DTYPE_F32 ? 3u : 1u;
+  if ((reinterpret_cast<uintptr_t>(p->target_probs) & mask) || (reinterpret_cast<uintptr_t>(p->draft_probs) & mask) ||
+      !aligned4(p->draft_tokens) || !aligned4(p->uniforms) || !aligned4(p->cu_target) || !aligned4(p->draft_lens) ||
+      !aligned4(p->kv_lens) || !aligned4(p->tokens) || !aligned4(p->accepted) || !aligned4(p->keep_lens))
+    return ATTN_ERR_ALIGNMENT;
+  DeviceState* s = nullptr;
+  const int st = device_state(&s);
+  if (st != ATTN_OK) return st;
+  attn::VerifyDraftsLaunch L{};
+  L.drafts = p->draft_tokens;
+  L.target = p->target_probs;
+  L.draft = p->K > 0 ? p->draft_probs : nullptr;
+  L.uniforms = p->uniforms;
+  L.cu = p->cu_target;
+  L.draft_lens = p->cu_target == nullptr ? p->draft_lens : nullptr;
+  L.kv_lens = p->kv_lens;
+  L.tokens = p->tokens;
+  L.accepted = p->accepted;
+  L.keep_lens = p->keep_lens;
+  L.B = p->B;
+  L.K = p->K;
+  L.V = p->V;
+  L.total = p->total;
+  L.f32 = p->dtype == ATTN_DTYPE_F32;
+  // the strides of axes of one element say nothing
+  L.ts[0] = p->cu_target == nullptr && p->B > 1 ? p->target_stride[0] : 0;
+  L.ts[1] = (p->cu_target == nullptr ? p->K + 1 : p->total) > 1 ? p->target_stride[1] : 0;
+  L.ds[0] = p->B > 1 ? p->draft_stride[0] : 0;
+  L.ds[1] = p->K > 1 ? p->draft_stride[1] : 0;
+  L.num_sms = s->num_sms;
+  L.status = s->status;
+  L.stream = static_cast<cudaStream_t>(p->stream);
+  return map_cuda(attn::launch_verify_drafts(L));
+}
+
 int attn_get_device_status(void* stream) {
   std::lock_guard<std::mutex> lock(g_mu);
   DeviceState* s = nullptr;
@@ -945,6 +1198,7 @@ int attn_get_device_status(void* stream) {
     cudaDeviceSynchronize();
     if (s->ws != nullptr) cudaMemset(s->ws, 0, kCounterBytes);
     if (s->ws_q4 != nullptr) cudaMemset(s->ws_q4, 0, s->ws_q4_bytes);
+    if (s->ws_paged != nullptr) cudaMemset(s->ws_paged, 0, kCounterBytes);
     if (dev >= 0 && dev < kMaxDevices && g_noalloc_ptr[dev] != nullptr) cudaMemset(g_noalloc_ptr[dev], 0, kCounterBytes);
     cudaDeviceSynchronize();
     cudaGetLastError();
@@ -966,6 +1220,9 @@ void attn_release_workspace(void) {
   if (s.ws_q4 != nullptr) cudaFree(s.ws_q4);
   s.ws_q4 = nullptr;
   s.ws_q4_bytes = 0;
+  if (s.ws_paged != nullptr) cudaFree(s.ws_paged);
+  s.ws_paged = nullptr;
+  s.ws_paged_bytes = 0;
 }
 
 }  // extern "C"

@@ -1,5 +1,6 @@
 // decode_multi.cu -- decode of several new tokens per sequence (multi-token or
-// speculative decode) over a KV cache, on the 5th-generation tensor cores.
+// speculative decode) over a KV cache, contiguous or in pages, on the 5th-generation
+// tensor cores.
 //
 // What it computes: rows 0..n-1 of sequence b's cache (n = kv_lens[b]) hold
 // all of its keys, the Lq new tokens' own keys being the last Lq of them; new
@@ -33,6 +34,15 @@
 //    n - 128, its keys below the previous tile's end are masked out, and
 //    before key 0 the TMA box reads zeros.  No cache row at or past kv_len is
 //    read, so whatever those rows hold cannot reach O through 0 * NaN.
+//  * Over pages (PAGED) a tile comes as boxes of gcd(page_size, 128) rows, a lane
+//    of the TMA warp for each box and 64-column block: every box lies in one page
+//    and on whole 8-row swizzle groups.  Tiles stay on multiples of 128 keys (a
+//    tile that ended at key n would not meet the boxes); boxes past n are not
+//    loaded, and the softmax threads zero the last tile's V rows past n before the
+//    MMA warp reads them, so stale rows cannot reach O there either.  The next
+//    tile's page ids are read while the ring's slots are waited for.  q and out
+//    are packed [T, Hq, D], and a tile's rows are (token, head), which the box
+//    (64 columns, GP heads, max_new tokens) of a (D, Hq, T) map brings in order.
 //  * A piece holding a whole item writes O / l and the log-sum-exp directly;
 //    otherwise it writes (O, m, l) to its partial slot and the CTA that lands
 //    an item's last partial (per-item counter, reset by that CTA) merges them.
@@ -111,14 +121,44 @@ struct MultiArgs {
   unsigned* status;
   RopeArgs rope;       // style != 0: the softmax threads rotate the Q tile's rows before the S MMAs
   int fault_skip_arrive;  // test hook: CTA 0 withholds one P-ready arrival (its MMA warp's wait runs out)
+  // PAGED only (Lq: the most new tokens of a sequence, Lmax: max_pages * page_size)
+  const int* block_table;
+  const int* cu_new;   // [B + 1]: tokens of sequence b are rows cu_new[b] .. cu_new[b + 1] - 1 of q and out
+  int T, max_pages, num_pages;
+  int box_rows;        // gcd(page_size, 128)
+  FastDiv page;        // by page_size
 };
 
 __device__ __forceinline__ int clamp_len(int len, int Lmax) { return len < 0 ? 0 : (len > Lmax ? Lmax : len); }
 __device__ __forceinline__ int tiles_of(int n) { return (n + BN - 1) / BN; }
 
+// What sequence b has to do: its keys, and (PAGED) where its new tokens start and how many they are.  Without new tokens
+// there is nothing to do, whatever it holds; offsets that fall, leave [0, T] or give more than Lq tokens count as none.
+struct Seq {
+  int n, q0, nq;
+};
+template <bool PAGED>
+__device__ __forceinline__ Seq load_seq(const MultiArgs& a, int b, bool flag) {
+  Seq s{0, 0, a.Lq};
+  const int raw = a.kv_lens[b];
+  s.n = clamp_len(raw, a.Lmax);
+  bool bad = raw != s.n;
+  if constexpr (PAGED) {
+    const int q0 = a.cu_new[b], q1 = a.cu_new[b + 1];
+    const bool ok = q0 >= 0 && q1 >= q0 && q1 <= a.T && q1 - q0 <= a.Lq;
+    bad = bad || !ok;
+    s.q0 = q0;
+    s.nq = ok ? q1 - q0 : 0;
+    if (s.nq == 0) s.n = 0;
+  }
+  if (bad && flag) record_status(a.status, ATTN_ERR_DEVICE_BOUNDS);
+  return s;
+}
+
 // One piece of work: tiles [t0, t1) of item (b, hk), whose sequence has n keys in T tiles.
 struct Piece {
   int b, hk, n, T, t0, t1;
+  int q0, nq;  // PAGED: the sequence's first row of q, its new tokens
   int np;      // CTAs holding a piece of the item (1: the whole item is here)
   int slot;    // this CTA's partial slot for the piece
   int cta_lo;  // first CTA holding a piece of the item
@@ -141,16 +181,16 @@ constexpr int kItemCost = ATTN_DMULTI_ITEM_COST;
 struct Walk {
   long long per, lo, hi, pos, start;  // start: first cost position of the current item
   int b, hk, n, T;
+  int q0, nq;
 };
 
 // Warp-cooperative set-up: every lane of the calling warp must call it; all lanes get the same walk.
+template <bool PAGED>
 __device__ Walk walk_init(const MultiArgs& a, int lane) {
   Walk w;
   long long part = 0;
   for (int b = lane; b < a.B; b += 32) {
-    const int raw = a.kv_lens[b];
-    const int n = clamp_len(raw, a.Lmax);
-    if (raw != n && blockIdx.x == 0) record_status(a.status, ATTN_ERR_DEVICE_BOUNDS);
+    const int n = load_seq<PAGED>(a, b, blockIdx.x == 0).n;
     part += n > 0 ? tiles_of(n) + kItemCost : 0;
   }
 #pragma unroll
@@ -166,6 +206,8 @@ __device__ Walk walk_init(const MultiArgs& a, int lane) {
   w.hk = 0;
   w.n = 0;
   w.T = 0;
+  w.q0 = 0;
+  w.nq = 0;
   w.start = 0;
   if (w.lo >= w.hi) {
     w.pos = w.hi;
@@ -177,7 +219,7 @@ __device__ Walk walk_init(const MultiArgs& a, int lane) {
     const int b = c0 + lane;
     long long v = 0;
     if (b < a.B) {
-      const int n = clamp_len(a.kv_lens[b], a.Lmax);
+      const int n = load_seq<PAGED>(a, b, false).n;
       v = n > 0 ? (long long)(tiles_of(n) + kItemCost) * a.Hkv : 0;
     }
     long long incl = v;
@@ -192,7 +234,10 @@ __device__ Walk walk_init(const MultiArgs& a, int lane) {
       const int src = __ffs(hit) - 1;
       const long long excl = __shfl_sync(0xffffffffu, incl - v, src);
       w.b = c0 + src;
-      w.n = clamp_len(a.kv_lens[w.b], a.Lmax);
+      const Seq sq = load_seq<PAGED>(a, w.b, false);
+      w.n = sq.n;
+      w.q0 = sq.q0;
+      w.nq = sq.nq;
       w.T = tiles_of(w.n);
       const long long first = base + excl;  // first cost position of sequence w.b
       w.hk = (int)floor_div(w.lo - first, w.T + kItemCost);
@@ -204,6 +249,7 @@ __device__ Walk walk_init(const MultiArgs& a, int lane) {
   return w;
 }
 
+template <bool PAGED>
 __device__ __forceinline__ bool walk_next(Walk& w, const MultiArgs& a, Piece& p) {
   while (w.pos < w.hi) {
     const long long ts = w.start + kItemCost;  // the item's tiles: cost positions [ts, ts + T)
@@ -214,6 +260,8 @@ __device__ __forceinline__ bool walk_next(Walk& w, const MultiArgs& a, Piece& p)
       p.hk = w.hk;
       p.n = w.n;
       p.T = w.T;
+      p.q0 = w.q0;
+      p.nq = w.nq;
       p.t0 = (int)(s - ts);
       p.t1 = (int)(e - ts);
       const long long clo = floor_div(ts, w.per);
@@ -229,7 +277,10 @@ __device__ __forceinline__ bool walk_next(Walk& w, const MultiArgs& a, Piece& p)
       if (++w.hk == a.Hkv) {
         w.hk = 0;
         for (++w.b; w.b < a.B; ++w.b) {
-          w.n = clamp_len(a.kv_lens[w.b], a.Lmax);
+          const Seq sq = load_seq<PAGED>(a, w.b, false);
+          w.n = sq.n;
+          w.q0 = sq.q0;
+          w.nq = sq.nq;
           if (w.n > 0) break;
         }
         if (w.b >= a.B) w.pos = w.hi;  // cannot happen while pos < hi; stop rather than read past kv_lens
@@ -243,6 +294,20 @@ __device__ __forceinline__ bool walk_next(Walk& w, const MultiArgs& a, Piece& p)
 
 // Partial slot of the i-th CTA holding a piece of an item.
 __device__ __forceinline__ int slot_of(const Piece& p, int i) { return 2 * (p.cta_lo + i) + (i == 0 ? p.lo_odd : 0); }
+
+// Row of out (and lse) that row r of the item's tile is, and how many rows of the tile are tokens of the sequence.
+template <bool PAGED>
+__device__ __forceinline__ size_t out_row(const MultiArgs& a, const Piece& p, int r) {
+  if constexpr (PAGED) {
+    const int t = r / a.GP;
+    return (size_t)(p.q0 + t) * a.Hq + p.hk * a.GP + (r - t * a.GP);
+  }
+  return (size_t)(p.b * a.Hq + p.hk * a.GP) * a.Lq + r;
+}
+template <bool PAGED>
+__device__ __forceinline__ int rows_of(const MultiArgs& a, const Piece& p) {
+  return PAGED ? a.GP * p.nq : a.R;
+}
 
 template <int D>
 __device__ __forceinline__ void store_row(const MultiArgs& a, size_t orow, int cc, const uint32_t (&orr)[32],
@@ -267,7 +332,7 @@ __device__ __forceinline__ void store_row(const MultiArgs& a, size_t orow, int c
   }
 }
 
-template <int D>
+template <int D, bool PAGED>
 __global__ void __launch_bounds__(kThreads, 1)
     decode_multi_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                         const __grid_constant__ CUtensorMap tmv, const MultiArgs a) {
@@ -321,10 +386,109 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::fence_after_sync();
   const uint32_t tbase = *tmem_slot;
 
-  Walk walk = walk_init(a, lane);  // every warp, all lanes
+  Walk walk = walk_init<PAGED>(a, lane);  // every warp, all lanes
   Piece pc;
 
-  if (warp == kWarpTMA) {
+  if (PAGED && warp == kWarpTMA) {
+    // ---------------- TMA producer over pages: the whole warp, a box a lane ----------------
+    // The order of loads and waits is that of the contiguous producer below; every decision is the warp's.
+    if constexpr (PAGED) {
+      const uint64_t kv_policy = l2_policy_evict_first();
+      const int box = lane / C::NDB, db = lane % C::NDB;
+      const int boxes = BN / a.box_rows;  // of a whole tile; boxes * NDB <= 32
+      int kv = 0, q_issued = 0;
+      bool q_pending = false, ok = true;
+      int q_head = 0, q_tok = 0;
+      auto issue_q = [&]() {
+        if (lane == 0) {
+          mbar_arrive_expect_tx(q_full, (uint32_t)a.q_box_bytes);
+          for (int d = 0; d < C::NDB; ++d) tc::tma_load_3d(Qs + d * C::BLOCK_BYTES, &tmq, d * 64, q_head, q_tok, q_full);
+        }
+        ++q_issued;
+        q_pending = false;
+      };
+      auto poll_q = [&]() {
+        if (!q_pending) return;
+        if (q_issued == 0 || __all_sync(0xffffffffu, mbar_try_wait(q_empty, (q_issued - 1) & 1))) issue_q();
+      };
+      auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
+        const uint64_t t0 = globaltimer_ns();
+        while (true) {
+          poll_q();
+          if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+          if (__any_sync(0xffffffffu, *abort_flag != 0)) return false;
+          if (__any_sync(0xffffffffu, globaltimer_ns() - t0 > kWaitLimitNs)) {
+            if (lane == 0) record_status(a.status, ATTN_ERR_DEVICE_TIMEOUT);
+            *abort_flag = 1;
+            return false;
+          }
+        }
+      };
+      while (ok && walk_next<PAGED>(walk, a, pc)) {
+        if (q_pending) {  // the previous piece's Q is still waiting for the buffer: it goes first
+          if (!wait_all(q_empty, (q_issued - 1) & 1)) {
+            ok = false;
+            break;
+          }
+          if (q_pending) issue_q();
+        }
+        const int* row = a.block_table + (size_t)pc.b * a.max_pages;
+        // the page of this lane's box of tile tt (entries past the sequence's keys are not read)
+        auto page_of = [&](int tt) -> int {
+          const int key = tt * BN + box * a.box_rows;
+          return (tt < pc.t1 && box < boxes && key < pc.n) ? __ldg(row + a.page.div((unsigned)key)) : 0;
+        };
+        int id = page_of(pc.t0);
+        q_head = pc.hk * a.GP;
+        q_tok = pc.q0;
+        q_pending = true;
+        poll_q();
+        for (int tt = pc.t0; tt < pc.t1; ++tt) {
+          const int slot = kv % C::NS;
+          const int id_next = page_of(tt + 1);
+          const int left = min(BN, pc.n - tt * BN);
+          const int nbox = (left + a.box_rows - 1) / a.box_rows;  // boxes that hold keys
+          const uint32_t bytes = (uint32_t)(nbox * a.box_rows * 128 * C::NDB);
+          const bool mine = box < nbox;
+          const int key = tt * BN + box * a.box_rows;
+          const int off = key - (int)a.page.div((unsigned)key) * (int)a.page.d;
+          if (mine && (id < 0 || id >= a.num_pages)) {
+            record_status(a.status, ATTN_ERR_DEVICE_BOUNDS);
+            id = 0;
+          }
+          const int head = id * a.Hkv + pc.hk;
+          const uint32_t at = slot * C::TILE_BYTES + db * C::BLOCK_BYTES + box * a.box_rows * 128;
+          if (kv >= C::NS && !wait_all(&k_empty[slot], ((kv / C::NS) - 1) & 1)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(&k_full[slot], bytes);
+          __syncwarp();
+          if (mine) tc::tma_load_3d_hint(Ks + at, &tmk, db * 64, off, head, &k_full[slot], kv_policy);
+          if (kv >= C::NS && !wait_all(&v_empty[slot], ((kv / C::NS) - 1) & 1)) {
+            mbar_wait(&k_full[slot], (kv / C::NS) & 1, a.status, nullptr);  // K is in flight: let it land
+            ok = false;
+            break;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(&v_full[slot], bytes);
+          __syncwarp();
+          if (mine) tc::tma_load_3d_hint(Vs + at, &tmv, db * 64, off, head, &v_full[slot], kv_policy);
+          ++kv;
+          id = id_next;
+        }
+      }
+      if (ok && q_pending && wait_all(q_empty, (q_issued - 1) & 1) && q_pending) issue_q();
+      __syncwarp();
+      if (*abort_flag) {  // let in-flight copies land before shared memory is released
+        if (q_issued > 0) mbar_wait(q_full, (q_issued - 1) & 1, a.status, nullptr);
+        for (int g = (kv > C::NS ? kv - C::NS : 0); g < kv; ++g) {
+          mbar_wait(&k_full[g % C::NS], (g / C::NS) & 1, a.status, nullptr);
+          mbar_wait(&v_full[g % C::NS], (g / C::NS) & 1, a.status, nullptr);
+        }
+      }
+      __syncwarp();
+    }
+  } else if (warp == kWarpTMA) {
     // ---------------- TMA producer ----------------
     // A piece's Q load must wait until every S MMA of the previous piece has completed (one Q buffer), but its
     // K/V tiles need only free ring slots: they are issued as soon as slots free up, and the Q load goes out
@@ -360,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       };
-      while (ok && walk_next(walk, a, pc)) {
+      while (ok && walk_next<PAGED>(walk, a, pc)) {
         if (q_pending) {  // the previous piece's Q is still waiting for the buffer: it goes first
           if (!mbar_wait(q_empty, (q_issued - 1) & 1, a.status, abort_flag)) {
             ok = false;
@@ -432,10 +596,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       int g = 0;   // tiles processed before the current piece (global tile index)
       int qj = 0;
       bool ok = true;
-      while (ok && walk_next(walk, a, pc)) {
+      while (ok && walk_next<PAGED>(walk, a, pc)) {
         const int nt = pc.t1 - pc.t0;
         // the piece's Q: landed, and with RoPE rotated by the softmax threads
-        if (!mbar_wait(a.rope.style != 0 ? q_ready : q_full, qj & 1, a.status, abort_flag)) {
+        if (!mbar_wait(!PAGED && a.rope.style != 0 ? q_ready : q_full, qj & 1, a.status, abort_flag)) {
           ok = false;
           break;
         }
@@ -494,19 +658,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
     const uint32_t o_addr = tbase + lane_addr + C::TM_O;
     const float c = a.scale_log2;
-    const int t_row = row % a.Lq;  // which new token this row is (padding rows: meaningless)
+    const int t_row = PAGED ? row / a.GP : row % a.Lq;  // which new token this row is (padding rows: meaningless)
     int g = 0;
     int sp = 0;  // pieces seen (q_full / q_ready phases)
     bool ok = true;
 
     // After a failed wait the softmax threads keep walking their pieces without touching TMEM or waiting, so
     // all of them still pass the same named barriers (a barrier cannot time out).
-    while (walk_next(walk, a, pc)) {
+    while (walk_next<PAGED>(walk, a, pc)) {
       const int nt = pc.t1 - pc.t0;
-      const int horizon = pc.n - a.Lq + t_row;  // last key this row sees
+      const int nq = PAGED ? pc.nq : a.Lq;
+      const int horizon = pc.n - nq + t_row;    // last key this row sees
       float m_ref = -INFINITY;                  // running max, scaled log2 units
       float l = 0.f;
-      if (a.rope.style != 0) {
+      if (!PAGED && a.rope.style != 0) {
         // Rotate this thread's query row to its position n - Lq + t (rows that see no key stay as they are),
         // then hand the tile to the MMA warp.
         if (ok) ok = mbar_wait(q_full, sp & 1, a.status, abort_flag);
@@ -534,11 +699,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::tmem_ld_wait();
 
         const bool last = (tt == pc.T - 1);
-        const int ks = last ? pc.n - BN : tt * BN;  // key of column 0
+        const int ks = last && !PAGED ? pc.n - BN : tt * BN;  // key of column 0
         // The mask acts on the scaled logits (scale, then mask): the factor is positive (a negative scale negates
         // Q in the S MMA), so a raw -inf stays -inf once scaled; with scale == 0 every visible logit is 0.
-        if (last || ks + BN - 1 > pc.n - a.Lq || a.uniform) {
-          const int lo_key = last ? (pc.T - 1) * BN : 0;  // earlier keys belong to the previous tile
+        if (last || ks + BN - 1 > pc.n - nq || a.uniform) {
+          const int lo_key = last && !PAGED ? (pc.T - 1) * BN : 0;  // earlier keys belong to the previous tile
           if (a.uniform) {
 #pragma unroll
             for (int cc = 0; cc < 4; ++cc)
@@ -612,6 +777,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::tmem_st32(o_addr + cc * 32, orr);
           }
         }
+        if constexpr (PAGED) {
+          // V rows past the sequence's keys hold what an earlier tile or another sequence left there: zeros, so that
+          // their weights of 0 do not meet a NaN (0 * NaN), before the P V MMA that this thread's arrival lets go
+          if (last && pc.n < (tt + 1) * BN) {
+            const int slot = gi % C::NS;
+            if (!mbar_wait(&v_full[slot], (gi / C::NS) & 1, a.status, abort_flag)) {
+              ok = false;
+              break;
+            }
+            if (tt * BN + row >= pc.n) {
+#pragma unroll
+              for (int db = 0; db < C::NDB; ++db) {
+                uint4* dst = reinterpret_cast<uint4*>(Vs + slot * C::TILE_BYTES + db * C::BLOCK_BYTES + row * 128);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) dst[(j + lane) & 7] = make_uint4(0, 0, 0, 0);
+              }
+            }
+            fence_proxy_async_smem();  // the tensor cores read the zeros (async proxy)
+          }
+        }
         tc::tmem_st_wait();
         tc::fence_before_sync();
         // (the test hook: one thread of CTA 0 withholds its arrival for the CTA's second tile, so the MMA warp's
@@ -627,8 +812,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
 
       // ---------------- epilogue ----------------
-      const bool real = row < a.R;
-      const size_t row0 = (size_t)(pc.b * a.Hq + pc.hk * a.GP) * a.Lq;  // first out row of the item
+      const int rows = rows_of<PAGED>(a, pc);
+      const bool real = row < rows;
+      const size_t orow0 = out_row<PAGED>(a, pc, row);  // this thread's row of out
       if (pc.np == 1) {
         if (!ok) continue;
         const float inv_l = (l > 0.f) ? 1.f / l : 0.f;
@@ -637,9 +823,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t orr[32];
           tc::tmem_ld32(o_addr + cc * 32, orr);
           tc::tmem_ld_wait();
-          if (real) store_row<D>(a, row0 + row, cc, orr, inv_l);
+          if (real) store_row<D>(a, orow0, cc, orr, inv_l);
         }
-        if (real && a.lse != nullptr) a.lse[row0 + row] = (l > 0.f) ? (m_ref + log2f(l)) * kLn2 : -INFINITY;
+        if (real && a.lse != nullptr) a.lse[orow0] = (l > 0.f) ? (m_ref + log2f(l)) * kLn2 : -INFINITY;
         continue;
       }
       // partial: unnormalised O, m, l into this CTA's slot
@@ -685,7 +871,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t mlbytes = (uint32_t)a.R * 8;     // its (m, l) rows
         Walk peek = walk;
         Piece pn;
-        const bool in_smem = (a.R % 2 == 0) && !walk_next(peek, a, pn) &&
+        const bool in_smem = (a.R % 2 == 0) && !walk_next<PAGED>(peek, a, pn) &&
                              (size_t)pc.np * (pbytes + mlbytes) <= (size_t)2 * C::NS * C::TILE_BYTES;
         const float* sm_o = reinterpret_cast<const float*>(Ks);                                // [np][R][D]
         const float2* sm_ml = reinterpret_cast<const float2*>(Ks + (size_t)pc.np * pbytes);  // [np][R]
@@ -703,7 +889,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // after a failed wait the copies may still be landing: let them, before shared memory is released
           if (!merge_ok) mbar_wait(merge_bar, 0, a.status, nullptr);
         }
-        for (int e = stid; merge_ok && e < a.R * CPR; e += kSoftmaxThreads) {
+        for (int e = stid; merge_ok && e < rows * CPR; e += kSoftmaxThreads) {
           const int r = e / CPR;
           const int ch = e - r * CPR;
           float M = -INFINITY, L = 0.f;
@@ -765,7 +951,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             fold(ml0, o0);
           }
           const float inv_L = (L > 0.f) ? 1.f / L : 0.f;
-          const size_t orow = row0 + r;
+          const size_t orow = out_row<PAGED>(a, pc, r);
           if (a.out_f32) {
             float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + orow * D + ch * 32);
 #pragma unroll
@@ -792,11 +978,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok) {
       constexpr int VPT = D / 32;
       for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-        if (clamp_len(a.kv_lens[b], a.Lmax) != 0) continue;
+        const Seq sq = load_seq<PAGED>(a, b, false);
+        if (sq.n != 0) continue;
+        Piece pz;
+        pz.b = b;
+        pz.q0 = sq.q0;
+        pz.nq = sq.nq;
         for (int hk = 0; hk < a.Hkv; ++hk) {
-          const size_t row0 = (size_t)(b * a.Hq + hk * a.GP) * a.Lq;
-          for (int r = sw; r < a.R; r += 4) {
-            const size_t orow = row0 + r;
+          pz.hk = hk;
+          const int zrows = rows_of<PAGED>(a, pz);
+          for (int r = sw; r < zrows; r += 4) {
+            const size_t orow = out_row<PAGED>(a, pz, r);
             if (a.out_f32) {
               float* dst = reinterpret_cast<float*>(a.out) + orow * D + lane * VPT;
 #pragma unroll
@@ -821,7 +1013,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D>
+template <int D, bool PAGED>
 cudaError_t launch_d(const DecodeMultiLaunch& p) {
   using C = MCfg<D>;
   static bool attr_set[64] = {};
@@ -830,26 +1022,46 @@ cudaError_t launch_d(const DecodeMultiLaunch& p) {
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!attr_set[dev]) {
-    e = cudaFuncSetAttribute(decode_multi_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_ALLOC);
+    e = cudaFuncSetAttribute(decode_multi_kernel<D, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_ALLOC);
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
   }
   const int GP = p.Hq / p.Hkv;
   const int R = GP * p.Lq;
   if (R < 1 || R > BM) return cudaErrorInvalidValue;
-  const int qbox = ((R + 7) / 8) * 8;  // whole 8-row swizzle atoms
   const uint64_t row_b = (uint64_t)D * 2;
-  const uint64_t qrows = (uint64_t)p.B * p.Hq * p.Lq;
-  const uint64_t Lk = p.Lmax > 0 ? (uint64_t)p.Lmax : 1;
-  const void* kb = p.Lmax > 0 ? p.kcache : p.q;  // Lmax == 0: never read, any valid map
-  const void* vb = p.Lmax > 0 ? p.vcache : p.q;
+  MultiArgs a{};
   CUtensorMap tmq, tmk, tmv;
-  // q as rows (b, h, t) of D columns; caches as (d, key, b * Hkv + hk) like dense prefill K/V
-  const bool ok = make_tmap_bf16_3d(&tmq, p.q, D, qrows, 1, row_b, row_b * qrows, 64, (uint32_t)qbox, 1) &&
-                  make_tmap_bf16_3d(&tmk, kb, D, Lk, (uint64_t)p.B * p.Hkv, row_b, row_b * Lk, 64, BN, 1) &&
-                  make_tmap_bf16_3d(&tmv, vb, D, Lk, (uint64_t)p.B * p.Hkv, row_b, row_b * Lk, 64, BN, 1);
+  bool ok;
+  if constexpr (PAGED) {
+    a.box_rows = BN;
+    while (p.page_size % a.box_rows != 0) a.box_rows /= 2;  // gcd(page_size, 128), at least 8
+    if (a.box_rows < 8) return cudaErrorInvalidValue;
+    const uint64_t heads = (uint64_t)p.num_pages * p.Hkv, page_b = row_b * p.page_size;
+    a.q_box_bytes = R * 128 * C::NDB;
+    // q as (column, head, token); pools as (column, key of the page, page * Hkv + hk)
+    ok = make_tmap_bf16_3d(&tmq, p.q, D, p.Hq, p.T, row_b, row_b * p.Hq, 64, (uint32_t)GP, (uint32_t)p.Lq) &&
+         make_tmap_bf16_3d(&tmk, p.kcache, D, p.page_size, heads, row_b, page_b, 64, (uint32_t)a.box_rows, 1) &&
+         make_tmap_bf16_3d(&tmv, p.vcache, D, p.page_size, heads, row_b, page_b, 64, (uint32_t)a.box_rows, 1);
+    a.block_table = p.block_table;
+    a.cu_new = p.cu_new;
+    a.T = p.T;
+    a.max_pages = p.max_pages;
+    a.num_pages = p.num_pages;
+    a.page = make_fast_div((unsigned)p.page_size);
+  } else {
+    const int qbox = ((R + 7) / 8) * 8;  // whole 8-row swizzle atoms
+    const uint64_t qrows = (uint64_t)p.B * p.Hq * p.Lq;
+    const uint64_t Lk = p.Lmax > 0 ? (uint64_t)p.Lmax : 1;
+    const void* kb = p.Lmax > 0 ? p.kcache : p.q;  // Lmax == 0: never read, any valid map
+    const void* vb = p.Lmax > 0 ? p.vcache : p.q;
+    a.q_box_bytes = qbox * 128 * C::NDB;
+    // q as rows (b, h, t) of D columns; caches as (d, key, b * Hkv + hk) like dense prefill K/V
+    ok = make_tmap_bf16_3d(&tmq, p.q, D, qrows, 1, row_b, row_b * qrows, 64, (uint32_t)qbox, 1) &&
+         make_tmap_bf16_3d(&tmk, kb, D, Lk, (uint64_t)p.B * p.Hkv, row_b, row_b * Lk, 64, BN, 1) &&
+         make_tmap_bf16_3d(&tmv, vb, D, Lk, (uint64_t)p.B * p.Hkv, row_b, row_b * Lk, 64, BN, 1);
+  }
   if (!ok) return cudaErrorInvalidValue;
-  MultiArgs a;
   a.kv_lens = p.kv_lens;
   a.out = p.out;
   a.lse = p.lse;
@@ -863,7 +1075,6 @@ cudaError_t launch_d(const DecodeMultiLaunch& p) {
   a.Lmax = p.Lmax;
   a.GP = GP;
   a.R = R;
-  a.q_box_bytes = qbox * 128 * C::NDB;
   // a positive factor on the logits: a negative scale negates Q in the S MMA (exact); scale == 0 is uniform weights
   a.uniform = (p.scale == 0.f) ? 1 : 0;
   a.scale_log2 = a.uniform ? 1.f : fabsf(p.scale) * kLog2e;
@@ -872,7 +1083,7 @@ cudaError_t launch_d(const DecodeMultiLaunch& p) {
   a.status = p.status;
   a.rope = p.rope;
   a.fault_skip_arrive = p.fault_skip_arrive;
-  decode_multi_kernel<D><<<decode_multi_grid(p.num_sms), kThreads, C::SMEM_ALLOC, p.stream>>>(tmq, tmk, tmv, a);
+  decode_multi_kernel<D, PAGED><<<decode_multi_grid(p.num_sms), kThreads, C::SMEM_ALLOC, p.stream>>>(tmq, tmk, tmv, a);
   return cudaGetLastError();
 }
 
@@ -881,9 +1092,9 @@ cudaError_t launch_d(const DecodeMultiLaunch& p) {
 int decode_multi_grid(int num_sms) { return num_sms > 0 ? num_sms : 148; }
 
 cudaError_t launch_decode_multi(const DecodeMultiLaunch& p) {
-  if (p.D == 64) return launch_d<64>(p);
-  if (p.D == 128) return launch_d<128>(p);
-  return cudaErrorNotSupported;
+  if (p.D != 64 && p.D != 128) return cudaErrorNotSupported;
+  if (p.block_table != nullptr) return p.D == 64 ? launch_d<64, true>(p) : launch_d<128, true>(p);
+  return p.D == 64 ? launch_d<64, false>(p) : launch_d<128, false>(p);
 }
 
 }  // namespace attn

@@ -49,11 +49,15 @@ constexpr int kDecodeCounterSlots = 65536;
 // One persistent launch that also merges the split partials.
 cudaError_t launch_decode(const DecodeLaunch& p, int num_sms);
 
-// Multi-token decode (tcgen05 tensor-core path): Lq new tokens per sequence over a contiguous KV cache.
+// Multi-token decode (tcgen05 tensor-core path): Lq new tokens per sequence over a contiguous KV cache, or up to Lq over
+// pages (block_table given: q, out [T, Hq, D] and lse [T, Hq] are packed by cu_new, Lmax = max_pages * page_size).
 struct DecodeMultiLaunch {
   const void* q;        // bf16 [B, Hq, Lq, D]
-  const void* kcache;   // bf16 [B, Hkv, Lmax, D]
+  const void* kcache;   // bf16 [B, Hkv, Lmax, D], or the page pool [num_pages, Hkv, page_size, D]
   const void* vcache;   // same layout as kcache
+  const int* block_table;  // null: contiguous cache; else int32 [B, max_pages]
+  const int* cu_new;       // int32 [B + 1]
+  int T, page_size, max_pages, num_pages;
   const int* kv_lens;   // int32 [B] (device); keys of every token, the new ones included
   void* out;            // [B, Hq, Lq, D], bf16 or fp32
   float* lse;           // fp32 [B, Hq, Lq] or null
@@ -200,6 +204,61 @@ constexpr int kDecodeQ4Owners = 4;  // warps of a CTA that hold its partial
 size_t decode_q4_partials(int num_sms);
 size_t decode_q4_counts(int num_sms);  // counts of all CTAs in any variant
 cudaError_t launch_decode_q4(const DecodeQ4Launch& p);
+
+// Rotary tables: rows of cos and sin of (start + row) * turn[i] turns.
+constexpr int kMaxRotaryPairs = 64;
+struct RopeTablesLaunch {
+  float* cos;  // [rows, pairs]
+  float* sin;
+  int rows, start, pairs;
+  float amplitude;
+  int num_sms;
+  cudaStream_t stream;
+  unsigned long long turn[kMaxRotaryPairs];  // turns a position of pair i, times 2^64, modulo 2^64
+};
+cudaError_t launch_rope_tables(const RopeTablesLaunch& p);
+
+// Rows of k (rotated) and v into bf16 pages, q rotated on the way; strides in elements: token, head.
+struct KvAppendPagedLaunch {
+  const void* k;
+  const void* v;
+  const void* q;         // or null (Hq = 0)
+  void* kpages;          // [num_pages, Hkv, page_size, D]
+  void* vpages;
+  void* q_out;
+  void* k_out;           // rotated k packed as well, or null
+  const int* slots;
+  const int* positions;  // or null: every token is valid, no rotation
+  int T, Hq, Hkv, D, page_size, num_pages;
+  int rotary;            // dims that rotate (a multiple of 16), 0: none
+  long long ks[2], vs[2], qs[2], qos[2], kos[2];
+  RopeArgs rope;         // tables [max_pos, rotary / 2]
+  int num_sms;
+  unsigned* status;
+  cudaStream_t stream;
+};
+cudaError_t launch_kv_append_paged(const KvAppendPagedLaunch& p);
+
+// Which drafted tokens stand, and the token after them (attn_verify_drafts); strides in elements: sequence, row.
+struct VerifyDraftsLaunch {
+  const int* drafts;      // [B, K]
+  const void* target;     // bf16 or fp32, rows of V
+  const void* draft;      // or null: drafts without a distribution
+  const float* uniforms;  // [B, K + 1]
+  const int* cu;          // [B + 1], or null: sequence b's target rows are at b * ts[0]
+  const int* draft_lens;  // [B], or null
+  const int* kv_lens;     // [B], or null
+  int* tokens;            // [B, K + 1]
+  int* accepted;          // [B]
+  int* keep_lens;         // [B], or null
+  int B, K, V, total;
+  int f32;
+  long long ts[2], ds[2];
+  int num_sms;
+  unsigned* status;
+  cudaStream_t stream;
+};
+cudaError_t launch_verify_drafts(const VerifyDraftsLaunch& p);
 
 // One thread waits on a barrier nothing arrives on, with the kernels' bounded wait and a limit of limit_ns.
 cudaError_t launch_selftest_timeout(unsigned long long limit_ns, unsigned* status, cudaStream_t stream);

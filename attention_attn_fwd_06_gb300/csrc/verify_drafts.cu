@@ -1,0 +1,401 @@
+// verify_drafts.cu -- which drafted tokens stand, and the token that follows them, from given random numbers.
+//
+// Sequence b has n drafted tokens x_0 .. x_{n-1}, drawn from q_0 .. q_{n-1}, and n + 1 rows p_0 .. p_n of the target's
+// probabilities.  Draft i stands while u_i q_i(x_i) < p_i(x_i) (both sides exact: products of 24-bit numbers in 64-bit
+// floats).  The token after the ones that stand has the weights max(p_r - q_r, 0), r being the refused draft, or p_n where
+// all stand; it is the lowest j with w_0 + .. + w_j > u (w_0 + .. + w_{V-1}).  Accepting and then drawing so leaves a token
+// distributed as p.
+//
+// The sums decide which token comes out, so they carry more than 32 bits: a lane adds fp32 terms into a pair of floats (a
+// sum and the sum of its roundings, Knuth's two-sum), a difference p - q enters with its own rounding, and lanes, warps and
+// CTAs are joined in 64-bit floats in a fixed order: 2^-42 of the sum, and the same bits every time.  (Adding every term in
+// 64-bit floats would take longer than reading it: 2 of them a clock and SM.)
+//
+// What bounds it: for few sequences the chain of launch, drafts, their probabilities, the row, the exchange and the search;
+// for many, reading one row of p and of q each.  A cluster of CTAs takes a sequence: every CTA decides which drafts stand
+// by itself, its warps sum a segment of the row each, the segments' sums go to every CTA of the cluster through distributed
+// shared memory, and the CTA that holds the segment where the sum passes u's share reads that segment again (from L2), its
+// warps a piece each, and finds the token.
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "rope.cuh"
+
+namespace attn {
+namespace {
+
+constexpr int kVerifyWarps = 16;
+constexpr int kVerifyMaxCluster = 8;
+constexpr int kVerifySegments = kVerifyWarps * kVerifyMaxCluster;
+
+template <typename T>
+__device__ __forceinline__ float as_float(T x);
+template <>
+__device__ __forceinline__ float as_float<float>(float x) {
+  return x;
+}
+template <>
+__device__ __forceinline__ float as_float<__nv_bfloat16>(__nv_bfloat16 x) {
+  return __bfloat162float(x);
+}
+
+// A sum and the sum of its roundings.
+struct Sum {
+  float s = 0.f, e = 0.f;
+  __device__ __forceinline__ void add(float x, float rest) {
+    const float t = s + x;
+    const float z = t - s;
+    e += ((s - (t - z)) + (x - z)) + rest;
+    s = t;
+  }
+  __device__ __forceinline__ double value() const { return (double)s + (double)e; }
+};
+
+__device__ __forceinline__ double warp_sum(double v) {
+#pragma unroll
+  for (int m = 16; m >= 1; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+  return v;
+}
+
+// The row that the token is drawn from.
+template <typename T>
+struct Row {
+  const T* p;
+  const T* q;    // taken away; or null
+  int skip;      // this token's weight is 0 (a refused draft without a distribution); or -1
+  // weight of token j with probabilities pj, qj: d, and what rounding took from it; whatever is not a positive finite number counts as 0
+  __device__ __forceinline__ float weight(float pj, float qj, int j, float& rest) const {
+    float d = pj - qj;
+    rest = (pj - d) - qj;  // exact where pj >= qj
+    if (!(d > 0.f && d < INFINITY) || j == skip) {
+      d = 0.f;
+      rest = 0.f;
+    }
+    return d;
+  }
+};
+
+// Elements 16 bytes at a time, or one by one where rows do not start on 16 bytes.
+template <typename T, bool VEC>
+struct Access {
+  static constexpr int N = VEC ? 16 / sizeof(T) : 1;
+  struct Raw {
+    uint32_t w[VEC ? 4 : 1];
+  };
+  static __device__ __forceinline__ Raw load(const T* row, int j, int V) {
+    Raw r{};
+    if constexpr (!VEC) {
+      r.w[0] = __float_as_uint(as_float<T>(__ldg(row + j)));
+    } else if (j + N <= V) {
+      const uint4 x = __ldg(reinterpret_cast<const uint4*>(row + j));
+      r.w[0] = x.x;
+      r.w[1] = x.y;
+      r.w[2] = x.z;
+      r.w[3] = x.w;
+    } else {  // the row's end: what follows it is not read
+      constexpr int PER = 4 / sizeof(T);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        if (j + i >= V) break;
+        uint32_t e;
+        if constexpr (sizeof(T) == 4)
+          e = __float_as_uint(__ldg(row + j + i));
+        else
+          e = (uint32_t)__ldg(reinterpret_cast<const unsigned short*>(row) + j + i) << (16 * (i % PER));
+        r.w[i / PER] |= e;
+      }
+    }
+    return r;
+  }
+  static __device__ __forceinline__ void unpack(const Raw& r, float (&v)[N]) {
+    if constexpr (VEC && sizeof(T) == 2) {
+      unpack8(make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]), v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = __uint_as_float(r.w[i]);
+    }
+  }
+};
+
+// Sum of the weights of tokens [lo, hi) (lo and hi - lo multiples of a warp's step, or hi == V) over this lane's elements.
+template <typename T, bool VEC>
+__device__ __forceinline__ Sum lane_sum(const Row<T>& row, int lo, int hi, int V, int lane) {
+  using A = Access<T, VEC>;
+  constexpr int STEP = 32 * A::N;
+  constexpr int U = VEC ? 4 : 8;
+  Sum s;
+  for (int j0 = lo + lane * A::N; j0 < hi; j0 += U * STEP) {
+    typename A::Raw p[U], q[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int j = j0 + u * STEP;
+      p[u] = q[u] = typename A::Raw{};
+      if (j < hi) {
+        p[u] = A::load(row.p, j, V);
+        if (row.q != nullptr) q[u] = A::load(row.q, j, V);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float pj[A::N], qj[A::N];
+      A::unpack(p[u], pj);
+      A::unpack(q[u], qj);
+#pragma unroll
+      for (int i = 0; i < A::N; ++i) {
+        float rest;
+        const float w = row.weight(pj[i], qj[i], j0 + u * STEP + i, rest);
+        s.add(w, rest);
+      }
+    }
+  }
+  return s;
+}
+
+// The first of `count` parts, in order, at whose end the running sum (from `before`) passes `target`; where none does (u of 1
+// or more, or NaN), the last one that holds weight; -1 if none holds any.  One warp; `before` becomes the sum before that part.
+__device__ int pick(const double* parts, int count, double target, double& before, int lane) {
+  double base = before;
+  int last = -1;
+  double last_before = before;
+  for (int i0 = 0; i0 < count; i0 += 32) {
+    const double v = i0 + lane < count ? parts[i0 + lane] : 0.0;
+    double incl = v;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const double up = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += up;
+    }
+    const double end = base + incl;
+    const unsigned hit = __ballot_sync(0xffffffffu, v > 0.0 && end > target);
+    const unsigned any = __ballot_sync(0xffffffffu, v > 0.0);
+    if (hit != 0 || any != 0) {
+      const int at = hit != 0 ? __ffs(hit) - 1 : 31 - __clz(any);
+      last = i0 + at;
+      last_before = base + __shfl_sync(0xffffffffu, incl - v, at);
+      if (hit != 0) break;
+    }
+    base += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  before = last_before;
+  return last;
+}
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(32 * kVerifyWarps, 2) verify_drafts_kernel(const VerifyDraftsLaunch p, int segment) {
+  namespace cg = cooperative_groups;
+  using A = Access<T, VEC>;
+  constexpr int STEP = 32 * A::N;
+  __shared__ double sums[2][kVerifySegments];  // of all segments of the row; the second where the first try held no weight
+  __shared__ double pieces[kVerifyWarps];
+  __shared__ int s_n, s_stand, s_row;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int size = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int b = blockIdx.x / size;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int K = p.K, V = p.V;
+  cluster.barrier_arrive();  // (waited for before the first store into another CTA's shared memory: all have started)
+
+  if (warp == 0) {
+    // which drafts stand
+    int n = K, row0 = 0;
+    bool bad = false;
+    if (p.cu != nullptr) {
+      const int c0 = p.cu[b], c1 = p.cu[b + 1];
+      bad = c0 < 0 || c1 < c0 || c1 > p.total || c1 - c0 > K + 1;
+      n = bad ? -1 : c1 - c0 - 1;  // -1: no rows, nothing to draw from
+      row0 = c0;
+    } else if (p.draft_lens != nullptr) {
+      n = p.draft_lens[b];
+      if (n < 0 || n > K) {
+        bad = true;
+        n = n < 0 ? 0 : K;
+      }
+    }
+    int stand = n < 0 ? 0 : n;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      const int i = i0 + lane;
+      bool ok = true;
+      if (i < n) {
+        const int x = p.drafts[(long long)b * K + i];
+        ok = false;
+        if (x < 0 || x >= V) {
+          bad = true;
+        } else {
+          const T* pr = reinterpret_cast<const T*>(p.target) +
+                        (p.cu != nullptr ? (long long)(row0 + i) * p.ts[1] : (long long)b * p.ts[0] + (long long)i * p.ts[1]);
+          const double px = as_float<T>(__ldg(pr + x));
+          double qx = 1.0;
+          if (p.draft != nullptr)
+            qx = as_float<T>(__ldg(reinterpret_cast<const T*>(p.draft) + (long long)b * p.ds[0] + (long long)i * p.ds[1] + x));
+          ok = (double)p.uniforms[(long long)b * (K + 1) + i] * qx < px;
+        }
+      }
+      const unsigned refused = __ballot_sync(0xffffffffu, !ok);
+      if (refused != 0) {
+        stand = i0 + __ffs(refused) - 1;
+        break;
+      }
+    }
+    if (bad && rank == 0) record_status(p.status, ATTN_ERR_DEVICE_BOUNDS);
+    if (lane == 0) {
+      s_n = n;
+      s_stand = stand;
+      s_row = row0;
+    }
+  }
+  __syncthreads();
+  const int n = s_n, stand = s_stand;
+  int* tokens = p.tokens + (long long)b * (K + 1);
+  if (rank == 0) {
+    for (int i = threadIdx.x; i <= K; i += blockDim.x)
+      if (i != stand || n < 0) tokens[i] = i < stand ? p.drafts[(long long)b * K + i] : -1;
+    if (threadIdx.x == 0) {
+      p.accepted[b] = stand;
+      if (p.keep_lens != nullptr) p.keep_lens[b] = p.kv_lens[b] - (n < 0 ? 0 : n - stand);
+    }
+  }
+  cluster.barrier_wait();
+  if (n < 0) return;  // (every CTA of the cluster)
+
+  Row<T> row;
+  row.p = reinterpret_cast<const T*>(p.target) +
+          (p.cu != nullptr ? (long long)(s_row + stand) * p.ts[1] : (long long)b * p.ts[0] + (long long)stand * p.ts[1]);
+  row.q = nullptr;
+  row.skip = -1;
+  if (stand < n) {
+    if (p.draft != nullptr)
+      row.q = reinterpret_cast<const T*>(p.draft) + (long long)b * p.ds[0] + (long long)stand * p.ds[1];
+    else
+      row.skip = p.drafts[(long long)b * K + stand];
+  }
+  const int count = size * kVerifyWarps;
+  const int mine = rank * kVerifyWarps + warp;
+  const float u = p.uniforms[(long long)b * (K + 1) + K];
+  int seg = -1;
+  double before = 0.0, target = 0.0;
+  for (int attempt = 0; attempt < 2; ++attempt) {
+    const long long lo = (long long)mine * segment;
+    double v = 0.0;
+    if (lo < V) v = lane_sum<T, VEC>(row, (int)lo, (int)min(lo + segment, (long long)V), V, lane).value();
+    v = warp_sum(v);
+    if (lane < size) *cluster.map_shared_rank(&sums[attempt][mine], lane) = v;
+    cluster.sync();
+    // every warp of every CTA finds the segment for itself
+    double total = 0.0;
+    for (int i = lane; i < count; i += 32) total += sums[attempt][i];
+    total = warp_sum(total);
+    target = (double)u * total;
+    before = 0.0;
+    seg = pick(sums[attempt], count, target, before, lane);
+    if (seg >= 0 || (row.q == nullptr && row.skip < 0)) break;
+    row.q = nullptr;  // p nowhere above q: p itself
+    row.skip = -1;
+  }
+  if (seg < 0) {  // no weight at all
+    if (rank == 0 && threadIdx.x == 0) {
+      tokens[stand] = -1;
+      record_status(p.status, ATTN_ERR_DEVICE_BOUNDS);
+    }
+    return;
+  }
+  if (seg / kVerifyWarps != rank) return;
+  // the segment's pieces, one a warp
+  const int first = seg * segment, end = (int)min((long long)first + segment, (long long)V);
+  const int piece = ((segment + kVerifyWarps - 1) / kVerifyWarps + STEP - 1) / STEP * STEP;
+  {
+    const int lo = min(first + warp * piece, end);
+    const double v = warp_sum(lane_sum<T, VEC>(row, lo, min(lo + piece, end), V, lane).value());
+    if (lane == 0) pieces[warp] = v;
+  }
+  __syncthreads();
+  int w = pick(pieces, kVerifyWarps, target, before, lane);
+  if (w < 0) w = 0;  // (cannot be: the segment holds weight)
+  if (warp != w) return;
+  // a warp's step at a time; the step's sum in the order of tokens: lanes, then a lane's elements
+  const int lo = min(first + w * piece, end), hi = min(lo + piece, end);
+  int found = -1;
+  double base = before;
+  for (int j0 = lo; j0 < hi; j0 += STEP) {
+    const int j = j0 + lane * A::N;
+    float pj[A::N], qj[A::N];
+    typename A::Raw pr{}, qr{};
+    if (j < hi) {
+      pr = A::load(row.p, j, V);
+      if (row.q != nullptr) qr = A::load(row.q, j, V);
+    }
+    A::unpack(pr, pj);
+    A::unpack(qr, qj);
+    double own = 0.0, part[A::N];
+#pragma unroll
+    for (int i = 0; i < A::N; ++i) {
+      float rest;
+      const float d = row.weight(pj[i], qj[i], j + i, rest);
+      part[i] = (double)d + (double)rest;
+      own += part[i];
+    }
+    double incl = own;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const double up = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += up;
+    }
+    int at = -1, last = -1;
+    double run = base + (incl - own);
+#pragma unroll
+    for (int i = 0; i < A::N; ++i) {
+      run += part[i];
+      if (part[i] > 0.0) {
+        last = j + i;
+        if (at < 0 && run > target) at = j + i;
+      }
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, at >= 0), any = __ballot_sync(0xffffffffu, last >= 0);
+    if (hit != 0) {
+      found = __shfl_sync(0xffffffffu, at, __ffs(hit) - 1);
+      break;
+    }
+    if (any != 0) found = __shfl_sync(0xffffffffu, last, 31 - __clz(any));
+    base += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  if (lane == 0) tokens[stand] = found;
+}
+
+template <typename T, bool VEC>
+cudaError_t launch_t(const VerifyDraftsLaunch& p) {
+  constexpr int STEP = 32 * Access<T, VEC>::N;
+  int size = kVerifyMaxCluster;
+  while (size > 1 && ((long long)p.V <= (long long)STEP * kVerifyWarps * (size / 2))) size /= 2;
+  const long long warps = (long long)size * kVerifyWarps;
+  const long long segment = (((long long)p.V + warps - 1) / warps + STEP - 1) / STEP * STEP;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(p.B * size));
+  cfg.blockDim = dim3(32 * kVerifyWarps);
+  cfg.stream = p.stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = (unsigned)size;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, verify_drafts_kernel<T, VEC>, p, (int)segment);
+}
+
+template <typename T>
+cudaError_t dispatch_vec(const VerifyDraftsLaunch& p) {
+  constexpr int N = 16 / sizeof(T);
+  bool vec = reinterpret_cast<unsigned long long>(p.target) % 16 == 0 && p.ts[0] % N == 0 && p.ts[1] % N == 0;
+  if (p.draft != nullptr)
+    vec = vec && reinterpret_cast<unsigned long long>(p.draft) % 16 == 0 && p.ds[0] % N == 0 && p.ds[1] % N == 0;
+  return vec ? launch_t<T, true>(p) : launch_t<T, false>(p);
+}
+
+}  // namespace
+
+cudaError_t launch_verify_drafts(const VerifyDraftsLaunch& p) {
+  if (p.B == 0) return cudaSuccess;
+  return p.f32 ? dispatch_vec<float>(p) : dispatch_vec<__nv_bfloat16>(p);
+}
+
+}  // namespace attn

@@ -553,6 +553,217 @@ int attn_decode_q4(const attn_decode_q4_params* p);
 unsigned long long attn_decode_q4_workspace_bytes(int Hq, int Hkv, int Lq, int D);
 
 /*
+ * ---------------------------------------------------------------------------
+ * A draft step over a paged bf16 cache (the pools of attn_decode_paged).  Several
+ * drafted tokens of every sequence are checked at once; the step's tokens are packed,
+ * sequence after sequence, as attn_page_step lists them: attn_page_step (slots and
+ * positions, cu_new), attn_kv_append_paged (q and k rotated, k and v written),
+ * attn_decode_multi_paged, the model's output head, attn_verify_drafts (which drafts
+ * stand, the token that follows), attn_page_step again with its keep_lens.
+ * attn_rope_tables makes the rotation's tables.  What the serving step's calls promise
+ * holds here: no allocation and no synchronisation (attn_decode_multi_paged without a
+ * workspace of the caller's: see there), sizes checked before anything is enqueued, rows
+ * of indices out of range skipped and flagged ATTN_ERR_DEVICE_BOUNDS.  (The source pages
+ * name RoPE and PagedAttention, "Что такое kernel fusion и как он применяется в LLM
+ * serving?" §3.5 and §6, and several query tokens of a step at once, "Оптимизация
+ * Decoder Attention для LLM на GPU"; they give no formulas.)
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * attn_rope_tables -- rotary tables: row r of cos and sin holds
+ *     amplitude * cos((start + r) f_i),  amplitude * sin((start + r) f_i),
+ * i < rotary_dim / 2, with f_i = base^(-2i / rotary_dim) radians a position, changed for
+ * contexts longer than the model was trained on by
+ *     ATTN_ROPE_SCALE_NONE    nothing
+ *     ATTN_ROPE_SCALE_LINEAR  f_i / factor
+ *     ATTN_ROPE_SCALE_BASE    base * factor^(R / (R - 2)) for base, R = rotary_dim: the slowest
+ *                             pair is slowed by factor, the fastest not at all
+ *     ATTN_ROPE_SCALE_TURNS   f_i (g + (1 - g) / factor), g = clamp((t - low) / (high - low), 0, 1)
+ *                             with t = context f_i / (2 pi), the turns over the trained context
+ *     ATTN_ROPE_SCALE_INDEX   the same with g = 1 - clamp((i - a) / max(b - a, 0.001), 0, 1), where
+ *                             a = max(0, floor(c(high))) and b = min(R - 1, ceil(c(low))),
+ *                             c(t) = (R / 2) ln(context / (2 pi t)) / ln(base): the pair of t turns
+ * Angles are kept as fractions of a turn in 64 bits, so that far positions are about as exact
+ * as near ones: within 2^-22 + 2^-50 of the angle, times the amplitude.
+ *
+ *   cos, sin    fp32 [rows, rotary_dim / 2], 16-byte aligned, apart from each other
+ *   rotary_dim  16, 32 .. 128: the rotated dims of a head.  Tables of rotary_dim = D are
+ *               those of attn_rope; attn_kv_append_paged takes narrower ones too.
+ *   start       >= 0, start + rows below 2^31: tables can grow with the longest request
+ *   base        > 1 (also once factor has changed it); factor > 0; 0 < low < high and context > 0 where they are used; all
+ *               finite, the amplitude too (ATTN_ERR_INVALID_ARG otherwise)
+ * rows == 0: nothing is done.
+ */
+typedef enum attn_rope_scaling {
+  ATTN_ROPE_SCALE_NONE = 0,
+  ATTN_ROPE_SCALE_LINEAR = 1,
+  ATTN_ROPE_SCALE_BASE = 2,
+  ATTN_ROPE_SCALE_TURNS = 3,
+  ATTN_ROPE_SCALE_INDEX = 4
+} attn_rope_scaling;
+
+typedef struct attn_rope_tables_params {
+  float* cos;
+  float* sin;
+  int rows, start, rotary_dim, scaling;
+  double base, factor, context, low, high, amplitude;
+  void* stream;
+} attn_rope_tables_params;
+
+int attn_rope_tables(const attn_rope_tables_params* p);
+
+/*
+ * attn_kv_append_paged -- T rows of k, rotated, and of v into their slots of the pages, and
+ * the same tokens' q rotated, in one pass.  The first rotary_dim dims of a head turn as in
+ * attn_rope, pairs being dims (i, i + rotary_dim / 2) or (2i, 2i + 1), in fp32, rounded to
+ * bf16 once; the others, and v, are copied bit for bit.
+ *
+ *   k, v     bf16 [T, Hkv, D] with strides of token and head in elements (multiples of 8,
+ *            unless there is one; D contiguous; 16-byte aligned): views of a projection's
+ *            output will do
+ *   kpages, vpages  bf16 [num_pages, Hkv, page_size, D], page_size at least 1 here
+ *   slots    int32 [T], page * page_size + offset; -1: k and v of this token are not written.
+ *            Any other slot outside the pool is flagged and not written.  The slots of one
+ *            call must differ: rows of the same slot would be written over each other in no
+ *            order.
+ *   rope     tables [max_pos, rotary_dim / 2] and style (k_out unused); ATTN_ROPE_NONE:
+ *            nothing turns, and rotary_dim is not looked at
+ *   positions  int32 [T]; -1 marks a padded token, of which nothing is written.  Any other
+ *            value outside [0, max_pos) is flagged and its token left out alike.  May be NULL
+ *            without rotation.
+ *   q, q_out bf16 [T, Hq, D] with strides, both NULL when there is no q (Hq = 0); they go
+ *            with a rotation
+ *   k_out    bf16 [T, Hkv, D] with strides, or NULL: the rotated rows as well, for attn_fwd_ex
+ *            over a prompt's own keys, whatever the slot; goes with a rotation
+ *            q_out and k_out are either apart from every input, or exactly the rows of q (of k)
+ *            itself (same pointer and strides).  The pools are apart from everything else.
+ * rotary_dim is a multiple of 16, at most D (ATTN_ERR_UNSUPPORTED otherwise); num_pages *
+ * page_size below 2^31, Hq + 2 Hkv at most 65535.
+ */
+typedef struct attn_kv_append_paged_params {
+  const void* k;
+  const void* v;
+  void* kpages;
+  void* vpages;
+  const int* slots;
+  const int* positions;
+  const void* q;
+  void* q_out;
+  void* k_out;
+  int T, Hq, Hkv, D, page_size, num_pages, rotary_dim;
+  long long k_stride[2], v_stride[2], q_stride[2], q_out_stride[2], k_out_stride[2];
+  attn_rope rope;
+  void* stream;
+} attn_kv_append_paged_params;
+
+int attn_kv_append_paged(const attn_kv_append_paged_params* p);
+
+/*
+ * attn_decode_multi_paged -- attn_decode_multi over pages, with as many new tokens of each
+ * sequence as it has, packed.  q is taken as it is (rotated by attn_kv_append_paged).
+ *
+ *   q, out       [T, Hq, D]: bf16, and bf16 or fp32; lse fp32 [T, Hq] may be NULL
+ *   cu_new       DEVICE int32 [B + 1]: the tokens of sequence b are rows cu_new[b] ..
+ *                cu_new[b + 1] - 1.  A sequence without any is not looked at.  Offsets that
+ *                fall, leave [0, T] or give a sequence more than max_new tokens are flagged,
+ *                and its rows left as they were, as are rows of no sequence.
+ *   max_new      the most new tokens of a sequence, 1 .. 128 / (Hq / Hkv)
+ *                (ATTN_ERR_UNSUPPORTED above)
+ *   kpages, vpages, block_table, max_pages, num_pages  as attn_decode_paged
+ *   page_size    a multiple of 8, 8 .. 65536 (ATTN_ERR_UNSUPPORTED for others in that range)
+ *   kv_lens      DEVICE int32 [B], at most max_pages * page_size (clamped and flagged
+ *                otherwise): the keys of sequence b, its n = cu_new[b + 1] - cu_new[b] new
+ *                tokens' own among them.  Token t sits at kv_len - n + t and attends to keys
+ *                0 .. kv_len - n + t; one that sees no key gets O = 0, lse = -inf.  Keys at or
+ *                past kv_len may hold anything.  (Keys that a token does not see because they
+ *                are later tokens' own count with weight 0, so a NaN or an infinity in their
+ *                values still reaches it.)
+ *   out          apart from every input
+ *   workspace    as attn_decode_q4: NULL for one of the library, its own, made by the first
+ *                call on a device, which must not be one that is captured; or a DEVICE buffer
+ *                of at least attn_decode_multi_paged_workspace_bytes, 16-byte aligned, all
+ *                zeros before its first call.  Calls that can overlap, and graphs that can be
+ *                replayed at once, each take a buffer of their own.  After
+ *                ATTN_ERR_DEVICE_TIMEOUT the caller zeroes it again.
+ * B * Hkv at most 65534, num_pages * Hkv and T * Hq below 2^31 (ATTN_ERR_UNSUPPORTED
+ * otherwise).
+ */
+typedef struct attn_decode_multi_paged_params {
+  const void* q;
+  const void* kpages;
+  const void* vpages;
+  const int* block_table;
+  const int* kv_lens;
+  const int* cu_new;
+  void* out;
+  float* lse;
+  int B, T, Hq, Hkv, D, max_new;
+  int page_size, max_pages, num_pages;
+  float scale;
+  int out_dtype;
+  void* workspace;
+  unsigned long long workspace_bytes;
+  void* stream;
+} attn_decode_multi_paged_params;
+
+int attn_decode_multi_paged(const attn_decode_multi_paged_params* p);
+
+/* attn_decode_multi_paged_workspace_bytes -- bytes a workspace of attn_decode_multi_paged needs on the current device
+ * (0 on invalid sizes; 148 SMs assumed when no device is visible). */
+unsigned long long attn_decode_multi_paged_workspace_bytes(int Hq, int Hkv, int max_new, int D);
+
+/*
+ * attn_verify_drafts -- which drafted tokens stand, and the token that follows them, so that
+ * every token comes out as if drawn from the target's probabilities.  Sequence b has n drafts
+ * x_0 .. x_{n-1} drawn from q_0 .. q_{n-1}, and rows p_0 .. p_n of the target.  Draft i stands
+ * if those before it do and u_i q_i(x_i) < p_i(x_i) (products and comparison exact).  With r
+ * standing drafts the next token has the weights max(p_r - q_r, 0) if r < n, or p_n if all
+ * stand, and is the lowest j with w_0 + .. + w_j > u_K (w_0 + .. + w_{V-1}).  Weights that are
+ * not positive finite numbers count as 0; where p_r is nowhere above q_r the weights are p_r;
+ * where u_K is 1 or more, or NaN, the token is the last one with any weight.
+ *
+ *   draft_tokens  int32 [B, K]; K may be 0.  A token outside [0, V) does not stand, and is flagged.
+ *   target_probs  bf16 or fp32 (dtype) rows of V probabilities, strides in elements.  With
+ *                 cu_target: [total, V], rows cu_target[b] .. cu_target[b + 1] - 1 of sequence b
+ *                 (n = their number - 1; a sequence without rows gets no token); target_stride[1]
+ *                 is a row's.  Without: [B, K + 1, V], strides of sequence and row.
+ *   draft_probs   [B, K, V] of the same type, strides of sequence and row; or NULL for drafts
+ *                 that were not drawn (looked up, or the drafter's likeliest token): q_i is 1 at x_i
+ *   uniforms      fp32 [B, K + 1], random numbers in [0, 1): entry i < K for draft i, entry K for
+ *                 the token that follows
+ *   cu_target     int32 [B + 1] or NULL.  Offsets that fall, leave [0, total] or give more than
+ *                 K + 1 rows are flagged, and the sequence counts as one without rows.
+ *   draft_lens    int32 [B], n of every sequence, without cu_target; NULL: K.  A value outside
+ *                 [0, K] is clamped and flagged.
+ *   tokens        int32 [B, K + 1]: the drafts that stand, the token that follows them, then -1
+ *   accepted      int32 [B]: r
+ *   kv_lens, keep_lens  int32 [B], both or neither: keep = kv_lens - (n - r), what attn_page_step
+ *                 takes to drop the refused drafts' keys (kv_lens as the step that added the n + 1
+ *                 tokens left them)
+ * A row that holds no weight at all gives -1 and is flagged.  The sums are exact to 2^-40 of
+ * themselves and the same every time.  Outputs are apart from inputs and from each other.  K
+ * below 2^20, V below 2^30, B (K + 1) below 2^28 (ATTN_ERR_UNSUPPORTED otherwise).
+ */
+typedef struct attn_verify_drafts_params {
+  const int* draft_tokens;
+  const void* target_probs;
+  const void* draft_probs;
+  const float* uniforms;
+  const int* cu_target;
+  const int* draft_lens;
+  const int* kv_lens;
+  int* tokens;
+  int* accepted;
+  int* keep_lens;
+  int B, K, V, total, dtype;
+  long long target_stride[2], draft_stride[2];
+  void* stream;
+} attn_verify_drafts_params;
+
+int attn_verify_drafts(const attn_verify_drafts_params* p);
+
+/*
  * attn_get_device_status -- synchronises `stream`, then returns and clears the
  * current device's status word (ATTN_OK if no kernel flagged a problem since
  * the last read).  Of several problems it holds the first, but

@@ -28,3 +28,12 @@ from .sdpa import (  # noqa: F401
 )
 from .brute import attention_loops  # noqa: F401
 from .serving import page_step, quantise_q4, read_q4, rms_norm, values_q4, write_q4  # noqa: F401
+from .drafts import (  # noqa: F401
+    append_paged,
+    decode_multi_paged,
+    read_paged,
+    rope_frequencies,
+    rope_table_rows,
+    rotate_part,
+    verify_drafts,
+)
