@@ -8,8 +8,8 @@
 //
 // The sums decide which token comes out, so they carry more than 32 bits: a lane adds fp32 terms into a pair of floats (a
 // sum and the sum of its roundings, Knuth's two-sum), a difference p - q enters with its own rounding, and lanes, warps and
-// CTAs are joined in 64-bit floats in a fixed order: 2^-42 of the sum, and the same bits every time.  (Adding every term in
-// 64-bit floats would take longer than reading it: 2 of them a clock and SM.)
+// CTAs are joined as such pairs in a fixed order: 2^-42 of the sum, and the same bits every time.  (64-bit floats run at two
+// adds a clock and SM: in them the joins alone took most of the time, B = 8, V = 32,000: 17 us against 9.)
 //
 // What bounds it: for few sequences the chain of launch, drafts, their probabilities, the row, the exchange and the search;
 // for many, reading one row of p and of q each.  A cluster of CTAs takes a sequence: every CTA decides which drafts stand
@@ -44,19 +44,70 @@ __device__ __forceinline__ float as_float<__nv_bfloat16>(__nv_bfloat16 x) {
 // A sum and the sum of its roundings.
 struct Sum {
   float s = 0.f, e = 0.f;
+  // Knuth's two-sum of s and x; what it rounds off, and `rest`, go to e
   __device__ __forceinline__ void add(float x, float rest) {
     const float t = s + x;
     const float z = t - s;
     e += ((s - (t - z)) + (x - z)) + rest;
     s = t;
   }
-  __device__ __forceinline__ double value() const { return (double)s + (double)e; }
+  // the pair's sum in s, the rest in e (half an ulp of s at most)
+  __device__ __forceinline__ void settle() {
+    const float t = s + e;
+    const float z = t - s;
+    e = (s - (t - z)) + (e - z);
+    s = t;
+  }
+  __device__ __forceinline__ void add(Sum o) {
+    add(o.s, o.e);
+    settle();
+  }
 };
+__device__ __forceinline__ Sum plus(Sum a, Sum b) {
+  a.add(b);
+  return a;
+}
+// a > b, both settled (where the leading parts are near each other their difference is exact; where they are not it decides)
+__device__ __forceinline__ bool above(Sum a, Sum b) { return (a.s - b.s) + (a.e - b.e) > 0.f; }
+__device__ __forceinline__ bool positive(Sum a) { return a.s > 0.f; }
+// u times a
+__device__ __forceinline__ Sum share(float u, Sum a) {
+  Sum r;
+  r.s = u * a.s;
+  r.e = fmaf(u, a.s, -r.s) + u * a.e;
+  r.settle();
+  return r;
+}
 
-__device__ __forceinline__ double warp_sum(double v) {
+__device__ __forceinline__ Sum shuffle(Sum v, int lane) {
+  Sum r;
+  r.s = __shfl_sync(0xffffffffu, v.s, lane);
+  r.e = __shfl_sync(0xffffffffu, v.e, lane);
+  return r;
+}
+__device__ __forceinline__ Sum warp_sum(Sum v) {
 #pragma unroll
-  for (int m = 16; m >= 1; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+  for (int m = 16; m >= 1; m >>= 1) {
+    Sum o;
+    o.s = __shfl_xor_sync(0xffffffffu, v.s, m);
+    o.e = __shfl_xor_sync(0xffffffffu, v.e, m);
+    v = plus(v, o);
+  }
   return v;
+}
+// Of the lanes below and this one's (incl), and of the lanes below (excl).
+__device__ __forceinline__ void warp_scan(Sum v, Sum& incl, Sum& excl, int lane) {
+  incl = v;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    Sum up;
+    up.s = __shfl_up_sync(0xffffffffu, incl.s, off);
+    up.e = __shfl_up_sync(0xffffffffu, incl.e, off);
+    if (lane >= off) incl = plus(up, incl);
+  }
+  excl.s = __shfl_up_sync(0xffffffffu, incl.s, 1);
+  excl.e = __shfl_up_sync(0xffffffffu, incl.e, 1);
+  if (lane == 0) excl = Sum{};
 }
 
 // The row that the token is drawn from.
@@ -153,33 +204,39 @@ __device__ __forceinline__ Sum lane_sum(const Row<T>& row, int lo, int hi, int V
   return s;
 }
 
-// The first of `count` parts, in order, at whose end the running sum (from `before`) passes `target`; where none does (u of 1
-// or more, or NaN), the last one that holds weight; -1 if none holds any.  One warp; `before` becomes the sum before that part.
-__device__ int pick(const double* parts, int count, double target, double& before, int lane) {
-  double base = before;
-  int last = -1;
-  double last_before = before;
-  for (int i0 = 0; i0 < count; i0 += 32) {
-    const double v = i0 + lane < count ? parts[i0 + lane] : 0.0;
-    double incl = v;
+// The first of `count` <= 32 PER parts, in order, at whose end the running sum (from `before`) passes `target`; where none does
+// (u of 1 or more, or NaN), the last one that holds weight; -1 if none holds any.  One warp, PER parts a lane; `before` becomes
+// the sum before that part.
+template <int PER>
+__device__ int pick(const Sum* parts, int count, Sum target, Sum& before, int lane) {
+  Sum v[PER], own;
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const double up = __shfl_up_sync(0xffffffffu, incl, off);
-      if (lane >= off) incl += up;
-    }
-    const double end = base + incl;
-    const unsigned hit = __ballot_sync(0xffffffffu, v > 0.0 && end > target);
-    const unsigned any = __ballot_sync(0xffffffffu, v > 0.0);
-    if (hit != 0 || any != 0) {
-      const int at = hit != 0 ? __ffs(hit) - 1 : 31 - __clz(any);
-      last = i0 + at;
-      last_before = base + __shfl_sync(0xffffffffu, incl - v, at);
-      if (hit != 0) break;
-    }
-    base += __shfl_sync(0xffffffffu, incl, 31);
+  for (int i = 0; i < PER; ++i) {
+    v[i] = lane * PER + i < count ? parts[lane * PER + i] : Sum{};
+    own.add(v[i]);
   }
-  before = last_before;
-  return last;
+  Sum incl, excl;
+  warp_scan(own, incl, excl, lane);
+  Sum run = plus(before, excl), at_hit = run, at_last = run;
+  int hit = -1, last = -1;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const Sum end = plus(run, v[i]);
+    if (positive(v[i])) {
+      last = lane * PER + i;
+      at_last = run;
+      if (hit < 0 && above(end, target)) {
+        hit = last;
+        at_hit = run;
+      }
+    }
+    run = end;
+  }
+  const unsigned hits = __ballot_sync(0xffffffffu, hit >= 0), lasts = __ballot_sync(0xffffffffu, last >= 0);
+  if (lasts == 0) return -1;
+  const int src = hits != 0 ? __ffs(hits) - 1 : 31 - __clz(lasts);
+  before = shuffle(hits != 0 ? at_hit : at_last, src);
+  return __shfl_sync(0xffffffffu, hits != 0 ? hit : last, src);
 }
 
 template <typename T, bool VEC>
@@ -187,9 +244,9 @@ __global__ void __launch_bounds__(32 * kVerifyWarps, 2) verify_drafts_kernel(con
   namespace cg = cooperative_groups;
   using A = Access<T, VEC>;
   constexpr int STEP = 32 * A::N;
-  __shared__ double sums[2][kVerifySegments];  // of all segments of the row; the second where the first try held no weight
-  __shared__ double pieces[kVerifyWarps];
-  __shared__ int s_n, s_stand, s_row;
+  __shared__ Sum sums[2][kVerifySegments];  // of all segments of the row; the second where the first try held no weight
+  __shared__ Sum pieces[kVerifyWarps], s_before, s_target;
+  __shared__ int s_n, s_stand, s_row, s_seg;
   cg::cluster_group cluster = cg::this_cluster();
   const int size = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int b = blockIdx.x / size;
@@ -274,21 +331,29 @@ __global__ void __launch_bounds__(32 * kVerifyWarps, 2) verify_drafts_kernel(con
   const int mine = rank * kVerifyWarps + warp;
   const float u = p.uniforms[(long long)b * (K + 1) + K];
   int seg = -1;
-  double before = 0.0, target = 0.0;
   for (int attempt = 0; attempt < 2; ++attempt) {
     const long long lo = (long long)mine * segment;
-    double v = 0.0;
-    if (lo < V) v = lane_sum<T, VEC>(row, (int)lo, (int)min(lo + segment, (long long)V), V, lane).value();
+    Sum v;
+    if (lo < V) v = lane_sum<T, VEC>(row, (int)lo, (int)min(lo + segment, (long long)V), V, lane);
+    v.settle();
     v = warp_sum(v);
     if (lane < size) *cluster.map_shared_rank(&sums[attempt][mine], lane) = v;
     cluster.sync();
-    // every warp of every CTA finds the segment for itself
-    double total = 0.0;
-    for (int i = lane; i < count; i += 32) total += sums[attempt][i];
-    total = warp_sum(total);
-    target = (double)u * total;
-    before = 0.0;
-    seg = pick(sums[attempt], count, target, before, lane);
+    if (warp == 0) {  // the total, and the segment, found by every CTA for itself
+      Sum total;
+      for (int i = lane; i < count; i += 32) total.add(sums[attempt][i]);
+      total = warp_sum(total);
+      const Sum target = share(u, total);
+      Sum before;
+      const int found = pick<kVerifySegments / 32>(sums[attempt], count, target, before, lane);
+      if (lane == 0) {
+        s_seg = found;
+        s_before = before;
+        s_target = target;
+      }
+    }
+    __syncthreads();
+    seg = s_seg;
     if (seg >= 0 || (row.q == nullptr && row.skip < 0)) break;
     row.q = nullptr;  // p nowhere above q: p itself
     row.skip = -1;
@@ -306,17 +371,20 @@ __global__ void __launch_bounds__(32 * kVerifyWarps, 2) verify_drafts_kernel(con
   const int piece = ((segment + kVerifyWarps - 1) / kVerifyWarps + STEP - 1) / STEP * STEP;
   {
     const int lo = min(first + warp * piece, end);
-    const double v = warp_sum(lane_sum<T, VEC>(row, lo, min(lo + piece, end), V, lane).value());
+    Sum v = lane_sum<T, VEC>(row, lo, min(lo + piece, end), V, lane);
+    v.settle();
+    v = warp_sum(v);
     if (lane == 0) pieces[warp] = v;
   }
   __syncthreads();
-  int w = pick(pieces, kVerifyWarps, target, before, lane);
+  const Sum target = s_target;
+  Sum base = s_before;
+  int w = pick<1>(pieces, kVerifyWarps, target, base, lane);
   if (w < 0) w = 0;  // (cannot be: the segment holds weight)
   if (warp != w) return;
   // a warp's step at a time; the step's sum in the order of tokens: lanes, then a lane's elements
   const int lo = min(first + w * piece, end), hi = min(lo + piece, end);
   int found = -1;
-  double base = before;
   for (int j0 = lo; j0 < hi; j0 += STEP) {
     const int j = j0 + lane * A::N;
     float pj[A::N], qj[A::N];
@@ -327,28 +395,23 @@ __global__ void __launch_bounds__(32 * kVerifyWarps, 2) verify_drafts_kernel(con
     }
     A::unpack(pr, pj);
     A::unpack(qr, qj);
-    double own = 0.0, part[A::N];
+    Sum part[A::N], own;
 #pragma unroll
     for (int i = 0; i < A::N; ++i) {
-      float rest;
-      const float d = row.weight(pj[i], qj[i], j + i, rest);
-      part[i] = (double)d + (double)rest;
-      own += part[i];
+      part[i].s = row.weight(pj[i], qj[i], j + i, part[i].e);
+      own.add(part[i].s, part[i].e);
     }
-    double incl = own;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const double up = __shfl_up_sync(0xffffffffu, incl, off);
-      if (lane >= off) incl += up;
-    }
+    own.settle();
+    Sum incl, excl;
+    warp_scan(own, incl, excl, lane);
     int at = -1, last = -1;
-    double run = base + (incl - own);
+    Sum run = plus(base, excl);
 #pragma unroll
     for (int i = 0; i < A::N; ++i) {
-      run += part[i];
-      if (part[i] > 0.0) {
+      run.add(part[i]);
+      if (positive(part[i])) {
         last = j + i;
-        if (at < 0 && run > target) at = j + i;
+        if (at < 0 && above(run, target)) at = j + i;
       }
     }
     const unsigned hit = __ballot_sync(0xffffffffu, at >= 0), any = __ballot_sync(0xffffffffu, last >= 0);
@@ -357,7 +420,7 @@ __global__ void __launch_bounds__(32 * kVerifyWarps, 2) verify_drafts_kernel(con
       break;
     }
     if (any != 0) found = __shfl_sync(0xffffffffu, last, 31 - __clz(any));
-    base += __shfl_sync(0xffffffffu, incl, 31);
+    base = plus(base, shuffle(incl, 31));
   }
   if (lane == 0) tokens[stand] = found;
 }
