@@ -128,12 +128,13 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kAppendBlocks) kv_append_pa
         turn_b = cb < 2 * rot;
       }
       const int ia = STYLE == 1 ? 8 * sub : 4 * ca, ib = STYLE == 1 ? 8 * sub + 4 : 4 * cb;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        c[j] = turn_a ? tab[ia + j] : 1.f;
-        s[j] = turn_a ? tab[D / 2 + ia + j] : 0.f;
-        c[4 + j] = turn_b ? tab[ib + j] : 1.f;
-        s[4 + j] = turn_b ? tab[D / 2 + ib + j] : 0.f;
+if (turn_a) {
+        *reinterpret_cast<float4*>(c) = *reinterpret_cast<const float4*>(tab + ia);
+        *reinterpret_cast<float4*>(s) = *reinterpret_cast<const float4*>(tab + D / 2 + ia);
+      }
+      if (turn_b) {
+        *reinterpret_cast<float4*>(c + 4) = *reinterpret_cast<const float4*>(tab + ib);
+        *reinterpret_cast<float4*>(s + 4) = *reinterpret_cast<const float4*>(tab + D / 2 + ib);
       }
     }
     for (int r0 = 0; r0 < rounds; r0 += U) {

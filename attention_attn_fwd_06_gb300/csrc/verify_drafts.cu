@@ -255,9 +255,11 @@ __global__ void __launch_bounds__(32 * kVerifyWarps, 2) verify_drafts_kernel(con
   cluster.barrier_arrive();  // (waited for before the first store into another CTA's shared memory: all have started)
 
   if (warp == 0) {
-    // which drafts stand
+    // Which drafts stand.  The first 32 drafts and numbers are read beside the length, not after it.
     int n = K, row0 = 0;
     bool bad = false;
+    int x = lane < K ? p.drafts[(long long)b * K + lane] : 0;
+    float u = lane < K ? p.uniforms[(long long)b * (K + 1) + lane] : 0.f;
     if (p.cu != nullptr) {
       const int c0 = p.cu[b], c1 = p.cu[b + 1];
       bad = c0 < 0 || c1 < c0 || c1 > p.total || c1 - c0 > K + 1;
@@ -273,20 +275,22 @@ __global__ void __launch_bounds__(32 * kVerifyWarps, 2) verify_drafts_kernel(con
     int stand = n < 0 ? 0 : n;
     for (int i0 = 0; i0 < n; i0 += 32) {
       const int i = i0 + lane;
+      if (i0 > 0 && i < n) {
+        x = p.drafts[(long long)b * K + i];
+        u = p.uniforms[(long long)b * (K + 1) + i];
+      }
       bool ok = true;
       if (i < n) {
-        const int x = p.drafts[(long long)b * K + i];
         ok = false;
         if (x < 0 || x >= V) {
           bad = true;
         } else {
           const T* pr = reinterpret_cast<const T*>(p.target) +
                         (p.cu != nullptr ? (long long)(row0 + i) * p.ts[1] : (long long)b * p.ts[0] + (long long)i * p.ts[1]);
-          const double px = as_float<T>(__ldg(pr + x));
           double qx = 1.0;
           if (p.draft != nullptr)
             qx = as_float<T>(__ldg(reinterpret_cast<const T*>(p.draft) + (long long)b * p.ds[0] + (long long)i * p.ds[1] + x));
-          ok = (double)p.uniforms[(long long)b * (K + 1) + i] * qx < px;
+          ok = (double)u * qx < (double)as_float<T>(__ldg(pr + x));
         }
       }
       const unsigned refused = __ballot_sync(0xffffffffu, !ok);
