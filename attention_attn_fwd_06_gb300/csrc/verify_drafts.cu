@@ -9,13 +9,18 @@
 // The sums decide which token comes out, so they carry more than 32 bits: a lane adds fp32 terms into a pair of floats (a
 // sum and the sum of its roundings, Knuth's two-sum), a difference p - q enters with its own rounding, and lanes, warps and
 // CTAs are joined as such pairs in a fixed order: 2^-42 of the sum, and the same bits every time.  (64-bit floats run at two
-// adds a clock and SM: in them the joins alone took most of the time, B = 8, V = 32,000: 17 us against 9.)
+// adds a clock and SM: with the joins in them 8 sequences over 32,000 tokens took 20.5 us a call, 12 without.)
 //
-// What bounds it: for few sequences the chain of launch, drafts, their probabilities, the row, the exchange and the search;
-// for many, reading one row of p and of q each.  A cluster of CTAs takes a sequence: every CTA decides which drafts stand
-// by itself, its warps sum a segment of the row each, the segments' sums go to every CTA of the cluster through distributed
-// shared memory, and the CTA that holds the segment where the sum passes u's share reads that segment again (from L2), its
-// warps a piece each, and finds the token.
+// What bounds it: for few sequences the chain of launch, drafts (1.4 us), the row (1.1), the exchange (0.7), the segment (0.6)
+// and the token in it (2 us), by timer stamps of 8 sequences; for many, reading one row of p and of q each, beside that chain.
+// A cluster of CTAs takes a sequence: every CTA decides which drafts stand by itself, its warps sum a segment of the row each,
+// the segments' sums go to every CTA of the cluster through distributed shared memory, and the CTA that holds the segment where
+// the sum passes u's share reads that segment again (from L2), its warps a piece each, and finds the token.  CTAs of 8 warps at 48
+// registers, so that five share an SM and one's chain runs beside another's reading.
+// Measured (CUDA-graph replays over rotating inputs): 8 sequences of 4 drafts over 32,000 tokens 6.2 us; 64 of up to 8 over
+// 131,072 15.7 us (4.3 TB/s, 0.64 of the copy bandwidth); 37 without distributions over 50,001 in bf16, one element a
+// load, 8.8 us.  Four CTAs an SM with twice the loads in flight 6.5 / 16.5 / 8.8 us, CTAs of 16 warps 7.6 / 21.2 / 11.5 us;
+// sums element by element with every weight's check 8.0 / 29.2 / 12.0 us, loads behind their conditions besides 7.9 / 28.6 / 15.6.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -26,7 +31,7 @@
 namespace attn {
 namespace {
 
-constexpr int kVerifyWarps = 16;
+constexpr int kVerifyWarps = 8;
 constexpr int kVerifyMaxCluster = 8;
 constexpr int kVerifySegments = kVerifyWarps * kVerifyMaxCluster;
 
@@ -116,7 +121,8 @@ struct Row {
   const T* p;
   const T* q;    // taken away; or null
   int skip;      // this token's weight is 0 (a refused draft without a distribution); or -1
-  // weight of token j with probabilities pj, qj: d, and what rounding took from it; whatever is not a positive finite number counts as 0
+  // Weight of token j with probabilities pj, qj: d, and what rounding took from it; whatever is not a positive finite number
+  // counts as 0.
   __device__ __forceinline__ float weight(float pj, float qj, int j, float& rest) const {
     float d = pj - qj;
     rest = (pj - d) - qj;  // exact where pj >= qj
@@ -135,28 +141,17 @@ struct Access {
   struct Raw {
     uint32_t w[VEC ? 4 : 1];
   };
-  static __device__ __forceinline__ Raw load(const T* row, int j, int V) {
-    Raw r{};
+  // tokens j .. j + N - 1, all of them in the row
+  static __device__ __forceinline__ Raw load(const T* row, int j) {
+    Raw r;
     if constexpr (!VEC) {
       r.w[0] = __float_as_uint(as_float<T>(__ldg(row + j)));
-    } else if (j + N <= V) {
+    } else {
       const uint4 x = __ldg(reinterpret_cast<const uint4*>(row + j));
       r.w[0] = x.x;
       r.w[1] = x.y;
       r.w[2] = x.z;
       r.w[3] = x.w;
-    } else {  // the row's end: what follows it is not read
-      constexpr int PER = 4 / sizeof(T);
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        if (j + i >= V) break;
-        uint32_t e;
-        if constexpr (sizeof(T) == 4)
-          e = __float_as_uint(__ldg(row + j + i));
-        else
-          e = (uint32_t)__ldg(reinterpret_cast<const unsigned short*>(row) + j + i) << (16 * (i % PER));
-        r.w[i / PER] |= e;
-      }
     }
     return r;
   }
@@ -168,83 +163,173 @@ struct Access {
       for (int i = 0; i < N; ++i) v[i] = __uint_as_float(r.w[i]);
     }
   }
+  // of a row that may end among them: what lies past it is not read, and 0
+  static __device__ __forceinline__ void load_to(const T* row, int j, int V, float (&v)[N]) {
+    if (j + N <= V) {
+      unpack(load(row, j), v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = j + i < V ? as_float<T>(__ldg(row + j + i)) : 0.f;
+    }
+  }
 };
 
-// Sum of the weights of tokens [lo, hi) (lo and hi - lo multiples of a warp's step, or hi == V) over this lane's elements.
-template <typename T, bool VEC>
-__device__ __forceinline__ Sum lane_sum(const Row<T>& row, int lo, int hi, int V, int lane) {
+__device__ __forceinline__ float2 two(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 minus(float2 a, float2 b) { return __ffma2_rn(b, two(-1.f), a); }
+
+// Two sums side by side (packed adds), of weights that are finite where positive: one that is not makes the sum so.
+struct Sum2 {
+  float2 s = make_float2(0.f, 0.f), e = make_float2(0.f, 0.f);
+  // the weights max(p - q, 0)
+  template <bool HAS_Q>
+  __device__ __forceinline__ void add(float2 p, float2 q) {
+    float2 d = p, rest = two(0.f);
+    if constexpr (HAS_Q) {
+      d = minus(p, q);
+      rest = minus(minus(p, d), q);
+      rest.x = d.x > 0.f ? rest.x : 0.f;
+      rest.y = d.y > 0.f ? rest.y : 0.f;
+    }
+    d.x = fmaxf(d.x, 0.f);  // (0 for a NaN too)
+    d.y = fmaxf(d.y, 0.f);
+    const float2 t = __fadd2_rn(s, d);
+    const float2 z = minus(t, s);
+    float2 r = __fadd2_rn(minus(s, minus(t, z)), minus(d, z));
+    if constexpr (HAS_Q) r = __fadd2_rn(r, rest);
+    e = __fadd2_rn(e, r);
+    s = t;
+  }
+  __device__ __forceinline__ Sum joined() const {
+    Sum a, b;
+    a.s = s.x;
+    a.e = e.x;
+    b.s = s.y;
+    b.e = e.y;
+    a.settle();
+    a.add(b);
+    return a;
+  }
+};
+
+// Sum of the weights of tokens [lo, hi) (lo and hi - lo multiples of a warp's step, or hi == V) over this lane's elements, the
+// positive ones taken to be finite.  A round's loads go out together: none waits behind a condition (in the last round those
+// past the end read the first tokens again).
+template <typename T, bool VEC, bool HAS_Q>
+__device__ __forceinline__ Sum lane_sum_of(const Row<T>& row, int lo, int hi, int V, int lane) {
   using A = Access<T, VEC>;
   constexpr int STEP = 32 * A::N;
-  constexpr int U = VEC ? 4 : 8;
-  Sum s;
-  for (int j0 = lo + lane * A::N; j0 < hi; j0 += U * STEP) {
+  constexpr int U = VEC ? 2 : 8;
+  Sum2 s;
+  const int whole = VEC && hi == V ? V - V % A::N : hi;  // end of the row's whole 16 bytes
+  auto round = [&](int base, bool all) {
     typename A::Raw p[U], q[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int j = j0 + u * STEP;
-      p[u] = q[u] = typename A::Raw{};
-      if (j < hi) {
-        p[u] = A::load(row.p, j, V);
-        if (row.q != nullptr) q[u] = A::load(row.q, j, V);
-      }
+      int j = base + u * STEP + lane * A::N;
+      if (!all && j >= whole) j = lo;
+      p[u] = A::load(row.p, j);
+      if constexpr (HAS_Q) q[u] = A::load(row.q, j);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      float pj[A::N], qj[A::N];
-      A::unpack(p[u], pj);
-      A::unpack(q[u], qj);
+      const int j = base + u * STEP + lane * A::N;
+      float pj[A::N + 1], qj[A::N + 1];
+      A::unpack(p[u], *reinterpret_cast<float(*)[A::N]>(pj));
+      if constexpr (HAS_Q) A::unpack(q[u], *reinterpret_cast<float(*)[A::N]>(qj));
+      if (!all && j >= whole)
 #pragma unroll
-      for (int i = 0; i < A::N; ++i) {
-        float rest;
-        const float w = row.weight(pj[i], qj[i], j0 + u * STEP + i, rest);
-        s.add(w, rest);
+        for (int i = 0; i < A::N; ++i) pj[i] = 0.f, qj[i] = 0.f;
+      if (!HAS_Q && (unsigned)(row.skip - j) < (unsigned)A::N)
+#pragma unroll
+        for (int i = 0; i < A::N; ++i)
+          if (j + i == row.skip) pj[i] = 0.f;
+      if constexpr (VEC) {
+#pragma unroll
+        for (int i = 0; i < A::N; i += 2) s.add<HAS_Q>(make_float2(pj[i], pj[i + 1]), make_float2(qj[i], qj[i + 1]));
+      } else if (u % 2 == 0) {
+        pj[1] = 0.f;  // (paired below)
+        p[u].w[0] = __float_as_uint(pj[0]);
+        q[u].w[0] = HAS_Q ? __float_as_uint(qj[0]) : 0u;
+      } else {
+        s.add<HAS_Q>(make_float2(__uint_as_float(p[u - 1].w[0]), pj[0]),
+                     make_float2(__uint_as_float(q[u - 1].w[0]), HAS_Q ? qj[0] : 0.f));
       }
     }
+  };
+  int base = lo;
+  for (; base + U * STEP <= whole; base += U * STEP) round(base, true);
+  if (base < whole) round(base, false);
+  if (VEC && whole + lane < hi) {  // the row's last tokens, short of 16 bytes
+    const int j = whole + lane;
+    const float p = j == row.skip ? 0.f : as_float<T>(__ldg(row.p + j));
+    s.add<HAS_Q>(make_float2(p, 0.f), make_float2(HAS_Q ? as_float<T>(__ldg(row.q + j)) : 0.f, 0.f));
   }
+  return s.joined();
+}
+// The same with every weight looked at (rows with infinities).
+template <typename T>
+__device__ __noinline__ Sum lane_sum_careful(const Row<T> row, int lo, int hi, int lane) {
+  Sum s;
+  for (int j = lo + lane; j < hi; j += 32) {
+    float rest;
+    const float w = row.weight(as_float<T>(__ldg(row.p + j)), row.q != nullptr ? as_float<T>(__ldg(row.q + j)) : 0.f, j, rest);
+    s.add(w, rest);
+  }
+  s.settle();
   return s;
 }
-
-// The first of `count` <= 32 PER parts, in order, at whose end the running sum (from `before`) passes `target`; where none does
-// (u of 1 or more, or NaN), the last one that holds weight; -1 if none holds any.  One warp, PER parts a lane; `before` becomes
-// the sum before that part.
-template <int PER>
-__device__ int pick(const Sum* parts, int count, Sum target, Sum& before, int lane) {
-  Sum v[PER], own;
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    v[i] = lane * PER + i < count ? parts[lane * PER + i] : Sum{};
-    own.add(v[i]);
-  }
-  Sum incl, excl;
-  warp_scan(own, incl, excl, lane);
-  Sum run = plus(before, excl), at_hit = run, at_last = run;
-  int hit = -1, last = -1;
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const Sum end = plus(run, v[i]);
-    if (positive(v[i])) {
-      last = lane * PER + i;
-      at_last = run;
-      if (hit < 0 && above(end, target)) {
-        hit = last;
-        at_hit = run;
-      }
-    }
-    run = end;
-  }
-  const unsigned hits = __ballot_sync(0xffffffffu, hit >= 0), lasts = __ballot_sync(0xffffffffu, last >= 0);
-  if (lasts == 0) return -1;
-  const int src = hits != 0 ? __ffs(hits) - 1 : 31 - __clz(lasts);
-  before = shuffle(hits != 0 ? at_hit : at_last, src);
-  return __shfl_sync(0xffffffffu, hits != 0 ? hit : last, src);
+template <typename T, bool VEC>
+__device__ __forceinline__ Sum lane_sum(const Row<T>& row, int lo, int hi, int V, int lane, bool careful) {
+  if (careful) return lane_sum_careful<T>(row, lo, hi, lane);
+  return row.q != nullptr ? lane_sum_of<T, VEC, true>(row, lo, hi, V, lane) : lane_sum_of<T, VEC, false>(row, lo, hi, V, lane);
 }
 
+// Parts of a sum, PER a lane, one warp: their running sums.
+template <int PER>
+struct Parts {
+  Sum v[PER], incl, excl;
+  __device__ __forceinline__ Parts(const Sum* parts, int count, int lane) {
+    Sum own;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      v[i] = lane * PER + i < count ? parts[lane * PER + i] : Sum{};
+      own.add(v[i]);
+    }
+    warp_scan(own, incl, excl, lane);
+  }
+  __device__ __forceinline__ Sum total() const { return shuffle(incl, 31); }
+  // The first part, in order, at whose end the running sum (from `before`) passes `target`; where none does (u of 1 or more, or
+  // NaN), the last one that holds weight; -1 if none holds any.  `before` becomes the sum before that part.
+  __device__ __forceinline__ int pick(Sum target, Sum& before, int lane) const {
+    Sum run = plus(before, excl), at_hit = run, at_last = run;
+    int hit = -1, last = -1;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const Sum end = plus(run, v[i]);
+      if (positive(v[i])) {
+        last = lane * PER + i;
+        at_last = run;
+        if (hit < 0 && above(end, target)) {
+          hit = last;
+          at_hit = run;
+        }
+      }
+      run = end;
+    }
+    const unsigned hits = __ballot_sync(0xffffffffu, hit >= 0), lasts = __ballot_sync(0xffffffffu, last >= 0);
+    if (lasts == 0) return -1;
+    const int src = hits != 0 ? __ffs(hits) - 1 : 31 - __clz(lasts);
+    before = shuffle(hits != 0 ? at_hit : at_last, src);
+    return __shfl_sync(0xffffffffu, hits != 0 ? hit : last, src);
+  }
+};
+
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(32 * kVerifyWarps, 2) verify_drafts_kernel(const VerifyDraftsLaunch p, int segment) {
+__global__ void __launch_bounds__(32 * kVerifyWarps, 5) verify_drafts_kernel(const VerifyDraftsLaunch p, int segment) {
   namespace cg = cooperative_groups;
   using A = Access<T, VEC>;
   constexpr int STEP = 32 * A::N;
-  __shared__ Sum sums[2][kVerifySegments];  // of all segments of the row; the second where the first try held no weight
+  __shared__ Sum sums[2][kVerifySegments];  // of all segments of the row, of one try and the next
   __shared__ Sum pieces[kVerifyWarps], s_before, s_target;
   __shared__ int s_n, s_stand, s_row, s_seg;
   cg::cluster_group cluster = cg::this_cluster();
@@ -334,22 +419,24 @@ __global__ void __launch_bounds__(32 * kVerifyWarps, 2) verify_drafts_kernel(con
   const int count = size * kVerifyWarps;
   const int mine = rank * kVerifyWarps + warp;
   const float u = p.uniforms[(long long)b * (K + 1) + K];
+  // Up to three tries: with weights taken to be finite; if their sum is not, with every one looked at; if there is none and
+  // something was taken from p, with p itself (looked at again).
   int seg = -1;
-  for (int attempt = 0; attempt < 2; ++attempt) {
+  bool careful = false;
+  for (int attempt = 0;; ++attempt) {
     const long long lo = (long long)mine * segment;
     Sum v;
-    if (lo < V) v = lane_sum<T, VEC>(row, (int)lo, (int)min(lo + segment, (long long)V), V, lane);
-    v.settle();
+    if (lo < V) v = lane_sum<T, VEC>(row, (int)lo, (int)min(lo + segment, (long long)V), V, lane, careful);
     v = warp_sum(v);
-    if (lane < size) *cluster.map_shared_rank(&sums[attempt][mine], lane) = v;
+    Sum* const parts = sums[attempt & 1];  // (the tries before the last one have been read: a cluster barrier lies between)
+    if (lane < size) *cluster.map_shared_rank(&parts[mine], lane) = v;
     cluster.sync();
     if (warp == 0) {  // the total, and the segment, found by every CTA for itself
-      Sum total;
-      for (int i = lane; i < count; i += 32) total.add(sums[attempt][i]);
-      total = warp_sum(total);
-      const Sum target = share(u, total);
+      const Parts<kVerifySegments / 32> all(parts, count, lane);
+      const Sum total = all.total(), target = share(u, total);
       Sum before;
-      const int found = pick<kVerifySegments / 32>(sums[attempt], count, target, before, lane);
+      int found = all.pick(target, before, lane);
+      if (!(total.s < INFINITY)) found = -2;
       if (lane == 0) {
         s_seg = found;
         s_before = before;
@@ -358,9 +445,15 @@ __global__ void __launch_bounds__(32 * kVerifyWarps, 2) verify_drafts_kernel(con
     }
     __syncthreads();
     seg = s_seg;
-    if (seg >= 0 || (row.q == nullptr && row.skip < 0)) break;
-    row.q = nullptr;  // p nowhere above q: p itself
-    row.skip = -1;
+    if (seg == -2 && !careful) {
+      careful = true;
+    } else if (seg < 0 && (row.q != nullptr || row.skip >= 0)) {
+      row.q = nullptr;  // p nowhere above q: p itself
+      row.skip = -1;
+      careful = true;
+    } else {
+      break;
+    }
   }
   if (seg < 0) {  // no weight at all
     if (rank == 0 && threadIdx.x == 0) {
@@ -375,15 +468,13 @@ __global__ void __launch_bounds__(32 * kVerifyWarps, 2) verify_drafts_kernel(con
   const int piece = ((segment + kVerifyWarps - 1) / kVerifyWarps + STEP - 1) / STEP * STEP;
   {
     const int lo = min(first + warp * piece, end);
-    Sum v = lane_sum<T, VEC>(row, lo, min(lo + piece, end), V, lane);
-    v.settle();
-    v = warp_sum(v);
+    const Sum v = warp_sum(lane_sum<T, VEC>(row, lo, min(lo + piece, end), V, lane, careful));
     if (lane == 0) pieces[warp] = v;
   }
   __syncthreads();
   const Sum target = s_target;
   Sum base = s_before;
-  int w = pick<1>(pieces, kVerifyWarps, target, base, lane);
+  int w = Parts<1>(pieces, kVerifyWarps, lane).pick(target, base, lane);
   if (w < 0) w = 0;  // (cannot be: the segment holds weight)
   if (warp != w) return;
   // a warp's step at a time; the step's sum in the order of tokens: lanes, then a lane's elements
@@ -391,14 +482,11 @@ __global__ void __launch_bounds__(32 * kVerifyWarps, 2) verify_drafts_kernel(con
   int found = -1;
   for (int j0 = lo; j0 < hi; j0 += STEP) {
     const int j = j0 + lane * A::N;
-    float pj[A::N], qj[A::N];
-    typename A::Raw pr{}, qr{};
+    float pj[A::N] = {}, qj[A::N] = {};
     if (j < hi) {
-      pr = A::load(row.p, j, V);
-      if (row.q != nullptr) qr = A::load(row.q, j, V);
+      A::load_to(row.p, j, V, pj);
+      if (row.q != nullptr) A::load_to(row.q, j, V, qj);
     }
-    A::unpack(pr, pj);
-    A::unpack(qr, qj);
     Sum part[A::N], own;
 #pragma unroll
     for (int i = 0; i < A::N; ++i) {
