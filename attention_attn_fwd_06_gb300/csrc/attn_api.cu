@@ -5,6 +5,7 @@
 // and the kernel launches.  No compute happens here and there is no CPU path.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 #include <cstdlib>
 #include <cmath>
@@ -291,6 +292,17 @@ DecodeMultiShape decode_multi_shape(long long rows, int D, int num_sms) {
   s.part_o_elems = slots * (size_t)rows * D;
   s.bytes = kCounterBytes + (s.part_o_elems + slots * (size_t)rows * 2) * sizeof(float);
   return s;
+}
+
+// A workspace of attn_decode_multi_paged: the region of the kernel for few rows, all zeros between calls, sized for its
+// largest call; behind it, for calls of more rows, decode_multi_shape's.  Calls of any sizes can so follow one another.
+size_t decode_rows_region(int num_sms) {
+  return std::max(attn::decode_rows_shape(attn::kDecodeRowsMax, 128, num_sms).bytes,
+                  attn::decode_rows_shape(attn::kDecodeRowsMax, 64, num_sms).bytes);
+}
+size_t decode_multi_paged_bytes(long long rows, int D, int num_sms) {
+  if (rows <= attn::kDecodeRowsMax) return attn::decode_rows_shape((int)rows, D, num_sms).bytes;
+  return decode_rows_region(num_sms) + decode_multi_shape(rows, D, num_sms).bytes;
 }
 
 constexpr double kTwoPi = 6.283185307179586476925286766559;
@@ -1059,7 +1071,7 @@ unsigned long long attn_decode_multi_paged_workspace_bytes(int Hq, int Hkv, int 
   if (validate_decode_q4_heads(Hq, Hkv, max_new, D) != ATTN_OK) return 0;
   DeviceState* s = nullptr;
   const int sms = device_state(&s) == ATTN_OK ? s->num_sms : 0;
-  return decode_multi_shape((long long)(Hq / Hkv) * max_new, D, sms).bytes;
+  return decode_multi_paged_bytes((long long)(Hq / Hkv) * max_new, D, sms);
 }
 
 int attn_decode_multi_paged(const attn_decode_multi_paged_params* p) {
@@ -1089,15 +1101,15 @@ int attn_decode_multi_paged(const attn_decode_multi_paged_params* p) {
   DeviceState* s = nullptr;
   st = device_state_locked(&s);
   if (st != ATTN_OK) return st;
-  const DecodeMultiShape sh = decode_multi_shape((long long)(p->Hq / p->Hkv) * p->max_new, p->D, s->num_sms);
+  const long long rows = (long long)(p->Hq / p->Hkv) * p->max_new;
   char* ws = static_cast<char*>(p->workspace);
   if (ws == nullptr) {
     // made for the largest call, so that it never has to grow under a graph that was captured with it
-    st = ensure_buffer_locked(s->ws_paged, s->ws_paged_bytes, decode_multi_shape(128, 128, s->num_sms).bytes, kCounterBytes,
-                              stream);
+    const size_t bytes = decode_multi_paged_bytes(128, 128, s->num_sms);
+    st = ensure_buffer_locked(s->ws_paged, s->ws_paged_bytes, bytes, bytes, stream);
     if (st != ATTN_OK) return st;
     ws = static_cast<char*>(s->ws_paged);
-  } else if (p->workspace_bytes < sh.bytes) {
+  } else if (p->workspace_bytes < decode_multi_paged_bytes(rows, p->D, s->num_sms)) {
     return ATTN_ERR_SCRATCH_TOO_SMALL;
   }
   attn::DecodeMultiLaunch L{};
@@ -1113,9 +1125,7 @@ int attn_decode_multi_paged(const attn_decode_multi_paged_params* p) {
   L.kv_lens = p->kv_lens;
   L.out = p->out;
   L.lse = p->lse;
-  L.counters = reinterpret_cast<unsigned*>(ws);
-  L.part_o = reinterpret_cast<float*>(ws + kCounterBytes);
-  L.part_ml = L.part_o + sh.part_o_elems;
+  L.rows_ws = ws;
   L.B = p->B;
   L.Hq = p->Hq;
   L.Hkv = p->Hkv;
@@ -1128,6 +1138,11 @@ int attn_decode_multi_paged(const attn_decode_multi_paged_params* p) {
   L.status = s->status;
   L.fault_skip_arrive = fault_skip_arrive();
   L.stream = stream;
+  if (rows <= attn::kDecodeRowsMax) return map_cuda(attn::launch_decode_rows(L));
+  ws += decode_rows_region(s->num_sms);
+  L.counters = reinterpret_cast<unsigned*>(ws);
+  L.part_o = reinterpret_cast<float*>(ws + kCounterBytes);
+  L.part_ml = L.part_o + decode_multi_shape(rows, p->D, s->num_sms).part_o_elems;
   return map_cuda(attn::launch_decode_multi(L));
 }
 
@@ -1198,7 +1213,7 @@ int attn_get_device_status(void* stream) {
     cudaDeviceSynchronize();
     if (s->ws != nullptr) cudaMemset(s->ws, 0, kCounterBytes);
     if (s->ws_q4 != nullptr) cudaMemset(s->ws_q4, 0, s->ws_q4_bytes);
-    if (s->ws_paged != nullptr) cudaMemset(s->ws_paged, 0, kCounterBytes);
+    if (s->ws_paged != nullptr) cudaMemset(s->ws_paged, 0, s->ws_paged_bytes);
     if (dev >= 0 && dev < kMaxDevices && g_noalloc_ptr[dev] != nullptr) cudaMemset(g_noalloc_ptr[dev], 0, kCounterBytes);
     cudaDeviceSynchronize();
     cudaGetLastError();

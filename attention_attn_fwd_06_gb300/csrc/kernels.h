@@ -71,8 +71,17 @@ struct DecodeMultiLaunch {
   unsigned* status;
   RopeArgs rope;        // rotates q (token t to kv_len - Lq + t) when style != 0
   int fault_skip_arrive;  // test hook: CTA 0 withholds one P-ready arrival (its MMA warp's wait runs out)
+  void* rows_ws;          // launch_decode_rows: counts and partials of decode_rows_shape, all zeros between calls
   cudaStream_t stream;
 };
+
+// The same over pages for up to kDecodeRowsMax query rows a kv head (decode_rows.cu).
+constexpr int kDecodeRowsMax = 32;
+struct DecodeRowsShape {
+  size_t count_bytes, ml_bytes, bytes;
+};
+DecodeRowsShape decode_rows_shape(int rows, int D, int num_sms);
+cudaError_t launch_decode_rows(const DecodeMultiLaunch& p);
 
 // CTAs of the persistent multi-token decode launch (one per SM); the partial slots number 2 * grid.
 int decode_multi_grid(int num_sms);
