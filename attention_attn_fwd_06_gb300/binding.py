@@ -911,37 +911,36 @@ def attn_kv_append_paged(k, v, kpages, vpages, slots, rope=None, positions=None,
     alike.  k_out (made where ``want_k``) takes the rotated k packed.  q_out/k_out may be q/k themselves.
     -> (q_out, k_out)"""
     sk, at = _rows(k, "k", 3), k.get_device()
+    shape = k.shape
     sv = _rows(v, "v", 3, at)
-    T, Hkv, D = k.shape
-    if v.shape != k.shape:
-        raise ValueError(f"k/v shapes {tuple(k.shape)} {tuple(v.shape)} differ")
-    if not isinstance(kpages, torch.Tensor) or kpages.dim() != 4:
-        raise ValueError("kpages must be a tensor [num_pages,Hkv,page_size,D]")
-    num_pages, _, page_size, _ = kpages.shape
-    pool = (num_pages, Hkv, page_size, D)
-    R, Hq, qp, qop, kop = 0, 0, 0, 0, 0
+    T, Hkv, D = shape
+    if v.shape != shape:
+        raise ValueError(f"k/v shapes {tuple(shape)} {tuple(v.shape)} differ")
+    pool = _pool_pages(kpages, Hkv, D)
+    R = Hq = qp = qop = kop = 0
     sq = sqo = sko = (0, 0)
     r = _NO_ROPE
     if rope is None:
         if q is not None or q_out is not None or k_out is not None or want_k:
             raise ValueError("q and k_out go with a rotation")
     else:
-        if len(rope) > 3 and rope[3] is not None:
-            raise ValueError("rope k_out is taken by prefill calls only")
-        cos, sin, style = rope[:3]
+        cos, sin, style = rope if len(rope) == 3 else _rope3(rope)
+        try:
+            max_pos, pairs = tab = cos.shape
+        except (AttributeError, ValueError):
+            raise ValueError("rope tables must be tensors [max_pos, R/2]") from None
+        if max_pos == 0 or pairs == 0:
+            raise ValueError("rope tables must have rows")
         if style not in _ROPE_STYLES:
             raise ValueError("rope style must be 'half' or 'interleaved'")
-        tab = tuple(cos.shape) if isinstance(cos, torch.Tensor) and cos.dim() == 2 else (0, 0)
-        if tab[0] == 0 or tab[1] == 0:
-            raise ValueError("rope tables must be [max_pos, R/2] and have rows")
-        R = 2 * tab[1]
-        r = (_fit(cos, "rope cos", torch.float32, tab, at), _fit(sin, "rope sin", torch.float32, tab, at), tab[0],
+        R = 2 * pairs
+        r = (_fit(cos, "rope cos", torch.float32, tab, at), _fit(sin, "rope sin", torch.float32, tab, at), max_pos,
              _ROPE_STYLES[style], 0)
         if q is not None:
             sq = _rows(q, "q", 3, at)
             Hq = q.shape[1]
             if q.shape != (T, Hq, D) or Hq == 0:
-                raise ValueError(f"q shape {tuple(q.shape)} does not match k {tuple(k.shape)}")
+                raise ValueError(f"q shape {tuple(q.shape)} does not match k {tuple(shape)}")
             if q_out is None:
                 q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
             sqo = _out_rows(q_out, "q_out", q, 3, at)
@@ -949,7 +948,7 @@ def attn_kv_append_paged(k, v, kpages, vpages, slots, rope=None, positions=None,
         elif q_out is not None:
             raise ValueError("q_out goes with q")
         if k_out is None and want_k:
-            k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=k.device)
+            k_out = torch.empty(shape, dtype=torch.bfloat16, device=k.device)
         if k_out is not None:
             sko = _out_rows(k_out, "k_out", k, 3, at)
             kop = k_out.data_ptr()
@@ -957,9 +956,24 @@ def attn_kv_append_paged(k, v, kpages, vpages, slots, rope=None, positions=None,
           k.data_ptr(), v.data_ptr(), _fit(kpages, "kpages", torch.bfloat16, pool, at),
           _fit(vpages, "vpages", torch.bfloat16, pool, at), _fit(slots, "slots", torch.int32, (T,), at),
           0 if positions is None else _fit(positions, "positions", torch.int32, (T,), at), qp, qop, kop,
-          T, Hq, Hkv, D, page_size, num_pages, R,
+          T, Hq, Hkv, D, pool[2], pool[0], R,
           sk[0], sk[1], sv[0], sv[1], sq[0], sq[1], sqo[0], sqo[1], sko[0], sko[1], *r, _stream_of(stream, at))
     return q_out, k_out
+
+
+def _rope3(rope):
+    if len(rope) > 3 and rope[3] is not None:
+        raise ValueError("rope k_out is taken by prefill calls only")
+    return rope[:3]
+
+
+def _pool_pages(pages, Hkv, D):
+    """The shape of a pool [num_pages,Hkv,page_size,D] (Hkv, D where they are given)."""
+    try:
+        n, heads, size, dim = pages.shape
+    except (AttributeError, ValueError):
+        raise ValueError("kpages must be a tensor [num_pages,Hkv,page_size,D]") from None
+    return n, heads if Hkv is None else Hkv, size, dim if D is None else D
 
 
 def attn_decode_multi_paged(q, kpages, vpages, block_table, kv_lens, cu_new, max_new, out=None, lse=None, scale=None,
@@ -971,17 +985,16 @@ def attn_decode_multi_paged(q, kpages, vpages, block_table, kv_lens, cu_new, max
     -> (out [T,Hq,D], lse [T,Hq])"""
     _need(q, "q", torch.bfloat16, 3)
     at = q.get_device()
-    T, Hq, D = q.shape
-    if not isinstance(kpages, torch.Tensor) or kpages.dim() != 4:
-        raise ValueError("kpages must be a tensor [num_pages,Hkv,page_size,D]")
-    num_pages, Hkv, page_size, _ = kpages.shape
-    pool = (num_pages, Hkv, page_size, D)
+    T, Hq, D = shape = q.shape
+    num_pages, Hkv, page_size, _ = pool = _pool_pages(kpages, None, D)
     if out_dtype not in (torch.bfloat16, torch.float32):
         raise TypeError("out must be bf16 or fp32")
-    B = kv_lens.shape[0] if isinstance(kv_lens, torch.Tensor) and kv_lens.dim() else 0
-    width = block_table.shape[-1] if isinstance(block_table, torch.Tensor) and block_table.dim() else 0
+    try:
+        B, width = block_table.shape
+    except (AttributeError, ValueError):
+        raise ValueError("block_table must be a tensor [B,max_pages]") from None
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=out_dtype, device=q.device)
+        out = torch.empty(shape, dtype=out_dtype, device=q.device)
     if lse is None and want_lse:
         lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
     if workspace is not None:
@@ -991,7 +1004,7 @@ def attn_decode_multi_paged(q, kpages, vpages, block_table, kv_lens, cu_new, max
           q.data_ptr(), _fit(kpages, "kpages", torch.bfloat16, pool, at),
           _fit(vpages, "vpages", torch.bfloat16, pool, at), _fit(block_table, "block_table", i32, (B, width), at),
           _fit(kv_lens, "kv_lens", i32, (B,), at), _fit(cu_new, "cu_new", i32, (B + 1,), at),
-          _fit(out, "out", out_dtype, (T, Hq, D), at), 0 if lse is None else _fit(lse, "lse", torch.float32, (T, Hq), at),
+          _fit(out, "out", out_dtype, shape, at), 0 if lse is None else _fit(lse, "lse", torch.float32, (T, Hq), at),
           B, T, Hq, Hkv, D, int(max_new), page_size, width, num_pages, 1.0 / math.sqrt(D) if scale is None else scale,
           ATTN_DTYPE_F32 if out_dtype == torch.float32 else ATTN_DTYPE_BF16,
           0 if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.shape[0],
