@@ -1070,7 +1070,7 @@ int attn_kv_append_paged(const attn_kv_append_paged_params* p) {
 unsigned long long attn_decode_multi_paged_workspace_bytes(int Hq, int Hkv, int max_new, int D) {
   if (validate_decode_q4_heads(Hq, Hkv, max_new, D) != ATTN_OK) return 0;
   DeviceState* s = nullptr;
-  const int sms = device_state(&s) == ATTN_OK ? s->num_sms : 0;
+  const int sms = device_state(&s) == ATTN_OK ? s->num_sms : 152;
   return decode_multi_paged_bytes((long long)(Hq / Hkv) * max_new, D, sms);
 }
 

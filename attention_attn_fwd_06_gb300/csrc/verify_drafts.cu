@@ -525,7 +525,7 @@ cudaError_t launch_t(const VerifyDraftsLaunch& p) {
   const long long warps = (long long)size * kVerifyWarps;
   const long long segment = (((long long)p.V + warps - 1) / warps + STEP - 1) / STEP * STEP;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(p.B * size));
+  cfg.gridDim = dim3((unsigned)p.B * (unsigned)size);
   cfg.blockDim = dim3(32 * kVerifyWarps);
   cfg.stream = p.stream;
   cudaLaunchAttribute attr{};

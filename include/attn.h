@@ -679,7 +679,7 @@ int attn_kv_append_paged(const attn_kv_append_paged_params* p);
  *                past kv_len may hold anything.  (Keys that a token does not see because they
  *                are later tokens' own count with weight 0, so a NaN or an infinity in their
  *                values still reaches it.)
- *   out          apart from every input
+ *   out          apart from every input.  Weights are rounded to bf16 before they meet V.
  *   workspace    as attn_decode_q4: NULL for one of the library, its own, made by the first
  *                call on a device, which must not be one that is captured; or a DEVICE buffer
  *                of at least attn_decode_multi_paged_workspace_bytes, 16-byte aligned, all
@@ -710,7 +710,8 @@ typedef struct attn_decode_multi_paged_params {
 int attn_decode_multi_paged(const attn_decode_multi_paged_params* p);
 
 /* attn_decode_multi_paged_workspace_bytes -- bytes a workspace of attn_decode_multi_paged needs on the current device
- * (0 on invalid sizes; 148 SMs assumed when no device is visible). */
+ * (0 on invalid sizes; 152 SMs assumed when no device is visible).  A buffer can serve calls of several sizes if it is
+ * large enough for each. */
 unsigned long long attn_decode_multi_paged_workspace_bytes(int Hq, int Hkv, int max_new, int D);
 
 /*

@@ -331,6 +331,11 @@ def check_decode(cache, new, Hq, scale=None, f32=False, seed=5, extra=0, gap=0, 
     ([513], [128], 1, 1, 64, 64),                              # 128 tokens of one head
     ([333, 90, 1], [1, 1, 1], 28, 4, 128, 32),                 # a token each, seven heads
     ([70, 80, 90], [1, 5, 2], 15, 3, 64, 72),
+    ([300, 129, 5], [5, 4, 3], 32, 4, 128, 24),                # 40 rows; pages that end inside a tile
+    ([640, 1, 200, 0], [3, 5, 1, 2], 48, 2, 64, 8),            # 120 rows
+    ([260, 131], [16, 9], 8, 2, 128, 200),                     # 64 rows
+    ([95, 33, 32, 31], [4, 1, 4, 4], 16, 4, 128, 8),           # ends around a stage of 32 keys, pages of 8
+    ([191, 65, 64, 63], [4, 1, 4, 4], 32, 4, 64, 16),          # 32 rows, stages of 64 keys
 ])
 def test_decode_multi_paged(lens, new, Hq, Hkv, D, page):
     for f32 in (False, True):
@@ -357,11 +362,12 @@ def test_decode_multi_paged_many_sequences():
     check_decode(Cache(lens, 2, 64, 32, 4), new, 4)
 
 
-@pytest.mark.parametrize("D,page", [(128, 16), (64, 48)])
-def test_decode_multi_paged_long_sequences_split_over_all_ctas(D, page):
+@pytest.mark.parametrize("D,page,Hq", [(128, 16, 4), (64, 48, 4), (128, 8, 8), (64, 32, 8), (128, 40, 24), (64, 128, 32)])
+def test_decode_multi_paged_long_sequences_split_over_all_ctas(D, page, Hq):
+    """16, 32 and more query rows; a tile whose rows one of the sequences does not have."""
     c = Cache([9000, 0, 33, 4000], 1, D, page, 6)
-    a = check_decode(c, [4, 2, 3, 1], 4)
-    b = check_decode(c, [4, 2, 3, 1], 4)
+    a = check_decode(c, [4, 2, 3, 1], Hq)
+    b = check_decode(c, [4, 2, 3, 1], Hq)
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
@@ -467,9 +473,10 @@ def test_decode_multi_paged_bad_lengths_pages_and_offsets_are_flagged():
         assert (out[5 if 5 not in left else 0] != 7).any() or 5 in left
 
 
-def test_decode_multi_paged_timeout_is_reported_and_the_next_call_is_right(monkeypatch):
+@pytest.mark.parametrize("Hq", [8, 16, 80])
+def test_decode_multi_paged_timeout_is_reported_and_the_next_call_is_right(monkeypatch, Hq):
     # one softmax thread of CTA 0 withholds an arrival: a bounded wait runs out after a second, the CTA winds down
-    B, Hq, Hkv, page, D = 2, 8, 8, 64, 128
+    B, Hkv, page, D = 2, 8, 64, 128
     lens = [16384, 16000]
     pages = sum(-(-n // page) for n in lens)
     k, v = bf16((2, pages, Hkv, page, D), 3).to(DEV)
@@ -498,6 +505,20 @@ def test_decode_multi_paged_workspaces():
         assert torch.equal(out, want) and torch.equal(lse, wl)
     with pytest.raises(AB.AttnError, match="SCRATCH"):
         AB.attn_decode_multi_paged(q, k, v, table, lens, cu, 3, workspace=ws[:-16])
+    # one buffer for calls of few rows and of many, one after another
+    big = AB.attn_decode_multi_paged_workspace(8, 2, 64, 32, device=DEV)
+    long = Cache([6000, 700], 2, 64, 16, 9)
+    lk = long.on_gpu()
+    few = AB.attn_decode_multi_paged(q, *lk, cu, 3)
+    q2, cu2 = bf16((40, 8, 64), 3).to(DEV), i32([0, 20, 40])
+    many = AB.attn_decode_multi_paged(q2, *lk, cu2, 32)
+    for _ in range(3):
+        for args, ref in (((q, *lk, cu, 3), few), ((q2, *lk, cu2, 32), many)):
+            out, lse = AB.attn_decode_multi_paged(*args, workspace=big)
+            assert torch.equal(out, ref[0]) and torch.equal(lse, ref[1])
+    O, L, bO, bL = decode_bound(q2.cpu(), long.k, long.v, long.table, long.lens, [0, 20, 40], 0.125, False)
+    assert_within(many[0], O, bO)
+    assert_within(many[1], L, bL)
     with pytest.raises((ValueError, TypeError)):
         AB.attn_decode_multi_paged(q, k, v, table, lens, cu, 3, workspace=ws.view(torch.int16))
     st = torch.cuda.Stream()
