@@ -40,35 +40,33 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kRowCost = 2;            // stages charged to a row for its piece-end work
 constexpr float kRescale = 8.f;        // a row's reference rises when its maximum passes it by this (log2): weights up to 2^8
 
-// BIG: one CTA of eight consumer warps an SM, else two (three at D = 64) of four.
-template <int D, int RT, bool BIG>
+template <int D, int RT>
 struct RowsCfg {
   static constexpr int NDB = D / 64;          // 64-column blocks
   static constexpr int SK = D == 128 ? 32 : 64;  // keys a stage
-  static constexpr int NW = BIG ? 8 : 4;      // consumer warps
+  static constexpr int NW = 4;                // consumer warps
   static constexpr int KW = NW / RT;          // of them on one row tile
   static constexpr int GS = SK / 32;          // groups of 32 keys a stage
   static constexpr int BLOCK = SK * 128;      // one column block of K (or V)
   static constexpr int HALF = NDB * BLOCK;    // K, then V
   static constexpr int STAGE = 2 * HALF;
-  static constexpr int MINB = BIG ? 1 : D == 128 ? 2 : 3;
-  static constexpr int NS = BIG ? 10 : MINB == 2 ? 6 : 4;
+  static constexpr int MINB = D == 128 ? 2 : 3;
+  static constexpr int NS = MINB == 2 ? 6 : 4;
   static constexpr int THREADS = 32 * (NW + 1);
   static constexpr int NT = D / 8;            // column tiles of O
   static constexpr int NTW = NT / KW;         // of them a warp's share at a piece's end
   static constexpr int SCR = RT * KW * (KW - 1) * NTW * 512;  // the exchange: [tile][owner][from][NTW][lane] float4
-  static constexpr int ROUNDS = BIG || SCR <= STAGE ? 1 : (SCR + STAGE - 1) / STAGE;  // through the piece's last stage, or (BIG)
-  static constexpr int NTR = NTW / ROUNDS;    // room of its own; column tiles of a share exchanged a round
+  static constexpr int ROUNDS = (SCR + STAGE - 1) / STAGE;    // through the piece's last stage
+  static constexpr int NTR = NTW / ROUNDS;    // column tiles of a share exchanged a round
   static constexpr int LENS_CACHE = 512;
-  static constexpr int OFF_SCR = NS * STAGE;
-  static constexpr int OFF_BAR = OFF_SCR + (BIG ? SCR : 0);  // full[NS], empty[NS], told[NS]
+  static constexpr int OFF_BAR = NS * STAGE;  // full[NS], empty[NS], told[NS]
   static constexpr int OFF_INFO = OFF_BAR + 3 * NS * 8;
   static constexpr int OFF_ML = OFF_INFO + NS * 48;  // (m, l) [NW][16]
   static constexpr int OFF_LENS = OFF_ML + NW * 16 * 8;
   static constexpr int OFF_MISC = OFF_LENS + LENS_CACHE * 4;
   static constexpr int SMEM_USED = OFF_MISC + 16;
   static constexpr int SMEM = SMEM_USED + 1024;  // slack to align the ring to 1024
-  static_assert(NTW % ROUNDS == 0 && (BIG || SCR / ROUNDS <= STAGE), "the exchange has room");
+  static_assert(NTW % ROUNDS == 0 && SCR / ROUNDS <= STAGE, "the exchange takes the last stage");
   static_assert(SMEM <= 227 * 1024 && MINB * (SMEM + 1024) <= 228 * 1024, "MINB CTAs per SM");
 };
 
@@ -121,15 +119,15 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <int D, int RT, bool BIG>
-__global__ void __launch_bounds__(RowsCfg<D, RT, BIG>::THREADS, RowsCfg<D, RT, BIG>::MINB)
+template <int D, int RT>
+__global__ void __launch_bounds__(RowsCfg<D, RT>::THREADS, RowsCfg<D, RT>::MINB)
     decode_rows_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, const RowsArgs a) {
-  using C = RowsCfg<D, RT, BIG>;
+  using C = RowsCfg<D, RT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* empty = full + C::NS;
-  uint64_t* told = empty + C::NS;  // a piece's record is written (its data may still be on the way)
+  uint64_t* told = empty + C::NS;  // the record of piece i % NS is written (its data may still be on the way)
   RowsPiece* info = reinterpret_cast<RowsPiece*>(smem + C::OFF_INFO);
   float2* mlbuf = reinterpret_cast<float2*>(smem + C::OFF_ML);
   int* lens_s = reinterpret_cast<int*>(smem + C::OFF_LENS);
@@ -203,14 +201,15 @@ __global__ void __launch_bounds__(RowsCfg<D, RT, BIG>::THREADS, RowsCfg<D, RT, B
     const long long lo = sm.start(cta), hi = sm.start(cta + 1);
 
     int t = 0;  // stages issued
+    int piece = 0;  // record of the next piece: at most NS are on the way, as each has a stage
     int slot = 0;
     uint32_t freed = 1;  // parity of the phase in which the slot's last stage was released
     bool ok = true;
     const uint64_t policy = l2_policy_evict_first();  // the cache is read once
     const int ps = (int)a.page.d;
     // Lane 8 w + i (w 0: K, 1: V) brings column block i % NDB of box i / NDB of every stage.  A stage's instructions are one warp's
-    // chain, which an SM's stream passes through once in 0.4 us: no divisions in it, and block-table entries come 32 at a time,
-    // the next 32 ahead.
+    // chain, and a chain of each of an SM's CTAs has to keep up with its stream (1400 cycles a stage of two CTAs, stamps of an
+    // earlier form 900 to 1350): no divisions in it, and each lane reads its box's block-table entry a stage ahead.
     const int which = lane >> 3, box = (lane & 7) / C::NDB, db = (lane & 7) % C::NDB;
     const bool has_box = lane < 16 && box * a.box_rows < C::SK;
     const int per_stage = C::SK / a.box_rows;
@@ -218,7 +217,6 @@ __global__ void __launch_bounds__(RowsCfg<D, RT, BIG>::THREADS, RowsCfg<D, RT, B
     const int step_pages = C::SK / ps, step_off = C::SK - step_pages * ps;  // a stage further
     const uint32_t dst0 = (uint32_t)(which * C::HALF + db * C::BLOCK + box * a.box_rows * 128);
     const void* const tm = which ? &tmv : &tmk;
-    int win_b = -1, win_base = 0, my_page = 0, my_next = 0;  // lane i: entries of pages win_base + i and 32 on, of sequence win_b
     auto wait_empty = [&]() -> bool {
       return t < C::NS || __all_sync(0xffffffffu, mbar_wait(&empty[slot], freed, a.status, abort_flag));
     };
@@ -245,17 +243,7 @@ __global__ void __launch_bounds__(RowsCfg<D, RT, BIG>::THREADS, RowsCfg<D, RT, B
       int boxes = n > 0 ? (len - ub * C::SK + a.box_rows - 1) / a.box_rows : 0;
       const int* const row = a.block_table + (size_t)b * a.max_pages;
       const int pages = len > 0 ? (int)a.page.div((unsigned)(len - 1)) + 1 : 0;  // that hold keys: entries past them are not read
-      auto entry = [&](int at) -> int { return at < pages ? __ldg(row + at) : 0; };
-      auto window = [&](int base) {
-        win_base = base;
-        my_page = entry(base + lane);
-        my_next = entry(base + 32 + lane);
-      };
-      if (n > 0) {
-        const int base = __shfl_sync(0xffffffffu, pg, 0);
-        if (b != win_b || base < win_base || base >= win_base + 32) window(base);
-        win_b = b;
-      }
+      int page = has_box && pg < pages ? __ldg(row + pg) : 0;
       for (int u = 0; u < nst; ++u, next_slot()) {
         if (!wait_empty()) return false;
         if (n > 0) {
@@ -263,17 +251,6 @@ __global__ void __launch_bounds__(RowsCfg<D, RT, BIG>::THREADS, RowsCfg<D, RT, B
           boxes -= now;
           if (lane == 0) mbar_arrive_expect_tx(&full[slot], (uint32_t)now * box_bytes);
           const bool mine = has_box && box < now;
-          if (__any_sync(0xffffffffu, mine && pg >= win_base + 32)) {
-            const int base = __shfl_sync(0xffffffffu, pg, 0);  // of the first box: the least
-            if (base >= win_base + 32) {
-              win_base += 32;  // (a stage's pages are fewer than 32)
-              my_page = my_next;
-              my_next = entry(win_base + 32 + lane);
-            } else {
-              window(base);
-            }
-          }
-          int page = __shfl_sync(0xffffffffu, my_page, (pg - win_base) & 31);
           if (mine) {
             if (page < 0 || page >= a.num_pages) {
               record_status(a.status, ATTN_ERR_DEVICE_BOUNDS);  // out-of-pool page id: read page 0 instead
@@ -287,6 +264,7 @@ __global__ void __launch_bounds__(RowsCfg<D, RT, BIG>::THREADS, RowsCfg<D, RT, B
             off -= ps;
             ++pg;
           }
+          page = has_box && pg < pages ? __ldg(row + pg) : 0;
         } else if (lane == 0) {
           mbar_arrive(&full[slot]);
         }
@@ -311,8 +289,8 @@ __global__ void __launch_bounds__(RowsCfg<D, RT, BIG>::THREADS, RowsCfg<D, RT, B
           np = c_hi - c_lo + 1;
           row_lo = c_lo;
         }
-        if (lane == 0) {
-          if (u == 0) {
+        if (u == 0) {
+          if (lane == 0) {
             RowsPiece pi;
             pi.b = b;
             pi.hk = hk;
@@ -323,9 +301,10 @@ __global__ void __launch_bounds__(RowsCfg<D, RT, BIG>::THREADS, RowsCfg<D, RT, B
             pi.c_lo = row_lo;
             pi.q0 = q0;
             pi.nq = nq;
-            info[slot] = pi;
+            info[piece] = pi;
+            mbar_arrive(&told[piece]);
           }
-          mbar_arrive(&told[slot]);  // every stage, so that its phases run with the others'
+          if (++piece == C::NS) piece = 0;
         }
       }
       return true;
@@ -382,13 +361,9 @@ __global__ void __launch_bounds__(RowsCfg<D, RT, BIG>::THREADS, RowsCfg<D, RT, B
         if (seq_len(b) == 0 && seq_new(b, q0, bad) > 0) ok = emit(b, (int)(e - (long long)b * Hkv), 0, 0, 0);
       }
     }
-    if (ok) {  // end-of-work marker
-      if (wait_empty()) {
-        if (lane == 0) {
-          info[slot].b = -1;
-          mbar_arrive(&told[slot]);
-        }
-      }
+    if (ok && wait_empty() && lane == 0) {  // end-of-work marker
+      info[piece].b = -1;
+      mbar_arrive(&told[piece]);
     }
     if (lane == 0 && *abort_flag) {
       // Let copies already in flight land before the CTA's shared memory is released.
@@ -414,7 +389,9 @@ __global__ void __launch_bounds__(RowsCfg<D, RT, BIG>::THREADS, RowsCfg<D, RT, B
       phase ^= 1;
     }
   };
-  auto wait = [&](uint64_t* bar) -> bool { return mbar_wait(bar, phase, a.status, abort_flag); };
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return mbar_wait(bar, parity, a.status, abort_flag); };
+  int piece = 0;  // the next record, and its phase
+  uint32_t piece_phase = 0;
   // Addresses within a stage of the lane's rows for ldmatrix: K's matrices are (keys 0-7, 8-15) x (dims 0-7, 8-15) of a step of
   // 16 dims, V's (keys 0-7, 8-15) x (dims 0-7, 8-15) with keys first; chunks of 8 dims XOR-swizzled by the key's low bits.
   const int lk = lane & 7;
@@ -424,10 +401,14 @@ __global__ void __launch_bounds__(RowsCfg<D, RT, BIG>::THREADS, RowsCfg<D, RT, B
   while (true) {
     // Every warp takes part in one vote for each record, the end's among them: a wait can run out in one warp and just succeed
     // in another.
-    bool alive = wait(&told[slot]);
+    bool alive = wait(&told[piece], piece_phase);
     RowsPiece si;
     si.b = -1;
-    if (alive) si = info[slot];
+    if (alive) si = info[piece];
+    if (++piece == C::NS) {
+      piece = 0;
+      piece_phase ^= 1;
+    }
     float o[C::NT][4];
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     int valid = 0;  // rows of the tile that are tokens' (all tiles)
@@ -537,7 +518,7 @@ __global__ void __launch_bounds__(RowsCfg<D, RT, BIG>::THREADS, RowsCfg<D, RT, B
       };
       const int last = si.units > 0 ? si.units - 1 : 0;
       for (int u = 0;; ++u) {
-        if (!wait(&full[slot])) {
+        if (!wait(&full[slot], phase)) {
           alive = false;
           break;
         }
@@ -554,13 +535,11 @@ __global__ void __launch_bounds__(RowsCfg<D, RT, BIG>::THREADS, RowsCfg<D, RT, B
           }
         }
         __syncwarp();
-        if (!BIG && u == last) break;  // its slot is released after the exchange below
+        if (u == last) break;  // its slot is released after the exchange below
         release();
-        if (u == last) break;
       }
     }
-    // (and every warp is done with the piece's last stage, and with the exchange of the piece before)
-    if (named_bar_any(1, nct, !alive)) break;
+    if (named_bar_any(1, nct, !alive)) break;  // (and every warp is done with the piece's last stage)
     if (si.b < 0) break;
 
     // ---------------- end of a row piece ----------------
@@ -575,7 +554,7 @@ __global__ void __launch_bounds__(RowsCfg<D, RT, BIG>::THREADS, RowsCfg<D, RT, B
     float own[C::NTW][4];
     float M[2], L[2];
     {
-      float4* const scr = reinterpret_cast<float4*>(smem + (BIG ? C::OFF_SCR : slot * C::STAGE));
+      float4* const scr = reinterpret_cast<float4*>(smem + slot * C::STAGE);
       auto at = [&](int owner, int from, int k) {
         return ((rt * C::KW + owner) * (C::KW - 1) + (from < owner ? from : from - 1)) * C::NTR + k;
       };
@@ -635,13 +614,11 @@ __global__ void __launch_bounds__(RowsCfg<D, RT, BIG>::THREADS, RowsCfg<D, RT, B
         }
         if (round + 1 < C::ROUNDS) named_bar_sync(1, nct);
       }
-      if constexpr (!BIG) {
-        named_bar_sync(1, nct);    // (m, l) and the last stage are read
-        fence_proxy_async_smem();  // the exchange comes before the copy that refills the slot
-        __syncwarp();
-      }
+      named_bar_sync(1, nct);    // (m, l) and the last stage are read
+      fence_proxy_async_smem();  // the exchange comes before the copy that refills the slot
+      __syncwarp();
     }
-    if constexpr (!BIG) release();
+    release();
     auto write_out = [&]() {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
@@ -747,7 +724,7 @@ __global__ void __launch_bounds__(RowsCfg<D, RT, BIG>::THREADS, RowsCfg<D, RT, B
       }
       return true;
     };
-    constexpr int N = C::NTW <= 1 ? 8 : C::NTW <= 4 ? 4 : 2;
+    constexpr int N = C::NTW <= 4 ? 4 : 2;
     int i = 0;
     bool got = true;
     for (; got && i + N - 1 < si.np; i += N) got = fold(i, std::integral_constant<int, N>{});
@@ -756,16 +733,16 @@ __global__ void __launch_bounds__(RowsCfg<D, RT, BIG>::THREADS, RowsCfg<D, RT, B
   }
 }
 
-template <int D, int RT, bool BIG>
+template <int D, int RT>
 cudaError_t launch_one(const DecodeMultiLaunch& p) {
-  using C = RowsCfg<D, RT, BIG>;
+  using C = RowsCfg<D, RT>;
   static bool attr_set[64] = {};  // the shared-memory opt-in is per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!attr_set[dev]) {
-    e = cudaFuncSetAttribute(decode_rows_kernel<D, RT, BIG>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    e = cudaFuncSetAttribute(decode_rows_kernel<D, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
   }
@@ -805,17 +782,15 @@ cudaError_t launch_one(const DecodeMultiLaunch& p) {
   a.out_f32 = p.out_f32;
   a.status = p.status;
   a.fault_skip_arrive = p.fault_skip_arrive;
-  decode_rows_kernel<D, RT, BIG><<<grid, C::THREADS, C::SMEM, p.stream>>>(tmk, tmv, a);
+  decode_rows_kernel<D, RT><<<grid, C::THREADS, C::SMEM, p.stream>>>(tmk, tmv, a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-// (The larger of both kernels': as many warps an SM, or more, and as many bytes a CTA's partials or more of its CTAs.)
 DecodeRowsShape decode_rows_shape(int rows, int D, int num_sms) {
   const int tiles = rows <= 16 ? 1 : 2;
-  const int per_sm = D == 128 ? RowsCfg<128, 1, false>::MINB : RowsCfg<64, 1, false>::MINB;
-  static_assert(RowsCfg<128, 1, false>::MINB * 4 >= 8 && RowsCfg<64, 1, false>::MINB * 4 >= 8, "counts of the larger kernel");
+  const int per_sm = D == 128 ? RowsCfg<128, 1>::MINB : RowsCfg<64, 1>::MINB;
   const size_t grid = (size_t)(num_sms > 0 ? num_sms : 152) * per_sm;
   DecodeRowsShape s;
   s.count_bytes = (grid * 4 * sizeof(unsigned) + 127) / 128 * 128;
@@ -824,15 +799,10 @@ DecodeRowsShape decode_rows_shape(int rows, int D, int num_sms) {
   return s;
 }
 
-template <int D, int RT>
-cudaError_t launch_rows(const DecodeMultiLaunch& p) {
-  return (long long)p.B * p.Hkv < 2ll * p.num_sms ? launch_one<D, RT, true>(p) : launch_one<D, RT, false>(p);
-}
-
 cudaError_t launch_decode_rows(const DecodeMultiLaunch& p) {
   const int rows = p.Hq / p.Hkv * p.Lq;
-  if (p.D == 64) return rows <= 16 ? launch_rows<64, 1>(p) : launch_rows<64, 2>(p);
-  return rows <= 16 ? launch_rows<128, 1>(p) : launch_rows<128, 2>(p);
+  if (p.D == 64) return rows <= 16 ? launch_one<64, 1>(p) : launch_one<64, 2>(p);
+  return rows <= 16 ? launch_one<128, 1>(p) : launch_one<128, 2>(p);
 }
 
 }  // namespace attn
