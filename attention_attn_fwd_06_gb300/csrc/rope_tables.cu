@@ -15,6 +15,7 @@ namespace attn {
 namespace {
 
 constexpr int kTableThreads = 256;
+constexpr int kTableBlocks = 5;  // an SM
 constexpr int kTablePairs = 4;  // of one row, a thread
 
 struct TableArgs {
@@ -43,15 +44,15 @@ __device__ __forceinline__ void sincos_half_turns(float2 x, float2& s, float2& c
   c = __ffma2_rn(q, z, two(1.f));
 }
 
-// `phase` / 2^64 turns as a quarter turn (its low two bits) and a rest of at most an eighth of a turn, in half turns.
+// `phase` / 2^64 turns as a quarter turn (its low two bits) and a rest of at most an eighth of a turn, in half turns: 32 of the
+// rest's 62 bits (2^-35 of a turn), by one conversion.
 __device__ __forceinline__ float split_phase(unsigned long long phase, unsigned& quarter) {
   const unsigned hi = (unsigned)(phase >> 32);
   quarter = (hi + (1u << 29)) >> 30;
-  const int rest = (int)(hi - (quarter << 30));  // in [-2^29, 2^29)
-  return fmaf((float)rest, 0x1p-31f, (float)(unsigned)phase * 0x1p-63f);
+  return (float)(int)__funnelshift_l((unsigned)phase, hi, 2) * 0x1p-33f;  // (the quarter's bits leave at the top)
 }
 
-__global__ void __launch_bounds__(kTableThreads) rope_tables_kernel(const TableArgs a) {
+__global__ void __launch_bounds__(kTableThreads, kTableBlocks) rope_tables_kernel(const TableArgs a) {
   const int r0 = threadIdx.x / a.groups, g = threadIdx.x - r0 * a.groups;
   if (r0 >= a.block_rows) return;
   unsigned long long f[kTablePairs], phase[kTablePairs], step[kTablePairs];
@@ -104,7 +105,7 @@ cudaError_t launch_rope_tables(const RopeTablesLaunch& p) {
   a.amplitude = p.amplitude;
   for (int i = 0; i < kMaxRotaryPairs; ++i) a.turn[i] = i < p.pairs ? p.turn[i] : 0;
   const long long need = ((long long)p.rows + a.block_rows - 1) / a.block_rows;
-  const long long most = (long long)p.num_sms * 8;
+  const long long most = (long long)p.num_sms * kTableBlocks;
   rope_tables_kernel<<<(unsigned)(need < most ? need : most), kTableThreads, 0, p.stream>>>(a);
   return cudaGetLastError();
 }
