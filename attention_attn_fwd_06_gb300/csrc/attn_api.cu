@@ -312,23 +312,30 @@ double rope_base(const attn_rope_tables_params& p) {
   return p.scaling == ATTN_ROPE_SCALE_BASE ? p.base * std::pow(p.factor, R / (R - 2)) : p.base;
 }
 
-// Radians a position of pair i of a rotary table (attn_rope_tables), sizes checked.
-double rope_frequency(const attn_rope_tables_params& p, int i) {
+// Radians a position of every pair of a rotary table (attn_rope_tables), sizes checked.  base^(-2i / R) is a product of two of
+// sixteen powers (64 calls of pow would take 1 us of a call).
+void rope_frequencies(const attn_rope_tables_params& p, double* f) {
   const double R = p.rotary_dim, base = rope_base(p);
-  const double f = std::pow(base, -2.0 * i / R);
-  double keep = 1.0;  // the share of the pair's speed that stays as it is
-  if (p.scaling == ATTN_ROPE_SCALE_LINEAR) {
-    keep = 0.0;
-  } else if (p.scaling == ATTN_ROPE_SCALE_TURNS) {
-    keep = (p.context * f / kTwoPi - p.low) / (p.high - p.low);
-  } else if (p.scaling == ATTN_ROPE_SCALE_INDEX) {
+  const int pairs = p.rotary_dim / 2;
+  double fine[8], coarse[8], a = 0.0, b = 1.0;
+  for (int i = 0; i < 8; ++i) fine[i] = std::pow(base, -2.0 * i / R);
+  for (int i = 0; 8 * i < pairs; ++i) coarse[i] = std::pow(base, -16.0 * i / R);
+  if (p.scaling == ATTN_ROPE_SCALE_INDEX) {
     const double per = R / 2 / std::log(base);
-    const double a = std::fmax(0.0, std::floor(per * std::log(p.context / (kTwoPi * p.high))));
-    const double b = std::fmin(R - 1, std::ceil(per * std::log(p.context / (kTwoPi * p.low))));
-    keep = 1.0 - (i - a) / std::fmax(b - a, 0.001);
+    a = std::fmax(0.0, std::floor(per * std::log(p.context / (kTwoPi * p.high))));
+    b = std::fmin(R - 1, std::ceil(per * std::log(p.context / (kTwoPi * p.low))));
   }
-  keep = std::fmin(1.0, std::fmax(0.0, keep));
-  return f * keep + f * (1.0 - keep) / p.factor;
+  for (int i = 0; i < pairs; ++i) {
+    f[i] = coarse[i / 8] * fine[i % 8];
+    if (p.scaling == ATTN_ROPE_SCALE_NONE || p.scaling == ATTN_ROPE_SCALE_BASE) continue;
+    double keep = 0.0;  // the share of the pair's speed that stays as it is
+    if (p.scaling == ATTN_ROPE_SCALE_TURNS)
+      keep = (p.context * f[i] / kTwoPi - p.low) / (p.high - p.low);
+    else if (p.scaling == ATTN_ROPE_SCALE_INDEX)
+      keep = 1.0 - (i - a) / std::fmax(b - a, 0.001);
+    keep = std::fmin(1.0, std::fmax(0.0, keep));
+    f[i] = f[i] * keep + f[i] * (1.0 - keep) / p.factor;
+  }
 }
 
 bool is_empty_fwd(const attn_fwd_params* p) {
@@ -992,8 +999,11 @@ int attn_rope_tables(const attn_rope_tables_params* p) {
   if (!aligned16(p->cos) || !aligned16(p->sin)) return ATTN_ERR_ALIGNMENT;
   attn::RopeTablesLaunch L{};
   L.pairs = p->rotary_dim / 2;
+  static_assert(attn::kMaxRotaryPairs <= 64, "rope_frequencies");
+  double f[attn::kMaxRotaryPairs];
+  rope_frequencies(*p, f);
   for (int i = 0; i < L.pairs; ++i) {
-    const double turn = rope_frequency(*p, i) / kTwoPi;
+    const double turn = f[i] / kTwoPi;
     const double part = turn - std::floor(turn);  // whole turns a position say nothing (a factor below 1)
     if (!std::isfinite(part)) return ATTN_ERR_INVALID_ARG;
     L.turn[i] = part >= 0.5 ? (unsigned long long)((part - 0.5) * 0x1p64 + 0.5) + (1ull << 63)

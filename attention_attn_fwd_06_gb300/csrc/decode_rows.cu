@@ -37,7 +37,7 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kRowCost = 2;            // stages charged to a row for its piece-end work
+constexpr int kRowCost = 3;            // stages charged to a row for its piece-end work
 constexpr float kRescale = 8.f;        // a row's reference rises when its maximum passes it by this (log2): weights up to 2^8
 
 template <int D, int RT>
