@@ -4,15 +4,16 @@
 // What it computes: token t of a sequence with n keys, nq of them its new tokens', sees keys 0 .. n - nq + t; softmax and the
 // product with V in one pass over the keys with a running maximum and sum, pieces of a row joined by their log-sum-exp.
 //
-// What bounds it: HBM (each key and value is read once for all rows of its kv head), and for short rows the chain of a launch
-// and of each row.  A tile of 128 tcgen05 rows is one CTA an SM, whose roles wait for one another: 64 short sequences of 16
-// heads and a few tokens took 54 us there.  Here three CTAs share an SM, and a warp takes 16 keys by itself:
+// What bounds it: HBM (each key and value is read once for all rows of its kv head), and over short caches the chain of a launch
+// and of each row.  A tile of 128 tcgen05 rows is one CTA an SM, whose roles wait for one another tile by tile: 64 short
+// sequences of 16 heads and a few tokens took 50.5 us there, 23.6 here.  Here two or three CTAs share an SM, and a warp takes 32
+// keys by itself:
 //  * mma.sync m16n8k16 (bf16): A is 16 query rows, kept in registers for a whole piece, B 16 dims of 8 keys by ldmatrix.  The
 //    scores' accumulators are, packed to bf16, the second product's A operand as they stand; V comes by transposing ldmatrix.
-//    Sixteen query rows cost 2 matrix instructions a key at D = 128; an SM takes a key of one head in 22 clocks at the copy
-//    bandwidth.
-//  * RT tiles of 16 rows: 4 / RT warps share a tile's keys, group after group of 16.
-//  * The split is decode.cu's: persistent CTAs take slices of the stages (16 KB: 32 keys at D = 128, 64 at D = 64) of all
+//    Sixteen query rows cost 2 matrix instructions a key at D = 128 (the tensor pipe is a third busy with 32 rows at the copy
+//    bandwidth; with 64 rows 428 us against the tcgen05 tiles' 282 over 4 x 32k to 131k keys, 39 against 31 over 8 x 4096).
+//  * RT tiles of 16 rows: 4 / RT warps share a tile's keys, 32 after 32.
+//  * The split is decode.cu's: persistent CTAs take equal slices of the stages (16 KB: 32 keys at D = 128, 64 at D = 64) of all
 //    (sequence, kv head) rows, a row charged kRowCost stages beside its own.  A producer warp brings a stage with TMA boxes of
 //    gcd(page_size, stage) rows, each in one page, a lane a box, into a ring in the 128-byte swizzle that keeps ldmatrix free
 //    of bank conflicts.  Boxes past a sequence's last key are not loaded, and V's keys past it are masked to zero in registers.
@@ -21,6 +22,17 @@
 //    decode_q4.cu: complemented words over zeros, no fences, no CTA waits for one that may not have started).
 // Scores, maxima, sums and accumulators are fp32; weights are rounded to bf16 before the second product (2^-8 of themselves,
 // as in decode_multi.cu), whose adds truncate: over a slice of 131,072 keys some 2^-13 of the terms' sum.
+//
+// Measured (CUDA-graph replays over rotating pools; 32 query and 8 kv heads, D = 128; in brackets the tcgen05 tiles): 8 sequences
+// of 512 to 4096 keys on 16-key pages, 4 tokens each 21.6 us (25.7), 8 tokens 24.6 (27.1); 4 of 32k to 131k keys, 8 tokens
+// 270 us, 6.7 TB/s, the copy bandwidth (270.6); 64 of 512 to 1536 keys, 8 tokens 50.8 (69.1); one token to 5 of 64 sequences
+// of up to 700 keys with 16 heads of D = 64, 48-key pages 23.6 us (50.5).
+// Of the 24.6 us, by timer stamps of an earlier form: 2.5 to the first copy, 0.9 until it lands, 12 of stream, 1 of exchange, 3.5
+// (rows of 5 pieces) to 8 (of 10) of merge.  Six stages a CTA in place of five: 24.8, and 282 us over the long caches (the
+// SMs nearer to memory run further ahead, and finish 4 % apart); three CTAs at D = 128: 32 to 38 and 370 to 440 us; one CTA of
+// eight warps with ten stages: 27 to 34 and 327 to 504 us (one producer warp's chain is the stream's bound); two producers
+// for two CTAs: 25.7 and 278 us; a piece counted before it is published: 27.4 against 26.2 us that day; divisions in the
+// producer's stage: 26.2, 59 against 51 us over the 64.
 #include <cmath>
 #include <type_traits>
 
@@ -51,7 +63,7 @@ struct RowsCfg {
   static constexpr int HALF = NDB * BLOCK;    // K, then V
   static constexpr int STAGE = 2 * HALF;
   static constexpr int MINB = D == 128 ? 2 : 3;
-  static constexpr int NS = MINB == 2 ? 6 : 4;
+  static constexpr int NS = MINB == 2 ? 5 : 4;
   static constexpr int THREADS = 32 * (NW + 1);
   static constexpr int NT = D / 8;            // column tiles of O
   static constexpr int NTW = NT / KW;         // of them a warp's share at a piece's end

@@ -9,6 +9,9 @@
 // a token's heads.  Table rows come after the position, two round trips to memory, so a warp takes a run of tokens, as many
 // as make one wave of the grid, reads the run's positions and slots at once, brings the next token's table rows into shared
 // memory while it works on this one's, and loads a round's heads two rounds ahead, across tokens.
+// 65,536 tokens of 32 + 8 heads at D = 128 take 256 us (6.3 TB/s, 0.95 of the copy bandwidth), 8,158 of 16 + 16 heads at D = 64
+// with half of each turned 19.7 us (5.1 TB/s), 8 tokens 2.4.  Six blocks an SM: 274 and 19.3 us; three rounds in flight: 259 and
+// 20.2.
 #include <cuda_bf16.h>
 
 #include "common.cuh"

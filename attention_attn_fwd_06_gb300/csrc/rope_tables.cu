@@ -7,7 +7,9 @@
 // of its size.  The fraction's nearest quarter turn picks which of sin and cos is which, and its sign; the rest, at most an
 // eighth of a turn, is rounded to fp32 (2^-24 of itself) before polynomials give its sine and cosine.
 //
-// What bounds it: the writes, 8 bytes a pair.
+// What bounds it: the writes, 8 bytes a pair, and closely behind them the arithmetic.  131,072 rows of 64 pairs take 11.8 us (5.7
+// TB/s; 10.1 at the copy bandwidth), 4096 rows 2.5.  CUDA's sincospif for a pair at a time and two conversions: 17.8 us; eight
+// blocks an SM, of which five fit at once: 12.0 us, as many as fit at 32 registers 13.5.
 #include "common.cuh"
 #include "kernels.h"
 

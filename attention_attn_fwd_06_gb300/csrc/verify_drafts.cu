@@ -17,9 +17,9 @@
 // the segments' sums go to every CTA of the cluster through distributed shared memory, and the CTA that holds the segment where
 // the sum passes u's share reads that segment again (from L2), its warps a piece each, and finds the token.  CTAs of 8 warps at 48
 // registers, so that five share an SM and one's chain runs beside another's reading.
-// Measured (CUDA-graph replays over rotating inputs): 8 sequences of 4 drafts over 32,000 tokens 6.2 us; 64 of up to 8 over
-// 131,072 15.7 us (4.3 TB/s, 0.64 of the copy bandwidth); 37 without distributions over 50,001 in bf16, one element a
-// load, 8.8 us.  Four CTAs an SM with twice the loads in flight 6.5 / 16.5 / 8.8 us, CTAs of 16 warps 7.6 / 21.2 / 11.5 us;
+// Measured (CUDA-graph replays over rotating inputs): 8 sequences of 4 drafts over 32,000 tokens 6.3 us; 64 of up to 8 over
+// 131,072 15.9 us (4.2 TB/s, 0.63 of the copy bandwidth); 37 without distributions over 50,001 in bf16, one element a
+// load, 8.9 us.  Four CTAs an SM with twice the loads in flight 6.5 / 16.5 / 8.8 us, CTAs of 16 warps 7.6 / 21.2 / 11.5 us;
 // sums element by element with every weight's check 8.0 / 29.2 / 12.0 us, loads behind their conditions besides 7.9 / 28.6 / 15.6.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
