@@ -534,7 +534,8 @@ cudaError_t launch_t(const VerifyDraftsLaunch& p) {
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, verify_drafts_kernel<T, VEC>, p, (int)segment);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, verify_drafts_kernel<T, VEC>, p, (int)segment);
+  return e != cudaSuccess ? (cudaGetLastError(), e) : e;  // (an error that is told does not wait for the next call)
 }
 
 template <typename T>

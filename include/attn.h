@@ -665,7 +665,8 @@ int attn_kv_append_paged(const attn_kv_append_paged_params* p);
  *
  *   q, out       [T, Hq, D]: bf16, and bf16 or fp32; lse fp32 [T, Hq] may be NULL
  *   cu_new       DEVICE int32 [B + 1]: the tokens of sequence b are rows cu_new[b] ..
- *                cu_new[b + 1] - 1.  A sequence without any is not looked at.  Offsets that
+ *                cu_new[b + 1] - 1.  A sequence without any is left out (a length of its out of
+ *                range is flagged all the same).  Offsets that
  *                fall, leave [0, T] or give a sequence more than max_new tokens are flagged,
  *                and its rows left as they were, as are rows of no sequence.
  *   max_new      the most new tokens of a sequence, 1 .. 128 / (Hq / Hkv)

@@ -2,6 +2,10 @@
 sequence over pages, verification of drafts, and a server's steps of all of them together.
 
 Copied bits and decisions are compared for equality; computed values against fp64 with bounds counted in roundings."""
+import pathlib
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -835,3 +839,64 @@ def test_two_captured_steps_replayed_at_once():
     assert AB.attn_get_device_status() == AB.ATTN_OK
     for s, w in zip(servers, want):
         assert all(torch.equal(a, b) for a, b in zip(w, (s.out, s.lse, s.tokens, s.keep, s.lens)))
+
+
+FIRST_CALLS = """
+import torch
+from attention_attn_fwd_06_gb300 import binding as AB
+i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+lens, table, free, count, new = i32([0] * 3), i32([[-1, -1]] * 3), i32(range(8)), i32([8]), i32([5, 17, 0])
+slots, pos, cu = i32([0] * 22), i32([0] * 22), i32([0] * 4)
+x = torch.randn(22, 8, 64, device="cuda").to(torch.bfloat16)
+pages = torch.zeros(2, 8, 2, 16, 64, dtype=torch.bfloat16, device="cuda")
+cos, sin = torch.empty(2, 32, 16, device="cuda")
+q, out, out2 = torch.empty(22, 4, 64, dtype=torch.bfloat16, device="cuda"), *torch.empty(2, 22, 4, 64, dtype=torch.bfloat16, device="cuda")
+lse, lse2 = torch.empty(2, 22, 4, device="cuda")
+ws = AB.attn_decode_multi_paged_workspace(4, 2, 64, 64)  # (a size only: nothing has run)
+drafts, p, u = i32([[3] * 16] * 3), torch.rand(22, 40, device="cuda"), torch.rand(3, 17, device="cuda")
+tokens, accepted, keep = i32([[0] * 17] * 3), i32([0] * 3), i32([0] * 3)
+
+def step():
+    AB.attn_rope_tables(32, 32, cos=cos, sin=sin)
+    AB.attn_page_step(lens, table, free, count, 16, new_lens=new, slots=slots, positions=pos, cu_new=cu)
+    AB.attn_kv_append_paged(x[:, 4:6], x[:, 6:], pages[0], pages[1], slots, (cos, sin, "half"), pos, q=x[:, :4], q_out=q)
+    AB.attn_decode_multi_paged(q, pages[0], pages[1], table, lens, cu, 17, out=out, lse=lse, workspace=ws)    # 34 query rows
+    AB.attn_decode_multi_paged(q, pages[0], pages[1], table, lens, cu, 64, out=out2, lse=lse2, workspace=ws)
+    AB.attn_verify_drafts(drafts, p, u, cu_target=cu, kv_lens=lens, tokens=tokens, accepted=accepted, keep_lens=keep)
+
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    step()
+graph.replay()
+state = (cos, sin, lens, table, slots, pos, cu, q, pages, out, lse, out2, lse2, tokens, accepted, keep)
+got = [t.clone() for t in state]
+lens.zero_(), table.fill_(-1), free.copy_(i32(range(8))), count.fill_(8), pages.zero_()
+step()
+assert AB.attn_get_device_status() == AB.ATTN_OK
+assert all(torch.equal(a, b) for a, b in zip(got, state))
+assert lens.tolist() == [5, 17, 0] and torch.isfinite(lse).all() and tokens[2].tolist() == [-1] * 17
+few = [torch.empty_like(out), torch.empty_like(lse)]
+cu5 = i32([0, 5, 5, 5])
+status = None
+try:
+    g2 = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g2):
+        AB.attn_decode_multi_paged(q, pages[0], pages[1], table, lens, cu5, 5, out=few[0], lse=few[1])
+except AB.AttnError as e:
+    status = e.status  # the library's workspace is not made inside a capture
+assert status == AB.ATTN_ERR_INVALID_ARG, status
+AB.attn_decode_multi_paged(q, pages[0], pages[1], table, lens, cu5, 5, out=few[0], lse=few[1])
+g2 = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g2):
+    AB.attn_decode_multi_paged(q, pages[0], pages[1], table, lens, cu5, 5, out=few[0], lse=few[1])
+few[0].zero_()
+g2.replay()
+assert (few[0][:5].float() - out[:5].float()).abs().max() < 2e-2 and AB.attn_get_device_status() == AB.ATTN_OK
+"""
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], capture_output=True, text=True, timeout=120,
+                       cwd=pathlib.Path(__file__).parents[1])
+    assert r.returncode == 0, r.stderr
