@@ -366,6 +366,16 @@ def test_decode_multi_paged_many_sequences():
     check_decode(Cache(lens, 2, 64, 32, 4), new, 4)
 
 
+@pytest.mark.parametrize("Hq", [2, 40])
+def test_decode_multi_paged_hundreds_of_sequences(Hq):
+    """More sequences than the lengths kept in shared memory, most of them with nothing to do, for both kernels."""
+    g = np.random.default_rng(Hq)
+    lens = [int(x) for x in g.integers(0, 60, 700)]
+    new = [int(x) if g.random() < 0.3 else 0 for x in g.integers(1, 4, 700)]
+    lens[650], new[650], lens[699], new[699] = 500, 3, 0, 2
+    check_decode(Cache(lens, 1, 64, 24, 4), new, Hq)
+
+
 @pytest.mark.parametrize("D,page,Hq", [(128, 16, 4), (64, 48, 4), (128, 8, 8), (64, 32, 8), (128, 40, 24), (64, 128, 32)])
 def test_decode_multi_paged_long_sequences_split_over_all_ctas(D, page, Hq):
     """16, 32 and more query rows; a tile whose rows one of the sequences does not have."""
