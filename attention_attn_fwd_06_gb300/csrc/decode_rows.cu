@@ -32,7 +32,9 @@
 // SMs nearer to memory run further ahead, and finish 4 % apart); three CTAs at D = 128: 32 to 38 and 370 to 440 us; one CTA of
 // eight warps with ten stages: 27 to 34 and 327 to 504 us (one producer warp's chain is the stream's bound); two producers
 // for two CTAs: 25.7 and 278 us; a piece counted before it is published: 27.4 against 26.2 us that day; divisions in the
-// producer's stage: 26.2, 59 against 51 us over the 64.
+// producer's stage: 26.2, 59 against 51 us over the 64.  A CTA's last row merged through the idle ring, all of its pieces' words
+// in flight at once: 24.1, but 18.0 against 16.8 us with 8 rows over one sequence of 4000 keys and 57.5 against 55.5 with 32
+// rows of D = 64 over 64 of 3000: the words themselves are on their way when they are asked for.
 #include <cmath>
 #include <type_traits>
 

@@ -239,7 +239,7 @@ __device__ __forceinline__ Sum lane_sum_of(const Row<T>& row, int lo, int hi, in
       if (!all && j >= whole)
 #pragma unroll
         for (int i = 0; i < A::N; ++i) pj[i] = 0.f, qj[i] = 0.f;
-      if (!HAS_Q && (unsigned)(row.skip - j) < (unsigned)A::N)
+      if (!HAS_Q && (unsigned)row.skip - (unsigned)j < (unsigned)A::N)
 #pragma unroll
         for (int i = 0; i < A::N; ++i)
           if (j + i == row.skip) pj[i] = 0.f;
