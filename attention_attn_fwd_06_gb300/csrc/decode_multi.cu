@@ -174,6 +174,11 @@ struct Piece {
 #define ATTN_DMULTI_ITEM_COST 3
 #endif
 constexpr int kItemCost = ATTN_DMULTI_ITEM_COST;
+// Over pages a share is no shorter than the merge of the partials it makes is worth: with c cost positions an item in shares of s,
+// both the stream (s) and the merge (c / s) are alike at s ~ sqrt(c); sqrt(1.5 c) measured best.  64 query rows over one head of
+// 30,000 keys 72 us (274 with shares of one position), over 8 heads of 4000 27 (51), 49 rows over 8 of 1000 20 (31).  (The
+// contiguous kernel keeps its split, and so its bits.)
+constexpr float kShareCost = 1.5f;
 
 // Walks this CTA's share [lo, hi) of the flattened cost space.  Item (b, hk) occupies [start, start + kItemCost
 // + T): its tiles are the last T positions, so a share that takes on an item start also takes fewer tiles, and a
@@ -189,16 +194,25 @@ template <bool PAGED>
 __device__ Walk walk_init(const MultiArgs& a, int lane) {
   Walk w;
   long long part = 0;
+  int items = 0;
   for (int b = lane; b < a.B; b += 32) {
     const int n = load_seq<PAGED>(a, b, blockIdx.x == 0).n;
     part += n > 0 ? tiles_of(n) + kItemCost : 0;
+    items += n > 0 ? 1 : 0;
   }
 #pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) part += __shfl_xor_sync(0xffffffffu, part, off);
+  for (int off = 16; off >= 1; off >>= 1) {
+    part += __shfl_xor_sync(0xffffffffu, part, off);
+    if (PAGED) items += __shfl_xor_sync(0xffffffffu, items, off);
+  }
   const long long W = part * a.Hkv;
   const long long G = gridDim.x;
   w.per = floor_div(W + G - 1, G);
   if (w.per < 1) w.per = 1;
+  if constexpr (PAGED) {
+    const long long least = (long long)sqrtf(kShareCost * to_f32(part) / (float)max(1, items));
+    if (w.per < least) w.per = least;
+  }
   w.lo = (long long)blockIdx.x * w.per;
   w.hi = min(w.lo + w.per, W);
   w.pos = w.lo;
