@@ -32,7 +32,11 @@ namespace attn {
 namespace {
 
 constexpr int kVerifyWarps = 8;
-constexpr int kVerifyMaxCluster = 8;
+constexpr int kVerifyMaxCluster = 16;
+// Sixteen CTAs a sequence in place of eight where a row is this long and all sequences' CTAs still fit at four an SM: 2 sequences
+// over 220,000 tokens 8.6 against 11.6 us, 32 over 131,072 11.4 against 13.4, 19 over them 9.0 against 10.3; below, the larger
+// exchange costs more (8 over 32,000 7.0 against 6.5).
+constexpr int kVerifyLongRow = 65536;
 constexpr int kVerifySegments = kVerifyWarps * kVerifyMaxCluster;
 
 template <typename T>
@@ -520,7 +524,18 @@ __global__ void __launch_bounds__(32 * kVerifyWarps, 5) verify_drafts_kernel(con
 template <typename T, bool VEC>
 cudaError_t launch_t(const VerifyDraftsLaunch& p) {
   constexpr int STEP = 32 * Access<T, VEC>::N;
+  static bool attr_set[64] = {};  // clusters of more than 8 CTAs are opted into, per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!attr_set[dev]) {
+    e = cudaFuncSetAttribute(verify_drafts_kernel<T, VEC>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    attr_set[dev] = true;
+  }
   int size = kVerifyMaxCluster;
+  if (p.V < kVerifyLongRow || (long long)p.B * size > 4ll * p.num_sms) size /= 2;
   while (size > 1 && ((long long)p.V <= (long long)STEP * kVerifyWarps * (size / 2))) size /= 2;
   const long long warps = (long long)size * kVerifyWarps;
   const long long segment = (((long long)p.V + warps - 1) / warps + STEP - 1) / STEP * STEP;
@@ -534,7 +549,7 @@ cudaError_t launch_t(const VerifyDraftsLaunch& p) {
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, verify_drafts_kernel<T, VEC>, p, (int)segment);
+  e = cudaLaunchKernelEx(&cfg, verify_drafts_kernel<T, VEC>, p, (int)segment);
   return e != cudaSuccess ? (cudaGetLastError(), e) : e;  // (an error that is told does not wait for the next call)
 }
 
