@@ -688,6 +688,23 @@ def test_verify_drafts_sums_carry_more_than_32_bits():
         assert tokens.item() == want
 
 
+def test_verify_drafts_offsets_past_32_bits():
+    """The last rows of probabilities of over 2^31 elements."""
+    rows, V = 17000, 131072
+    p = torch.zeros(rows, V, dtype=torch.bfloat16, device=DEV)
+    q = torch.zeros(1, 2, V, dtype=torch.bfloat16, device=DEV)
+    p[-3, 70000], p[-2, 5], p[-2, 131071], p[-1, 9] = 0.75, 0.25, 0.5, 1.0
+    q[0, 0, 70000], q[0, 1, 5] = 0.5, 0.75
+    cu, d = i32([rows - 3, rows]), i32([[70000, 5]])
+    u = torch.tensor([[0.9, 0.5, 0.3]], device=DEV)
+    tokens, accepted, _ = AB.attn_verify_drafts(d, p, u, draft_probs=q, cu_target=cu)
+    assert tokens.tolist() == [[70000, 131071, -1]] and accepted.item() == 1  # 0.45 < 0.75; 0.375 is not below 0.25
+    u[0, 1] = 0.25
+    tokens, accepted, _ = AB.attn_verify_drafts(d, p, u, draft_probs=q, cu_target=cu)
+    assert tokens.tolist() == [[70000, 5, 9]] and accepted.item() == 2
+    assert AB.attn_get_device_status() == AB.ATTN_OK
+
+
 def test_verify_drafts_lengths_and_offsets_out_of_range_are_flagged():
     p = torch.rand(3, 3, 50, device=DEV)
     u, d = torch.full((3, 3), 0.5, device=DEV), i32([[1, 2]] * 3)
