@@ -297,8 +297,10 @@ DecodeMultiShape decode_multi_shape(long long rows, int D, int num_sms) {
 // A workspace of attn_decode_multi_paged: the region of the kernel for few rows, all zeros between calls, sized for its
 // largest call; behind it, for calls of more rows, decode_multi_shape's.  Calls of any sizes can so follow one another.
 size_t decode_rows_region(int num_sms) {
-  return std::max(attn::decode_rows_shape(attn::kDecodeRowsMax, 128, num_sms).bytes,
-                  attn::decode_rows_shape(attn::kDecodeRowsMax, 64, num_sms).bytes);
+  size_t most = 0;
+  for (int D : {64, 128})
+    for (int rows : {16, attn::kDecodeRowsMax}) most = std::max(most, attn::decode_rows_shape(rows, D, num_sms).bytes);
+  return most;
 }
 size_t decode_multi_paged_bytes(long long rows, int D, int num_sms) {
   if (rows <= attn::kDecodeRowsMax) return attn::decode_rows_shape((int)rows, D, num_sms).bytes;

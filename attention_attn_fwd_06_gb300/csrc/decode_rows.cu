@@ -29,7 +29,8 @@
 // of up to 700 keys with 16 heads of D = 64, 48-key pages 23.6 us (50.5).
 // Of the 24.6 us, by timer stamps of an earlier form: 2.5 to the first copy, 0.9 until it lands, 12 of stream, 1 of exchange, 3.5
 // (rows of 5 pieces) to 8 (of 10) of merge.  Six stages a CTA in place of five: 24.8, and 282 us over the long caches (the
-// SMs nearer to memory run further ahead, and finish 4 % apart); three CTAs at D = 128: 32 to 38 and 370 to 440 us; one CTA of
+// SMs nearer to memory run further ahead, and finish 4 % apart); three CTAs at D = 128: 32 to 38 and 370 to 440 us, at D = 64
+// with 32 rows 36.1 against 32.3 us (64 sequences of 350 to 700 keys, 16 kv heads; with 16 rows 28.7 against 30.2); one CTA of
 // eight warps with ten stages: 27 to 34 and 327 to 504 us (one producer warp's chain is the stream's bound); two producers
 // for two CTAs: 25.7 and 278 us; a piece counted before it is published: 27.4 against 26.2 us that day; divisions in the
 // producer's stage: 26.2, 59 against 51 us over the 64.  A CTA's last row merged through the idle ring, all of its pieces' words
@@ -64,7 +65,7 @@ struct RowsCfg {
   static constexpr int BLOCK = SK * 128;      // one column block of K (or V)
   static constexpr int HALF = NDB * BLOCK;    // K, then V
   static constexpr int STAGE = 2 * HALF;
-  static constexpr int MINB = D == 128 ? 2 : 3;
+  static constexpr int MINB = D == 64 && RT == 1 ? 3 : 2;
   static constexpr int NS = MINB == 2 ? 5 : 4;
   static constexpr int THREADS = 32 * (NW + 1);
   static constexpr int NT = D / 8;            // column tiles of O
@@ -804,7 +805,7 @@ cudaError_t launch_one(const DecodeMultiLaunch& p) {
 
 DecodeRowsShape decode_rows_shape(int rows, int D, int num_sms) {
   const int tiles = rows <= 16 ? 1 : 2;
-  const int per_sm = D == 128 ? RowsCfg<128, 1>::MINB : RowsCfg<64, 1>::MINB;
+  const int per_sm = D == 128 ? RowsCfg<128, 1>::MINB : tiles == 1 ? RowsCfg<64, 1>::MINB : RowsCfg<64, 2>::MINB;
   const size_t grid = (size_t)(num_sms > 0 ? num_sms : 152) * per_sm;
   DecodeRowsShape s;
   s.count_bytes = (grid * 4 * sizeof(unsigned) + 127) / 128 * 128;
