@@ -299,11 +299,12 @@ DecodeMultiShape decode_multi_shape(long long rows, int D, int num_sms) {
 size_t decode_rows_region(int num_sms) {
   size_t most = 0;
   for (int D : {64, 128})
-    for (int rows : {16, attn::kDecodeRowsMax}) most = std::max(most, attn::decode_rows_shape(rows, D, num_sms).bytes);
+    for (int rows = 16; rows <= attn::decode_rows_max(D); rows *= 2)
+      most = std::max(most, attn::decode_rows_shape(rows, D, num_sms).bytes);
   return most;
 }
 size_t decode_multi_paged_bytes(long long rows, int D, int num_sms) {
-  if (rows <= attn::kDecodeRowsMax) return attn::decode_rows_shape((int)rows, D, num_sms).bytes;
+  if (rows <= attn::decode_rows_max(D)) return attn::decode_rows_shape((int)rows, D, num_sms).bytes;
   return decode_rows_region(num_sms) + decode_multi_shape(rows, D, num_sms).bytes;
 }
 
@@ -1150,7 +1151,7 @@ int attn_decode_multi_paged(const attn_decode_multi_paged_params* p) {
   L.status = s->status;
   L.fault_skip_arrive = fault_skip_arrive();
   L.stream = stream;
-  if (rows <= attn::kDecodeRowsMax) return map_cuda(attn::launch_decode_rows(L));
+  if (rows <= attn::decode_rows_max(p->D)) return map_cuda(attn::launch_decode_rows(L));
   ws += decode_rows_region(s->num_sms);
   L.counters = reinterpret_cast<unsigned*>(ws);
   L.part_o = reinterpret_cast<float*>(ws + kCounterBytes);

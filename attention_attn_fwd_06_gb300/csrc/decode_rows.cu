@@ -1,5 +1,5 @@
-// decode_rows.cu -- decode of a few new tokens of each sequence over a paged bf16 cache, for up to 32 query rows a kv head
-// (attn_decode_multi_paged; more rows take decode_multi.cu's tcgen05 tiles of 128).
+// decode_rows.cu -- decode of a few new tokens of each sequence over a paged bf16 cache, for up to 32 query rows a kv head, 64
+// of D = 64 (attn_decode_multi_paged; more rows take decode_multi.cu's tcgen05 tiles of 128).
 //
 // What it computes: token t of a sequence with n keys, nq of them its new tokens', sees keys 0 .. n - nq + t; softmax and the
 // product with V in one pass over the keys with a running maximum and sum, pieces of a row joined by their log-sum-exp.
@@ -12,7 +12,10 @@
 //    scores' accumulators are, packed to bf16, the second product's A operand as they stand; V comes by transposing ldmatrix.
 //    Sixteen query rows cost 2 matrix instructions a key at D = 128 (the tensor pipe is a third busy with 32 rows at the copy
 //    bandwidth; with 64 rows 428 us against the tcgen05 tiles' 282 over 4 x 32k to 131k keys, 39 against 31 over 8 x 4096).
-//  * RT tiles of 16 rows: 4 / RT warps share a tile's keys, 32 after 32.
+//    At D = 64 a key costs half of that, and 33 to 64 rows (in brackets the tcgen05 tiles) of 8 kv heads took 10.6 us (12.9)
+//    over 4 x 300 to 500 keys, 21.6 (21.7) over 8 x 512 to 4096, 89 (106) over 4 x 30k to 60k on 16-key pages, 45 (55) over
+//    40 x 1000 to 3000 with 40 rows; only over large pages and long caches more, 137 (128) over 4 x 50k to 100k on 64-key pages.
+//  * RT tiles of 16 rows: 4 / RT warps share a tile's keys, 32 after 32; a tile of no rows is passed over.
 //  * The split is decode.cu's: persistent CTAs take equal slices of the stages (16 KB: 32 keys at D = 128, 64 at D = 64) of all
 //    (sequence, kv head) rows, a row charged kRowCost stages beside its own.  A producer warp brings a stage with TMA boxes of
 //    gcd(page_size, stage) rows, each in one page, a lane a box, into a ring in the 128-byte swizzle that keeps ldmatrix free
@@ -71,7 +74,7 @@ struct RowsCfg {
   static constexpr int NT = D / 8;            // column tiles of O
   static constexpr int NTW = NT / KW;         // of them a warp's share at a piece's end
   static constexpr int SCR = RT * KW * (KW - 1) * NTW * 512;  // the exchange: [tile][owner][from][NTW][lane] float4
-  static constexpr int ROUNDS = (SCR + STAGE - 1) / STAGE;    // through the piece's last stage
+  static constexpr int ROUNDS = KW == 1 ? 1 : (SCR + STAGE - 1) / STAGE;  // through the piece's last stage
   static constexpr int NTR = NTW / ROUNDS;    // column tiles of a share exchanged a round
   static constexpr int LENS_CACHE = 512;
   static constexpr int OFF_BAR = NS * STAGE;  // full[NS], empty[NS], told[NS]
@@ -81,7 +84,7 @@ struct RowsCfg {
   static constexpr int OFF_MISC = OFF_LENS + LENS_CACHE * 4;
   static constexpr int SMEM_USED = OFF_MISC + 16;
   static constexpr int SMEM = SMEM_USED + 1024;  // slack to align the ring to 1024
-  static_assert(NTW % ROUNDS == 0 && SCR / ROUNDS <= STAGE, "the exchange takes the last stage");
+  static_assert(NTR * ROUNDS == NTW && SCR / ROUNDS <= STAGE, "the exchange takes the last stage");
   static_assert(SMEM <= 227 * 1024 && MINB * (SMEM + 1024) <= 228 * 1024, "MINB CTAs per SM");
 };
 
@@ -543,6 +546,7 @@ __global__ void __launch_bounds__(RowsCfg<D, RT>::THREADS, RowsCfg<D, RT>::MINB)
           for (int j = 0; j < C::GS; ++j) {
             if ((u * C::GS + j) % C::KW != kw) continue;
             const int key0 = (si.unit0 + u) * C::SK + 32 * j;
+            if (rt * 16 >= valid) continue;  // (a tile of no rows)
             if (key0 + 32 <= all_see)
               process(base + 32 * j * 128, key0, std::false_type{});
             else if (key0 < si.len)
@@ -562,13 +566,19 @@ __global__ void __launch_bounds__(RowsCfg<D, RT>::THREADS, RowsCfg<D, RT>::MINB)
     for (int c = 0; c < 2; ++c) {
       l[c] += __shfl_xor_sync(0xffffffffu, l[c], 1);
       l[c] += __shfl_xor_sync(0xffffffffu, l[c], 2);
-      if (t4 == 0) mlbuf[warp * 16 + g + 8 * c] = make_float2(m[c], l[c]);
+      if (C::KW > 1 && t4 == 0) mlbuf[warp * 16 + g + 8 * c] = make_float2(m[c], l[c]);
     }
     // Column tiles kw NTW .. + NTW - 1 of this row tile are summed by this warp, weighted by 2^(m_w - M), in warp order (bitwise
     // reproducible).
     float own[C::NTW][4];
     float M[2], L[2];
-    {
+    if constexpr (C::KW == 1) {  // a warp has all of its tile's keys
+#pragma unroll
+      for (int k = 0; k < C::NTW; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) own[k][e] = o[k][e];
+      M[0] = m[0], M[1] = m[1], L[0] = l[0], L[1] = l[1];
+    } else {
       float4* const scr = reinterpret_cast<float4*>(smem + slot * C::STAGE);
       auto at = [&](int owner, int from, int k) {
         return ((rt * C::KW + owner) * (C::KW - 1) + (from < owner ? from : from - 1)) * C::NTR + k;
@@ -804,7 +814,7 @@ cudaError_t launch_one(const DecodeMultiLaunch& p) {
 }  // namespace
 
 DecodeRowsShape decode_rows_shape(int rows, int D, int num_sms) {
-  const int tiles = rows <= 16 ? 1 : 2;
+  const int tiles = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
   const int per_sm = D == 128 ? RowsCfg<128, 1>::MINB : tiles == 1 ? RowsCfg<64, 1>::MINB : RowsCfg<64, 2>::MINB;
   const size_t grid = (size_t)(num_sms > 0 ? num_sms : 152) * per_sm;
   DecodeRowsShape s;
@@ -816,7 +826,7 @@ DecodeRowsShape decode_rows_shape(int rows, int D, int num_sms) {
 
 cudaError_t launch_decode_rows(const DecodeMultiLaunch& p) {
   const int rows = p.Hq / p.Hkv * p.Lq;
-  if (p.D == 64) return rows <= 16 ? launch_one<64, 1>(p) : launch_one<64, 2>(p);
+  if (p.D == 64) return rows <= 16 ? launch_one<64, 1>(p) : rows <= 32 ? launch_one<64, 2>(p) : launch_one<64, 4>(p);
   return rows <= 16 ? launch_one<128, 1>(p) : launch_one<128, 2>(p);
 }
 

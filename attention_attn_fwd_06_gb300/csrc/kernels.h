@@ -75,8 +75,8 @@ struct DecodeMultiLaunch {
   cudaStream_t stream;
 };
 
-// The same over pages for up to kDecodeRowsMax query rows a kv head (decode_rows.cu).
-constexpr int kDecodeRowsMax = 32;
+// The same over pages for up to so many query rows a kv head (decode_rows.cu).
+constexpr int decode_rows_max(int D) { return D == 64 ? 64 : 32; }
 struct DecodeRowsShape {
   size_t count_bytes, ml_bytes, bytes;
 };

@@ -340,6 +340,8 @@ def check_decode(cache, new, Hq, scale=None, f32=False, seed=5, extra=0, gap=0, 
     ([260, 131], [16, 9], 8, 2, 128, 200),                     # 64 rows
     ([95, 33, 32, 31], [4, 1, 4, 4], 16, 4, 128, 8),           # ends around a stage of 32 keys, pages of 8
     ([191, 65, 64, 63], [4, 1, 4, 4], 32, 4, 64, 16),          # 32 rows, stages of 64 keys
+    ([191, 65, 64, 63, 0], [5, 1, 4, 5, 2], 36, 4, 64, 16),    # 45 rows, a tile a warp, some tiles of no rows
+    ([800, 7, 130], [8, 8, 3], 16, 2, 64, 40),                 # 64 rows
 ])
 def test_decode_multi_paged(lens, new, Hq, Hkv, D, page):
     for f32 in (False, True):
@@ -376,7 +378,8 @@ def test_decode_multi_paged_hundreds_of_sequences(Hq):
     check_decode(Cache(lens, 1, 64, 24, 4), new, Hq)
 
 
-@pytest.mark.parametrize("D,page,Hq", [(128, 16, 4), (64, 48, 4), (128, 8, 8), (64, 32, 8), (128, 40, 24), (64, 128, 32)])
+@pytest.mark.parametrize("D,page,Hq", [(128, 16, 4), (64, 48, 4), (128, 8, 8), (64, 32, 8), (64, 16, 9), (64, 8, 16), (128, 40, 24),
+                                       (64, 128, 32)])
 def test_decode_multi_paged_long_sequences_split_over_all_ctas(D, page, Hq):
     """16, 32 and more query rows; a tile whose rows one of the sequences does not have."""
     c = Cache([9000, 0, 33, 4000], 1, D, page, 6)
