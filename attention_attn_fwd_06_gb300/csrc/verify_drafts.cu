@@ -282,8 +282,10 @@ __device__ __noinline__ Sum lane_sum_careful(const Row<T> row, int lo, int hi, i
   s.settle();
   return s;
 }
+// (No tokens: nothing.  A row's last tokens, short of 16 bytes, are those of the part that they end.)
 template <typename T, bool VEC>
 __device__ __forceinline__ Sum lane_sum(const Row<T>& row, int lo, int hi, int V, int lane, bool careful) {
+  if (lo >= hi) return Sum{};
   if (careful) return lane_sum_careful<T>(row, lo, hi, lane);
   return row.q != nullptr ? lane_sum_of<T, VEC, true>(row, lo, hi, V, lane) : lane_sum_of<T, VEC, false>(row, lo, hi, V, lane);
 }
@@ -429,8 +431,7 @@ __global__ void __launch_bounds__(32 * kVerifyWarps, 5) verify_drafts_kernel(con
   bool careful = false;
   for (int attempt = 0;; ++attempt) {
     const long long lo = (long long)mine * segment;
-    Sum v;
-    if (lo < V) v = lane_sum<T, VEC>(row, (int)lo, (int)min(lo + segment, (long long)V), V, lane, careful);
+    Sum v = lane_sum<T, VEC>(row, (int)min(lo, (long long)V), (int)min(lo + segment, (long long)V), V, lane, careful);
     v = warp_sum(v);
     Sum* const parts = sums[attempt & 1];  // (the tries before the last one have been read: a cluster barrier lies between)
     if (lane < size) *cluster.map_shared_rank(&parts[mine], lane) = v;
