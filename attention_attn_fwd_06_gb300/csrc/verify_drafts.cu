@@ -7,8 +7,9 @@
 // distributed as p.
 //
 // The sums decide which token comes out, so they carry more than 32 bits: a lane adds fp32 terms into a pair of floats (a
-// sum and the sum of its roundings, Knuth's two-sum), a difference p - q enters with its own rounding, and lanes, warps and
-// CTAs are joined as such pairs in a fixed order: 2^-42 of the sum, and the same bits every time.  (64-bit floats run at two
+// sum and the sum of its roundings, Knuth's two-sum), a difference p - q enters with its own rounding, and the lane's pairs of
+// some 2048 tokens, lanes, warps and CTAs are joined as such pairs, 2^-47 each, in a fixed order: 2^-39 of the sum up to 2^20
+// tokens, 2^-34 up to 2^30 (thousands of joins one after another), and the same bits every time.  (64-bit floats run at two
 // adds a clock and SM: with the joins in them 8 sequences over 32,000 tokens took 20.5 us a call, 12 without.)
 //
 // What bounds it: for few sequences the chain of launch, drafts (1.4 us), the row (1.1), the exchange (0.7), the segment (0.6)
@@ -217,9 +218,13 @@ struct Sum2 {
 
 // Sum of the weights of tokens [lo, hi) (lo and hi - lo multiples of a warp's step, or hi == V) over this lane's elements, the
 // positive ones taken to be finite.  A round's loads go out together: none waits behind a condition (in the last round those
-// past the end read the first tokens again).
-template <typename T, bool VEC, bool HAS_Q>
-__device__ __forceinline__ Sum lane_sum_of(const Row<T>& row, int lo, int hi, int V, int lane) {
+// past the end read the first tokens again).  The roundings that a sum gathers (Sum2::e) are rounded themselves: 65,536 adds of
+// 0.1 to one pair are off by 2^-22 of their sum, n alike ones by n^2 / 6 2^-48 at most, 2^-40.6 for the 32 of kSumTokens.  FAR, for
+// segments of more: after so many a sum is joined to the lane's word of `far` (shared memory: two more registers here would spill)
+// and starts again.  (64 sequences over 131,072 tokens, whose segments are no longer: 17.5 us a call with it, 17.2 without.)
+constexpr int kSumTokens = 2048;
+template <typename T, bool VEC, bool FAR, bool HAS_Q>
+__device__ __forceinline__ Sum lane_sum_of(const Row<T>& row, int lo, int hi, int V, int lane, Sum* far) {
   using A = Access<T, VEC>;
   constexpr int STEP = 32 * A::N;
   constexpr int U = VEC ? 2 : 8;
@@ -261,33 +266,52 @@ __device__ __forceinline__ Sum lane_sum_of(const Row<T>& row, int lo, int hi, in
     }
   };
   int base = lo;
-  for (; base + U * STEP <= whole; base += U * STEP) round(base, true);
+  static_assert(kSumTokens % (U * STEP) == 0, "whole rounds");
+  for (; base + U * STEP <= whole; base += U * STEP) {
+    if (FAR && base != lo && (base - lo) % kSumTokens == 0) {
+      Sum v = s.joined();
+      if (base - lo > kSumTokens) v.add(far[threadIdx.x]);
+      far[threadIdx.x] = v;
+      s = Sum2{};
+    }
+    round(base, true);
+  }
   if (base < whole) round(base, false);
   if (VEC && whole + lane < hi) {  // the row's last tokens, short of 16 bytes
     const int j = whole + lane;
     const float p = j == row.skip ? 0.f : as_float<T>(__ldg(row.p + j));
     s.add<HAS_Q>(make_float2(p, 0.f), make_float2(HAS_Q ? as_float<T>(__ldg(row.q + j)) : 0.f, 0.f));
   }
-  return s.joined();
+  Sum v = s.joined();
+  if (FAR && base - lo > kSumTokens) v.add(far[threadIdx.x]);
+  return v;
 }
 // The same with every weight looked at (rows with infinities).
 template <typename T>
 __device__ __noinline__ Sum lane_sum_careful(const Row<T> row, int lo, int hi, int lane) {
   Sum s;
+  int n = 0;
+  Sum far;
   for (int j = lo + lane; j < hi; j += 32) {
     float rest;
     const float w = row.weight(as_float<T>(__ldg(row.p + j)), row.q != nullptr ? as_float<T>(__ldg(row.q + j)) : 0.f, j, rest);
     s.add(w, rest);
+    s.settle();
+    if (++n % (kSumTokens / 32) == 0) {
+      far.add(s);
+      s = Sum{};
+    }
   }
-  s.settle();
+  s.add(far);
   return s;
 }
 // (No tokens: nothing.  A row's last tokens, short of 16 bytes, are those of the part that they end.)
-template <typename T, bool VEC>
-__device__ __forceinline__ Sum lane_sum(const Row<T>& row, int lo, int hi, int V, int lane, bool careful) {
+template <typename T, bool VEC, bool FAR>
+__device__ __forceinline__ Sum lane_sum(const Row<T>& row, int lo, int hi, int V, int lane, bool careful, Sum* far) {
   if (lo >= hi) return Sum{};
   if (careful) return lane_sum_careful<T>(row, lo, hi, lane);
-  return row.q != nullptr ? lane_sum_of<T, VEC, true>(row, lo, hi, V, lane) : lane_sum_of<T, VEC, false>(row, lo, hi, V, lane);
+  return row.q != nullptr ? lane_sum_of<T, VEC, FAR, true>(row, lo, hi, V, lane, far)
+                          : lane_sum_of<T, VEC, FAR, false>(row, lo, hi, V, lane, far);
 }
 
 // Parts of a sum, PER a lane, one warp: their running sums.
@@ -330,13 +354,14 @@ struct Parts {
   }
 };
 
-template <typename T, bool VEC>
+template <typename T, bool VEC, bool FAR>
 __global__ void __launch_bounds__(32 * kVerifyWarps, 5) verify_drafts_kernel(const VerifyDraftsLaunch p, int segment) {
   namespace cg = cooperative_groups;
   using A = Access<T, VEC>;
   constexpr int STEP = 32 * A::N;
   __shared__ Sum sums[2][kVerifySegments];  // of all segments of the row, of one try and the next
   __shared__ Sum pieces[kVerifyWarps], s_before, s_target;
+  __shared__ Sum far[FAR ? 32 * kVerifyWarps : 1];
   __shared__ int s_n, s_stand, s_row, s_seg;
   cg::cluster_group cluster = cg::this_cluster();
   const int size = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -431,7 +456,7 @@ __global__ void __launch_bounds__(32 * kVerifyWarps, 5) verify_drafts_kernel(con
   bool careful = false;
   for (int attempt = 0;; ++attempt) {
     const long long lo = (long long)mine * segment;
-    Sum v = lane_sum<T, VEC>(row, (int)min(lo, (long long)V), (int)min(lo + segment, (long long)V), V, lane, careful);
+    Sum v = lane_sum<T, VEC, FAR>(row, (int)min(lo, (long long)V), (int)min(lo + segment, (long long)V), V, lane, careful, far);
     v = warp_sum(v);
     Sum* const parts = sums[attempt & 1];  // (the tries before the last one have been read: a cluster barrier lies between)
     if (lane < size) *cluster.map_shared_rank(&parts[mine], lane) = v;
@@ -473,7 +498,7 @@ __global__ void __launch_bounds__(32 * kVerifyWarps, 5) verify_drafts_kernel(con
   const int piece = ((segment + kVerifyWarps - 1) / kVerifyWarps + STEP - 1) / STEP * STEP;
   {
     const int lo = min(first + warp * piece, end);
-    const Sum v = warp_sum(lane_sum<T, VEC>(row, lo, min(lo + piece, end), V, lane, careful));
+    const Sum v = warp_sum(lane_sum<T, VEC, FAR>(row, lo, min(lo + piece, end), V, lane, careful, far));
     if (lane == 0) pieces[warp] = v;
   }
   __syncthreads();
@@ -522,24 +547,18 @@ __global__ void __launch_bounds__(32 * kVerifyWarps, 5) verify_drafts_kernel(con
   if (lane == 0) tokens[stand] = found;
 }
 
-template <typename T, bool VEC>
-cudaError_t launch_t(const VerifyDraftsLaunch& p) {
-  constexpr int STEP = 32 * Access<T, VEC>::N;
+template <typename T, bool VEC, bool FAR>
+cudaError_t launch_t(const VerifyDraftsLaunch& p, int size, int segment) {
   static bool attr_set[64] = {};  // clusters of more than 8 CTAs are opted into, per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!attr_set[dev]) {
-    e = cudaFuncSetAttribute(verify_drafts_kernel<T, VEC>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    e = cudaFuncSetAttribute(verify_drafts_kernel<T, VEC, FAR>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
   }
-  int size = kVerifyMaxCluster;
-  if (p.V < kVerifyLongRow || (long long)p.B * size > 4ll * p.num_sms) size /= 2;
-  while (size > 1 && ((long long)p.V <= (long long)STEP * kVerifyWarps * (size / 2))) size /= 2;
-  const long long warps = (long long)size * kVerifyWarps;
-  const long long segment = (((long long)p.V + warps - 1) / warps + STEP - 1) / STEP * STEP;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)p.B * (unsigned)size);
   cfg.blockDim = dim3(32 * kVerifyWarps);
@@ -550,8 +569,19 @@ cudaError_t launch_t(const VerifyDraftsLaunch& p) {
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, verify_drafts_kernel<T, VEC>, p, (int)segment);
+  e = cudaLaunchKernelEx(&cfg, verify_drafts_kernel<T, VEC, FAR>, p, segment);
   return e != cudaSuccess ? (cudaGetLastError(), e) : e;  // (an error that is told does not wait for the next call)
+}
+
+template <typename T, bool VEC>
+cudaError_t dispatch_far(const VerifyDraftsLaunch& p) {
+  constexpr int STEP = 32 * Access<T, VEC>::N;
+  int size = kVerifyMaxCluster;
+  if (p.V < kVerifyLongRow || (long long)p.B * size > 4ll * p.num_sms) size /= 2;
+  while (size > 1 && ((long long)p.V <= (long long)STEP * kVerifyWarps * (size / 2))) size /= 2;
+  const long long warps = (long long)size * kVerifyWarps;
+  const long long segment = (((long long)p.V + warps - 1) / warps + STEP - 1) / STEP * STEP;
+  return segment > kSumTokens ? launch_t<T, VEC, true>(p, size, (int)segment) : launch_t<T, VEC, false>(p, size, (int)segment);
 }
 
 template <typename T>
@@ -560,7 +590,7 @@ cudaError_t dispatch_vec(const VerifyDraftsLaunch& p) {
   bool vec = reinterpret_cast<unsigned long long>(p.target) % 16 == 0 && p.ts[0] % N == 0 && p.ts[1] % N == 0;
   if (p.draft != nullptr)
     vec = vec && reinterpret_cast<unsigned long long>(p.draft) % 16 == 0 && p.ds[0] % N == 0 && p.ds[1] % N == 0;
-  return vec ? launch_t<T, true>(p) : launch_t<T, false>(p);
+  return vec ? dispatch_far<T, true>(p) : dispatch_far<T, false>(p);
 }
 
 }  // namespace

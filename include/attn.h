@@ -744,7 +744,8 @@ unsigned long long attn_decode_multi_paged_workspace_bytes(int Hq, int Hkv, int 
  *                 takes to drop the refused drafts' keys (kv_lens as the step that added the n + 1
  *                 tokens left them)
  * A row that holds no weight at all, or weights whose sum passes fp32's range, gives -1 and is
- * flagged.  The sums are exact to 2^-40 of themselves and the same every time.  Outputs are apart from inputs and from each other.  K
+ * flagged.  The sums are exact to 2^-39 of themselves for V up to 2^20, to 2^-34 beyond (sums below
+ * 2^-100: to fp32's smallest number), and the same every time.  Outputs are apart from inputs and from each other.  K
  * below 2^20, V below 2^30, B (K + 1) below 2^28 (ATTN_ERR_UNSUPPORTED otherwise).
  */
 typedef struct attn_verify_drafts_params {

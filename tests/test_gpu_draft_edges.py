@@ -65,3 +65,28 @@ def test_verify_drafts_rows_that_end_inside_a_load(V, dtype, form):
         assert (accepted == 1).all()
 
 
+@pytest.mark.parametrize("odd", [None, float("inf")], ids=["finite", "with an infinity"])
+def test_verify_drafts_sums_of_half_a_billion_equal_weights(odd):
+    """0.1 for the first half of the row and 1/16, whose sums are exact, for the rest.  A sum that is off by d of the first half's
+    moves a token of the second half by d V 0.8 (1 - u): within 2^-34 of it not by one, as the tokens' shares of u are 0.3 to 0.7."""
+    V, half = (1 << 29) + 77, 1 << 28
+    p = torch.full((1, 1, V), 0.1, device=DEV)
+    p[..., half:] = 0.0625
+    first = half
+    if odd is not None:
+        p[..., 5] = odd  # counts as nothing, and every weight is looked at
+        first -= 1
+    w, scale = float(np.float32(0.1)).as_integer_ratio()
+    x = scale // 16
+    total = first * w + (V - half) * x  # of 1 / scale
+    found = 0
+    for k in range(1, 40):
+        u = float(np.float32(0.62 + 0.0093 * k))
+        num, den = u.as_integer_ratio()
+        want, part = divmod(num * total - den * first * w, den * x)
+        if not 0.3 < part / (den * x) < 0.7:
+            continue
+        found += 1
+        tokens, _, _ = AB.attn_verify_drafts(torch.zeros(1, 0, dtype=torch.int32, device=DEV), p, torch.tensor([[u]], device=DEV))
+        assert tokens.item() == half + want
+    assert found > 8 and AB.attn_get_device_status() == AB.ATTN_OK
