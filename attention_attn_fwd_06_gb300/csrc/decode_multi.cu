@@ -323,6 +323,17 @@ __device__ __forceinline__ int rows_of(const MultiArgs& a, const Piece& p) {
   return PAGED ? a.GP * p.nq : a.R;
 }
 
+// 1 / l, 0 for a row that sees no key, and its log-sum-exp.  Over pages a NaN sum (a query, a key or a logit that is no number) gives
+// NaN, as decode_rows.cu does; the contiguous kernel keeps its results (O = 0 for a NaN query, lse = -inf for any NaN sum).
+template <bool PAGED>
+__device__ __forceinline__ float inverse_of(float l) {
+  return (PAGED ? l != 0.f : l > 0.f) ? 1.f / l : 0.f;
+}
+template <bool PAGED>
+__device__ __forceinline__ float lse_of(float m, float l) {
+  return (PAGED ? l != 0.f : l > 0.f) ? (m + log2f(l)) * kLn2 : -INFINITY;
+}
+
 template <int D>
 __device__ __forceinline__ void store_row(const MultiArgs& a, size_t orow, int cc, const uint32_t (&orr)[32],
                                           float inv_l) {
@@ -764,7 +775,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float2 x =
                 __ffma2_rn(make_float2(__uint_as_float(sr[cc][2 * e]), __uint_as_float(sr[cc][2 * e + 1])), c2, n2);
             float2 pp = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-            if (!live) pp = make_float2(0.f, 0.f);
+            if (!PAGED && !live) pp = make_float2(0.f, 0.f);  // (the exponentials of -inf are 0; those of a NaN stay)
             rs[e & 1] = __fadd2_rn(rs[e & 1], pp);
             pk[cc >> 1][(cc & 1) * 16 + e] = tc::pack_bf16x2(pp.x, pp.y);
           }
@@ -831,15 +842,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       const size_t orow0 = out_row<PAGED>(a, pc, row);  // this thread's row of out
       if (pc.np == 1) {
         if (!ok) continue;
-        const float inv_l = (l > 0.f) ? 1.f / l : 0.f;
+        const float inv_l = inverse_of<PAGED>(l);
 #pragma unroll
         for (int cc = 0; cc < D / 32; ++cc) {
           uint32_t orr[32];
           tc::tmem_ld32(o_addr + cc * 32, orr);
           tc::tmem_ld_wait();
+          if (PAGED && l == 0.f) {  // (weights of 0 that met a NaN value)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) orr[e] = 0u;
+          }
           if (real) store_row<D>(a, orow0, cc, orr, inv_l);
         }
-        if (real && a.lse != nullptr) a.lse[orow0] = (l > 0.f) ? (m_ref + log2f(l)) * kLn2 : -INFINITY;
+        if (real && a.lse != nullptr) a.lse[orow0] = lse_of<PAGED>(m_ref, l);
         continue;
       }
       // partial: unnormalised O, m, l into this CTA's slot
@@ -964,7 +979,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < 8; ++j) o0[j] = __ldcg(s0 + j);
             fold(ml0, o0);
           }
-          const float inv_L = (L > 0.f) ? 1.f / L : 0.f;
+          const float inv_L = inverse_of<PAGED>(L);
+          if (PAGED && L == 0.f) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+          }
           const size_t orow = out_row<PAGED>(a, pc, r);
           if (a.out_f32) {
             float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + orow * D + ch * 32);
@@ -983,7 +1002,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               dst[j] = wv;
             }
           }
-          if (ch == 0 && a.lse != nullptr) a.lse[orow] = (L > 0.f) ? (M + log2f(L)) * kLn2 : -INFINITY;
+          if (ch == 0 && a.lse != nullptr) a.lse[orow] = lse_of<PAGED>(M, L);
         }
       }
       named_bar_sync(1, kSoftmaxThreads);  // last_flag is reused by the next piece

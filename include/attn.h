@@ -679,7 +679,9 @@ int attn_kv_append_paged(const attn_kv_append_paged_params* p);
  *                0 .. kv_len - n + t; one that sees no key gets O = 0, lse = -inf.  Keys at or
  *                past kv_len may hold anything.  (Keys that a token does not see because they
  *                are later tokens' own count with weight 0, so a NaN or an infinity in their
- *                values still reaches it.)
+ *                values still reaches it, unless it sees no key at all.)  A NaN among a head's
+ *                logits of a token, or one of +infinity, gives NaN in its O and its lse, and in
+ *                no other row's.
  *   out          apart from every input.  Weights are rounded to bf16 before they meet V.
  *   workspace    as attn_decode_q4: NULL for one of the library, its own, made by the first
  *                call on a device, which must not be one that is captured; or a DEVICE buffer

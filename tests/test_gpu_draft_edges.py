@@ -1,4 +1,5 @@
-"""GPU parity of a draft step's calls at the edges of what they allow: rows of probabilities that end inside a 16-byte load."""
+"""GPU parity of a draft step's calls at the edges of what they allow: rows of probabilities that end inside a 16-byte load or are
+very long, queries and values that are not numbers."""
 import numpy as np
 import pytest
 import torch
@@ -6,7 +7,7 @@ import torch
 import oracle
 from attention_attn_fwd_06_gb300 import binding as AB
 from attention_attn_fwd_06_gb300.build import build
-from tests.test_gpu_drafts import bf16, i32, probabilities
+from tests.test_gpu_drafts import Cache, bf16, i32, probabilities
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -90,3 +91,42 @@ def test_verify_drafts_sums_of_half_a_billion_equal_weights(odd):
         tokens, _, _ = AB.attn_verify_drafts(torch.zeros(1, 0, dtype=torch.int32, device=DEV), p, torch.tensor([[u]], device=DEV))
         assert tokens.item() == half + want
     assert found > 8 and AB.attn_get_device_status() == AB.ATTN_OK
+
+
+# ---------------------------------------------------------------- decode over pages
+
+def decode(c, q, new, f32=False, gap=0):
+    cu = i32(gap + np.concatenate([[0], np.cumsum(new)]))
+    o, ls = AB.attn_decode_multi_paged(q.to(DEV), *c.on_gpu(), cu, max(new), out_dtype=torch.float32 if f32 else torch.bfloat16)
+    assert AB.attn_get_device_status() == AB.ATTN_OK
+    return o, ls
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("lens", [[20], [9000, 300]])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq,new", [(8, 1), (11, 3), (8, 8), (13, 5), (16, 8)])  # 8, 33, 64, 65 and 128 rows of a kv head
+def test_decode_multi_paged_nan_queries_stay_in_their_rows(Hq, new, D, lens, bad):
+    c = Cache(lens, 1, D, 16, 3)
+    news = [new] + [1] * (len(lens) - 1)
+    q = bf16((sum(news), Hq, D), Hq)
+    hurt = q.clone()
+    hurt[0, 3, 5] = bad
+    for f32 in (False, True):
+        O, lse = decode(c, q, news, f32)
+        o, ls = decode(c, hurt, news, f32)
+        assert o[0, 3].isnan().all() and ls[0, 3].isnan()
+        o[0, 3], ls[0, 3] = O[0, 3], lse[0, 3]
+        assert torch.equal(o, O) and torch.equal(ls, lse)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq,new", [(2, 4), (16, 8)])
+def test_decode_multi_paged_tokens_without_keys_are_zero_beside_nan_values(Hq, new, D):
+    """A sequence of fewer keys than new tokens: the first ones see none, whatever the others' values are."""
+    c = Cache([new - 2], 1, D, 16, 3)
+    c.v[c.table[0, 0], :, new - 3] = float("nan")
+    q = bf16((new, Hq, D), 1)
+    for f32 in (False, True):
+        o, ls = decode(c, q, [new], f32)
+        assert (o[:2] == 0).all() and torch.isneginf(ls[:2]).all() and ls[2:].isfinite().all() and o[new - 1].isnan().all()
