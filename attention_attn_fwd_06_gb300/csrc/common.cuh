@@ -94,6 +94,12 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, unsign
   }
 }
 
+// The same for a whole warp, with one answer: a wait can run out in one lane while it just succeeds in another, and what a warp does
+// next (votes, shuffles, tensor memory) takes all of its lanes.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, unsigned* status, volatile int* abort) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, status, abort));
+}
+
 // 1-D bulk copy global -> shared on the TMA engine, completion counted in bytes on `bar`.
 // dst, src 16-byte aligned; bytes a multiple of 16.
 __device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {

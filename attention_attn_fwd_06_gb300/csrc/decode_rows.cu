@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(RowsCfg<D, RT>::THREADS, RowsCfg<D, RT>::MINB)
     const uint32_t dst0 = (uint32_t)(which * C::HALF + db * C::BLOCK + box * a.box_rows * 128);
     const void* const tm = which ? &tmv : &tmk;
     auto wait_empty = [&]() -> bool {
-      return t < C::NS || __all_sync(0xffffffffu, mbar_wait(&empty[slot], freed, a.status, abort_flag));
+      return t < C::NS || mbar_wait_warp(&empty[slot], freed, a.status, abort_flag);
     };
     auto next_slot = [&]() {
       ++t;
@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(RowsCfg<D, RT>::THREADS, RowsCfg<D, RT>::MINB)
       phase ^= 1;
     }
   };
-  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return mbar_wait(bar, parity, a.status, abort_flag); };
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return mbar_wait_warp(bar, parity, a.status, abort_flag); };
   int piece = 0;  // the next record, and its phase
   uint32_t piece_phase = 0;
   // Addresses within a stage of the lane's rows for ldmatrix: K's matrices are (keys 0-7, 8-15) x (dims 0-7, 8-15) of a step of

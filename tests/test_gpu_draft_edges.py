@@ -130,3 +130,19 @@ def test_decode_multi_paged_tokens_without_keys_are_zero_beside_nan_values(Hq, n
     for f32 in (False, True):
         o, ls = decode(c, q, [new], f32)
         assert (o[:2] == 0).all() and torch.isneginf(ls[:2]).all() and ls[2:].isfinite().all() and o[new - 1].isnan().all()
+
+
+@pytest.mark.parametrize("Hq", [8, 64, 128, 136])  # 4, 32, 64 and 68 rows of a kv head
+def test_decode_multi_paged_timeout_leaves_every_warp_together(monkeypatch, Hq):
+    """D = 64: CTA 0 withholds an arrival, so a bounded wait runs out after a second; all warps wind down, the next call is right."""
+    c = Cache([16384, 16000], 8, 64, 64, 3)
+    args = bf16((8, Hq, 64), 1).to(DEV), *c.on_gpu(), i32([0, 4, 8]), 4
+    want, wl = AB.attn_decode_multi_paged(*args)
+    assert AB.attn_get_device_status() == AB.ATTN_OK
+    monkeypatch.setenv("ATTN_FAULT_INJECT", "skip_arrive")
+    AB.attn_decode_multi_paged(*args)
+    assert AB.attn_get_device_status() == AB.ATTN_ERR_DEVICE_TIMEOUT
+    monkeypatch.delenv("ATTN_FAULT_INJECT")
+    out, lse = AB.attn_decode_multi_paged(*args)
+    assert AB.attn_get_device_status() == AB.ATTN_OK
+    assert torch.equal(out, want) and torch.equal(lse, wl)
