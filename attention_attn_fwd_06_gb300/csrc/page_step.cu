@@ -11,6 +11,8 @@
 // is one launch of one thread-block cluster: every CTA reads all lengths and scans them in its own shared memory
 // (three running sums: tokens, pages taken, pages given back), and a cluster barrier separates these reads from the
 // in-place writes, which needs no scratch memory and no second launch.
+#include <atomic>
+
 #include "common.cuh"
 #include "intdiv.h"
 #include "kernels.h"
@@ -225,7 +227,8 @@ __global__ void __launch_bounds__(kPageThreads) page_step_kernel(const PageStepL
 }  // namespace
 
 cudaError_t launch_page_step(const PageStepLaunch& p) {
-  static bool attr_set[64] = {};  // the shared-memory opt-in is per device
+  // the shared-memory opt-in is per device; host threads may be here at once
+  static std::atomic<bool> attr_set[64] = {};
   const size_t smem = ((size_t)6 * p.B + 3) * sizeof(int);
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);

@@ -40,6 +40,7 @@
 //
 // Every wait is bounded (common.cuh); on a timeout the CTA records the status,
 // drains its in-flight copies and MMAs, frees TMEM and exits.
+#include <atomic>
 #include <cmath>
 
 #include "common.cuh"
@@ -604,7 +605,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
 template <int D>
 cudaError_t launch_d(const PrefillLaunch& p) {
   using C = Cfg<D>;
-  static bool attr_set[64] = {};
+  // the shared-memory opt-in is per device; host threads may be here at once
+  static std::atomic<bool> attr_set[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;

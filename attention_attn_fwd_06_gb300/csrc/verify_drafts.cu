@@ -22,6 +22,7 @@
 // 131,072 15.9 us (4.2 TB/s, 0.63 of the copy bandwidth); 37 without distributions over 50,001 in bf16, one element a
 // load, 8.9 us.  Four CTAs an SM with twice the loads in flight 6.5 / 16.5 / 8.8 us, CTAs of 16 warps 7.6 / 21.2 / 11.5 us;
 // sums element by element with every weight's check 8.0 / 29.2 / 12.0 us, loads behind their conditions besides 7.9 / 28.6 / 15.6.
+#include <atomic>
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -549,7 +550,8 @@ __global__ void __launch_bounds__(32 * kVerifyWarps, 5) verify_drafts_kernel(con
 
 template <typename T, bool VEC, bool FAR>
 cudaError_t launch_t(const VerifyDraftsLaunch& p, int size, int segment) {
-  static bool attr_set[64] = {};  // clusters of more than 8 CTAs are opted into, per device
+  // clusters of more than 8 CTAs are opted into, per device; host threads may be here at once
+  static std::atomic<bool> attr_set[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;

@@ -1,5 +1,9 @@
 """GPU parity of a draft step's calls at the edges of what they allow: rows of probabilities that end inside a 16-byte load or are
 very long, queries and values that are not numbers."""
+import pathlib
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -146,3 +150,54 @@ def test_decode_multi_paged_timeout_leaves_every_warp_together(monkeypatch, Hq):
     out, lse = AB.attn_decode_multi_paged(*args)
     assert AB.attn_get_device_status() == AB.ATTN_OK
     assert torch.equal(out, want) and torch.equal(lse, wl)
+
+
+def test_calls_of_several_host_threads_at_once():
+    """In a process of its own, so that the threads' calls are the first ones: each gets its own results."""
+    code = """
+import threading, torch
+from attention_attn_fwd_06_gb300 import binding as AB
+AB.load()
+D = "cuda:0"
+g = torch.Generator().manual_seed(1)
+i32 = lambda *s, hi=100: torch.randint(0, hi, s, generator=g, dtype=torch.int32).to(D)
+probs = [torch.softmax(torch.randn(8, 5, V, generator=g), -1).to(D) for V in (1000, 1001, 70000, 300000)]
+drafts, u = i32(8, 4), torch.rand(8, 5, generator=g).to(D)
+q = torch.randn(1, 2, 200, 64, generator=g).bfloat16().to(D)
+gate, got, lock = threading.Barrier(12), {}, threading.Lock()
+torch.cuda.synchronize()
+
+def page():
+    lens, table, free, count = (torch.zeros(4, dtype=torch.int32, device=D), torch.zeros(4, 8, dtype=torch.int32, device=D),
+                                torch.arange(32, dtype=torch.int32, device=D), torch.tensor([32], dtype=torch.int32, device=D))
+    AB.attn_page_step(lens, table, free, count, 16, new_lens=torch.full((4,), 20, dtype=torch.int32, device=D))
+    return lens, table
+
+def work(i):
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        gate.wait()
+        outs = []
+        for _ in range(20):
+            if i < 8:
+                outs.append(AB.attn_verify_drafts(drafts, probs[i % 4], u)[:2])
+            elif i < 10:
+                outs.append(page())
+            else:
+                outs.append(AB.attn_fwd(q, q, q))
+        stream.synchronize()
+    with lock:
+        got[i] = outs
+
+threads = [threading.Thread(target=work, args=(i,)) for i in range(12)]
+[t.start() for t in threads]
+[t.join() for t in threads]
+assert len(got) == 12 and AB.attn_get_device_status() == AB.ATTN_OK
+want = [AB.attn_verify_drafts(drafts, p, u)[:2] for p in probs]
+for i, outs in got.items():
+    ref = want[i % 4] if i < 8 else page() if i < 10 else AB.attn_fwd(q, q, q)
+    assert all(torch.equal(a, b) for o in outs for a, b in zip(o, ref)), i
+print("alike")
+"""
+    run = subprocess.run([sys.executable, "-c", code], cwd=pathlib.Path(__file__).parent.parent, capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0 and "alike" in run.stdout, run.stderr[-2000:]
