@@ -2,8 +2,8 @@
 //
 // A pair's frequency comes in turns a position, as a 64-bit binary fraction F = round(2^64 f / 2 pi): the product with the
 // position, modulo 2^64, is the angle's fraction of a turn without rounding, whatever the position, where a product in
-// 32 bits would be off by whole radians (2^20 positions of a first pair: 2^-4 of a radian) and one in 64-bit floats runs at
-// a fiftieth of the rate.  F's own rounding moves the angle of position p by p 2^-65 turns, the host's 64-bit f by p 2^-53
+// 32 bits would be off by 2^-4 of a radian at position 2^20 of a first pair (by 2^6 near 2^31) and one in 64-bit floats runs at
+// a fiftieth of the rate.  F's own rounding moves the angle of position p by p 2^-65 turns, the host's 64-bit f by p 2^-51
 // of its size.  The fraction's nearest quarter turn picks which of sin and cos is which, and its sign; the rest, at most an
 // eighth of a turn, is rounded to fp32 (2^-24 of itself) before polynomials give its sine and cosine.
 //

@@ -585,7 +585,8 @@ unsigned long long attn_decode_q4_workspace_bytes(int Hq, int Hkv, int Lq, int D
  *                             a = max(0, floor(c(high))) and b = min(R - 1, ceil(c(low))),
  *                             c(t) = (R / 2) ln(context / (2 pi t)) / ln(base): the pair of t turns
  * Angles are kept as fractions of a turn in 64 bits, so that far positions are about as exact
- * as near ones: within 2^-22 + 2^-50 of the angle, times the amplitude.
+ * as near ones: within 2^-22 + 2^-50 of the angle, times the amplitude.  (On the ramps of TURNS and
+ * INDEX g is rounded too, in 64 bits: TURNS' by 2^-49 high / (high - low).)
  *
  *   cos, sin    fp32 [rows, rotary_dim / 2], 16-byte aligned, apart from each other
  *   rotary_dim  16, 32 .. 128: the rotated dims of a head.  Tables of rotary_dim = D are

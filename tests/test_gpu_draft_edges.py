@@ -1,8 +1,10 @@
 """GPU parity of a draft step's calls at the edges of what they allow: rows of probabilities that end inside a 16-byte load or are
-very long, queries and values that are not numbers."""
+very long, queries and values that are not numbers, rotary tables of large bases."""
+import math
 import pathlib
 import subprocess
 import sys
+from decimal import Decimal, localcontext
 
 import numpy as np
 import pytest
@@ -201,3 +203,38 @@ print("alike")
 """
     run = subprocess.run([sys.executable, "-c", code], cwd=pathlib.Path(__file__).parent.parent, capture_output=True, text=True, timeout=300)
     assert run.returncode == 0 and "alike" in run.stdout, run.stderr[-2000:]
+
+
+# ---------------------------------------------------------------- rotary tables
+
+PI = Decimal("3.141592653589793238462643383279502884197169399375105820974944592307816406286")
+
+
+def exact_frequencies(R, base, scaling):
+    """Radians a position, to some 70 digits."""
+    log = Decimal(base).ln()
+    if scaling and scaling[0] == "base":
+        log += Decimal(R) / (R - 2) * Decimal(scaling[1]).ln()
+    return [(-Decimal(2 * i) / R * log).exp() / (Decimal(scaling[1]) if scaling and scaling[0] == "linear" else 1)
+            for i in range(R // 2)]
+
+
+@pytest.mark.parametrize("base,R,scaling", [
+    (1e8, 112, None), (1e8, 80, ("linear", 4.0)), (1e4, 96, ("base", 1e10)), (1e20, 128, None),
+    (1e20, 112, ("linear", 1e-12)),  # pairs of many turns a position: the angle's own bound counts
+    (1e300, 112, ("linear", 1e-18)), (1e8, 48, ("linear", 1e-10)), (1e20, 80, ("base", 1e100)),
+])
+def test_rope_tables_of_large_bases_far_out(base, R, scaling):
+    """The header's bound, 2^-22 and 2^-50 of the angle, against 70 digits."""
+    start, rows, amplitude = 2 ** 31 - 8, 6, 1.3
+    cos, sin = (t.double().cpu() for t in AB.attn_rope_tables(rows, R, base=base, scaling=scaling, amplitude=amplitude, start=start,
+                                                              device=DEV))
+    with localcontext(prec=70):
+        f = exact_frequencies(R, base, scaling)
+        for r in range(rows):
+            for i in range(R // 2):
+                ang = (start + r) * f[i]
+                rest = float(ang % (2 * PI))
+                bound = amplitude * (2.0 ** -22 + 2.0 ** -50 * float(ang))
+                assert abs(cos[r, i].item() - amplitude * math.cos(rest)) <= bound, (r, i, float(ang))
+                assert abs(sin[r, i].item() - amplitude * math.sin(rest)) <= bound, (r, i, float(ang))
