@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kAppendBlocks) kv_append_pa
         turn_b = cb < 2 * rot;
       }
       const int ia = STYLE == 1 ? 8 * sub : 4 * ca, ib = STYLE == 1 ? 8 * sub + 4 : 4 * cb;
-if (turn_a) {
+      if (turn_a) {
         *reinterpret_cast<float4*>(c) = *reinterpret_cast<const float4*>(tab + ia);
         *reinterpret_cast<float4*>(s) = *reinterpret_cast<const float4*>(tab + D / 2 + ia);
       }
