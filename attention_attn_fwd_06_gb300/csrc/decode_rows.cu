@@ -6,7 +6,7 @@
 //
 // What bounds it: HBM (each key and value is read once for all rows of its kv head), and over short caches the chain of a launch
 // and of each row.  A tile of 128 tcgen05 rows is one CTA an SM, whose roles wait for one another tile by tile: 64 short
-// sequences of 16 heads and a few tokens took 50.5 us there, 23.6 here.  Here two or three CTAs share an SM, and a warp takes 32
+// sequences of 16 heads and a few tokens took 50.5 us there, 23.2 here.  Here two or three CTAs share an SM, and a warp takes 32
 // keys by itself:
 //  * mma.sync m16n8k16 (bf16): A is 16 query rows, kept in registers for a whole piece, B 16 dims of 8 keys by ldmatrix.  The
 //    scores' accumulators are, packed to bf16, the second product's A operand as they stand; V comes by transposing ldmatrix.
@@ -27,17 +27,17 @@
 // as in decode_multi.cu), whose adds truncate: over a slice of 131,072 keys some 2^-13 of the terms' sum.
 //
 // Measured (CUDA-graph replays over rotating pools; 32 query and 8 kv heads, D = 128; in brackets the tcgen05 tiles): 8 sequences
-// of 512 to 4096 keys on 16-key pages, 4 tokens each 21.6 us (25.7), 8 tokens 24.6 (27.1); 4 of 32k to 131k keys, 8 tokens
-// 270 us, 6.7 TB/s, the copy bandwidth (270.6); 64 of 512 to 1536 keys, 8 tokens 50.8 (69.1); one token to 5 of 64 sequences
-// of up to 700 keys with 16 heads of D = 64, 48-key pages 23.6 us (50.5).
-// Of the 24.6 us, by timer stamps of an earlier form: 2.5 to the first copy, 0.9 until it lands, 12 of stream, 1 of exchange, 3.5
-// (rows of 5 pieces) to 8 (of 10) of merge.  Six stages a CTA in place of five: 24.8, and 282 us over the long caches (the
+// of 512 to 4096 keys on 16-key pages, 4 tokens each 21.6 us (25.7), 8 tokens 24.9 (27.1); 4 of 32k to 131k keys, 8 tokens
+// 265 us, 6.8 TB/s, the copy bandwidth (270.6); 64 of 512 to 1536 keys, 8 tokens 50.8 (69.1); one token to 5 of 64 sequences
+// of up to 700 keys with 16 heads of D = 64, 48-key pages 23.2 us (50.5).  At D = 128 4 to 24 bytes of registers spill, at D = 64 none.
+// Of the 24.9 us, by timer stamps of an earlier form: 2.5 to the first copy, 0.9 until it lands, 12 of stream, 1 of exchange, 3.5
+// (rows of 5 pieces) to 8 (of 10) of merge.  Six stages a CTA in place of five: 24.8 against 24.6, and 282 us over the long caches (the
 // SMs nearer to memory run further ahead, and finish 4 % apart); three CTAs at D = 128: 32 to 38 and 370 to 440 us, at D = 64
 // with 32 rows 36.1 against 32.3 us (64 sequences of 350 to 700 keys, 16 kv heads; with 16 rows 28.7 against 30.2); one CTA of
 // eight warps with ten stages: 27 to 34 and 327 to 504 us (one producer warp's chain is the stream's bound); two producers
 // for two CTAs: 25.7 and 278 us; a piece counted before it is published: 27.4 against 26.2 us that day; divisions in the
 // producer's stage: 26.2, 59 against 51 us over the 64.  A CTA's last row merged through the idle ring, all of its pieces' words
-// in flight at once: 24.1, but 18.0 against 16.8 us with 8 rows over one sequence of 4000 keys and 57.5 against 55.5 with 32
+// in flight at once: 24.1 against 24.6, but 18.0 against 16.8 us with 8 rows over one sequence of 4000 keys and 57.5 against 55.5 with 32
 // rows of D = 64 over 64 of 3000: the words themselves are on their way when they are asked for.
 #include <cmath>
 #include <type_traits>

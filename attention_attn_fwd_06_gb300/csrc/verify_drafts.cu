@@ -13,15 +13,16 @@
 // adds a clock and SM: with the joins in them 8 sequences over 32,000 tokens took 20.5 us a call, 12 without.)
 //
 // What bounds it: for few sequences the chain of launch, drafts (1.4 us), the row (1.1), the exchange (0.7), the segment (0.6)
-// and the token in it (2 us), by timer stamps of 8 sequences; for many, reading one row of p and of q each, beside that chain.
-// A cluster of CTAs takes a sequence: every CTA decides which drafts stand by itself, its warps sum a segment of the row each,
+// and the token in it (2 us), by timer stamps of 8 sequences; for many, reading a row of p each, and of q where a draft is refused,
+// beside that chain.  A cluster of CTAs takes a sequence: every CTA decides which drafts stand by itself, its warps sum a segment of the row each,
 // the segments' sums go to every CTA of the cluster through distributed shared memory, and the CTA that holds the segment where
 // the sum passes u's share reads that segment again (from L2), its warps a piece each, and finds the token.  CTAs of 8 warps at 48
 // registers, so that five share an SM and one's chain runs beside another's reading.
-// Measured (CUDA-graph replays over rotating inputs): 8 sequences of 4 drafts over 32,000 tokens 6.3 us; 64 of up to 8 over
-// 131,072 15.9 us (4.2 TB/s, 0.63 of the copy bandwidth); 37 without distributions over 50,001 in bf16, one element a
-// load, 8.9 us.  Four CTAs an SM with twice the loads in flight 6.5 / 16.5 / 8.8 us, CTAs of 16 warps 7.6 / 21.2 / 11.5 us;
-// sums element by element with every weight's check 8.0 / 29.2 / 12.0 us, loads behind their conditions besides 7.9 / 28.6 / 15.6.
+// Measured (CUDA-graph replays over rotating inputs): 8 sequences of 4 drafts over 32,000 tokens 6.6 us; 64 of up to 8 over
+// 131,072 16.2 us (a draft refused in half of them: 51.5 MB, 3.2 TB/s, 0.48 of the copy bandwidth); 37 without distributions over
+// 50,001 in bf16, one element a load, 9.3 us.  Beside 6.3 / 15.9 / 8.9 us of the day: four CTAs an SM with twice the loads in
+// flight 6.5 / 16.5 / 8.8 us, CTAs of 16 warps 7.6 / 21.2 / 11.5 us; sums element by element with every weight's check 8.0 / 29.2 /
+// 12.0 us, loads behind their conditions besides 7.9 / 28.6 / 15.6.
 #include <atomic>
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
