@@ -82,10 +82,11 @@ __device__ __forceinline__ Sum plus(Sum a, Sum b) {
 // a > b, both settled (where the leading parts are near each other their difference is exact; where they are not it decides)
 __device__ __forceinline__ bool above(Sum a, Sum b) { return (a.s - b.s) + (a.e - b.e) > 0.f; }
 __device__ __forceinline__ bool positive(Sum a) { return a.s > 0.f; }
-// u times a
+// u times a; NaN, which nothing is above, unless u < 1: added up otherwise, the weights short of the last ones may come out as their
+// total or an ulp of the rests past it
 __device__ __forceinline__ Sum share(float u, Sum a) {
   Sum r;
-  r.s = u * a.s;
+  r.s = u < 1.f ? u * a.s : NAN;
   r.e = fmaf(u, a.s, -r.s) + u * a.e;
   r.settle();
   return r;

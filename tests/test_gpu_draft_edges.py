@@ -72,6 +72,24 @@ def test_verify_drafts_rows_that_end_inside_a_load(V, dtype, form):
         assert (accepted == 1).all()
 
 
+@pytest.mark.parametrize("last", [1.0, 2.0, float("inf"), float("nan")])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("V", [9, 300, 1003, 70000, 600000])
+def test_verify_drafts_numbers_of_one_and_more_draw_the_last_token_with_any_weight(V, dtype, last):
+    """The last weights are far below the sum's last bit, whatever the order that the others are added up in."""
+    g = torch.Generator(device=DEV).manual_seed(V)
+    B = 40 if V < 100000 else 6
+    p = torch.rand(B, 1, V, generator=g, device=DEV).to(dtype)
+    p[..., -4:] = 0
+    p[..., -3] = 1e-30
+    u = torch.full((B, 1), last, device=DEV)
+    for padding in (0, 3):
+        wide = torch.full((B, 1, V + padding), 1.0, dtype=dtype, device=DEV)
+        wide[..., :V] = p
+        tokens, _, _ = AB.attn_verify_drafts(torch.zeros(B, 0, dtype=torch.int32, device=DEV), wide[..., :V], u)
+        assert tokens.flatten().tolist() == [V - 3] * B and AB.attn_get_device_status() == AB.ATTN_OK
+
+
 @pytest.mark.parametrize("odd", [None, float("inf")], ids=["finite", "with an infinity"])
 def test_verify_drafts_sums_of_half_a_billion_equal_weights(odd):
     """0.1 for the first half of the row and 1/16, whose sums are exact, for the rest.  A sum that is off by d of the first half's
