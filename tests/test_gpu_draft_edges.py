@@ -90,6 +90,17 @@ def test_verify_drafts_numbers_of_one_and_more_draw_the_last_token_with_any_weig
         assert tokens.flatten().tolist() == [V - 3] * B and AB.attn_get_device_status() == AB.ATTN_OK
 
 
+@pytest.mark.parametrize("V", [4, 5000])
+def test_verify_drafts_weights_of_the_smallest_numbers(V):
+    """Multiples of fp32's smallest number, and numbers whose share of their sum is one: exact."""
+    w = np.zeros(V, np.float32)
+    w[[0, 1, V - 2, V - 1]] = np.array([3, 5, 7, 1]) * 2.0 ** -149
+    p = torch.from_numpy(w).view(1, 1, V).to(DEV)
+    for u, want in ((0.0, 0), (0.125, 0), (0.25, 1), (0.5, V - 2), (0.9375, V - 1), (1.0, V - 1)):
+        tokens, _, _ = AB.attn_verify_drafts(torch.zeros(1, 0, dtype=torch.int32, device=DEV), p, torch.tensor([[u]], device=DEV))
+        assert tokens.item() == want and AB.attn_get_device_status() == AB.ATTN_OK
+
+
 @pytest.mark.parametrize("odd", [None, float("inf")], ids=["finite", "with an infinity"])
 def test_verify_drafts_sums_of_half_a_billion_equal_weights(odd):
     """0.1 for the first half of the row and 1/16, whose sums are exact, for the rest.  A sum that is off by d of the first half's
